@@ -1,7 +1,9 @@
 """CONF-KV decode-step cache manager for GB300: thin Python binding.
 
 This module only marshals arguments to the C ABI declared in
-``include/confkv.h`` (``libconfkv.so``, built in-tree by ``build.py``).  Every
+``include/confkv.h`` (``libconfkv.so``, built in-tree by ``build.py``); the
+paged cache and beam selection of ``include/confkv_paged.h`` are bound in
+``paged.py`` and reached from here as ``PagedKV`` and ``BeamSelect``.  Every
 step of the path runs in the library's CUDA kernels; if the library is
 missing, importing the binding's entry points raises -- there is no CPU
 fallback.
@@ -28,14 +30,20 @@ POLICY_CONFKV, POLICY_WINDOW, POLICY_H2O, POLICY_RANDOM = 0, 1, 2, 3
 FLAG_NONFINITE = 1
 FLAG_CAPACITY = 2
 FLAG_TIMEOUT = 4
+FLAG_BAD_PAGE = 8
+FLAG_BAD_INDEX = 16
 
-# every symbol declared in include/confkv.h
+# every symbol declared in include/*.h
 EXPORTS = ("confkv_create", "confkv_prefill", "confkv_step", "confkv_step_host",
            "confkv_stats", "confkv_read_cache", "confkv_profile_enable",
            "confkv_profile_read", "confkv_last_error", "confkv_free",
            "confkv_confidence_noalloc", "confkv_step_begin", "confkv_step_layer",
            "confkv_attention_path", "confkv_selftest_bounded_wait",
-           "confkv_read_channel_exponents")
+           "confkv_read_channel_exponents",
+           "confkv_paged_create", "confkv_paged_free", "confkv_paged_last_error",
+           "confkv_paged_status", "confkv_paged_append", "confkv_paged_attend",
+           "confkv_paged_commit", "confkv_paged_fork", "confkv_beam_workspace",
+           "confkv_beam_select")
 
 
 def selftest_bounded_wait(device=0, timeout_us=1000):
@@ -127,6 +135,8 @@ def load_library(path=LIB_PATH):
     L.confkv_read_channel_exponents.argtypes = [vp, ci, ci, vp, vp]
     L.confkv_confidence_noalloc.restype = ci
     L.confkv_confidence_noalloc.argtypes = [vp, ci, ci, cf, ci, ci, vp, vp, vp, vp]
+    from . import paged
+    paged.declare(L)
     _lib = L
     return L
 
@@ -322,3 +332,6 @@ class ConfKV:
         p = Profile()
         self._check(self._L.confkv_profile_read(self._h, ctypes.byref(p)))
         return {p.names[i].decode(): (p.launches[i], p.total_ms[i]) for i in range(p.n_kernels)}
+
+
+from .paged import BeamSelect, PagedBatch, PagedKV  # noqa: E402

@@ -1,0 +1,434 @@
+// Beam selection: the best K of beams x vocabulary by summed log-probability.
+//
+//   score(w, v) = scores[w] + z_wv - lse_w,   lse_w = ln sum_u exp z_wu
+//
+// Within a beam the order is that of its logits, so only each row's best K
+// can be among the best K of all.  One pass over the logits: a CTA holds one
+// slice of one row in registers, reduces it to (max, sum of exponentials) and
+// its best K logits; the CTA that takes a sequence's last ticket (no CTA
+// waits) joins the slices and orders the candidates.
+//
+// Best K of a block's values: every lane knows its own largest value; the
+// r-th largest of a warp's lane maxima bounds the warp's r-th largest value
+// from below, so the best bound over the warps keeps K values at least and,
+// on data in no particular order, few more.  The kept ones are ranked by
+// counting.  Should more be kept than the buffer holds (long runs of equal
+// values, or an order that follows the lanes), K rounds of a block-wide
+// maximum give the same answer.
+//
+// Precision: exponentials and their sums per thread are fp32, relative to the
+// slice's maximum (the largest terms are exact); sums over threads and slices,
+// lse and the candidates' scores are double, so candidates of different beams
+// are ordered to ~1e-8; scores are rounded to fp32 once, at the end.  Equal
+// scores go to the lower (beam, token).
+#include <cmath>
+
+#include "paged_internal.cuh"
+
+namespace confkv {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCap = 1024;            // candidates ranked by counting
+constexpr int kMaxBeams = 32;
+constexpr float kL2E = 1.4426950408889634f;
+
+struct SlicePart {
+  double sum;       // sum of exp(z - max) over the slice
+  float max;
+  int bad;          // a NaN or +inf was seen
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// order-preserving integers (-0 counts as +0)
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
+}
+__device__ __forceinline__ unsigned long long ordered(double x) {
+  const unsigned long long u = __double_as_longlong(x + 0.0);
+  return u ^ (static_cast<unsigned long long>(static_cast<long long>(u) >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double unordered(unsigned long long u) {
+  return __longlong_as_double((u & 0x8000000000000000ull) ? u ^ 0x8000000000000000ull : ~u);
+}
+
+// (key, tie) pairs order by key, then by the larger tie
+struct Cand {
+  unsigned long long key, tie;
+};
+__device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
+  return a.key > b.key || (a.key == b.key && a.tie > b.tie);
+}
+
+// r-th largest (r = 1 .. 32) of the warp's 32 values, in every lane: a bitonic
+// sort by shuffles
+template <typename T>
+__device__ __forceinline__ T warp_rth(T x, int r) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1) {
+#pragma unroll
+    for (int step = size >> 1; step > 0; step >>= 1) {
+      const T y = __shfl_xor_sync(0xffffffffu, x, step);
+      const bool desc = (lane & size) == 0;
+      const bool low = (lane & step) == 0;
+      x = (low == desc) ? (x > y ? x : y) : (x < y ? x : y);
+    }
+  }
+  return __shfl_sync(0xffffffffu, x, r - 1);
+}
+
+// A value that at least K of the block's values reach, from each thread's
+// largest (all threads call it; two barriers)
+template <typename T>
+__device__ __forceinline__ T block_bound(T mine, int K, T* s_w) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nw = (K + 31) >> 5;
+  const T t = warp_rth(mine, (K + nw - 1) / nw);
+  if (lane == 0) s_w[warp] = t;
+  __syncthreads();
+  const T w = warp_rth(s_w[lane & (kWarps - 1)], 2 * nw - 1);   // each warp's bound twice: ranks 1, 3, ..
+  __syncthreads();
+  return w;
+}
+
+template <int DT>
+__device__ __forceinline__ float elem(uint32_t w, int half) {
+  if constexpr (DT == CONFKV_BF16) {
+    return __uint_as_float(half ? (w & 0xffff0000u) : (w << 16));
+  } else {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(half ? w >> 16 : w)));
+  }
+}
+
+__device__ __forceinline__ Cand block_best(Cand c, Cand* s_best) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Cand d;
+    d.key = __shfl_xor_sync(0xffffffffu, c.key, o);
+    d.tie = __shfl_xor_sync(0xffffffffu, c.tie, o);
+    if (before(d, c)) c = d;
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s_best[threadIdx.x >> 5] = c;
+  __syncthreads();
+  c = s_best[0];
+  for (int w = 1; w < kWarps; ++w)
+    if (before(s_best[w], c)) c = s_best[w];
+  return c;
+}
+
+template <int DT, int EPT>
+__global__ void __launch_bounds__(kThreads, 2)
+k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand, unsigned int* ticket) {
+  constexpr int VEC = DT == CONFKV_FP32 ? 4 : 8;      // elements of a 16-byte word
+  constexpr int NV = EPT / VEC;
+  __shared__ Cand s_list[kCap];
+  __shared__ double s_sum[kWarps];
+  __shared__ float s_f[kWarps];
+  __shared__ double s_d[kWarps];
+  __shared__ Cand s_best[kWarps];
+  __shared__ double s_base[kMaxBeams];
+  __shared__ int s_cnt, s_bad, s_last;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = blockIdx.y, b = row / a.W;
+  const size_t slice = static_cast<size_t>(row) * C + blockIdx.x;
+  if (tid == 0) s_cnt = s_bad = 0;
+  pdl_wait();
+  pdl_trigger();
+  const float score = a.scores[row];
+  const bool skip = (a.finished && a.finished[row]) || !(score > -INFINITY) || !(score < INFINITY);
+  if (!skip) {
+    uint4 x[NV];
+    // 16-byte words counted from the aligned address at or before the row
+    const int size = DT == CONFKV_FP32 ? 4 : 2;
+    const char* base = static_cast<const char*>(a.logits) + static_cast<size_t>(row) * a.stride * size;
+    const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15) / size);
+    const long long w0 = static_cast<long long>(blockIdx.x) * (kThreads * NV);
+    const uint32_t ninf = DT == CONFKV_FP32 ? 0xff800000u : DT == CONFKV_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const long long v = (w0 + i * kThreads + tid) * VEC - lead;   // token of the word's first element
+      if (v >= 0 && v + VEC <= a.V) {
+        x[i] = __ldcs(reinterpret_cast<const uint4*>(base + v * size));
+      } else {
+        uint32_t w[4] = {ninf, ninf, ninf, ninf};
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          if (v + e < 0 || v + e >= a.V) continue;
+          if constexpr (DT == CONFKV_FP32) {
+            w[e] = reinterpret_cast<const uint32_t*>(base)[v + e];
+          } else {
+            const uint32_t h = reinterpret_cast<const uint16_t*>(base)[v + e];
+            w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | (h << 16) : (w[e >> 1] & 0xffff0000u) | h;
+          }
+        }
+        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    auto value = [&](int i, int e) -> float {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i]);
+      if constexpr (DT == CONFKV_FP32) return __uint_as_float(w[e]);
+      else return elem<DT>(w[e >> 1], e & 1);
+    };
+    float m = -INFINITY;
+    int bad = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float z = value(i, e);
+        bad |= !(z < INFINITY);
+        m = fmaxf(m, z);
+      }
+    const float bound = block_bound(m, a.K, s_f);
+    float bm = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+    if (lane == 0) s_f[warp] = bm;
+    if (bad) s_bad = 1;
+    __syncthreads();
+    bm = s_f[0];
+    for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, s_f[w]);
+    float sum = 0.0f;
+    if (bm > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float z = value(i, e);
+          // (z - max) exactly first: the product alone would lose the digits of large logits
+          sum += ex2((z - bm) * kL2E);
+          if (z >= bound && z > -INFINITY) {
+            const int at = atomicAdd(&s_cnt, 1);
+            if (at < kCap) {
+              const uint32_t v = static_cast<uint32_t>((w0 + i * kThreads + tid) * VEC - lead + e);
+              s_list[at].key = (static_cast<unsigned long long>(ordered(z)) << 32) | (0xffffffffu - v);
+            }
+          }
+        }
+    }
+    double ds = sum;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
+    if (lane == 0) s_sum[warp] = ds;
+    __syncthreads();
+    const int cnt = s_cnt;
+    unsigned long long* out = cand + slice * a.K;
+    if (tid == 0) {
+      double t = 0.0;
+      for (int w = 0; w < kWarps; ++w) t += s_sum[w];
+      part[slice] = SlicePart{t, bm, s_bad};
+    }
+    if (cnt <= kCap) {
+      for (int i = tid; i < cnt; i += kThreads) {
+        const unsigned long long k = s_list[i].key;
+        int rank = 0;
+        for (int j = 0; j < cnt; ++j) rank += s_list[j].key > k;
+        if (rank < a.K) out[rank] = k;
+      }
+      for (int i = cnt + tid; i < a.K; i += kThreads) out[i] = 0;
+    } else {
+      Cand last{~0ull, 0};
+      for (int r = 0; r < a.K; ++r) {
+        Cand c{0, 0};
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float z = value(i, e);
+            const uint32_t v = static_cast<uint32_t>((w0 + i * kThreads + tid) * VEC - lead + e);
+            const unsigned long long k = (static_cast<unsigned long long>(ordered(z)) << 32) | (0xffffffffu - v);
+            if (z > -INFINITY && k < last.key && k > c.key) c.key = k;
+          }
+        last = block_best(c, s_best);
+        if (tid == 0) out[r] = last.key;
+        if (last.key == 0) {        // nothing left: the rest is empty
+          for (int i = r + 1 + tid; i < a.K; i += kThreads) out[i] = 0;
+          break;
+        }
+      }
+    }
+  }
+  // the sequence's last CTA goes on
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    s_last = atomicAdd(&ticket[b], 1u) == static_cast<unsigned>(C * a.W - 1);
+    s_cnt = 0;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  if (tid == 0) ticket[b] = 0u;
+
+  // each beam's score minus lse (NaN: no candidates of its logits)
+  for (int w = warp; w < a.W; w += kWarps) {
+    const int r = b * a.W + w;
+    const float sc = a.scores[r];
+    int flag = 0;
+    double base = __longlong_as_double(0x7ff8000000000000ll);
+    if (!(sc < INFINITY)) {
+      flag = CONFKV_FLAG_NONFINITE;
+    } else if (sc > -INFINITY && !(a.finished && a.finished[r])) {
+      const SlicePart* pp = part + static_cast<size_t>(r) * C;
+      float m = -INFINITY;
+      int bad = 0;
+      for (int c = lane; c < C; c += 32) {
+        m = fmaxf(m, __ldcg(&pp[c].max));
+        bad |= __ldcg(&pp[c].bad);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      bad = __any_sync(0xffffffffu, bad);
+      if (bad || !(m > -INFINITY)) {
+        flag = CONFKV_FLAG_NONFINITE;
+      } else {
+        double s = 0.0;
+        for (int c = lane; c < C; c += 32)
+          s += __ldcg(&pp[c].sum) * exp(static_cast<double>(__ldcg(&pp[c].max)) - static_cast<double>(m));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        base = static_cast<double>(sc) - (static_cast<double>(m) + log(s));
+      }
+    }
+    if (lane == 0) {
+      s_base[w] = base;
+      if (a.flags_out) a.flags_out[r] = flag;
+    }
+  }
+  __syncthreads();
+
+  // candidate i of the sequence: slice lists, then one of each finished beam
+  const int per = C * a.K, n = a.W * per;
+  auto candidate = [&](int i) -> Cand {
+    Cand c{0, 0};
+    if (i < n) {
+      const int w = i / per;
+      const double base = s_base[w];
+      if (base == base) {
+        const unsigned long long k = __ldcg(cand + static_cast<size_t>(b) * n + i);
+        if (k) {
+          c.key = ordered(base + static_cast<double>(unordered(static_cast<uint32_t>(k >> 32))));
+          c.tie = ~((static_cast<unsigned long long>(w) << 32) | (0xffffffffu - static_cast<uint32_t>(k)));
+        }
+      }
+    } else {
+      const int w = i - n;
+      const float sc = a.scores[b * a.W + w];
+      if (a.finished && a.finished[b * a.W + w] && sc > -INFINITY && sc < INFINITY) {
+        c.key = ordered(static_cast<double>(sc));
+        c.tie = ~((static_cast<unsigned long long>(w) << 32) | static_cast<unsigned>(a.pad));
+      }
+    }
+    return c;
+  };
+  unsigned long long top = 0;
+  for (int i = tid; i < n + a.W; i += kThreads) {
+    const unsigned long long k = candidate(i).key;
+    top = k > top ? k : top;
+  }
+  const unsigned long long bound = block_bound(top, a.K, reinterpret_cast<unsigned long long*>(s_d));
+  for (int i = tid; i < n + a.W; i += kThreads) {
+    const Cand c = candidate(i);
+    if (c.key && c.key >= bound) {
+      const int at = atomicAdd(&s_cnt, 1);
+      if (at < kCap) s_list[at] = c;
+    }
+  }
+  __syncthreads();
+  const int cnt = s_cnt;
+  auto put = [&](int r, const Cand& c) {
+    const size_t o = static_cast<size_t>(b) * a.K + r;
+    const unsigned long long at = ~c.tie;
+    a.score_out[o] = c.key ? static_cast<float>(unordered(c.key)) : -INFINITY;
+    a.parent_out[o] = c.key ? static_cast<int>(at >> 32) : -1;
+    a.token_out[o] = c.key ? static_cast<int>(at & 0xffffffffull) : -1;
+  };
+  if (cnt <= kCap) {
+    for (int i = tid; i < cnt; i += kThreads) {
+      const Cand c = s_list[i];
+      int rank = 0;
+      for (int j = 0; j < cnt; ++j) rank += before(s_list[j], c);
+      if (rank < a.K) put(rank, c);
+    }
+    for (int i = cnt + tid; i < a.K; i += kThreads) put(i, Cand{0, 0});
+  } else {
+    Cand last{~0ull, ~0ull};
+    for (int r = 0; r < a.K; ++r) {
+      Cand best{0, 0};
+      for (int i = tid; i < n + a.W; i += kThreads) {
+        const Cand c = candidate(i);
+        if (c.key && before(last, c) && before(c, best)) best = c;
+      }
+      last = block_best(best, s_best);
+      if (tid == 0) put(r, last);
+      if (!last.key) {
+        for (int i = r + 1 + tid; i < a.K; i += kThreads) put(i, Cand{0, 0});
+        break;
+      }
+    }
+  }
+}
+
+// Elements per thread: short slices while they do not fill the GPU twice (a
+// slice's fixed cost is then latency), long ones where there are many rows.
+int beam_ept(long long rows, int V, int dtype) {
+  const long long short_slices = rows * ((V + kThreads * 8 - 1) / (kThreads * 8));
+  if (short_slices <= 2 * 152) return 8;
+  return dtype == CONFKV_FP32 ? 32 : 64;
+}
+int beam_slices(long long rows, int V, int dtype) {
+  const int per = kThreads * beam_ept(rows, V, dtype);
+  const int lead = dtype == CONFKV_FP32 ? 3 : 7;     // a row may start inside a 16-byte word
+  return static_cast<int>((static_cast<long long>(V) + lead + per - 1) / per);
+}
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <int DT>
+cudaError_t launch_dt(const BeamArgs& a, int C, SlicePart* part, unsigned long long* cand,
+                      unsigned int* ticket, cudaStream_t s) {
+  const dim3 grid(C, a.B * a.W);
+  constexpr int kLong = DT == CONFKV_FP32 ? 32 : 64;
+  if (beam_ept(static_cast<long long>(a.B) * a.W, a.V, DT) == 8)
+    return launch_pdl(k_beam_select<DT, 8>, grid, dim3(kThreads), 0, s, a, C, part, cand, ticket);
+  return launch_pdl(k_beam_select<DT, kLong>, grid, dim3(kThreads), 0, s, a, C, part, cand, ticket);
+}
+
+}  // namespace
+
+// [tickets: batch][parts: rows x slices][candidates: rows x slices x K]
+size_t beam_workspace(int B, int W, int V, int K, int dtype) {
+  const size_t n = static_cast<size_t>(B) * W * beam_slices(static_cast<long long>(B) * W, V, dtype);
+  return round256(sizeof(unsigned int) * B) + round256(sizeof(SlicePart) * n) + sizeof(unsigned long long) * n * K;
+}
+
+cudaError_t launch_beam(const BeamArgs& a, cudaStream_t s) {
+  const int C = beam_slices(static_cast<long long>(a.B) * a.W, a.V, a.dtype);
+  const size_t n = static_cast<size_t>(a.B) * a.W * C;
+  char* w = static_cast<char*>(a.ws);
+  unsigned int* ticket = reinterpret_cast<unsigned int*>(w);
+  w += round256(sizeof(unsigned int) * a.B);
+  SlicePart* part = reinterpret_cast<SlicePart*>(w);
+  w += round256(sizeof(SlicePart) * n);
+  unsigned long long* cand = reinterpret_cast<unsigned long long*>(w);
+  cudaError_t e;
+  if (a.dtype == CONFKV_FP32) e = launch_dt<CONFKV_FP32>(a, C, part, cand, ticket, s);
+  else if (a.dtype == CONFKV_BF16) e = launch_dt<CONFKV_BF16>(a, C, part, cand, ticket, s);
+  else e = launch_dt<CONFKV_FP16>(a, C, part, cand, ticket, s);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace paged
+}  // namespace confkv
