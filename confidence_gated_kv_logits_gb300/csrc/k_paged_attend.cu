@@ -1,133 +1,389 @@
-// Attention of new rows (single tokens, prompt chunks, trees of drafted
-// tokens) over a paged cache.
+// Attention of few new rows per sequence over a paged cache (single tokens,
+// small trees): up to 16 query rows of a KV head at a time, streaming its
+// cached K and V once.
 //
-// One warp per (row, query head): each lane scores one key of a 32-key block
-// (fp32), the block joins the running softmax (maximum and sum in fp32), and
-// the lanes then add up their channels of the visible V rows.  Keys that the
-// row does not see are never read into the sums.
-#include <cfloat>
+//   o_r = sum_j p_rj v_j / sum_j p_rj,  p_rj = exp(scale (q_r k_j) - max)
+//
+// The work is the cache's bytes, so everything serves the stream of tiles:
+// each warp reads its own chunks of 8 KB (16 tokens at d = 128, 32 at d = 64;
+// K and V boxes of the page, by TMA with the 128-byte swizzle) through a ring
+// of its own, with no barrier between warps until the unit's end.  A chunk is
+// 16 query rows x its tokens on mma.sync m16n8k16 (rows on M: the query
+// fragments stay in registers, S's accumulators are P's A fragments as they
+// are); these rows are too few for tcgen05's 64 or 128, and the matrix work is
+// far below the memory's time.  Softmax statistics are fp32 per row and warp;
+// P is rounded to the cache's type (relative 2^-12 / 2^-9), which weighs as
+// much as the output's own rounding.  Warps join through shared memory, pieces
+// of a unit that was cut (paged_sched.cuh) through the handle's scratch.
+//
+// Chunks that reach past what every row sees are masked by bits per row; in
+// them V's rows past the end are zeroed in shared memory, and so are
+// non-finite elements (0 x NaN would reach rows that do not see them), which
+// the rows that do see them get added by hand.
+#include <cstring>
 
-#include "paged_internal.cuh"
+#include "paged_attend.cuh"
 
 namespace confkv {
 namespace paged {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 2;
+constexpr int kRows = kFewRows;
+constexpr int kChunkBytes = 4 * kFewChunk;
 constexpr float kL2E = 1.4426950408889634f;
 
+template <int D>
+struct Few {
+  static constexpr int CH = kFewChunk / D;             // tokens of a chunk
+  static constexpr int NT = CH / 8;                // score column tiles
+  static constexpr int KS = D / 16;                // k-steps of q k
+  static constexpr int OT = D / 8;                 // output column tiles
+  static constexpr int KV = CH * D * 2;            // bytes of K (of V) in a chunk
+  static constexpr int HALF = CH * 128;            // bytes of one 64-channel half
+  static constexpr int OVER = 2 * kWarps;          // a unit's fixed cost in chunks
+};
+
 template <bool BF, int D>
-__global__ void __launch_bounds__(kWarps * 32)
-k_attend_rows(const Pool p, const AttendArgs a) {
-  __shared__ float s_q[kWarps][D];
+__global__ void __launch_bounds__(kThreads, 3)
+k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_constant__ CUtensorMap mk,
+             const __grid_constant__ CUtensorMap mv) {
+  using F = Few<D>;
+  extern __shared__ unsigned char s_raw[];
+  __shared__ __align__(8) unsigned long long s_bar[kWarps * kStages];
+  __shared__ float s_ml[kWarps][kRows][2];
+  __shared__ Sched s_sched;
+  __shared__ long long s_scan[kWarps];
+  __shared__ int s_abort, s_last;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring0 = (smem_addr(s_raw) + 1023u) & ~1023u;
+  const uint32_t ring = ring0 + warp * (kStages * kChunkBytes);
+  const uint32_t bar = smem_addr(&s_bar[warp * kStages]);
+  if (lane == 0)
+    for (int i = 0; i < kStages; ++i) bar_init(bar + 8 * i, 1);
+  if (tid == 0) s_abort = 0;
+  fence_bar_init();
+  fence_async();
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long item = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  const int row = static_cast<int>(item / p.Hq), hq = static_cast<int>(item - static_cast<long long>(row) * p.Hq);
-  if (row >= a.rows) return;
-  const int b = sequence_of(a.bt.q_start, a.bt.B, row);
-  if (b >= a.bt.B) return;
-  const int first = a.bt.q_start[b], last = a.bt.q_start[b + 1];
-  if (row < first) return;
-  int ctx = a.bt.ctx[b];
-  if (ctx < 0) {
-    if (lane == 0) atomicOr(p.err, CONFKV_FLAG_BAD_INDEX);
-    ctx = 0;
-  }
-  const int t = row - first;
-  long long len = static_cast<long long>(ctx) + (last - first);
-  const long long cap = static_cast<long long>(a.bt.max_blocks) * p.ps;
-  if (len > cap) {
-    if (lane == 0) atomicOr(p.err, CONFKV_FLAG_CAPACITY);
-    len = cap;
-  }
-  const uint16_t* q = a.q + row * a.qs + hq * D;
-  constexpr int C = D / 32;
-  for (int i = lane; i < D; i += 32) s_q[warp][i] = to_f(q[i], BF) * a.scale;
-  __syncwarp();
-  const int h = hq / p.g;
-  float m = -INFINITY, l = 0.0f, acc[C] = {};
-  for (long long base = 0; base < len; base += 32) {
-    const long long j = base + lane;
-    bool seen = j < len;
-    const uint16_t* kr = nullptr;
-    const uint16_t* vr = nullptr;
-    if (seen && j >= ctx) {
-      const int x = static_cast<int>(j - ctx);
-      if (a.bt.mask)
-        seen = x < 32 * a.bt.mask_words &&
-               ((a.bt.mask[static_cast<size_t>(row) * a.bt.mask_words + (x >> 5)] >> (x & 31)) & 1u);
-      else
-        seen = x <= t;
-    }
-    if (seen) {
-      const int page = a.bt.table[static_cast<size_t>(b) * a.bt.max_blocks + (j >> p.ps_shift)];
-      if (page < 0 || page >= p.NP) {
-        atomicOr(p.err, CONFKV_FLAG_BAD_PAGE);
-        seen = false;
-      } else {
-        const size_t off = (((static_cast<size_t>(a.layer) * p.NP + page) * p.Hkv + h) * p.ps + (j & (p.ps - 1))) * D;
-        kr = p.k + off;
-        vr = p.v + off;
+
+  Walk<kRows, F::CH, F::OVER> w(p, a.bt, a.rows);
+  sched_init<kThreads>(w, &s_sched, s_scan, 4 * kWarps);
+  w.start(s_sched);
+  const uint64_t pol = stream_policy();
+  const float c = a.scale * kL2E;
+  unsigned turn = 0;                                // chunks this warp has taken so far
+  const int r0 = lane >> 2, t4 = lane & 3;
+
+  while (w.next()) {
+    const int b = w.pb, h = w.ph;
+    const int32_t* table = a.bt.table + static_cast<size_t>(b) * a.bt.max_blocks;
+    const int layer_row = (a.layer * p.NP) * p.Hkv;  // page of head h: (layer_row + page * Hkv + h) * ps
+    int flag = 0;
+    auto issue = [&](int ci, unsigned k) {
+      // boxes of 16 rows (or the whole chunk, where a page holds it)
+      const int st = k % kStages;
+      const uint32_t dst = ring + st * kChunkBytes, fb = bar + 8 * st;
+      const int j0 = ci * F::CH;
+      const int box = p.ps < F::CH ? p.ps : F::CH;
+      const int nb = F::CH / box;
+      const int live = (w.plen - j0 + box - 1) / box;       // boxes with tokens of the sequence
+      const int n = live < nb ? live : nb;
+      if (lane == 0) bar_expect(fb, static_cast<unsigned>(n * box * D * 4));
+      __syncwarp();
+      if (lane < n * (D / 64)) {
+        const int i = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
+        const int j = j0 + i * box;
+        int page = table[j >> p.ps_shift];
+        if (page < 0 || page >= p.NP) {
+          flag = CONFKV_FLAG_BAD_PAGE;
+          page = 0;
+        }
+        const int y = ((layer_row + page * p.Hkv + h) << p.ps_shift) + (j & (p.ps - 1));
+        const uint32_t o = dst + half * F::HALF + i * box * 128;
+        tma_box(o, &mk, 64 * half, y, fb, pol);
+        tma_box(o + F::KV, &mv, 64 * half, y, fb, pol);
+      }
+    };
+    const int first = w.lo + warp;
+    const unsigned turn0 = turn;
+    unsigned issued = turn0;
+    bool dead = false;
+#pragma unroll
+    for (int i = 0; i < kStages; ++i)
+      if (first + i * kWarps < w.hi) issue(first + i * kWarps, issued++);
+
+    // the tile's query rows as A fragments (zero behind the sequence's rows)
+    const int R = w.pT * p.g, base = w.pmt * kRows;
+    const int ra = base + r0, rb = ra + 8;            // this thread's rows
+    const int ta = ra / p.g, tb = rb / p.g;
+    uint32_t qf[F::KS][4];
+    {
+      const uint16_t* qa = a.q + (w.prow0 + ta) * a.qs + (h * p.g + ra - ta * p.g) * D + 2 * t4;
+      const uint16_t* qb = a.q + (w.prow0 + tb) * a.qs + (h * p.g + rb - tb * p.g) * D + 2 * t4;
+#pragma unroll
+      for (int k = 0; k < F::KS; ++k) {
+        qf[k][0] = ra < R ? *reinterpret_cast<const uint32_t*>(qa + 16 * k) : 0u;
+        qf[k][1] = rb < R ? *reinterpret_cast<const uint32_t*>(qb + 16 * k) : 0u;
+        qf[k][2] = ra < R ? *reinterpret_cast<const uint32_t*>(qa + 16 * k + 8) : 0u;
+        qf[k][3] = rb < R ? *reinterpret_cast<const uint32_t*>(qb + 16 * k + 8) : 0u;
       }
     }
-    float s = -INFINITY;
-    if (seen) {
-      s = 0.0f;
-#pragma unroll 4
-      for (int i = 0; i < D; i += 8) {
-        const uint4 w = *reinterpret_cast<const uint4*>(kr + i);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    // tokens that every row of the tile sees
+    const int all_seen = a.bt.mask ? w.pctx : w.pctx + base / p.g + 1;
+    float o[F::OT][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = unpack2<BF>(ww[e]);
-          s = fmaf(x.x, s_q[warp][i + 2 * e], s);
-          s = fmaf(x.y, s_q[warp][i + 2 * e + 1], s);
+    for (int i = 0; i < F::OT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+    float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
+
+    for (int ci = first; ci < w.hi; ci += kWarps) {
+      const unsigned st = turn % kStages;
+      if (!bar_wait_warp(bar + 8 * st, (turn / kStages) & 1, &s_abort)) {
+        dead = true;
+        break;
+      }
+      const uint32_t kt = ring + st * kChunkBytes, vt = kt + F::KV;
+      const int j0 = ci * F::CH;
+      float s[F::NT][4];
+#pragma unroll
+      for (int i = 0; i < F::NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < F::KS; ++k) {
+#pragma unroll
+        for (int i = 0; i < F::NT; i += 2) {
+          uint32_t f[4];
+          // matrices: tokens 8i.., channels 16k..; channels +8; tokens + 8; both
+          const int row = 8 * i + ((lane >> 4) << 3) + (lane & 7), wd = 2 * k + ((lane >> 3) & 1);
+          ldsm4(f, swz128(kt + (wd >> 3) * F::HALF, row, wd & 7));
+          mma16816<BF>(s[i], qf[k], f[0], f[1]);
+          mma16816<BF>(s[i + 1], qf[k], f[2], f[3]);
         }
       }
+      if (j0 + F::CH > all_seen) {
+        const uint32_t ba = ra < R ? seen_bits(a.bt, w.prow0 + ta, ta, w.pctx, w.plen, j0) : 0u;
+        const uint32_t bb = rb < R ? seen_bits(a.bt, w.prow0 + tb, tb, w.pctx, w.plen, j0) : 0u;
+#pragma unroll
+        for (int i = 0; i < F::NT; ++i) {
+          const int x = 8 * i + 2 * t4;
+          if (!(ba >> x & 1u)) s[i][0] = -INFINITY;
+          if (!(ba >> (x + 1) & 1u)) s[i][1] = -INFINITY;
+          if (!(bb >> x & 1u)) s[i][2] = -INFINITY;
+          if (!(bb >> (x + 1) & 1u)) s[i][3] = -INFINITY;
+        }
+        // V: zeroes past the end; non-finite elements by hand
+        bool odd = false;
+        for (int i = lane; i < F::KV / 16; i += 32) {
+          const int row = (i >> 3) % F::CH;           // words in order: halves, rows, words
+          const uint32_t ad = vt + i * 16;
+          uint32_t x[4];
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(ad) : "memory");
+          if (j0 + row >= w.plen) {
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(ad), "r"(0u) : "memory");
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd |= nonfinite2<BF>(x[e]) != 0u;
+          }
+        }
+        if (__any_sync(0xffffffffu, odd)) {
+          __syncwarp();
+          for (int j = 0; j < F::CH && j0 + j < w.plen; ++j) {
+            const bool sa = ba >> j & 1u, sb = bb >> j & 1u;
+#pragma unroll
+            for (int i = 0; i < F::OT; ++i) {
+              uint32_t x;
+              const int ch = 8 * i + 2 * t4;
+              asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(x)
+                           : "r"(swz128(vt + (ch >> 6) * F::HALF, j, (ch & 63) >> 3) + 2 * (ch & 7)) : "memory");
+              const uint32_t bad = nonfinite2<BF>(x);
+              const float2 v = unpack2<BF>(x);
+              if (bad & 0xffffu) {
+                if (sa) o[i][0] += v.x;
+                if (sb) o[i][2] += v.x;
+              }
+              if (bad >> 16) {
+                if (sa) o[i][1] += v.y;
+                if (sb) o[i][3] += v.y;
+              }
+            }
+          }
+          __syncwarp();
+          for (int i = lane; i < F::KV / 4; i += 32) {
+            uint32_t x;
+            asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(x) : "r"(vt + 4 * i) : "memory");
+            x &= ~nonfinite2<BF>(x);
+            asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(vt + 4 * i), "r"(x) : "memory");
+          }
+        }
+        fence_async();        // these writes before the next box in this stage
+        __syncwarp();
+      }
+      // running maximum and sum of the two rows (4 lanes share a row)
+      float xa = fmaxf(s[0][0], s[0][1]), xb = fmaxf(s[0][2], s[0][3]);
+#pragma unroll
+      for (int i = 1; i < F::NT; ++i) {
+        xa = fmaxf(xa, fmaxf(s[i][0], s[i][1]));
+        xb = fmaxf(xb, fmaxf(s[i][2], s[i][3]));
+      }
+      xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 1));
+      xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
+      xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
+      xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
+      if (__any_sync(0xffffffffu, xa > ma || xb > mb)) {
+        const float na = fmaxf(ma, xa), nb = fmaxf(mb, xb);
+        const float fa = ma == -INFINITY ? 0.0f : ex2f((ma - na) * c);
+        const float fb = mb == -INFINITY ? 0.0f : ex2f((mb - nb) * c);
+        if (turn != turn0) {
+#pragma unroll
+          for (int i = 0; i < F::OT; ++i) {
+            o[i][0] *= fa;
+            o[i][1] *= fa;
+            o[i][2] *= fb;
+            o[i][3] *= fb;
+          }
+        }
+        la *= fa;
+        lb *= fb;
+        ma = na;
+        mb = nb;
+      }
+      const float ca = ma == -INFINITY ? 0.0f : ma * c, cb = mb == -INFINITY ? 0.0f : mb * c;
+#pragma unroll
+      for (int i = 0; i < F::NT; ++i) {
+        s[i][0] = ex2f(fmaf(s[i][0], c, -ca));
+        s[i][1] = ex2f(fmaf(s[i][1], c, -ca));
+        s[i][2] = ex2f(fmaf(s[i][2], c, -cb));
+        s[i][3] = ex2f(fmaf(s[i][3], c, -cb));
+        la += s[i][0] + s[i][1];
+        lb += s[i][2] + s[i][3];
+      }
+#pragma unroll
+      for (int i = 0; i < F::NT; i += 2) {
+        const uint32_t pf[4] = {pack2<BF>(s[i][0], s[i][1]), pack2<BF>(s[i][2], s[i][3]),
+                                pack2<BF>(s[i + 1][0], s[i + 1][1]), pack2<BF>(s[i + 1][2], s[i + 1][3])};
+#pragma unroll
+        for (int n = 0; n < F::OT; n += 2) {
+          uint32_t f[4];
+          // matrices (transposed): tokens 8i.., channels 8n..; tokens +8; channels +8; both
+          const int row = 8 * i + (((lane >> 3) & 1) << 3) + (lane & 7), wd = n + (lane >> 4);
+          ldsm4t(f, swz128(vt + (wd >> 3) * F::HALF, row, wd & 7));
+          mma16816<BF>(o[n], pf, f[0], f[1]);
+          mma16816<BF>(o[n + 1], pf, f[2], f[3]);
+        }
+      }
+      __syncwarp();           // every lane has read the stage
+      if (ci + kStages * kWarps < w.hi) issue(ci + kStages * kWarps, issued++);
+      ++turn;
     }
-    float bm = s;
+    if (dead)                 // no copy may land after the CTA has gone
+      for (unsigned k = turn; k < issued; ++k) bar_drain(bar + 8 * (k % kStages), (k / kStages) & 1);
+    if (flag) atomicOr(p.err, flag);
+    la += __shfl_xor_sync(0xffffffffu, la, 1);
+    lb += __shfl_xor_sync(0xffffffffu, lb, 1);
+    la += __shfl_xor_sync(0xffffffffu, la, 2);
+    lb += __shfl_xor_sync(0xffffffffu, lb, 2);
+
+    // the warps' partials: each in its own ring (rows of D floats), then joined
+    {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
-    const float mn = fmaxf(m, bm);
-    if (mn == -INFINITY) continue;
-    const float f = m == -INFINITY ? 0.0f : exp2f((m - mn) * kL2E);
-    const float pr = s == -INFINITY ? 0.0f : exp2f((s - mn) * kL2E);
-    m = mn;
-    float ps = pr;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-    l = l * f + ps;
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] *= f;
-    for (int jj = 0; jj < 32; ++jj) {
-      const float w = __shfl_sync(0xffffffffu, pr, jj);
-      const uint16_t* r = reinterpret_cast<const uint16_t*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vr), jj));
-      if (!r) continue;
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] = fmaf(w, to_f(r[lane * C + c], BF), acc[c]);
+      for (int i = 0; i < F::OT; ++i) {
+        const uint32_t ch = 8 * i + 2 * t4;
+        asm volatile("st.shared.v2.f32 [%0], {%1,%2};\n" ::"r"(ring + (r0 * D + ch) * 4), "f"(o[i][0]), "f"(o[i][1]) : "memory");
+        asm volatile("st.shared.v2.f32 [%0], {%1,%2};\n" ::"r"(ring + ((r0 + 8) * D + ch) * 4), "f"(o[i][2]), "f"(o[i][3]) : "memory");
+      }
+      if (t4 == 0) {
+        s_ml[warp][r0][0] = ma;
+        s_ml[warp][r0][1] = la;
+        s_ml[warp][r0 + 8][0] = mb;
+        s_ml[warp][r0 + 8][1] = lb;
+      }
     }
+    __syncthreads();
+    if (s_abort) break;       // set before the barrier or not at all
+    constexpr int PER = kRows * D / kThreads;        // 16 or 8 channels of one row
+    const int row = tid / (D / PER), ch0 = (tid % (D / PER)) * PER;
+    const bool whole = w.pieces == 1;
+    float m = -INFINITY, l = 0.0f, x[PER];
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) m = fmaxf(m, s_ml[i][row][0]);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) x[e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const float mi = s_ml[i][row][0];
+      if (mi == -INFINITY) continue;
+      const float f = ex2f((mi - m) * c);
+      l += f * s_ml[i][row][1];
+      const uint32_t src = ring0 + i * (kStages * kChunkBytes) + (row * D + ch0) * 4;
+#pragma unroll
+      for (int e = 0; e < PER; e += 4) {
+        float v[4];
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];\n"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(src + 4 * e) : "memory");
+#pragma unroll
+        for (int y = 0; y < 4; ++y) x[e + y] = fmaf(f, v[y], x[e + y]);
+      }
+    }
+    const int rr = base + row;
+    bool mine = whole;
+    if (!whole) {
+      const size_t at = (2 * static_cast<size_t>(blockIdx.x) + (w.lo == 0 ? 1 : 0)) * kRows + row;
+      if (rr < R) {
+#pragma unroll
+        for (int e = 0; e < PER; e += 4)
+          *reinterpret_cast<float4*>(sc.acc + at * D + ch0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        if (ch0 == 0) *reinterpret_cast<float2*>(sc.ml + at * 2) = make_float2(m, l);
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        s_last = atomicAdd(sc.ticket + w.first_cta, 1u) == static_cast<unsigned>(w.pieces - 1);
+        if (s_last) sc.ticket[w.first_cta] = 0u;
+      }
+      __syncthreads();
+      mine = s_last;
+      if (mine && rr < R) {
+        __threadfence();
+        join_row<kRows>(sc, w, row, ch0, D, c, x, m, l);
+      }
+    }
+    if (mine && rr < R) {
+      const int t = rr / p.g;
+      store_row<BF, PER>(a, p, w.prow0 + t, h * p.g + rr - t * p.g, ch0, x, m, l);
+    }
+    fence_async();
+    __syncthreads();          // the rings are free again
   }
-  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-  uint16_t* out = a.out + (static_cast<size_t>(row) * p.Hq + hq) * D + lane * C;
-#pragma unroll
-  for (int c = 0; c < C; c += 2) *reinterpret_cast<uint32_t*>(out + c) = pack2<BF>(acc[c] * inv, acc[c + 1] * inv);
-  if (a.lse && lane == 0) a.lse[static_cast<size_t>(row) * p.Hq + hq] = m + logf(l);
+  if (s_abort && tid == 0) atomicOr(p.err, CONFKV_FLAG_TIMEOUT);
 }
 
 }  // namespace
 
-cudaError_t launch_attend(const Pool& p, const AttendArgs& a, cudaStream_t s) {
-  const long long items = static_cast<long long>(a.rows) * p.Hq;
-  const dim3 grid(static_cast<unsigned>((items + kWarps - 1) / kWarps)), block(kWarps * 32);
+cudaError_t launch_attend_few(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
+                              int ctas, cudaStream_t s) {
+  const size_t smem = kWarps * kStages * kChunkBytes + 1024;
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem, s, p, a, sc, m.k_few, m.v_few);
+  };
   cudaError_t e;
-  if (p.bf16)
-    e = launch_pdl(p.d == 128 ? k_attend_rows<true, 128> : k_attend_rows<true, 64>, grid, block, 0, s, p, a);
-  else
-    e = launch_pdl(p.d == 128 ? k_attend_rows<false, 128> : k_attend_rows<false, 64>, grid, block, 0, s, p, a);
+  if (p.bf16) e = p.d == 128 ? go(k_attend_few<true, 128>) : go(k_attend_few<true, 64>);
+  else e = p.d == 128 ? go(k_attend_few<false, 128>) : go(k_attend_few<false, 64>);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t setup_attend_few() {
+  const int smem = kWarps * kStages * kChunkBytes + 1024;
+  for (const void* k : {reinterpret_cast<const void*>(k_attend_few<true, 128>), reinterpret_cast<const void*>(k_attend_few<true, 64>),
+                        reinterpret_cast<const void*>(k_attend_few<false, 128>), reinterpret_cast<const void*>(k_attend_few<false, 64>)}) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace paged

@@ -1,0 +1,533 @@
+// Attention of many new rows per sequence over a paged cache (prompt chunks,
+// trees of drafted tokens): tiles of 128 query rows on the fifth-generation
+// tensor cores.
+//
+//   S = Q K^T (fp32, tensor memory);  P = exp2(c S - c m), c = scale log2 e;
+//   O = P V (fp32, tensor memory);    out = O / sum P
+//
+// Roles of a CTA's twelve warps: two warpgroups do the softmax, one thread of
+// warp 8 issues every tcgen05.mma, warp 9 moves K and V blocks of 128 tokens
+// from the pages by TMA through a ring of 32 KB (d = 128) or 16 KB stages.
+// There are two streams of products, one per softmax warpgroup, so that the
+// tensor cores work on one while the other's exponentials are taken:
+//   NQ = 2: a unit is 256 query rows, a stream takes 128 of them and all blocks;
+//   NQ = 1: a unit is 128 query rows, a stream takes every second block, and
+//           the two are joined at the unit's end (few rows, where the bytes
+//           of the cache or the length of the dependent chain count).
+// The issue order is PV(s), QK(s) of that stream's next block, then the other
+// stream's; products of one thread complete in order, so a stream's S is
+// overwritten only behind the PV that read the P in its place, and O may be
+// rescaled whenever S is there.  P is written over S in tensor memory (the
+// first product operand may lie there) and V is read as it lies, rows of
+// channels (MN-major), so neither is transposed.
+//
+// The running maximum is raised only when it grows by a factor of 2^8 or more
+// (P <= 2^8 meanwhile: exact in fp32, and fp16 P keeps more small values), so
+// O is rarely rescaled.  Row statistics are fp32; P is rounded once to the
+// cache's type.  Masks and what masked places hold: as in k_paged_attend.cu,
+// with V mended in shared memory before the product, and non-finite elements
+// added behind it to the rows that see them.
+#include "paged_attend.cuh"
+
+namespace confkv {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 384;               // three warpgroups; the last one's warps 2 and 3 only lend registers
+constexpr int kSoft = 256;                  // softmax threads
+constexpr int BN = kManyBlock;
+constexpr float kL2E = 1.4426950408889634f;
+constexpr float kRaise = 8.0f;              // log2 of the growth that rescales
+constexpr int kOver = 2;                    // a unit's fixed cost in blocks
+
+template <int D, int NQ>
+struct Many {
+  static constexpr int TILE = 128 * D * 2;                  // bytes of a Q tile, K or V block
+  static constexpr int HALF = 128 * 128;                    // bytes of 64 channels of it
+  static constexpr int ST = D == 128 ? 5 : 8;               // ring stages
+  static constexpr int RING = NQ * TILE;
+  static constexpr int SMEM = NQ * TILE + ST * TILE + 1024; // alignment slack
+};
+
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
+
+template <bool BF, int D, int NQ>
+__global__ void __launch_bounds__(kThreads, 1)
+k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_constant__ CUtensorMap mk,
+              const __grid_constant__ CUtensorMap mv) {
+  using M = Many<D, NQ>;
+  constexpr int ST = M::ST;
+  constexpr int TM = 128 * NQ;
+  extern __shared__ unsigned char s_raw[];
+  __shared__ __align__(8) unsigned long long s_bar[2 * ST + 8];
+  __shared__ Sched s_sched;
+  __shared__ long long s_scan[kThreads / 32];
+  __shared__ float s_x[NQ == 1 ? 2 * 128 * 2 : 1];          // NQ = 1: the streams' (maximum, sum)
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_dead, s_last, s_poison;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_addr(s_raw) + 1023u) & ~1023u;
+  const uint32_t ring = base + M::RING;
+  const uint32_t bars = smem_addr(s_bar);
+  const uint32_t b_full = bars, b_empty = bars + 8 * ST, b_s = bars + 16 * ST, b_p = b_s + 16, b_o = b_p + 16,
+                 b_q = b_o + 16;
+  if (tid == 0) {
+    for (int i = 0; i < 2 * ST; ++i) bar_init(bars + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(b_s + 8 * i, 1);
+      bar_init(b_p + 8 * i, 128);
+      bar_init(b_o + 8 * i, 1);
+    }
+    bar_init(b_q, kSoft);
+    bar_init(b_q + 8, 1);
+    s_abort = s_dead = s_poison = 0;
+    fence_bar_init();
+    fence_async();
+  }
+    if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_addr(&s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+  }
+  pdl_wait();
+  pdl_trigger();
+  Walk<TM, BN, kOver> w(p, a.bt, a.rows);
+  tc_fence_before();
+  sched_init<kThreads>(w, &s_sched, s_scan, 4);
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  w.start(s_sched);
+
+  // 384 threads x 168 registers at launch = 256 x 224 + 128 x 56
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+    if (warp == 9) {
+    // ---- K and V blocks into the ring ----
+    const uint64_t once = stream_policy(), again = reuse_policy();
+    const int rows_per = p.ps < BN ? p.ps : BN;
+    const int boxes = BN / rows_per;
+    unsigned slot = 0;
+    int flag = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      const int32_t* table = a.bt.table + static_cast<size_t>(w.pb) * a.bt.max_blocks;
+      // other tiles of the head read the same blocks
+      const uint64_t pol = w.pT * p.g > TM ? again : once;
+      auto load = [&](const CUtensorMap* map, int blk) {
+        if (!ok) return;
+        const unsigned st = slot % ST;
+        if (slot >= ST && !bar_wait_warp(b_empty + 8 * st, (slot / ST - 1) & 1, &s_abort)) {
+          ok = false;
+          return;
+        }
+        const int j0 = blk * BN;
+        const int live = (w.plen - j0 + rows_per - 1) / rows_per;     // boxes with tokens of the sequence
+        const int n = live < boxes ? live : boxes;
+        if (lane == 0) bar_expect(b_full + 8 * st, static_cast<unsigned>(n * rows_per * D * 2));
+        __syncwarp();
+        if (lane < n * (D / 64)) {
+          const int i = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
+          const int j = j0 + i * rows_per;
+          int page = table[j >> p.ps_shift];
+          if (page < 0 || page >= p.NP) {
+            flag = CONFKV_FLAG_BAD_PAGE;
+            page = 0;
+          }
+          const int y = (((a.layer * p.NP + page) * p.Hkv + w.ph) << p.ps_shift) + (j & (p.ps - 1));
+          tma_box(ring + st * M::TILE + half * M::HALF + i * rows_per * 128, map, 64 * half, y, b_full + 8 * st, pol);
+        }
+        ++slot;
+      };
+      if (NQ == 2) {
+        for (int b = w.lo; b < w.hi; ++b) {
+          load(&mk, b);
+          load(&mv, b);
+        }
+      } else {
+        load(&mk, w.lo);
+        if (w.lo + 1 < w.hi) load(&mk, w.lo + 1);
+        for (int b = w.lo; b < w.hi; ++b) {
+          load(&mv, b);
+          if (b + 2 < w.hi) load(&mk, b + 2);
+        }
+      }
+    }
+    if (flag) atomicOr(p.err, flag);
+    if (!ok)                    // no copy may land after the CTA has gone
+      for (unsigned k = slot > ST ? slot - ST : 0; k < slot; ++k) bar_drain(b_full + 8 * (k % ST), (k / ST) & 1);
+  } else if (warp == 8) {
+    // ---- matrix products ----
+    if (lane == 0) {
+      constexpr uint32_t id_qk = umma_idesc(BF, 128, BN, false), id_pv = umma_idesc(BF, 128, D, true);
+      unsigned slot = 0, np[2] = {0, 0}, nq = 0;
+      bool ok = true;
+      auto full = [&](unsigned k) {
+        ok = ok && bar_wait(b_full + 8 * (k % ST), (k / ST) & 1, &s_abort);
+        return ok;
+      };
+      auto have_p = [&](int s) {
+        ok = ok && bar_wait(b_p + 8 * s, np[s] & 1, &s_abort);
+        ++np[s];
+        if (ok) tc_fence_after();
+        return ok;
+      };
+      auto qk = [&](int s, unsigned k) {          // S(s) = Q K^T
+        const uint32_t q = base + (NQ == 2 ? s * M::TILE : 0), kt = ring + (k % ST) * M::TILE;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t o = (i >> 2) * M::HALF + (i & 3) * 32;
+          umma_ss(tmem + s * 128, umma_desc(q + o, 16, 1024), umma_desc(kt + o, 16, 1024), id_qk, i > 0);
+        }
+        umma_commit(b_s + 8 * s);
+      };
+      auto pv = [&](int s, unsigned k, bool acc) {  // O(s) += P V
+        const uint32_t vt = ring + (k % ST) * M::TILE;
+#pragma unroll
+        for (int i = 0; i < BN / 16; ++i)
+          umma_ts(tmem + 256 + s * 128, tmem + s * 128 + i * 8, umma_desc(vt + i * 2048, M::HALF, 1024), id_pv,
+                  acc || i > 0);
+      };
+      auto release = [&](unsigned k) { umma_commit(b_empty + 8 * (k % ST)); };
+      while (ok && w.next()) {
+        const int nb = w.hi - w.lo;
+        ok = bar_wait(b_q, nq & 1, &s_abort);
+        ++nq;
+        if (!ok) break;
+        tc_fence_after();
+        if (NQ == 2) {
+          if (!full(slot)) break;
+          qk(0, slot);
+          qk(1, slot);
+          release(slot);
+          ++slot;
+          for (int b = 0; b < nb; ++b) {
+            const unsigned v = slot, k = slot + 1;
+            const bool more = b + 1 < nb;
+            if (!full(v) || !have_p(0)) break;
+            pv(0, v, b > 0);
+            if (more) {
+              if (!full(k)) break;
+              qk(0, k);
+            } else {
+              umma_commit(b_o);
+            }
+            if (!have_p(1)) break;
+            pv(1, v, b > 0);
+            release(v);
+            ++slot;
+            if (more) {
+              qk(1, k);
+              release(k);
+              ++slot;
+            } else {
+              umma_commit(b_o + 8);
+            }
+          }
+        } else {
+          for (int s = 0; s < 2 && s < nb; ++s) {
+            if (!full(slot)) break;
+            qk(s, slot);
+            release(slot);
+            ++slot;
+          }
+          if (!ok) break;
+          for (int b = 0; b < nb; ++b) {
+            const int s = b & 1;
+            if (!full(slot) || !have_p(s)) break;
+            pv(s, slot, b >= 2);
+            release(slot);
+            ++slot;
+            if (b + 2 < nb) {
+              if (!full(slot)) break;
+              qk(s, slot);
+              release(slot);
+              ++slot;
+            } else {
+              umma_commit(b_o + 8 * s);
+            }
+          }
+        }
+      }
+      if (!ok) {
+        // products in flight end before the CTA does
+        umma_commit(b_q + 8);
+        bar_drain(b_q + 8, 0);
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
+    // ---- softmax and epilogue ----
+    const int s = warp >> 2;                              // stream
+    const int r = (warp & 3) * 32 + lane;                 // row of its tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256;
+    const float c = a.scale * kL2E;
+    unsigned ns = 0, no = 0, slot0 = 0;
+    while (w.next()) {
+      const int nb = w.hi - w.lo;
+      const int R = w.pT * p.g;                           // rows of the head
+      const int tile0 = w.pmt * TM;
+      // query rows into shared memory
+      {
+        constexpr int WD = D / 8;
+        const int first = NQ == 2 ? s * 128 : 0;
+        constexpr int NTH = NQ == 2 ? 128 : 256;
+        const int me = NQ == 2 ? tid & 127 : tid;
+#pragma unroll 4
+        for (int i = me; i < 128 * WD; i += NTH) {
+          const int row = i / WD, wd = i % WD, x = tile0 + first + row;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (x < R) {
+            const int t = x / p.g;
+            v = *reinterpret_cast<const uint4*>(a.q + (w.prow0 + t) * a.qs + (w.ph * p.g + x - t * p.g) * D + 8 * wd);
+          }
+          const uint32_t ad = swz128(base + (NQ == 2 ? s * M::TILE : 0) + (wd >> 3) * M::HALF, row, wd & 7);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(ad), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+        }
+        fence_async();
+        bar_arrive(b_q);
+      }
+      const int x = tile0 + (NQ == 2 ? s * 128 : 0) + r;  // this thread's row of the head
+      const bool live = x - lane < R;                     // the warp holds rows
+      const int t = x < R ? x / p.g : 0;
+      const size_t row = w.prow0 + t;
+      const int all_seen = a.bt.mask ? w.pctx : w.pctx + tile0 / p.g + 1;   // tokens that the whole unit sees
+      float m = -INFINITY, l = 0.0f;
+      const int mine = NQ == 2 ? nb : (nb + 1 - s) >> 1;  // this stream's blocks
+      for (int j = 0; j < mine; ++j) {
+        const int bb = NQ == 2 ? j : 2 * j + s;
+        const int j0 = (w.lo + bb) * BN;
+        const bool masked = j0 + BN > all_seen;
+        if (!bar_wait_warp(b_s + 8 * s, ns & 1, &s_abort)) break;
+        ++ns;
+        tc_fence_after();
+        if (live) {
+          uint32_t sv[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(sv[q], ts + 32 * q);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_wait_ld(sv[q]);
+          if (masked) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t bits = x < R ? seen_bits(a.bt, row, t, w.pctx, w.plen, j0 + 32 * q) : 0u;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(bits >> i & 1u)) sv[q][i] = 0xff800000u;
+            }
+          }
+          float mx[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            mx[q] = __uint_as_float(sv[q][0]);
+#pragma unroll
+            for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(sv[q][i]));
+          }
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const float mn = fmaxf(m, top);
+          const bool raise = (m == -INFINITY) ? mn > -INFINITY : (mn - m) * c > kRaise;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float f = m == -INFINITY ? 0.0f : ex2f((m - mn) * c);
+            m = mn;
+            l *= f;
+            if (j > 0) {
+#pragma unroll 1
+              for (int q = 0; q < D; q += 32) {
+                uint32_t o[32];
+                tmem_ld32(o, to + s * 128 + q);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(to + s * 128 + q, o);
+              }
+            }
+          }
+          const float mc = m == -INFINITY ? 0.0f : m * c;
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float e0 = ex2f(fmaf(__uint_as_float(sv[q][i]), c, -mc));
+              const float e1 = ex2f(fmaf(__uint_as_float(sv[q][i + 1]), c, -mc));
+              sum[i & 2] += e0;
+              sum[(i & 2) + 1] += e1;
+              pk[i >> 1] = pack2<BF>(e0, e1);
+            }
+            tmem_st16(ts + 16 * q, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+        }
+        if (masked) {
+          // V's rows past the end and non-finite elements become zeroes
+          const unsigned k = slot0 + (NQ == 2 ? 2 * bb + 1 : (nb > 1 ? 2 : 1) + bb + (bb < nb - 2 ? bb : nb > 2 ? nb - 2 : 0));
+          if (!bar_wait_warp(b_full + 8 * (k % ST), (k / ST) & 1, &s_abort)) break;
+          const uint32_t vt = ring + (k % ST) * M::TILE;
+          for (int i = tid & 127; i < M::TILE / 16; i += 128) {
+            const uint32_t ad = vt + 16 * i;
+            uint32_t v[4], z = 0u;
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(ad) : "memory");
+            const bool past = j0 + ((i >> 3) & 127) >= w.plen;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t bad = past ? 0xffffffffu : nonfinite2<BF>(v[e]);
+              z |= v[e] & bad;
+              if (!past && bad) *const_cast<volatile int*>(&s_poison) = 1;
+              v[e] &= ~bad;
+            }
+            if (z) {
+              __threadfence_block();
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(ad), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+            }
+          }
+          fence_async();
+        }
+        tc_fence_before();
+        bar_arrive(b_p + 8 * s);
+      }
+      if (mine > 0) {
+        if (bar_wait_warp(b_o + 8 * s, no & 1, &s_abort)) tc_fence_after();
+        ++no;
+      }
+      slot0 += 2 * nb;
+      if (NQ == 1) {
+        s_x[(s * 128 + r) * 2] = m;
+        s_x[(s * 128 + r) * 2 + 1] = l;
+        tc_fence_before();
+      }
+      if (tid == 0) s_dead = s_abort;
+      soft_sync();
+      if (s_dead) break;
+      tc_fence_after();
+      float w0 = 1.0f, w1 = 0.0f;                         // NQ = 1: the streams' weights
+      if (NQ == 1) {
+        const float m0 = s_x[r * 2], m1 = s_x[(128 + r) * 2], l0 = s_x[r * 2 + 1], l1 = s_x[(128 + r) * 2 + 1];
+        m = fmaxf(m0, m1);
+        w0 = m0 == -INFINITY ? 0.0f : ex2f((m0 - m) * c);
+        w1 = m1 == -INFINITY ? 0.0f : ex2f((m1 - m) * c);
+        l = l0 * w0 + l1 * w1;
+      }
+      const bool whole = w.pieces == 1;
+      const bool poison = *const_cast<volatile int*>(&s_poison) != 0;
+      constexpr int COLS = NQ == 1 ? D / 2 : D;           // of this thread's row
+      const int col0 = NQ == 1 ? s * (D / 2) : 0;
+      const int xr = NQ == 1 ? r : s * 128 + r;           // row of the unit
+      const int hq = w.ph * p.g + x - t * p.g;
+      const size_t place = (2 * static_cast<size_t>(blockIdx.x) + (w.lo == 0 ? 1 : 0)) * TM + xr;
+      if (live) {
+#pragma unroll 1
+        for (int q = 0; q < COLS; q += 32) {
+          uint32_t o[32];
+          float y[32];
+          tmem_ld32(o, to + (NQ == 1 ? 0 : s * 128) + col0 + q);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]);
+          if (NQ == 1 && nb > 1) {
+            tmem_ld32(o, to + 128 + col0 + q);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = y[i] * w0 + __uint_as_float(o[i]) * w1;
+          }
+          if (x < R) {
+            if (poison) {
+              const int32_t* table = a.bt.table + static_cast<size_t>(w.pb) * a.bt.max_blocks;
+              int jb = all_seen / BN * BN;
+              jb = jb < w.lo * BN ? w.lo * BN : jb;
+              const int je = w.hi * BN < w.plen ? w.hi * BN : w.plen;
+              for (int j = jb; j < je; ++j) {
+                const int page = table[j >> p.ps_shift];
+                if (page < 0 || page >= p.NP || !(seen_bits(a.bt, row, t, w.pctx, w.plen, j) & 1u)) continue;
+                const uint16_t* v = p.v + (((static_cast<size_t>(a.layer) * p.NP + page) * p.Hkv + w.ph) * p.ps + (j & (p.ps - 1))) * D + col0 + q;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float z = to_f(v[i], BF);
+                  if (!(fabsf(z) < INFINITY)) y[i] += z;
+                }
+              }
+            }
+            if (whole) {
+              store_row<BF>(a, p, static_cast<int>(row), hq, col0 + q, y, m, l);
+            } else {
+              float* to_acc = sc.acc + place * D + col0 + q;
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(to_acc + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+              if (col0 + q == 0) *reinterpret_cast<float2*>(sc.ml + place * 2) = make_float2(m, l);
+            }
+          }
+        }
+        tc_fence_before();
+      }
+      if (!whole) {
+        __threadfence();
+        soft_sync();
+        if (tid == 0) {
+          s_last = atomicAdd(sc.ticket + w.first_cta, 1u) == static_cast<unsigned>(w.pieces - 1);
+          if (s_last) sc.ticket[w.first_cta] = 0u;
+        }
+        soft_sync();
+        if (s_last) {
+          __threadfence();
+          for (int i = tid; i < TM * (D / 4); i += kSoft) {
+            const int rr = i / (D / 4), ch = 4 * (i % (D / 4)), xx = tile0 + rr;
+            if (xx >= R) break;
+            float y[4], mm, ll;
+            join_row<TM>(sc, w, rr, ch, D, c, y, mm, ll);
+            const int tt = xx / p.g;
+            store_row<BF>(a, p, w.prow0 + tt, w.ph * p.g + xx - tt * p.g, ch, y, mm, ll);
+          }
+        }
+      } else if (NQ == 1) {
+        soft_sync();         // both streams' O has been read before either goes on
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (s_abort && tid == 0) atomicOr(p.err, CONFKV_FLAG_TIMEOUT);
+    if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+  }
+}
+
+template <bool BF, int D, int NQ>
+cudaError_t go(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m, int ctas, cudaStream_t s) {
+  return launch_pdl(k_attend_many<BF, D, NQ>, dim3(ctas), dim3(kThreads), Many<D, NQ>::SMEM, s, p, a, sc, m.k_many, m.v_many);
+}
+template <bool BF, int D, int NQ>
+cudaError_t set() {
+  return cudaFuncSetAttribute(k_attend_many<BF, D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, Many<D, NQ>::SMEM);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_many(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m, int ctas,
+                               bool two_tiles, cudaStream_t s) {
+  cudaError_t e;
+  if (two_tiles) {
+    if (p.bf16) e = p.d == 128 ? go<true, 128, 2>(p, a, sc, m, ctas, s) : go<true, 64, 2>(p, a, sc, m, ctas, s);
+    else e = p.d == 128 ? go<false, 128, 2>(p, a, sc, m, ctas, s) : go<false, 64, 2>(p, a, sc, m, ctas, s);
+  } else {
+    if (p.bf16) e = p.d == 128 ? go<true, 128, 1>(p, a, sc, m, ctas, s) : go<true, 64, 1>(p, a, sc, m, ctas, s);
+    else e = p.d == 128 ? go<false, 128, 1>(p, a, sc, m, ctas, s) : go<false, 64, 1>(p, a, sc, m, ctas, s);
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t setup_attend_many() {
+  cudaError_t e = cudaSuccess;
+  for (const cudaError_t r : {set<true, 128, 2>(), set<true, 64, 2>(), set<false, 128, 2>(), set<false, 64, 2>(),
+                              set<true, 128, 1>(), set<true, 64, 1>(), set<false, 128, 1>(), set<false, 64, 1>()})
+    if (e == cudaSuccess) e = r;
+  return e;
+}
+
+}  // namespace paged
+}  // namespace confkv

@@ -7,7 +7,7 @@
 #include <new>
 #include <string>
 
-#include "paged_internal.cuh"
+#include "paged_attend.cuh"
 
 using namespace confkv::paged;
 
@@ -50,6 +50,9 @@ bool rows_overlap(const void* a, int64_t sa, int64_t wa, const void* b, int64_t 
 
 struct confkv_paged {
   Pool pool{};
+  AttendMaps maps;
+  Scratch scratch{};
+  int sms = 0;
   int device = 0;
   const char* msg = "ok";     // static texts only: no allocation, so nothing can throw
 };
@@ -75,6 +78,38 @@ const char* check_batch(const confkv_paged_batch* b, bool masked) {
     return "page_table, ctx_len, q_start and mask must be 4-byte aligned";
   if (masked && b->mask && b->mask_words < 1) return "mask_words must be positive";
   return nullptr;
+}
+
+// Tensor maps of both pools for both kernels: rows of d elements in boxes of 64
+// channels (128 bytes, swizzled) x as many rows as a page and the kernel's tile share.
+cudaError_t encode_maps(const Pool& p, AttendMaps* m) {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+  if (e != cudaSuccess) return e;
+  if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  const Encode enc = reinterpret_cast<Encode>(fn);
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.d),
+                              static_cast<cuuint64_t>(p.L) * p.NP * p.Hkv * p.ps};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.d) * 2};
+  const cuuint32_t steps[2] = {1, 1};
+  const int few = std::min(p.ps, kFewChunk / p.d), many = std::min(p.ps, kManyBlock);
+  struct {
+    CUtensorMap* map;
+    uint16_t* pool;
+    int rows;
+  } const all[] = {{&m->k_few, p.k, few}, {&m->v_few, p.v, few}, {&m->k_many, p.k, many}, {&m->v_many, p.v, many}};
+  for (const auto& x : all) {
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(x.rows)};
+    if (enc(x.map, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x.pool, dims,
+            strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  return cudaSuccess;
 }
 
 Batch batch_of(const confkv_paged_batch* b) {
@@ -122,6 +157,20 @@ int confkv_paged_create(int layers, int heads, int kv_heads, int head_dim, int n
   p.bf16 = dtype == CONFKV_BF16;
   cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&p.err), sizeof(int32_t));
   if (e == cudaSuccess) e = cudaMemset(p.err, 0, sizeof(int32_t));
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&kv->sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) {
+    // two places per CTA: a CTA's share cuts at most the unit it starts in and the one it ends in
+    Scratch& sc = kv->scratch;
+    const size_t rows = 2 * static_cast<size_t>(kv->sms) * std::max(kFewCtasPerSm * kFewRows, kManyRows);
+    e = cudaMalloc(reinterpret_cast<void**>(&sc.acc), rows * p.d * sizeof(float));
+    if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&sc.ml), rows * 2 * sizeof(float));
+    const size_t nt = sizeof(unsigned int) * kFewCtasPerSm * kv->sms;
+    if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&sc.ticket), nt);
+    if (e == cudaSuccess) e = cudaMemset(sc.ticket, 0, nt);
+  }
+  if (e == cudaSuccess) e = encode_maps(p, &kv->maps);
+  if (e == cudaSuccess) e = setup_attend_few();
+  if (e == cudaSuccess) e = setup_attend_many();
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -135,7 +184,9 @@ int confkv_paged_create(int layers, int heads, int kv_heads, int head_dim, int n
 void confkv_paged_free(confkv_paged* kv) {
   if (!kv) return;
   DeviceGuard guard(kv->device);
-  if (kv->pool.err) cudaFree(kv->pool.err);
+  for (void* m : {static_cast<void*>(kv->pool.err), static_cast<void*>(kv->scratch.acc),
+                  static_cast<void*>(kv->scratch.ml), static_cast<void*>(kv->scratch.ticket)})
+    if (m) cudaFree(m);
   delete kv;
 }
 
@@ -211,7 +262,11 @@ int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int l
   DeviceGuard guard(kv->device);
   AttendArgs a{batch_of(batch), layer, rows, static_cast<const uint16_t*>(q), q_stride, static_cast<uint16_t*>(out),
                lse, scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(p.d))};
-  return launched(kv, launch_attend(p, a, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // by the query rows of a sequence's KV head, on average
+  const int64_t per = static_cast<int64_t>(rows) * p.g / batch->batch;
+  if (per <= kFewRows) return launched(kv, launch_attend_few(p, a, kv->scratch, kv->maps, kFewCtasPerSm * kv->sms, st));
+  return launched(kv, launch_attend_many(p, a, kv->scratch, kv->maps, kv->sms, per > kManyRows, st));
 }
 
 int confkv_paged_commit(confkv_paged* kv, int batch, int max_blocks, const int32_t* page_table,

@@ -1,0 +1,86 @@
+// Parts shared by the two paged attention kernels (k_paged_attend.cu: few rows
+// per sequence, k_paged_attend_many.cu: many).
+#pragma once
+#include "paged_internal.cuh"
+#include "paged_ptx.cuh"
+#include "paged_sched.cuh"
+
+namespace confkv {
+namespace paged {
+
+struct AttendMaps {                    // pools as rows of d elements, boxes of 64 channels
+  CUtensorMap k_few, v_few;            // x min(page_size, chunk) rows
+  CUtensorMap k_many, v_many;          // x min(page_size, 128) rows
+};
+
+constexpr int kFewRows = 16;           // query rows of a tile
+constexpr int kFewChunk = 2048;        // elements of K in a chunk (tokens x d)
+constexpr int kManyRows = 256;         // two tiles of 128
+constexpr int kManyBlock = 128;        // tokens of a block
+
+// CTAs of a launch: resident ones only, three per SM or one
+constexpr int kFewCtasPerSm = 3;
+
+cudaError_t launch_attend_few(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
+                              int ctas, cudaStream_t s);
+cudaError_t launch_attend_many(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
+                               int ctas, bool two_tiles, cudaStream_t s);
+cudaError_t setup_attend_few();
+cudaError_t setup_attend_many();
+
+// 0xffff in each half of a word whose element is NaN or infinite
+template <bool BF>
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
+  constexpr uint32_t E = BF ? 0x7f80u : 0x7c00u;
+  return ((x & E) == E ? 0xffffu : 0u) | (((x >> 16) & E) == E ? 0xffff0000u : 0u);
+}
+
+// N channels of an output row: acc / l (0 where nothing was seen), rounded once
+template <bool BF, int N>
+__device__ __forceinline__ void store_row(const AttendArgs& a, const Pool& p, int row, int hq, int ch, const float (&x)[N],
+                                          float m, float l) {
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const size_t at = static_cast<size_t>(row) * p.Hq + hq;
+  uint16_t* out = a.out + at * p.d + ch;
+#pragma unroll
+  for (int e = 0; e < N; e += 4)
+    *reinterpret_cast<uint2*>(out + e) =
+        make_uint2(pack2<BF>(x[e] * inv, x[e + 1] * inv), pack2<BF>(x[e + 2] * inv, x[e + 3] * inv));
+  if (a.lse && ch == 0) a.lse[at] = l == 0.0f ? -INFINITY : m * a.scale + logf(l);
+}
+
+// Where the pieces' partial results of the walk's current unit lie: piece i of
+// it, of CTA first + i, in that CTA's second place if it is the unit's first.
+template <typename W>
+__device__ __forceinline__ size_t piece_place(const W& w, int i) {
+  return 2 * static_cast<size_t>(w.first_cta + i) + (i == 0 ? 1 : 0);
+}
+
+// N channels of one row joined over a unit's pieces, in their order
+template <int TM, int N, typename W>
+__device__ __forceinline__ void join_row(const Scratch& sc, const W& w, int row, int ch, int d, float c, float (&x)[N],
+                                         float& m, float& l) {
+  m = -INFINITY;
+  for (int i = 0; i < w.pieces; ++i) m = fmaxf(m, __ldcg(sc.ml + (piece_place(w, i) * TM + row) * 2));
+  l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) x[e] = 0.0f;
+  for (int i = 0; i < w.pieces; ++i) {
+    const size_t at = piece_place(w, i) * TM + row;
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(sc.ml + at * 2));
+    if (ml.x == -INFINITY) continue;
+    const float f = ex2f((ml.x - m) * c);
+    l = fmaf(f, ml.y, l);
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(sc.acc + at * d + ch + e));
+      x[e] = fmaf(f, v.x, x[e]);
+      x[e + 1] = fmaf(f, v.y, x[e + 1]);
+      x[e + 2] = fmaf(f, v.z, x[e + 2]);
+      x[e + 3] = fmaf(f, v.w, x[e + 3]);
+    }
+  }
+}
+
+}  // namespace paged
+}  // namespace confkv

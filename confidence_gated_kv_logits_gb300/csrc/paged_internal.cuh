@@ -92,7 +92,6 @@ struct BeamArgs {
 };
 
 cudaError_t launch_append(const Pool& p, const AppendArgs& a, cudaStream_t s);
-cudaError_t launch_attend(const Pool& p, const AttendArgs& a, cudaStream_t s);
 cudaError_t launch_commit(const Pool& p, const CommitArgs& a, cudaStream_t s);
 cudaError_t launch_fork(const Pool& p, const ForkArgs& a, cudaStream_t s);
 cudaError_t launch_beam(const BeamArgs& a, cudaStream_t s);

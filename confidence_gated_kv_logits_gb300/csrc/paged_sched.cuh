@@ -1,0 +1,241 @@
+// How the paged attention's work is spread over its CTAs.
+//
+// A unit is one (sequence, KV head, tile of TM query rows); query row r of a
+// sequence's KV head is new token r / g, head r % g of the group.  A unit's
+// work is the blocks of KB tokens that its rows may see plus kOverhead blocks
+// for its prologue and epilogue.  All units' work is laid end to end (sequence,
+// head, tile) and cut into equal shares, one per CTA, so that the batch's
+// lengths, known on the device alone, balance whatever they are.  A unit that
+// is cut has its pieces' partial results joined by the CTA that finishes last,
+// in the pieces' order, so results do not depend on timing.
+#pragma once
+#include "paged_internal.cuh"
+
+namespace confkv {
+namespace paged {
+
+struct Sched {          // in shared memory, filled by sched_init
+  long long share;      // work per CTA
+  long long cur, end;   // this CTA's range of the work
+  long long seq0;       // where sequence b's work starts
+  int b;                // sequence in which the range starts
+};
+
+struct Scratch {        // of the handle: partial results of cut units
+  float* acc;           // [CTA][2][TM][d]
+  float* ml;            // [CTA][2][TM][2] (maximum, sum)
+  unsigned int* ticket; // [CTA]
+};
+
+template <int TM, int KB, int kOverhead>
+struct Walk {
+  const Pool& p;
+  const Batch& bt;
+  int rows;
+  long long share, cur, end, ustart;
+  int b, h, mt;
+  int T, ctx, len, row0, m;     // of sequence b; m = tiles per head
+
+  // a piece of a unit: blocks [lo, hi) of its n
+  int lo, hi, n;
+  int first_cta, pieces;        // CTAs that hold the unit's pieces
+
+  __device__ __forceinline__ Walk(const Pool& p_, const Batch& b_, int rows_) : p(p_), bt(b_), rows(rows_) {}
+
+  // what of sequence b's lengths is usable; `flag` collects what is not
+  __device__ __forceinline__ void sequence(int b_, int& flag) {
+    b = b_;
+    int s0 = bt.q_start[b], s1 = bt.q_start[b + 1];
+    ctx = bt.ctx[b];
+    if (ctx < 0) {
+      flag |= CONFKV_FLAG_BAD_INDEX;
+      ctx = 0;
+    }
+    s0 = s0 < 0 ? 0 : s0 > rows ? rows : s0;
+    s1 = s1 < s0 ? s0 : s1 > rows ? rows : s1;
+    row0 = s0;
+    T = s1 - s0;
+    const long long cap = static_cast<long long>(bt.max_blocks) << p.ps_shift;
+    long long l = static_cast<long long>(ctx) + T;
+    if (l > cap) {
+      if (T) flag |= CONFKV_FLAG_CAPACITY;
+      l = cap;
+    }
+    if (l > 0x7ffffff0ll) l = 0x7ffffff0ll;
+    len = static_cast<int>(l);
+    m = static_cast<int>((static_cast<long long>(T) * p.g + TM - 1) / TM);
+  }
+  // tokens that some row of tile t may see
+  __device__ __forceinline__ int tile_len(int t) const {
+    if (bt.mask) return len;
+    long long last = (static_cast<long long>(t + 1) * TM - 1) / p.g + 1;   // new tokens up to the tile's last row
+    last = last > T ? T : last;
+    const long long l = ctx + last;
+    return l < len ? static_cast<int>(l) : len;
+  }
+  __device__ __forceinline__ int blocks(int t) const { return (tile_len(t) + KB - 1) / KB; }
+  // work of one head of the sequence
+  __device__ __forceinline__ long long head_work() const {
+    if (bt.mask || m <= 1) return static_cast<long long>(m) * (blocks(0 < m ? m - 1 : 0) + kOverhead);
+    long long w = 0;
+    for (int t = 0; t < m; ++t) w += blocks(t) + kOverhead;
+    return w;
+  }
+
+  __device__ __forceinline__ void start(const Sched& s) {
+    share = s.share;
+    cur = s.cur;
+    end = s.end;
+    if (cur >= end) return;
+    int flag = 0;
+    sequence(s.b, flag);
+    const long long hw = head_work();
+    h = static_cast<int>((cur - s.seq0) / hw);
+    ustart = s.seq0 + h * hw;
+    mt = 0;
+    if (bt.mask) {
+      const long long u = blocks(0) + kOverhead;
+      mt = static_cast<int>((cur - ustart) / u);
+      ustart += mt * u;
+    } else {
+      for (long long u = blocks(0) + kOverhead; cur >= ustart + u; u = blocks(mt) + kOverhead) {
+        ustart += u;
+        ++mt;
+      }
+    }
+  }
+  __device__ __forceinline__ bool next() {
+    while (cur < end) {
+      n = blocks(mt);
+      const long long uend = ustart + n + kOverhead;
+      const long long x1 = end < uend ? end : uend;
+      const long long a = cur - ustart - kOverhead, z = x1 - ustart - kOverhead;
+      lo = a > 0 ? static_cast<int>(a) : 0;
+      hi = z > 0 ? static_cast<int>(z) : 0;
+      first_cta = static_cast<int>((ustart + kOverhead) / share);
+      pieces = static_cast<int>((uend - 1) / share) - first_cta + 1;
+      cur = x1;
+      // the piece's place, kept while the walk moves on
+      pb = b; ph = h; pmt = mt; pT = T; pctx = ctx; plen = len; prow0 = row0; ptile = tile_len(mt);
+      if (x1 == uend) {
+        ustart = uend;
+        if (++mt == m) {
+          mt = 0;
+          if (++h == p.Hkv) {
+            h = 0;
+            int flag = 0, nb = b;
+            if (cur < end) {
+              do sequence(++nb, flag); while (T <= 0);
+            }
+          }
+        }
+      }
+      if (hi > lo) return true;
+    }
+    return false;
+  }
+  int pb, ph, pmt, pT, pctx, plen, prow0, ptile;
+};
+
+// Every thread of the CTA calls it (kT threads; three barriers).  s_scan holds kT / 32
+// 64-bit words.
+template <int kT, typename W>
+__device__ __forceinline__ void sched_init(W& w, Sched* s, long long* s_scan, long long min_share) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kW = kT / 32;
+  const int B = w.bt.B;
+  int flag = 0;
+  long long mine = 0, total = 0;
+  // a thread's sequences: one each where the batch has no more than kT
+  for (int b = tid; b < B; b += kT) {
+    w.sequence(b, flag);
+    mine = w.T > 0 ? w.head_work() * w.p.Hkv : 0;
+    total += mine;
+  }
+  if (flag && blockIdx.x == 0) atomicOr(w.p.err, flag);
+  // with one pass the scan of `total` is that of the sequences
+  auto scan = [&](long long x, long long& sum) {       // exclusive, over the CTA
+    long long incl = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long before = 0;
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      const long long y = s_scan[i];
+      before += i < warp ? y : 0;
+      sum += y;
+    }
+    __syncthreads();
+    return before + incl - x;
+  };
+  long long all;
+  long long pre = scan(total, all);
+  long long share = (all + gridDim.x - 1) / gridDim.x;
+  share = share < min_share ? min_share : share;
+  const long long cur = static_cast<long long>(blockIdx.x) * share;
+  if (tid == 0) {
+    s->share = share;
+    s->cur = cur;
+    s->end = cur + share < all ? cur + share : all;
+    s->b = 0;
+    s->seq0 = 0;
+  }
+  __syncthreads();
+  if (cur < all) {
+    if (B <= kT) {
+      if (mine > 0 && cur >= pre && cur < pre + mine) {
+        s->b = tid;
+        s->seq0 = pre;
+      }
+    } else {
+      long long base = 0;
+      for (int b0 = 0; b0 < B; b0 += kT) {
+        long long x = 0, sum;
+        if (b0 + tid < B) {
+          w.sequence(b0 + tid, flag);
+          x = w.T > 0 ? w.head_work() * w.p.Hkv : 0;
+        }
+        const long long at = base + scan(x, sum);
+        if (x > 0 && cur >= at && cur < at + x) {
+          s->b = b0 + tid;
+          s->seq0 = at;
+        }
+        base += sum;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// Which of 32 tokens from place j0 on query row `t` (new token) of a sequence
+// sees: bit i is token j0 + i.
+__device__ __forceinline__ uint32_t seen_bits(const Batch& bt, size_t row, int t, int ctx, int len, int j0) {
+  const int left = len - j0;                       // tokens of the sequence from j0 on
+  if (left <= 0) return 0u;
+  uint32_t bits;
+  if (!bt.mask) {
+    const int nv = ctx + t + 1 - j0;
+    bits = nv <= 0 ? 0u : nv >= 32 ? 0xffffffffu : (1u << nv) - 1u;
+  } else {
+    const int x = j0 - ctx;
+    if (x <= -32) {
+      bits = 0xffffffffu;
+    } else {
+      const int k = x >> 5;                        // floor
+      const uint32_t* mw = bt.mask + row * bt.mask_words;
+      const uint32_t a = k < 0 ? 0xffffffffu : k < bt.mask_words ? mw[k] : 0u;
+      const uint32_t c = k + 1 < bt.mask_words ? mw[k + 1] : 0u;
+      bits = __funnelshift_r(a, c, x & 31);
+    }
+  }
+  return left >= 32 ? bits : bits & ((1u << left) - 1u);
+}
+
+}  // namespace paged
+}  // namespace confkv
