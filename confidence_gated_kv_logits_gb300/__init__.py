@@ -40,7 +40,7 @@ EXPORTS = ("confkv_create", "confkv_prefill", "confkv_step", "confkv_step_host",
            "confkv_confidence_noalloc", "confkv_step_begin", "confkv_step_layer",
            "confkv_attention_path", "confkv_selftest_bounded_wait",
            "confkv_read_channel_exponents",
-           "confkv_paged_create", "confkv_paged_free", "confkv_paged_last_error",
+           "confkv_paged_scratch", "confkv_paged_create", "confkv_paged_free", "confkv_paged_last_error",
            "confkv_paged_status", "confkv_paged_append", "confkv_paged_attend",
            "confkv_paged_commit", "confkv_paged_fork", "confkv_beam_workspace",
            "confkv_beam_select")

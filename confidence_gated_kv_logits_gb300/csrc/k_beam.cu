@@ -8,11 +8,9 @@
 // its best K logits; the CTA that takes a sequence's last ticket (no CTA
 // waits) joins the slices and orders the candidates.
 //
-// Best K of a block's values: every lane knows its own largest value; the
-// r-th largest of a warp's lane maxima bounds the warp's r-th largest value
-// from below, so the best bound over the warps keeps K values at least and,
-// on data in no particular order, few more.  The kept ones are ranked by
-// counting.  Should more be kept than the buffer holds (long runs of equal
+// Best K of a block's values: the K-th largest of the threads' own maxima is
+// reached by K values at least and, on data in no particular order, by few
+// more.  Those are ranked by counting.  Should more be kept than the buffer holds (long runs of equal
 // values, or an order that follows the lanes), K rounds of a block-wide
 // maximum give the same answer.
 //
@@ -70,10 +68,9 @@ __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
   return a.key > b.key || (a.key == b.key && a.tie > b.tie);
 }
 
-// r-th largest (r = 1 .. 32) of the warp's 32 values, in every lane: a bitonic
-// sort by shuffles
+// the warp's 32 values in falling order over its lanes: a bitonic sort by shuffles
 template <typename T>
-__device__ __forceinline__ T warp_rth(T x, int r) {
+__device__ __forceinline__ void warp_sort(T& x) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int size = 2; size <= 32; size <<= 1) {
@@ -85,21 +82,44 @@ __device__ __forceinline__ T warp_rth(T x, int r) {
       x = (low == desc) ? (x > y ? x : y) : (x < y ? x : y);
     }
   }
-  return __shfl_sync(0xffffffffu, x, r - 1);
 }
 
 // A value that at least K of the block's values reach, from each thread's
-// largest (all threads call it; two barriers)
+// largest (all threads call it): the K-th largest of the threads' maxima for
+// K <= 32, by merging the warps' sorted lanes pairwise; for more, the second
+// best of the warps' (K / 2)-th largest.  s_v: 32 values per warp.
 template <typename T>
-__device__ __forceinline__ T block_bound(T mine, int K, T* s_w) {
+__device__ __forceinline__ T block_bound(T mine, int K, T* s_v) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nw = (K + 31) >> 5;
-  const T t = warp_rth(mine, (K + nw - 1) / nw);
-  if (lane == 0) s_w[warp] = t;
+  T x = mine;
+  warp_sort(x);
+  s_v[warp * 32 + lane] = x;
   __syncthreads();
-  const T w = warp_rth(s_w[lane & (kWarps - 1)], 2 * nw - 1);   // each warp's bound twice: ranks 1, 3, ..
+  if (K > 32) {
+    T w = s_v[(lane & (kWarps - 1)) * 32 + ((K + 1) >> 1) - 1];    // each warp's bound twice
+    warp_sort(w);
+    w = __shfl_sync(0xffffffffu, w, 2);
+    __syncthreads();
+    return w;
+  }
+#pragma unroll
+  for (int step = kWarps / 2; step > 0; step >>= 1) {
+    if (warp < step) {
+      // the larger of a falling and a rising list: the 32 largest, bitonic
+      const T y = s_v[(warp + step) * 32 + 31 - lane];
+      x = x > y ? x : y;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) {
+        const T z = __shfl_xor_sync(0xffffffffu, x, d);
+        x = (lane & d) == 0 ? (x > z ? x : z) : (x < z ? x : z);
+      }
+      s_v[warp * 32 + lane] = x;
+    }
+    __syncthreads();
+  }
+  const T r = s_v[K - 1];
   __syncthreads();
-  return w;
+  return r;
 }
 
 template <int DT>
@@ -136,7 +156,7 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
   __shared__ Cand s_list[kCap];
   __shared__ double s_sum[kWarps];
   __shared__ float s_f[kWarps];
-  __shared__ double s_d[kWarps];
+  __shared__ unsigned long long s_v[kThreads];
   __shared__ Cand s_best[kWarps];
   __shared__ double s_base[kMaxBeams];
   __shared__ int s_cnt, s_bad, s_last;
@@ -192,7 +212,13 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
         bad |= !(z < INFINITY);
         m = fmaxf(m, z);
       }
-    const float bound = block_bound(m, a.K, s_f);
+    // the passes unpack the values anew instead of holding all of them as floats
+    auto again = [&] {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));
+    };
+    again();
+    const float bound = block_bound(m, a.K, reinterpret_cast<float*>(s_v));
     float bm = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
@@ -241,8 +267,10 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
       for (int i = cnt + tid; i < a.K; i += kThreads) out[i] = 0;
     } else {
       Cand last{~0ull, 0};
+#pragma unroll 1
       for (int r = 0; r < a.K; ++r) {
         Cand c{0, 0};
+        again();
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -334,19 +362,29 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
     }
     return c;
   };
+  constexpr int kHeld = 4;                  // candidates of a thread that stay in registers
+  Cand held[kHeld];
   unsigned long long top = 0;
-  for (int i = tid; i < n + a.W; i += kThreads) {
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) {
+    held[u] = Cand{0, 0};
+    if (tid + u * kThreads < n + a.W) held[u] = candidate(tid + u * kThreads);
+    top = held[u].key > top ? held[u].key : top;
+  }
+  for (int i = tid + kHeld * kThreads; i < n + a.W; i += kThreads) {
     const unsigned long long k = candidate(i).key;
     top = k > top ? k : top;
   }
-  const unsigned long long bound = block_bound(top, a.K, reinterpret_cast<unsigned long long*>(s_d));
-  for (int i = tid; i < n + a.W; i += kThreads) {
-    const Cand c = candidate(i);
+  const unsigned long long bound = block_bound(top, a.K, s_v);
+  auto keep = [&](const Cand& c) {
     if (c.key && c.key >= bound) {
       const int at = atomicAdd(&s_cnt, 1);
       if (at < kCap) s_list[at] = c;
     }
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) keep(held[u]);
+  for (int i = tid + kHeld * kThreads; i < n + a.W; i += kThreads) keep(candidate(i));
   __syncthreads();
   const int cnt = s_cnt;
   auto put = [&](int r, const Cand& c) {

@@ -71,7 +71,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
   pdl_trigger();
 
   Walk<kRows, F::CH, F::OVER> w(p, a.bt, a.rows);
-  sched_init<kThreads>(w, &s_sched, s_scan, 4 * kWarps);
+  sched_init<kThreads>(w, &s_sched, s_scan, 2 * kWarps);
   w.start(s_sched);
   const uint64_t pol = stream_policy();
   const float c = a.scale * kL2E;

@@ -5,19 +5,19 @@
 //   S = Q K^T (fp32, tensor memory);  P = exp2(c S - c m), c = scale log2 e;
 //   O = P V (fp32, tensor memory);    out = O / sum P
 //
-// Roles of a CTA's twelve warps: two warpgroups do the softmax, one thread of
-// warp 8 issues every tcgen05.mma, warp 9 moves K and V blocks of 128 tokens
-// from the pages by TMA through a ring of 32 KB (d = 128) or 16 KB stages.
-// There are two streams of products, one per softmax warpgroup, so that the
+// Roles of a CTA's twelve warps: two warpgroups do the softmax of a stream of
+// products each, one thread of warps 8 and 9 issues a stream's tcgen05.mma,
+// warp 10 moves K and V blocks of 128 tokens from the pages by TMA through a
+// ring of 32 KB (d = 128) or 16 KB stages.  There are two streams so that the
 // tensor cores work on one while the other's exponentials are taken:
 //   NQ = 2: a unit is 256 query rows, a stream takes 128 of them and all blocks;
 //   NQ = 1: a unit is 128 query rows, a stream takes every second block, and
 //           the two are joined at the unit's end (few rows, where the bytes
 //           of the cache or the length of the dependent chain count).
-// The issue order is PV(s), QK(s) of that stream's next block, then the other
-// stream's; products of one thread complete in order, so a stream's S is
-// overwritten only behind the PV that read the P in its place, and O may be
-// rescaled whenever S is there.  P is written over S in tensor memory (the
+// A stream goes on by sub-blocks of 64 tokens with two S buffers: behind PV of
+// sub-block i comes QK of i + 2 into the same buffer, so a softmax finds its
+// next S there already.  Products of one thread complete in order: S is
+// overwritten only behind the PV that read the P in its place.  P is written over S in tensor memory (the
 // first product operand may lie there) and V is read as it lies, rows of
 // channels (MN-major), so neither is transposed.
 //
@@ -36,6 +36,7 @@ namespace {
 constexpr int kThreads = 384;               // three warpgroups; the last one's warps 2 and 3 only lend registers
 constexpr int kSoft = 256;                  // softmax threads
 constexpr int BN = kManyBlock;
+constexpr int SB = BN / 2;                 // tokens of a sub-block
 constexpr float kL2E = 1.4426950408889634f;
 constexpr float kRaise = 8.0f;              // log2 of the growth that rescales
 constexpr int kOver = 2;                    // a unit's fixed cost in blocks
@@ -49,6 +50,14 @@ struct Many {
   static constexpr int SMEM = NQ * TILE + ST * TILE + 1024; // alignment slack
 };
 
+// The ring's order.  NQ = 2: K0 V0 K1 V1 ..; NQ = 1: K0 K1 V0 K2 V1 K3 .. V(n-1).
+// Place of V of block b of n; the K that its stream needs next lies behind it.
+template <int NQ>
+__device__ __forceinline__ unsigned v_slot(int b, int n) {
+  if (NQ == 2) return 2 * b + 1;
+  return (n > 1 ? 2 : 1) + b + (n > 2 ? (b < n - 2 ? b : n - 2) : 0);
+}
+
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
 
 template <bool BF, int D, int NQ>
@@ -59,7 +68,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
   constexpr int ST = M::ST;
   constexpr int TM = 128 * NQ;
   extern __shared__ unsigned char s_raw[];
-  __shared__ __align__(8) unsigned long long s_bar[2 * ST + 8];
+  __shared__ __align__(8) unsigned long long s_bar[2 * ST + 15];
   __shared__ Sched s_sched;
   __shared__ long long s_scan[kThreads / 32];
   __shared__ float s_x[NQ == 1 ? 2 * 128 * 2 : 1];          // NQ = 1: the streams' (maximum, sum)
@@ -70,22 +79,30 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
   const uint32_t base = (smem_addr(s_raw) + 1023u) & ~1023u;
   const uint32_t ring = base + M::RING;
   const uint32_t bars = smem_addr(s_bar);
-  const uint32_t b_full = bars, b_empty = bars + 8 * ST, b_s = bars + 16 * ST, b_p = b_s + 16, b_o = b_p + 16,
-                 b_q = b_o + 16;
+  // K and V stages full and empty; per stream: S there (two buffers), P there
+  // (two), PV done, O done; Q there; a giving-up stream's products done
+  const uint32_t b_full = bars, b_empty = bars + 8 * ST, b_s = bars + 16 * ST, b_p = b_s + 32, b_pv = b_p + 32,
+                 b_o = b_pv + 16, b_q = b_o + 16, b_end = b_q + 8;
   if (tid == 0) {
-    for (int i = 0; i < 2 * ST; ++i) bar_init(bars + 8 * i, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < ST; ++i) {
+      bar_init(b_full + 8 * i, 1);
+      bar_init(b_empty + 8 * i, NQ);      // the streams that read a stage
+    }
+    for (int i = 0; i < 4; ++i) {
       bar_init(b_s + 8 * i, 1);
       bar_init(b_p + 8 * i, 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(b_pv + 8 * i, 1);
       bar_init(b_o + 8 * i, 1);
+      bar_init(b_end + 8 * i, 1);
     }
     bar_init(b_q, kSoft);
-    bar_init(b_q + 8, 1);
     s_abort = s_dead = s_poison = 0;
     fence_bar_init();
     fence_async();
   }
-    if (warp == 9) {
+    if (warp == 10) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_addr(&s_tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
@@ -98,10 +115,10 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
   const uint32_t tmem = s_tmem;
   w.start(s_sched);
 
-  // 384 threads x 168 registers at launch = 256 x 224 + 128 x 56
+  // 384 threads x 168 registers at launch = 256 x 216 + 128 x 72
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
-    if (warp == 9) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+    if (warp == 10) {
     // ---- K and V blocks into the ring ----
     const uint64_t once = stream_policy(), again = reuse_policy();
     const int rows_per = p.ps < BN ? p.ps : BN;
@@ -155,109 +172,80 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
     if (flag) atomicOr(p.err, flag);
     if (!ok)                    // no copy may land after the CTA has gone
       for (unsigned k = slot > ST ? slot - ST : 0; k < slot; ++k) bar_drain(b_full + 8 * (k % ST), (k / ST) & 1);
-  } else if (warp == 8) {
-    // ---- matrix products ----
-    if (lane == 0) {
-      constexpr uint32_t id_qk = umma_idesc(BF, 128, BN, false), id_pv = umma_idesc(BF, 128, D, true);
-      unsigned slot = 0, np[2] = {0, 0}, nq = 0;
-      bool ok = true;
-      auto full = [&](unsigned k) {
-        ok = ok && bar_wait(b_full + 8 * (k % ST), (k / ST) & 1, &s_abort);
-        return ok;
-      };
-      auto have_p = [&](int s) {
-        ok = ok && bar_wait(b_p + 8 * s, np[s] & 1, &s_abort);
-        ++np[s];
-        if (ok) tc_fence_after();
-        return ok;
-      };
-      auto qk = [&](int s, unsigned k) {          // S(s) = Q K^T
-        const uint32_t q = base + (NQ == 2 ? s * M::TILE : 0), kt = ring + (k % ST) * M::TILE;
+  } else if (warp < 10) {
+    // ---- matrix products of one stream (the warp stays together; one elected thread issues) ----
+    constexpr uint32_t id_qk = umma_idesc(BF, 128, SB, false), id_pv = umma_idesc(BF, 128, D, true);
+    constexpr uint32_t hi = umma_hi(1024);
+    const int s = warp - 8;
+    const uint32_t ts = uniform(tmem + s * 128), to = uniform(tmem + 256 + s * 128),
+                   q_lo = uniform(umma_lo(base + (NQ == 2 ? s * M::TILE : 0), 16)), k_lo = uniform(umma_lo(ring, 16)),
+                   v_lo = uniform(umma_lo(ring, M::HALF));
+    unsigned slot0 = 0, np = 0, nq = 0;
+    bool ok = true;
+    auto full = [&](unsigned k) {
+      ok = bar_wait_warp(b_full + 8 * (k % ST), (k / ST) & 1, &s_abort);
+      return ok;
+    };
+    auto release = [&](unsigned k) { umma_commit(b_empty + 8 * (k % ST)); };
+    auto qk = [&](int i, unsigned k) {      // S of sub-block i = Q K^T, half i & 1 of K's stage
+      const uint32_t kt = uniform(k_lo + (k % ST) * (M::TILE / 16) + (i & 1) * (SB * 128 / 16));
+      const uint32_t d = uniform(ts + (i & 1) * SB);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t o = (i >> 2) * M::HALF + (i & 3) * 32;
-          umma_ss(tmem + s * 128, umma_desc(q + o, 16, 1024), umma_desc(kt + o, 16, 1024), id_qk, i > 0);
+      for (int x = 0; x < D / 16; ++x) {
+        const uint32_t o = ((x >> 2) * M::HALF + (x & 3) * 32) / 16;
+        umma_ss(d, q_lo + o, hi, kt + o, hi, id_qk, x > 0);
+      }
+      umma_commit(b_s + 16 * s + 8 * (i & 1));
+      if (i & 1) release(k);
+    };
+    auto pv = [&](int i, unsigned k) {      // O += P V
+      const uint32_t vt = uniform(v_lo + (k % ST) * (M::TILE / 16) + (i & 1) * (SB * 128 / 16));
+      const uint32_t pt = uniform(ts + (i & 1) * SB);
+#pragma unroll
+      for (int x = 0; x < SB / 16; ++x) umma_ts(to, pt + x * 8, vt + x * 128, hi, id_pv, i > 0 || x > 0);
+      umma_commit(b_pv + 8 * s);
+      if (i & 1) release(k);
+    };
+    while (ok && w.next()) {
+      const int nb = w.hi - w.lo;
+      ok = bar_wait_warp(b_q, nq & 1, &s_abort);
+      ++nq;
+      if (!ok) break;
+      tc_fence_after();
+      const int mine = NQ == 2 ? nb : (nb + 1 - s) >> 1;
+      if (mine > 0) {
+        const unsigned k0 = slot0 + (NQ == 2 ? 0 : s);
+        if (!full(k0)) break;
+        qk(0, k0);
+        qk(1, k0);
+      }
+      for (int i = 0; i < 2 * mine; ++i) {
+        const unsigned v = slot0 + v_slot<NQ>(NQ == 2 ? i >> 1 : (i & ~1) + s, nb);
+        const bool more = i + 2 < 2 * mine;  // this stream's next K lies behind V
+        if (!(i & 1)) {
+          if (!full(v)) break;
+          if (more && !full(v + 1)) break;
         }
-        umma_commit(b_s + 8 * s);
-      };
-      auto pv = [&](int s, unsigned k, bool acc) {  // O(s) += P V
-        const uint32_t vt = ring + (k % ST) * M::TILE;
-#pragma unroll
-        for (int i = 0; i < BN / 16; ++i)
-          umma_ts(tmem + 256 + s * 128, tmem + s * 128 + i * 8, umma_desc(vt + i * 2048, M::HALF, 1024), id_pv,
-                  acc || i > 0);
-      };
-      auto release = [&](unsigned k) { umma_commit(b_empty + 8 * (k % ST)); };
-      while (ok && w.next()) {
-        const int nb = w.hi - w.lo;
-        ok = bar_wait(b_q, nq & 1, &s_abort);
-        ++nq;
+        ok = bar_wait_warp(b_p + 16 * s + 8 * (i & 1), (np >> 1) & 1, &s_abort);
+        ++np;
         if (!ok) break;
         tc_fence_after();
-        if (NQ == 2) {
-          if (!full(slot)) break;
-          qk(0, slot);
-          qk(1, slot);
-          release(slot);
-          ++slot;
-          for (int b = 0; b < nb; ++b) {
-            const unsigned v = slot, k = slot + 1;
-            const bool more = b + 1 < nb;
-            if (!full(v) || !have_p(0)) break;
-            pv(0, v, b > 0);
-            if (more) {
-              if (!full(k)) break;
-              qk(0, k);
-            } else {
-              umma_commit(b_o);
-            }
-            if (!have_p(1)) break;
-            pv(1, v, b > 0);
-            release(v);
-            ++slot;
-            if (more) {
-              qk(1, k);
-              release(k);
-              ++slot;
-            } else {
-              umma_commit(b_o + 8);
-            }
-          }
-        } else {
-          for (int s = 0; s < 2 && s < nb; ++s) {
-            if (!full(slot)) break;
-            qk(s, slot);
-            release(slot);
-            ++slot;
-          }
-          if (!ok) break;
-          for (int b = 0; b < nb; ++b) {
-            const int s = b & 1;
-            if (!full(slot) || !have_p(s)) break;
-            pv(s, slot, b >= 2);
-            release(slot);
-            ++slot;
-            if (b + 2 < nb) {
-              if (!full(slot)) break;
-              qk(s, slot);
-              release(slot);
-              ++slot;
-            } else {
-              umma_commit(b_o + 8 * s);
-            }
-          }
-        }
+        pv(i, v);
+        if (more) qk(i, v + 1);
       }
-      if (!ok) {
-        // products in flight end before the CTA does
-        umma_commit(b_q + 8);
-        bar_drain(b_q + 8, 0);
-      }
+      if (!ok) break;
+      if (mine > 0) umma_commit(b_o + 8 * s);
+      slot0 += 2 * nb;
+    }
+    if (!ok) {
+      // products in flight end before the CTA does
+      umma_commit(b_end + 8 * s);
+      bar_drain(b_end + 8 * s, 0);
     }
     __syncwarp();
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
     // ---- softmax and epilogue ----
     const int s = warp >> 2;                              // stream
     const int r = (warp & 3) * 32 + lane;                 // row of its tile
@@ -296,83 +284,25 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
       const int all_seen = a.bt.mask ? w.pctx : w.pctx + tile0 / p.g + 1;   // tokens that the whole unit sees
       float m = -INFINITY, l = 0.0f;
       const int mine = NQ == 2 ? nb : (nb + 1 - s) >> 1;  // this stream's blocks
-      for (int j = 0; j < mine; ++j) {
-        const int bb = NQ == 2 ? j : 2 * j + s;
-        const int j0 = (w.lo + bb) * BN;
-        const bool masked = j0 + BN > all_seen;
-        if (!bar_wait_warp(b_s + 8 * s, ns & 1, &s_abort)) break;
+      for (int i = 0; i < 2 * mine; ++i) {
+        const int bb = NQ == 2 ? i >> 1 : (i & ~1) + s;
+        const int blk0 = (w.lo + bb) * BN, j0 = blk0 + (i & 1) * SB;
+        const bool masked = j0 + SB > all_seen;
+        const uint32_t tb = ts + (i & 1) * SB;
+        if (!bar_wait_warp(b_s + 16 * s + 8 * (i & 1), (ns >> 1) & 1, &s_abort)) break;
         ++ns;
         tc_fence_after();
-        if (live) {
-          uint32_t sv[4][32];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(sv[q], ts + 32 * q);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_wait_ld(sv[q]);
-          if (masked) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t bits = x < R ? seen_bits(a.bt, row, t, w.pctx, w.plen, j0 + 32 * q) : 0u;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(bits >> i & 1u)) sv[q][i] = 0xff800000u;
-            }
-          }
-          float mx[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            mx[q] = __uint_as_float(sv[q][0]);
-#pragma unroll
-            for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(sv[q][i]));
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const float mn = fmaxf(m, top);
-          const bool raise = (m == -INFINITY) ? mn > -INFINITY : (mn - m) * c > kRaise;
-          if (__any_sync(0xffffffffu, raise)) {
-            const float f = m == -INFINITY ? 0.0f : ex2f((m - mn) * c);
-            m = mn;
-            l *= f;
-            if (j > 0) {
-#pragma unroll 1
-              for (int q = 0; q < D; q += 32) {
-                uint32_t o[32];
-                tmem_ld32(o, to + s * 128 + q);
-                tmem_wait_ld(o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st32(to + s * 128 + q, o);
-              }
-            }
-          }
-          const float mc = m == -INFINITY ? 0.0f : m * c;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float e0 = ex2f(fmaf(__uint_as_float(sv[q][i]), c, -mc));
-              const float e1 = ex2f(fmaf(__uint_as_float(sv[q][i + 1]), c, -mc));
-              sum[i & 2] += e0;
-              sum[(i & 2) + 1] += e1;
-              pk[i >> 1] = pack2<BF>(e0, e1);
-            }
-            tmem_st16(ts + 16 * q, pk);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_wait_st();
-        }
-        if (masked) {
-          // V's rows past the end and non-finite elements become zeroes
-          const unsigned k = slot0 + (NQ == 2 ? 2 * bb + 1 : (nb > 1 ? 2 : 1) + bb + (bb < nb - 2 ? bb : nb > 2 ? nb - 2 : 0));
+        if (!(i & 1) && blk0 + BN > all_seen) {
+          // before the product may start: V's rows past the end and non-finite elements become zeroes
+          const unsigned k = slot0 + v_slot<NQ>(bb, nb);
           if (!bar_wait_warp(b_full + 8 * (k % ST), (k / ST) & 1, &s_abort)) break;
           const uint32_t vt = ring + (k % ST) * M::TILE;
-          for (int i = tid & 127; i < M::TILE / 16; i += 128) {
-            const uint32_t ad = vt + 16 * i;
+          for (int y = tid & 127; y < M::TILE / 16; y += 128) {
+            const uint32_t ad = vt + 16 * y;
             uint32_t v[4], z = 0u;
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(ad) : "memory");
-            const bool past = j0 + ((i >> 3) & 127) >= w.plen;
+            const bool past = blk0 + ((y >> 3) & 127) >= w.plen;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t bad = past ? 0xffffffffu : nonfinite2<BF>(v[e]);
@@ -387,8 +317,95 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
           }
           fence_async();
         }
+        if (live) {
+          // P with the maximum of what came before, while the sub-block's own is
+          // found beside it: only where that has grown by 2^kRaise (always at
+          // the start) is O rescaled and P taken again
+          uint32_t sv[2][32];
+          float mc = m == -INFINITY ? 0.0f : m * c;
+          uint64_t sum[4];
+          // 64 weights in groups of eight, the groups' steps interleaved (written
+          // in order: the schedule is otherwise one pipe after another)
+          float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+          auto weights = [&](bool top) {
+            uint32_t pk[2][16];
+            float z[2][8];
+            uint64_t e[2][4];
+            auto sval = [&](int k) { return __uint_as_float(sv[k >> 5][k & 31]); };
+#pragma unroll
+            for (int y = 0; y < 8; ++y) z[0][y] = fma_o(sval(y), c, -mc);
+#pragma unroll
+            for (int g = 0; g <= 8; ++g) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                if (g < 8) {
+                  const float e0 = ex2_o(z[g & 1][2 * y]);
+                  if (g < 7) {
+                    z[(g + 1) & 1][2 * y] = fma_o(sval(8 * g + 8 + 2 * y), c, -mc);
+                    z[(g + 1) & 1][2 * y + 1] = fma_o(sval(8 * g + 9 + 2 * y), c, -mc);
+                  }
+                  const float e1 = ex2_o(z[g & 1][2 * y + 1]);
+                  if (top) mx[y] = max3_o(mx[y], sval(8 * g + 2 * y), sval(8 * g + 2 * y + 1));
+                  e[g & 1][y] = pair(e0, e1);
+                }
+                if (g > 0) {
+                  const uint64_t d2 = e[(g - 1) & 1][y];
+                  sum[y] = add2_o(sum[y], d2);
+                  const float2 f2 = unpair(d2);
+                  pk[(g - 1) >> 2][((g - 1) & 3) * 4 + y] = pack2_o<BF>(f2.x, f2.y);
+                }
+              }
+              if (g == 4) tmem_st16(tb, pk[0]);          // over columns that have been read
+            }
+            tmem_st16(tb + 16, pk[1]);
+          };
+          sum[0] = sum[1] = sum[2] = sum[3] = 0ull;
+          {
+            tmem_ld32(sv[0], tb);
+            tmem_ld32(sv[1], tb + 32);
+            tmem_wait_ld(sv[0]);
+            tmem_wait_ld(sv[1]);
+            if (masked) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint32_t bits = x < R ? seen_bits(a.bt, row, t, w.pctx, w.plen, j0 + 32 * q) : 0u;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!(bits >> e & 1u)) sv[q][e] = 0xff800000u;
+              }
+            }
+            weights(true);
+          }
+          const float mn = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          const bool raise = (m == -INFINITY) ? mn > -INFINITY : (mn - m) * c > kRaise;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float f = m == -INFINITY ? 0.0f : ex2f((m - mn) * c);
+            m = mn;
+            l *= f;
+            mc = m == -INFINITY ? 0.0f : m * c;
+            tmem_wait_st();                   // the first P before its replacement
+            if (i > 0) {
+              // the product before this one has to be in O
+              if (bar_wait_warp(b_pv + 8 * s, (ns - 2) & 1, &s_abort)) tc_fence_after();
+#pragma unroll 1
+              for (int q = 0; q < D; q += 32) {
+                uint32_t o[32];
+                tmem_ld32(o, to + s * 128 + q);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(to + s * 128 + q, o);
+              }
+            }
+            sum[0] = sum[1] = sum[2] = sum[3] = 0ull;
+            weights(false);
+          }
+          const float2 y = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+          l += y.x + y.y;
+          tmem_wait_st();
+        }
         tc_fence_before();
-        bar_arrive(b_p + 8 * s);
+        bar_arrive(b_p + 16 * s + 8 * (i & 1));
       }
       if (mine > 0) {
         if (bar_wait_warp(b_o + 8 * s, no & 1, &s_abort)) tc_fence_after();
@@ -491,7 +508,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
   }
   __syncthreads();
   if (s_abort && tid == 0) atomicOr(p.err, CONFKV_FLAG_TIMEOUT);
-    if (warp == 9) {
+    if (warp == 10) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
   }

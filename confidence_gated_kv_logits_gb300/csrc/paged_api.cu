@@ -4,8 +4,8 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <mutex>
 #include <new>
-#include <string>
 
 #include "paged_attend.cuh"
 
@@ -17,7 +17,7 @@ struct DeviceGuard {
   int prev = -1;
   explicit DeviceGuard(int dev) {
     if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    if (dev == prev) prev = -1;
+    if (dev < 0 || dev == prev) prev = -1;
     else cudaSetDevice(dev);
   }
   ~DeviceGuard() {
@@ -112,6 +112,34 @@ cudaError_t encode_maps(const Pool& p, AttendMaps* m) {
   return cudaSuccess;
 }
 
+// The device's SM count and, the first time, the kernels' shared-memory limits
+// (function attributes hold per device).
+cudaError_t device_ready(int dev, int* sms) {
+  constexpr int kDevices = 64;
+  static std::mutex mu;
+  static int known[kDevices] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+  if (!known[dev]) {
+    int n = 0;
+    cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = setup_attend_few();
+    if (e == cudaSuccess) e = setup_attend_many();
+    if (e != cudaSuccess) return e;
+    known[dev] = n;
+  }
+  *sms = known[dev];
+  return cudaSuccess;
+}
+
+// [flags][tickets] (zeroed by the caller) [(maximum, sum)][accumulators]: two
+// places per CTA, as a CTA's share cuts at most the unit it starts in and the
+// one it ends in
+constexpr size_t kTicketsAt = 256;
+size_t scratch_rows(int sms) { return 2 * static_cast<size_t>(sms) * std::max(kFewCtasPerSm * kFewRows, kManyRows); }
+size_t scratch_bytes_of(int sms, int d) { return CONFKV_PAGED_ZEROED + scratch_rows(sms) * (2 + d) * sizeof(float); }
+bool tickets_fit(int sms) { return kTicketsAt + sizeof(unsigned int) * kFewCtasPerSm * sms <= CONFKV_PAGED_ZEROED; }
+
 Batch batch_of(const confkv_paged_batch* b) {
   return Batch{b->batch, b->max_blocks, b->page_table, b->ctx_len, b->q_start, b->mask, b->mask ? b->mask_words : 0};
 }
@@ -120,15 +148,26 @@ Batch batch_of(const confkv_paged_batch* b) {
 
 extern "C" {
 
+size_t confkv_paged_scratch(int head_dim, int device) {
+  int dev = device, sms = 0;
+  if ((head_dim != 64 && head_dim != 128) || (dev < 0 && cudaGetDevice(&dev) != cudaSuccess) ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || !tickets_fit(sms)) {
+    cudaGetLastError();
+    return 0;
+  }
+  return scratch_bytes_of(sms, head_dim);
+}
+
 int confkv_paged_create(int layers, int heads, int kv_heads, int head_dim, int num_pages, int page_size,
-                        int dtype, int device, void* k_pages, void* v_pages, confkv_paged** out) {
+                        int dtype, int device, void* k_pages, void* v_pages, void* scratch, size_t scratch_bytes,
+                        confkv_paged** out) {
   if (!out) return CONFKV_ERR_INVALID_ARG;
   *out = nullptr;
   if (layers < 1 || layers > 32767 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 ||
       heads / kv_heads > confkv::kMaxGroup || (head_dim != 64 && head_dim != 128) || num_pages < 1 ||
       (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256) ||
-      (dtype != CONFKV_FP16 && dtype != CONFKV_BF16) || !k_pages || !v_pages ||
-      ((reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 127))
+      (dtype != CONFKV_FP16 && dtype != CONFKV_BF16) || !k_pages || !v_pages || !scratch ||
+      (reinterpret_cast<uintptr_t>(scratch) & 255) || ((reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 127))
     return CONFKV_ERR_INVALID_ARG;
   // rows of a pool stay below 2^31 (checked factor by factor: no overflow)
   long long n = layers;
@@ -155,40 +194,23 @@ int confkv_paged_create(int layers, int heads, int kv_heads, int head_dim, int n
   p.ps = page_size;
   while ((1 << p.ps_shift) < page_size) ++p.ps_shift;
   p.bf16 = dtype == CONFKV_BF16;
-  cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&p.err), sizeof(int32_t));
-  if (e == cudaSuccess) e = cudaMemset(p.err, 0, sizeof(int32_t));
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&kv->sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) {
-    // two places per CTA: a CTA's share cuts at most the unit it starts in and the one it ends in
-    Scratch& sc = kv->scratch;
-    const size_t rows = 2 * static_cast<size_t>(kv->sms) * std::max(kFewCtasPerSm * kFewRows, kManyRows);
-    e = cudaMalloc(reinterpret_cast<void**>(&sc.acc), rows * p.d * sizeof(float));
-    if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&sc.ml), rows * 2 * sizeof(float));
-    const size_t nt = sizeof(unsigned int) * kFewCtasPerSm * kv->sms;
-    if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&sc.ticket), nt);
-    if (e == cudaSuccess) e = cudaMemset(sc.ticket, 0, nt);
-  }
+  cudaError_t e = device_ready(dev, &kv->sms);
   if (e == cudaSuccess) e = encode_maps(p, &kv->maps);
-  if (e == cudaSuccess) e = setup_attend_few();
-  if (e == cudaSuccess) e = setup_attend_many();
-  if (e == cudaSuccess) e = cudaDeviceSynchronize();
-  if (e != cudaSuccess) {
+  if (e != cudaSuccess || !tickets_fit(kv->sms) || scratch_bytes < scratch_bytes_of(kv->sms, head_dim)) {
     cudaGetLastError();
-    confkv_paged_free(kv);
-    return e == cudaErrorMemoryAllocation ? CONFKV_ERR_OOM : CONFKV_ERR_CUDA;
+    delete kv;
+    return e != cudaSuccess ? CONFKV_ERR_CUDA : CONFKV_ERR_CAPACITY;
   }
+  char* at = static_cast<char*>(scratch);
+  p.err = reinterpret_cast<int32_t*>(at);
+  kv->scratch.ticket = reinterpret_cast<unsigned int*>(at + kTicketsAt);
+  kv->scratch.ml = reinterpret_cast<float*>(at + CONFKV_PAGED_ZEROED);
+  kv->scratch.acc = kv->scratch.ml + 2 * scratch_rows(kv->sms);
   *out = kv;
   return CONFKV_OK;
 }
 
-void confkv_paged_free(confkv_paged* kv) {
-  if (!kv) return;
-  DeviceGuard guard(kv->device);
-  for (void* m : {static_cast<void*>(kv->pool.err), static_cast<void*>(kv->scratch.acc),
-                  static_cast<void*>(kv->scratch.ml), static_cast<void*>(kv->scratch.ticket)})
-    if (m) cudaFree(m);
-  delete kv;
-}
+void confkv_paged_free(confkv_paged* kv) { delete kv; }
 
 const char* confkv_paged_last_error(const confkv_paged* kv) { return kv ? kv->msg : "null handle"; }
 
@@ -329,7 +351,7 @@ size_t confkv_beam_workspace(int batch, int beams, int vocab, int keep, int dtyp
 int confkv_beam_select(const void* logits, int dtype, int64_t row_stride, int batch, int beams, int vocab, int keep,
                        const float* scores, const uint8_t* finished, int pad_token, float* score_out,
                        int32_t* parent_out, int32_t* token_out, int32_t* flags_out, void* workspace,
-                       size_t workspace_bytes, void* stream) {
+                       size_t workspace_bytes, int device, void* stream) {
   if (!beam_sizes(batch, beams, vocab, keep, dtype) || !logits || !scores || !score_out || !parent_out || !token_out ||
       !workspace || row_stride < vocab || row_stride >= (1ll << 40) || pad_token < 0 || pad_token >= vocab)
     return CONFKV_ERR_INVALID_ARG;
@@ -344,6 +366,7 @@ int confkv_beam_select(const void* logits, int dtype, int64_t row_stride, int ba
     return CONFKV_ERR_INVALID_ARG;
   const BeamArgs a{logits, dtype, row_stride, batch, beams, vocab, keep, scores, finished, pad_token, score_out,
                    parent_out, token_out, flags_out, workspace};
+  DeviceGuard guard(device);
   return launch_beam(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CONFKV_OK : CONFKV_ERR_CUDA;
 }
 

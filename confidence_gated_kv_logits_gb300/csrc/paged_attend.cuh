@@ -60,24 +60,47 @@ __device__ __forceinline__ size_t piece_place(const W& w, int i) {
 template <int TM, int N, typename W>
 __device__ __forceinline__ void join_row(const Scratch& sc, const W& w, int row, int ch, int d, float c, float (&x)[N],
                                          float& m, float& l) {
+  // several pieces' loads in flight: the chain of L2 round trips is what this costs
+  constexpr int U = N > 8 ? 4 : 8;
   m = -INFINITY;
-  for (int i = 0; i < w.pieces; ++i) m = fmaxf(m, __ldcg(sc.ml + (piece_place(w, i) * TM + row) * 2));
   l = 0.0f;
 #pragma unroll
   for (int e = 0; e < N; ++e) x[e] = 0.0f;
-  for (int i = 0; i < w.pieces; ++i) {
-    const size_t at = piece_place(w, i) * TM + row;
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(sc.ml + at * 2));
-    if (ml.x == -INFINITY) continue;
-    const float f = ex2f((ml.x - m) * c);
-    l = fmaf(f, ml.y, l);
+  for (int i0 = 0; i0 < w.pieces; i0 += U) {
+    float2 ml[U];
+    float4 v[U][N / 4];
 #pragma unroll
-    for (int e = 0; e < N; e += 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(sc.acc + at * d + ch + e));
-      x[e] = fmaf(f, v.x, x[e]);
-      x[e + 1] = fmaf(f, v.y, x[e + 1]);
-      x[e + 2] = fmaf(f, v.z, x[e + 2]);
-      x[e + 3] = fmaf(f, v.w, x[e + 3]);
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u < w.pieces) {
+        const size_t at = piece_place(w, i0 + u) * TM + row;
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(sc.ml + at * 2));
+#pragma unroll
+        for (int e = 0; e < N / 4; ++e) v[u][e] = __ldcg(reinterpret_cast<const float4*>(sc.acc + at * d + ch) + e);
+      } else {
+        ml[u] = make_float2(-INFINITY, 0.0f);
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
+    if (mn == -INFINITY) continue;
+    const float f0 = m == -INFINITY ? 0.0f : ex2f((m - mn) * c);
+    l *= f0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] *= f0;
+    m = mn;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ml[u].x == -INFINITY) continue;
+      const float f = ex2f((ml[u].x - m) * c);
+      l = fmaf(f, ml[u].y, l);
+#pragma unroll
+      for (int e = 0; e < N / 4; ++e) {
+        x[4 * e] = fmaf(f, v[u][e].x, x[4 * e]);
+        x[4 * e + 1] = fmaf(f, v[u][e].y, x[4 * e + 1]);
+        x[4 * e + 2] = fmaf(f, v[u][e].z, x[4 * e + 2]);
+        x[4 * e + 3] = fmaf(f, v[u][e].w, x[4 * e + 3]);
+      }
     }
   }
 }

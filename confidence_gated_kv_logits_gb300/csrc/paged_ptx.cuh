@@ -18,6 +18,59 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
+// three-operand maximum and paired fp32 arithmetic
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// the same kept in the order in which they are written (softmax pipeline)
+__device__ __forceinline__ float ex2_o(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3_o(float a, float b, float c) {
+  float y;
+  asm volatile("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float fma_o(float a, float b, float c) {
+  float y;
+  asm volatile("fma.rn.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ uint64_t add2_o(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm volatile("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2_o(float x, float y) {
+  uint32_t r;
+  if constexpr (BF)
+    asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(y), "f"(x));
+  else
+    asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+
 // ---- mbarriers; every wait is bounded by device time and polls ----
 __device__ __forceinline__ void bar_init(uint32_t bar, unsigned count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
@@ -42,14 +95,13 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 // False when the phase did not complete within the limit or another thread of
 // the CTA has given up (*abort, in shared memory, set); sets *abort then.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned parity, volatile int* abort) {
-  if (bar_try(bar, parity)) return true;
-  unsigned long long t0;
-  asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(t0));
+  unsigned long long t0 = 0;
   for (unsigned i = 1; i < kWaitPolls; ++i) {
     if (bar_try(bar, parity)) return true;
-    if ((i & 31u) == 0) {
+    if ((i & 63u) == 0) {
       unsigned long long t;
       asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(t));
+      t0 = t0 ? t0 : t;
       if (*abort || t - t0 > kWaitLimitNs) break;
     }
   }
@@ -127,36 +179,56 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // ---- tcgen05 ----
-// shared-memory operand descriptor, 128-byte swizzle (byte address and
-// strides; the strides' meaning is the caller's: K-major: sbo = 8 rows;
-// MN-major: lbo = from one 64-element block of MN to the next, sbo = 8 rows of K)
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// shared-memory operand descriptor, 128-byte swizzle: the low word holds the
+// byte address and `lbo`, the high word `sbo` (byte strides; K-major: sbo = 8
+// rows, lbo unused; MN-major: lbo = from one 64-element block of MN to the
+// next, sbo = 8 rows of K).  An offset of the address is added to the low word.
+__device__ __forceinline__ uint32_t umma_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16);
 }
+__host__ __device__ constexpr uint32_t umma_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
 // instruction descriptor of kind::f16: fp32 accumulator, A and B both fp16 or
 // both bf16, A K-major, B K-major or MN-major
 __host__ __device__ constexpr uint32_t umma_idesc(bool bf, int m, int n, bool b_mn) {
   return (1u << 4) | ((bf ? 1u : 0u) << 7) | ((bf ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// One product of a 128 x 16 by a 16 x n operand, issued by one elected thread:
+// the whole warp comes here together, so that the operands' words stay in
+// uniform registers (a branch taken by one lane moves each of them there for
+// every product: 120 cycles per product instead of the 64 that it takes).
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                        uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n elect.sync _|q, 0xffffffff;\n setp.ne.u32 p, %6, 0;\n"
+      " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                        uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n elect.sync _|q, 0xffffffff;\n setp.ne.u32 p, %5, 0;\n"
+      " mov.b64 b, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
       : "memory");
 }
+// arrives on `bar` once the products issued so far have completed
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
 }
+// one arrival by one elected thread of the warp
+__device__ __forceinline__ void bar_arrive_warp(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 // waits for this thread's loads; the registers pass through, so no use of them

@@ -7,10 +7,28 @@ selection.  Tensors are checked (device, type, layout) and passed on; nothing
 is copied, converted or computed here.  As everywhere in CUDA, a tensor that
 is used on another stream than its own must stay alive until that work is
 done (``Tensor.record_stream``).
+
+The checks are written for few attribute reads per tensor: for a single token
+they and the launch are the call's whole cost.
 """
 import ctypes
 
 FP16, BF16, FP32 = 0, 1, 2
+ZEROED = 16384                      # CONFKV_PAGED_ZEROED
+torch = None                        # imported with the first handle
+_raw_stream = None
+_F32 = _I32 = None
+
+
+def _load():
+    """The library; torch, on first use (importing the package needs none)."""
+    global torch, _raw_stream, _F32, _I32
+    from . import load_library
+    if torch is None:
+        import torch as t
+        torch, _raw_stream = t, t._C._cuda_getCurrentRawStream
+        _F32, _I32 = t.float32, t.int32
+    return load_library()
 
 
 class BatchStruct(ctypes.Structure):
@@ -25,7 +43,9 @@ def declare(L):
     vp, ci, cl, cf, sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
                           ctypes.c_size_t)
     L.confkv_paged_create.restype = ci
-    L.confkv_paged_create.argtypes = [ci] * 8 + [vp, vp, ctypes.POINTER(vp)]
+    L.confkv_paged_create.argtypes = [ci] * 8 + [vp, vp, vp, sz, ctypes.POINTER(vp)]
+    L.confkv_paged_scratch.restype = sz
+    L.confkv_paged_scratch.argtypes = [ci, ci]
     L.confkv_paged_free.restype = None
     L.confkv_paged_free.argtypes = [vp]
     L.confkv_paged_last_error.restype = ctypes.c_char_p
@@ -45,41 +65,53 @@ def declare(L):
     L.confkv_beam_workspace.argtypes = [ci] * 5
     L.confkv_beam_select.restype = ci
     L.confkv_beam_select.argtypes = [vp, ci, cl, ci, ci, ci, ci, vp, vp, ci, vp, vp, vp, vp, vp,
-                                     sz, vp]
+                                     sz, ci, vp]
 
 
 def _dtype_code(dtype):
-    import torch
     return {torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32}.get(dtype)
 
 
 class _Device:
     """Checks of tensor arguments against one device."""
 
-    def _ints(self, t, shape, name):
-        import torch
-        if t.dtype is not torch.int32 or t.get_device() != self._index or not t.is_contiguous() \
-                or tuple(t.shape) != shape:
-            raise ValueError(f"{name}: want contiguous int32 {shape} on {self.device}, got "
-                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    def _dense(self, t, dtype, shape, name):
+        """Address of a contiguous tensor."""
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
+            raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {self.device}, got "
+                             f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
         return t.data_ptr()
 
-    def _rows(self, t, rows, heads, name):
+    def _rows(self, t, shape, name):
         """Address and row stride of a [rows, heads, head_dim] tensor whose rows are dense."""
-        s = t.stride()
-        if t.dtype is not self.dtype or t.get_device() != self._index \
-                or t.shape != (rows, heads, self.head_dim) \
-                or s[2] != 1 or (s[1] != self.head_dim and heads > 1):
-            raise ValueError(f"{name}: want {self.dtype} {(rows, heads, self.head_dim)} on "
-                             f"{self.device} with dense rows, got {t.dtype} {tuple(t.shape)} "
-                             f"strides {s} on {t.device}")
-        return t.data_ptr(), (s[0] if rows > 1 else max(s[0], heads * self.head_dim))
+        if t.dtype is self.dtype and t.shape == shape and t.get_device() == self._index:
+            if t.is_contiguous():
+                return t.data_ptr(), shape[1] * shape[2]
+            s = t.stride()
+            if s[2] == 1 and (s[1] == shape[2] or shape[1] == 1):
+                return t.data_ptr(), s[0] if shape[0] > 1 else shape[1] * shape[2]
+        raise ValueError(f"{name}: want {self.dtype} {tuple(shape)} on {self.device} with dense rows, got "
+                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+
+    def _scratch(self, n, zeroed):
+        """Device scratch, its first `zeroed` bytes zero whichever stream comes first."""
+        self._mem = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self._mem[:zeroed].zero_()
+        home = torch.cuda.current_stream(self.device)
+        home.synchronize()
+        self._home, self._away = home.cuda_stream, False
+        return self._mem.data_ptr()
 
     def _stream(self, stream):
-        if stream is None:
-            import torch
-            stream = torch.cuda.current_stream(self.device)
-        return stream.cuda_stream
+        s = _raw_stream(self._index) if stream is None else stream.cuda_stream
+        if s != self._home:
+            self._away = True
+        return s
+
+    def _leave(self):
+        # the scratch goes back to its own stream's allocator: work of others has to be done
+        if self._away:
+            torch.cuda.synchronize(self.device)
 
 
 class PagedBatch:
@@ -96,12 +128,13 @@ class PagedBatch:
 
 class PagedKV(_Device):
     """Operators on a paged cache [layers, pages, kv_heads, page_size, head_dim]
-    (fp16 or bf16) that the caller owns; ``heads`` query heads."""
+    (fp16 or bf16) that the caller owns; ``heads`` query heads.  Keeps the
+    attention's scratch: attend calls on one object must be ordered."""
 
     def __init__(self, k_pages, v_pages, heads):
-        from . import ConfKVError, load_library
+        from . import ConfKVError, ERR_INVALID_ARG
         self._h = None
-        self._L = load_library()
+        self._L = _load()
         for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
             if t.dim() != 5 or not t.is_cuda or not t.is_contiguous() or _dtype_code(t.dtype) not in (FP16, BF16):
                 raise ValueError(f"{name}: want a contiguous fp16 or bf16 CUDA tensor [layers, pages, "
@@ -113,16 +146,21 @@ class PagedKV(_Device):
         self.k_pages, self.v_pages = k_pages, v_pages
         self.layers, self.pages, self.kv_heads, self.page_size, self.head_dim = k_pages.shape
         self.heads = heads
+        n = self._L.confkv_paged_scratch(self.head_dim, self._index)
+        if not n:
+            raise ConfKVError(ERR_INVALID_ARG, f"head_dim {self.head_dim} is not supported")
         h = ctypes.c_void_p()
         rc = self._L.confkv_paged_create(self.layers, heads, self.kv_heads, self.head_dim, self.pages,
                                          self.page_size, _dtype_code(self.dtype), self._index,
-                                         k_pages.data_ptr(), v_pages.data_ptr(), ctypes.byref(h))
+                                         k_pages.data_ptr(), v_pages.data_ptr(),
+                                         self._scratch(n, ZEROED), n, ctypes.byref(h))
         if rc:
             raise ConfKVError(rc, "confkv_paged_create failed")
-        self._h = h
+        self._h = h.value
 
     def close(self):
         if getattr(self, "_h", None):
+            self._leave()
             self._L.confkv_paged_free(self._h)
             self._h = None
 
@@ -133,8 +171,8 @@ class PagedKV(_Device):
             pass
 
     def _check(self, rc):
+        from . import ConfKVError
         if rc:
-            from . import ConfKVError
             raise ConfKVError(rc, self._L.confkv_paged_last_error(self._h).decode())
 
     def status(self, check=True):
@@ -149,22 +187,19 @@ class PagedKV(_Device):
     def batch(self, page_table, ctx_len, q_start, mask=None):
         """A ragged batch: page_table int32 [B, blocks], ctx_len int32 [B],
         q_start int32 [B + 1], mask int32 [rows, words] (ancestor bits) or None."""
-        import torch
         if page_table.dim() != 2:
             raise ValueError("page_table: want [batch, blocks]")
         B, blocks = page_table.shape
-        s = BatchStruct(B, blocks, self._ints(page_table, (B, blocks), "page_table"),
-                        self._ints(ctx_len, (B,), "ctx_len"), self._ints(q_start, (B + 1,), "q_start"),
-                        None, 0)
+        s = BatchStruct(B, blocks, self._dense(page_table, _I32, (B, blocks), "page_table"),
+                        self._dense(ctx_len, _I32, (B,), "ctx_len"),
+                        self._dense(q_start, _I32, (B + 1,), "q_start"), None, 0)
         rows = None
         if mask is not None:
-            if mask.dim() != 2 or mask.dtype is not torch.int32:
-                raise ValueError("mask: want int32 [rows, words]")
+            if mask.dim() != 2 or mask.shape[1] < 1:
+                raise ValueError("mask: want int32 [rows, words], a word per row at least")
             rows = mask.shape[0]
-            s.mask = self._ints(mask, tuple(mask.shape), "mask")
+            s.mask = self._dense(mask, _I32, mask.shape, "mask")
             s.mask_words = mask.shape[1]
-            if rows and mask.shape[1] < 1:
-                raise ValueError("mask: want at least one word per row")
         return PagedBatch(s, (page_table, ctx_len, q_start, mask), B, rows)
 
     def append(self, layer, batch, k, v, *, q=None, q_out=None, positions=None, inv_freq=None,
@@ -174,23 +209,24 @@ class PagedKV(_Device):
         the sequence) x `inv_freq` (fp32 [rotary / 2]; None: not rotated), and
         rotates q [rows, heads, head_dim] into q_out (q itself allowed)."""
         rows = k.shape[0]
-        kp, ks = self._rows(k, rows, self.kv_heads, "k")
-        vp, vs = self._rows(v, rows, self.kv_heads, "v")
-        qp = op = None
-        qs = os_ = 0
+        shape = (rows, self.kv_heads, self.head_dim)
+        kp, ks = self._rows(k, shape, "k")
+        vp, vs = self._rows(v, shape, "v")
+        qp = op = fp = pp = None
+        qs = os_ = rotary = 0
         if q is not None or q_out is not None:
             if q is None or q_out is None:
                 raise ValueError("q and q_out go together")
-            qp, qs = self._rows(q, rows, self.heads, "q")
-            op, os_ = self._rows(q_out, rows, self.heads, "q_out")
-        fp, rotary = None, 0
+            shape = (rows, self.heads, self.head_dim)
+            qp, qs = self._rows(q, shape, "q")
+            op, os_ = self._rows(q_out, shape, "q_out")
         if inv_freq is not None:
-            import torch
-            if inv_freq.dtype is not torch.float32 or inv_freq.get_device() != self._index \
-                    or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-                raise ValueError(f"inv_freq: want contiguous float32 [rotary / 2] on {self.device}")
-            fp, rotary = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
-        pp = None if positions is None else self._ints(positions, (rows,), "positions")
+            if inv_freq.dim() != 1:
+                raise ValueError("inv_freq: want [rotary / 2]")
+            rotary = 2 * inv_freq.shape[0]
+            fp = self._dense(inv_freq, _F32, inv_freq.shape, "inv_freq")
+        if positions is not None:
+            pp = self._dense(positions, _I32, (rows,), "positions")
         rc = self._L.confkv_paged_append(self._h, batch._ref, layer, rows, kp, ks, vp, vs, qp, qs, op,
                                          os_, pp, fp, rotary, 1 if interleaved else 0,
                                          self._stream(stream))
@@ -204,17 +240,10 @@ class PagedKV(_Device):
         rows = q.shape[0]
         if batch.mask_rows is not None and batch.mask_rows < rows:
             raise ValueError(f"the batch's mask has {batch.mask_rows} rows, q has {rows}")
-        qp, qs = self._rows(q, rows, self.heads, "q")
-        op, _ = self._rows(out, rows, self.heads, "out")
-        if not out.is_contiguous():
-            raise ValueError("out: want a contiguous tensor")
-        lp = None
-        if lse is not None:
-            import torch
-            if lse.dtype is not torch.float32 or lse.get_device() != self._index \
-                    or lse.shape != (rows, self.heads) or not lse.is_contiguous():
-                raise ValueError(f"lse: want contiguous float32 {(rows, self.heads)} on {self.device}")
-            lp = lse.data_ptr()
+        shape = (rows, self.heads, self.head_dim)
+        qp, qs = self._rows(q, shape, "q")
+        op = self._dense(out, self.dtype, shape, "out")
+        lp = None if lse is None else self._dense(lse, _F32, (rows, self.heads), "lse")
         rc = self._L.confkv_paged_attend(self._h, batch._ref, layer, rows, qp, qs, op, lp, scale,
                                          self._stream(stream))
         if rc:
@@ -226,25 +255,33 @@ class PagedKV(_Device):
         if page_table.dim() != 2 or path.dim() != 2:
             raise ValueError("page_table and path: want [batch, blocks] and [batch, cap]")
         B, blocks = page_table.shape
+        cap = path.shape[1]
+        one = (B,)
         rc = self._L.confkv_paged_commit(
-            self._h, B, blocks, self._ints(page_table, (B, blocks), "page_table"),
-            self._ints(ctx_len, (B,), "ctx_len"), self._ints(path, (B, path.shape[1]), "path"),
-            path.shape[1], self._ints(path_len, (B,), "path_len"), self._ints(new_len, (B,), "new_len"),
+            self._h, B, blocks, self._dense(page_table, _I32, (B, blocks), "page_table"),
+            self._dense(ctx_len, _I32, one, "ctx_len"), self._dense(path, _I32, (B, cap), "path"), cap,
+            self._dense(path_len, _I32, one, "path_len"), self._dense(new_len, _I32, one, "new_len"),
             self._stream(stream))
         if rc:
             self._check(rc)
 
     def fork(self, parent, beams, table_in, len_in, tail_pages, table_out, len_out, stream=None):
         """Reorders beams: row r of [batch x beams] takes over its parent's pages,
-        the part-filled last one as a copy in tail_pages[r]."""
+        the part-filled last one as a copy in tail_pages[r].  parent: int32
+        [rows] or [batch, beams]."""
         if table_in.dim() != 2:
             raise ValueError("table_in: want [rows, blocks]")
         n, blocks = table_in.shape
+        one = (n,)
+        if parent.dim() == 2 and parent.shape[1] == beams and parent.numel() == n:
+            pp = self._dense(parent, _I32, parent.shape, "parent")
+        else:
+            pp = self._dense(parent, _I32, one, "parent")
         rc = self._L.confkv_paged_fork(
-            self._h, n, beams, blocks, self._ints(parent.view(-1), (n,), "parent"),
-            self._ints(table_in, (n, blocks), "table_in"), self._ints(len_in, (n,), "len_in"),
-            self._ints(tail_pages, (n,), "tail_pages"), self._ints(table_out, (n, blocks), "table_out"),
-            self._ints(len_out, (n,), "len_out"), self._stream(stream))
+            self._h, n, beams, blocks, pp, self._dense(table_in, _I32, (n, blocks), "table_in"),
+            self._dense(len_in, _I32, one, "len_in"), self._dense(tail_pages, _I32, one, "tail_pages"),
+            self._dense(table_out, _I32, (n, blocks), "table_out"), self._dense(len_out, _I32, one, "len_out"),
+            self._stream(stream))
         if rc:
             self._check(rc)
 
@@ -254,10 +291,9 @@ class BeamSelect(_Device):
     `vocab` tokens.  Keeps the scratch: calls on one object must be ordered."""
 
     def __init__(self, batch, beams, vocab, keep, dtype=None, device=None):
-        import torch
-        from . import ConfKVError, ERR_INVALID_ARG, load_library
-        self._L = load_library()
-        self.logits_dtype = torch.float32 if dtype is None else dtype
+        from . import ConfKVError, ERR_INVALID_ARG
+        self._L = _load()
+        self.logits_dtype = _F32 if dtype is None else dtype
         self._code = _dtype_code(self.logits_dtype)
         if self._code is None:
             raise ValueError("dtype: want float16, bfloat16 or float32")
@@ -265,49 +301,46 @@ class BeamSelect(_Device):
         n = self._L.confkv_beam_workspace(batch, beams, vocab, keep, self._code)
         if not n:
             raise ConfKVError(ERR_INVALID_ARG, f"beam sizes {self.sizes} are not supported")
-        self.device = torch.device("cuda", torch.cuda.current_device() if device is None
-                                   else torch.device(device).index if not isinstance(device, int) else device)
-        self._index = self.device.index
-        self._ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
-        # the zeroes must be there whichever stream the first call comes on
-        torch.cuda.current_stream(self.device).synchronize()
+        if device is None:
+            device = torch.cuda.current_device()
+        self._index = device if isinstance(device, int) else torch.device(device).index or 0
+        self.device = torch.device("cuda", self._index)
+        self._bytes = n
+        self._ws = self._scratch(n, n)
+
+    def __del__(self):
+        try:
+            self._leave()
+        except Exception:
+            pass
 
     def select(self, logits, scores, score_out, parent_out, token_out, *, finished=None, pad_token=0,
                flags_out=None, stream=None):
         """logits [batch, beams, vocab] (rows may be strided), scores fp32
         [batch, beams]; score_out fp32, parent_out and token_out int32 [batch,
         keep]; finished bool [batch, beams]; flags_out int32 [batch, beams]."""
-        import torch
         B, W, V, K = self.sizes
-        s = logits.stride()
+        stride = V
         if logits.dtype is not self.logits_dtype or logits.get_device() != self._index \
-                or logits.shape != (B, W, V) or s[2] != 1 or (s[0] != W * s[1] and B > 1):
-            raise ValueError(f"logits: want {self.logits_dtype} {(B, W, V)} on {self.device} with evenly "
-                             f"spaced rows, got {logits.dtype} {tuple(logits.shape)} strides {s} on {logits.device}")
-        stride = s[1] if W > 1 else s[0] if B > 1 else max(V, s[1])
-        for t, n, name in ((scores, W, "scores"), (score_out, K, "score_out")):
-            if t.dtype is not torch.float32 or t.get_device() != self._index or t.shape != (B, n) \
-                    or not t.is_contiguous():
-                raise ValueError(f"{name}: want contiguous float32 {(B, n)} on {self.device}")
-        fp = None
+                or logits.shape != (B, W, V):
+            raise ValueError(f"logits: want {self.logits_dtype} {(B, W, V)} on {self.device}, got "
+                             f"{logits.dtype} {tuple(logits.shape)} on {logits.device}")
+        if not logits.is_contiguous():
+            s = logits.stride()
+            stride = s[1] if W > 1 else s[0]
+            if s[2] != 1 or (B > 1 and s[0] != W * stride) or stride < V:
+                raise ValueError(f"logits: want evenly spaced dense rows, got strides {s}")
+        at, out = (B, W), (B, K)
+        fp = gp = None
         if finished is not None:
-            if finished.dtype not in (torch.bool, torch.uint8) or finished.get_device() != self._index \
-                    or finished.shape != (B, W) or not finished.is_contiguous():
-                raise ValueError(f"finished: want contiguous bool {(B, W)} on {self.device}")
-            fp = finished.data_ptr()
-        gp = None if flags_out is None else self._ints(flags_out, (B, W), "flags_out")
-        cur = torch.cuda.current_device()
-        if cur != self._index:
-            torch.cuda.set_device(self._index)
-        try:
-            rc = self._L.confkv_beam_select(
-                logits.data_ptr(), self._code, stride, B, W, V, K, scores.data_ptr(), fp, pad_token,
-                score_out.data_ptr(), self._ints(parent_out, (B, K), "parent_out"),
-                self._ints(token_out, (B, K), "token_out"), gp, self._ws.data_ptr(), self._ws.numel(),
-                self._stream(stream))
-        finally:
-            if cur != self._index:
-                torch.cuda.set_device(cur)
+            fp = self._dense(finished, torch.uint8 if finished.dtype is torch.uint8 else torch.bool, at, "finished")
+        if flags_out is not None:
+            gp = self._dense(flags_out, _I32, at, "flags_out")
+        rc = self._L.confkv_beam_select(
+            logits.data_ptr(), self._code, stride, B, W, V, K, self._dense(scores, _F32, at, "scores"), fp,
+            pad_token, self._dense(score_out, _F32, out, "score_out"),
+            self._dense(parent_out, _I32, out, "parent_out"), self._dense(token_out, _I32, out, "token_out"),
+            gp, self._ws, self._bytes, self._index, self._stream(stream))
         if rc:
             from . import ConfKVError
             raise ConfKVError(rc, "confkv_beam_select refused its arguments" if rc == -1 else "confkv_beam_select")

@@ -20,13 +20,13 @@
  *     can see (a page number outside the pool, a length past the page table,
  *     a path that is none) is skipped there without any access out of range
  *     and latched as CONFKV_FLAG_* bits, which confkv_paged_status returns.
- *   - No call synchronises the host or allocates memory except create, free
- *     and status, so the others can be captured in CUDA graphs.
- *   - A cache handle owns the attention's split scratch: the GPU work of
- *     successive confkv_paged_attend calls on one handle must be ordered (one
- *     stream, or streams ordered by events; the same for graphs that were
- *     captured from it).  Handles are cheap; concurrent streams take one each
- *     over the same pools.
+ *   - No call allocates device memory or, but for status, synchronises the
+ *     host, so all but create, free and status can be captured in CUDA graphs.
+ *   - A cache handle holds the attention's scratch, memory of the caller: the
+ *     GPU work of successive confkv_paged_attend calls on one handle must be
+ *     ordered (one stream, or streams ordered by events; the same for graphs
+ *     that were captured from it).  Handles are cheap; concurrent streams take
+ *     one each, with a scratch of its own, over the same pools.
  */
 #ifndef CONFKV_PAGED_H_
 #define CONFKV_PAGED_H_
@@ -51,6 +51,16 @@ extern "C" {
 typedef struct confkv_paged confkv_paged;
 
 /*
+ * confkv_paged_scratch -- bytes of device scratch that a handle on `device`
+ * (negative: the current one) needs for this head_dim, 256-byte aligned; 0 for
+ * a head_dim that is refused or where the device cannot be read.  The caller
+ * zeroes its first CONFKV_PAGED_ZEROED bytes before the handle's first call;
+ * every call leaves them ready for the next.
+ */
+#define CONFKV_PAGED_ZEROED 16384
+size_t confkv_paged_scratch(int head_dim, int device);
+
+/*
  * confkv_paged_create -- a handle on caller-owned pools
  *   k_pages, v_pages: [layers][num_pages][kv_heads][page_size][head_dim],
  *   contiguous, 128-byte aligned.
@@ -58,14 +68,17 @@ typedef struct confkv_paged confkv_paged;
  *   page_size 16, 32, 64, 128 or 256, dtype CONFKV_FP16 or CONFKV_BF16;
  *   layers * num_pages * kv_heads * page_size < 2^31.
  *   device: CUDA device of the pools (negative: the current one).
+ *   scratch: confkv_paged_scratch bytes there, not shared with other handles.
  * *out receives the handle (NULL on failure): CONFKV_ERR_INVALID_ARG,
- * CONFKV_ERR_OOM or CONFKV_ERR_CUDA.
+ * CONFKV_ERR_CAPACITY (scratch too small), CONFKV_ERR_OOM (host memory) or
+ * CONFKV_ERR_CUDA.
  */
 int confkv_paged_create(int layers, int heads, int kv_heads, int head_dim, int num_pages,
                         int page_size, int dtype, int device, void* k_pages, void* v_pages,
-                        confkv_paged** out);
+                        void* scratch, size_t scratch_bytes, confkv_paged** out);
 
-/* Releases the handle and its scratch (NULL is a no-op); the pools stay. */
+/* Releases the handle (NULL is a no-op); pools and scratch stay the caller's,
+ * who keeps them until the handle's work is done. */
 void confkv_paged_free(confkv_paged* kv);
 
 /* Message of the last error of this handle (never NULL). */
@@ -151,7 +164,7 @@ int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int l
  *   path: [B][path_cap], rising (path[b][0] < path[b][1] < ...), path_cap
  *   <= 1024; path_len: [B]; new_len: [B], not ctx_len itself.
  * A sequence whose path is no such path stays as it is, with new_len = ctx_len
- * and a flag.
+ * and a flag.  The pages of the drafted tokens belong to one sequence each.
  */
 int confkv_paged_commit(confkv_paged* kv, int batch, int max_blocks, const int32_t* page_table,
                         const int32_t* ctx_len, const int32_t* path, int path_cap,
@@ -196,12 +209,16 @@ size_t confkv_beam_workspace(int batch, int beams, int vocab, int keep, int dtyp
  *   flags_out: int32 [batch][beams] or NULL: CONFKV_FLAG_NONFINITE where a row
  *           with a NaN or +inf logit, without a finite one, or with a NaN or
  *           +inf score was left out, else 0.
- * beams <= 32, keep <= 64, 2 <= vocab, pad_token in 0 .. vocab - 1.
+ *   device: CUDA device of the tensors and the workspace (negative: the
+ *   current one).
+ * beams <= 32, keep <= 64, 2 <= vocab <= 2^24, batch x beams <= 65535,
+ * pad_token in 0 .. vocab - 1.
  */
 int confkv_beam_select(const void* logits, int dtype, int64_t row_stride, int batch, int beams,
                        int vocab, int keep, const float* scores, const uint8_t* finished,
                        int pad_token, float* score_out, int32_t* parent_out, int32_t* token_out,
-                       int32_t* flags_out, void* workspace, size_t workspace_bytes, void* stream);
+                       int32_t* flags_out, void* workspace, size_t workspace_bytes, int device,
+                       void* stream);
 
 #ifdef __cplusplus
 }

@@ -14,26 +14,26 @@ def pkg():
     return pkg
 
 
-GOOD = dict(layers=2, heads=8, kv_heads=2, dim=128, pages=10, page=16, dtype=0, device=0, k=1 << 12, v=1 << 12)
+GOOD = dict(layers=2, heads=8, kv_heads=2, dim=128, pages=10, page=16, dtype=0, device=0, k=1 << 12, v=1 << 12, scratch=1 << 16)
 
 
 @pytest.mark.parametrize("bad", [
     dict(layers=0), dict(layers=40000), dict(heads=0), dict(kv_heads=0), dict(kv_heads=3), dict(heads=34),
     dict(dim=96), dict(dim=0), dict(pages=0), dict(page=8), dict(page=48), dict(page=512), dict(dtype=2),
     dict(dtype=-1), dict(k=None), dict(v=None), dict(k=(1 << 12) + 16), dict(pages=1 << 27),
-    dict(layers=30000, pages=1 << 30)])
+    dict(layers=30000, pages=1 << 30), dict(scratch=None), dict(scratch=(1 << 16) + 128)])
 def test_create_refuses(pkg, bad):
     a = {**GOOD, **bad}
     h = ctypes.c_void_p(7)
     rc = pkg.load_library().confkv_paged_create(
         a["layers"], a["heads"], a["kv_heads"], a["dim"], a["pages"], a["page"], a["dtype"], a["device"],
-        a["k"], a["v"], ctypes.byref(h))
+        a["k"], a["v"], a["scratch"], 1 << 40, ctypes.byref(h))
     assert rc == pkg.ERR_INVALID_ARG and not h.value
 
 
 def test_null_handles(pkg):
     L = pkg.load_library()
-    assert L.confkv_paged_create(2, 8, 2, 128, 10, 16, 0, 0, 4096, 4096, None) == pkg.ERR_INVALID_ARG
+    assert L.confkv_paged_create(2, 8, 2, 128, 10, 16, 0, 0, 4096, 4096, 65536, 1 << 40, None) == pkg.ERR_INVALID_ARG
     assert L.confkv_paged_last_error(None) == b"null handle"
     assert L.confkv_paged_status(None, None) == pkg.ERR_INVALID_ARG
     assert L.confkv_paged_append(None, None, 0, 1, *([0] * 8), None, None, 0, 0, None) == pkg.ERR_INVALID_ARG
@@ -41,6 +41,7 @@ def test_null_handles(pkg):
     assert L.confkv_paged_commit(None, 1, 1, None, None, None, 1, None, None, None) == pkg.ERR_INVALID_ARG
     assert L.confkv_paged_fork(None, 1, 1, 1, *([None] * 7)) == pkg.ERR_INVALID_ARG
     L.confkv_paged_free(None)
+    assert L.confkv_paged_scratch(96, 0) == 0
 
 
 BEAM = dict(batch=2, beams=4, vocab=100, keep=8, dtype=2, stride=100, logits=4096, scores=1 << 20, pad=0,
@@ -58,7 +59,7 @@ def test_beam_refuses(pkg, bad):
     need = L.confkv_beam_workspace(a["batch"], a["beams"], a["vocab"], a["keep"], a["dtype"])
     rc = L.confkv_beam_select(a["logits"], a["dtype"], a["stride"], a["batch"], a["beams"], a["vocab"], a["keep"],
                               a["scores"], None, a["pad"], a["so"], a["po"], a["to"], None, a["ws"],
-                              need if a["bytes"] is None else a["bytes"], None)
+                              need if a["bytes"] is None else a["bytes"], -1, None)
     assert rc == (pkg.ERR_CAPACITY if a["bytes"] == 16 else pkg.ERR_INVALID_ARG)
     if set(bad) & {"batch", "beams", "vocab", "keep", "dtype"}:
         assert need == 0
