@@ -79,7 +79,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
   const int r0 = lane >> 2, t4 = lane & 3;
 
   while (w.next()) {
-    const int b = w.pb, h = w.ph;
+    const int b = w.b, h = w.h;
     const int32_t* table = a.bt.table + static_cast<size_t>(b) * a.bt.max_blocks;
     const int layer_row = (a.layer * p.NP) * p.Hkv;  // page of head h: (layer_row + page * Hkv + h) * ps
     int flag = 0;
@@ -90,7 +90,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
       const int j0 = ci * F::CH;
       const int box = p.ps < F::CH ? p.ps : F::CH;
       const int nb = F::CH / box;
-      const int live = (w.plen - j0 + box - 1) / box;       // boxes with tokens of the sequence
+      const int live = (w.len - j0 + box - 1) / box;       // boxes with tokens of the sequence
       const int n = live < nb ? live : nb;
       if (lane == 0) bar_expect(fb, static_cast<unsigned>(n * box * D * 4));
       __syncwarp();
@@ -117,13 +117,13 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
       if (first + i * kWarps < w.hi) issue(first + i * kWarps, issued++);
 
     // the tile's query rows as A fragments (zero behind the sequence's rows)
-    const int R = w.pT * p.g, base = w.pmt * kRows;
+    const int R = w.T * p.g, base = w.mt * kRows;
     const int ra = base + r0, rb = ra + 8;            // this thread's rows
     const int ta = ra / p.g, tb = rb / p.g;
     uint32_t qf[F::KS][4];
     {
-      const uint16_t* qa = a.q + (w.prow0 + ta) * a.qs + (h * p.g + ra - ta * p.g) * D + 2 * t4;
-      const uint16_t* qb = a.q + (w.prow0 + tb) * a.qs + (h * p.g + rb - tb * p.g) * D + 2 * t4;
+      const uint16_t* qa = a.q + (w.row0 + ta) * a.qs + (h * p.g + ra - ta * p.g) * D + 2 * t4;
+      const uint16_t* qb = a.q + (w.row0 + tb) * a.qs + (h * p.g + rb - tb * p.g) * D + 2 * t4;
 #pragma unroll
       for (int k = 0; k < F::KS; ++k) {
         qf[k][0] = ra < R ? *reinterpret_cast<const uint32_t*>(qa + 16 * k) : 0u;
@@ -133,7 +133,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
       }
     }
     // tokens that every row of the tile sees
-    const int all_seen = a.bt.mask ? w.pctx : w.pctx + base / p.g + 1;
+    const int all_seen = a.bt.mask ? w.ctx : w.ctx + base / p.g + 1;
     float o[F::OT][4];
 #pragma unroll
     for (int i = 0; i < F::OT; ++i)
@@ -165,8 +165,8 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
         }
       }
       if (j0 + F::CH > all_seen) {
-        const uint32_t ba = ra < R ? seen_bits(a.bt, w.prow0 + ta, ta, w.pctx, w.plen, j0) : 0u;
-        const uint32_t bb = rb < R ? seen_bits(a.bt, w.prow0 + tb, tb, w.pctx, w.plen, j0) : 0u;
+        const uint32_t ba = ra < R ? seen_bits(a.bt, w.row0 + ta, ta, w.ctx, w.len, j0) : 0u;
+        const uint32_t bb = rb < R ? seen_bits(a.bt, w.row0 + tb, tb, w.ctx, w.len, j0) : 0u;
 #pragma unroll
         for (int i = 0; i < F::NT; ++i) {
           const int x = 8 * i + 2 * t4;
@@ -183,7 +183,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
           uint32_t x[4];
           asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
                        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(ad) : "memory");
-          if (j0 + row >= w.plen) {
+          if (j0 + row >= w.len) {
             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(ad), "r"(0u) : "memory");
           } else {
 #pragma unroll
@@ -192,7 +192,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
         }
         if (__any_sync(0xffffffffu, odd)) {
           __syncwarp();
-          for (int j = 0; j < F::CH && j0 + j < w.plen; ++j) {
+          for (int j = 0; j < F::CH && j0 + j < w.len; ++j) {
             const bool sa = ba >> j & 1u, sb = bb >> j & 1u;
 #pragma unroll
             for (int i = 0; i < F::OT; ++i) {
@@ -330,14 +330,18 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
       }
     }
     const int rr = base + row;
-    bool mine = whole;
-    if (!whole) {
-      const size_t at = (2 * static_cast<size_t>(blockIdx.x) + (w.lo == 0 ? 1 : 0)) * kRows + row;
+    if (whole) {
+      if (rr < R) {
+        const int t = rr / p.g;
+        store_row<BF, PER>(a, p, w.row0 + t, h * p.g + rr - t * p.g, ch0, x, m, l);
+      }
+    } else {
+      const size_t at = 2 * static_cast<size_t>(blockIdx.x) + (w.lo == 0 ? 1 : 0);
       if (rr < R) {
 #pragma unroll
         for (int e = 0; e < PER; e += 4)
-          *reinterpret_cast<float4*>(sc.acc + at * D + ch0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-        if (ch0 == 0) *reinterpret_cast<float2*>(sc.ml + at * 2) = make_float2(m, l);
+          *reinterpret_cast<float4*>(acc_at<kRows, D>(sc, at, row, ch0 + e)) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        if (ch0 == 0) *reinterpret_cast<float2*>(sc.ml + (at * kRows + row) * 2) = make_float2(m, l);
       }
       __threadfence();
       __syncthreads();
@@ -346,15 +350,14 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
         if (s_last) sc.ticket[w.first_cta] = 0u;
       }
       __syncthreads();
-      mine = s_last;
-      if (mine && rr < R) {
+      if (s_last) {
         __threadfence();
-        join_row<kRows>(sc, w, row, ch0, D, c, x, m, l);
+        if (rr < R) {
+          join_row<kRows, D, PER, (PER > 8 ? 2 : 5)>(sc, w, row, ch0, c, -1, x, m, l);
+          const int t = rr / p.g;
+          store_row<BF, PER>(a, p, w.row0 + t, h * p.g + rr - t * p.g, ch0, x, m, l);
+        }
       }
-    }
-    if (mine && rr < R) {
-      const int t = rr / p.g;
-      store_row<BF, PER>(a, p, w.prow0 + t, h * p.g + rr - t * p.g, ch0, x, m, l);
     }
     fence_async();
     __syncthreads();          // the rings are free again

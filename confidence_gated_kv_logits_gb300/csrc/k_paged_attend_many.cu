@@ -58,17 +58,27 @@ __device__ __forceinline__ unsigned v_slot(int b, int n) {
   return (n > 1 ? 2 : 1) + b + (n > 2 ? (b < n - 2 ? b : n - 2) : 0);
 }
 
+// A piece of a unit as the planning warp hands it to the others, through a
+// ring in shared memory: none of them carries the walk's state in registers.
+struct Piece {
+  int more;                              // 0: the CTA's share ends here
+  int b, h, mt, T, ctx, len, row0, lo, hi, pieces, first_cta;
+};
+constexpr int kPlan = 8;                 // pieces in the ring
+constexpr int kReaders = 11;             // warps that read it
+
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
 
 template <bool BF, int D, int NQ>
 __global__ void __launch_bounds__(kThreads, 1)
-k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_constant__ CUtensorMap mk,
+k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defer, const __grid_constant__ CUtensorMap mk,
               const __grid_constant__ CUtensorMap mv) {
   using M = Many<D, NQ>;
   constexpr int ST = M::ST;
   constexpr int TM = 128 * NQ;
   extern __shared__ unsigned char s_raw[];
-  __shared__ __align__(8) unsigned long long s_bar[2 * ST + 15];
+  __shared__ __align__(8) unsigned long long s_bar[2 * ST + 15 + 2 * kPlan];
+  __shared__ Piece s_plan[kPlan];
   __shared__ Sched s_sched;
   __shared__ long long s_scan[kThreads / 32];
   __shared__ float s_x[NQ == 1 ? 2 * 128 * 2 : 1];          // NQ = 1: the streams' (maximum, sum)
@@ -82,7 +92,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
   // K and V stages full and empty; per stream: S there (two buffers), P there
   // (two), PV done, O done; Q there; a giving-up stream's products done
   const uint32_t b_full = bars, b_empty = bars + 8 * ST, b_s = bars + 16 * ST, b_p = b_s + 32, b_pv = b_p + 32,
-                 b_o = b_pv + 16, b_q = b_o + 16, b_end = b_q + 8;
+                 b_o = b_pv + 16, b_q = b_o + 16, b_end = b_q + 8, b_plan = b_end + 16, b_read = b_plan + 8 * kPlan;
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       bar_init(b_full + 8 * i, 1);
@@ -98,6 +108,10 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
       bar_init(b_end + 8 * i, 1);
     }
     bar_init(b_q, kSoft);
+    for (int i = 0; i < kPlan; ++i) {
+      bar_init(b_plan + 8 * i, 1);
+      bar_init(b_read + 8 * i, kReaders);
+    }
     s_abort = s_dead = s_poison = 0;
     fence_bar_init();
     fence_async();
@@ -108,17 +122,41 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
   }
   pdl_wait();
   pdl_trigger();
-  Walk<TM, BN, kOver> w(p, a.bt, a.rows);
   tc_fence_before();
-  sched_init<kThreads>(w, &s_sched, s_scan, 4);
+  {
+    Walk<TM, BN, kOver> w(p, a.bt, a.rows);
+    sched_init<kThreads>(w, &s_sched, s_scan, 4);
+  }
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  w.start(s_sched);
+  // reading the plan, by whole warps: the next piece (false at the end or when
+  // another warp has given up), and done with it
+  unsigned plan = 0;
+  auto next_piece = [&] {
+    return bar_wait_warp(b_plan + 8 * (plan % kPlan), (plan / kPlan) & 1, &s_abort) && s_plan[plan % kPlan].more;
+  };
+  auto piece_done = [&] {
+    __syncwarp();
+    if (lane == 0) bar_arrive(b_read + 8 * (plan % kPlan));
+    ++plan;
+  };
 
   // 384 threads x 168 registers at launch = 256 x 216 + 128 x 72
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
-    if (warp == 10) {
+    if (warp == 11) {
+      // ---- the plan ----
+      Walk<TM, BN, kOver> w(p, a.bt, a.rows);
+      w.start(s_sched);
+      for (bool more = true; more; ++plan) {
+        more = w.next();
+        if (plan >= kPlan && !bar_wait_warp(b_read + 8 * (plan % kPlan), (plan / kPlan - 1) & 1, &s_abort)) break;
+        if (lane == 0) {
+          s_plan[plan % kPlan] = Piece{more, w.b, w.h, w.mt, w.T, w.ctx, w.len, w.row0, w.lo, w.hi, w.pieces, w.first_cta};
+          bar_arrive(b_plan + 8 * (plan % kPlan));
+        }
+      }
+    } else if (warp == 10) {
     // ---- K and V blocks into the ring ----
     const uint64_t once = stream_policy(), again = reuse_policy();
     const int rows_per = p.ps < BN ? p.ps : BN;
@@ -126,10 +164,11 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
     unsigned slot = 0;
     int flag = 0;
     bool ok = true;
-    while (ok && w.next()) {
-      const int32_t* table = a.bt.table + static_cast<size_t>(w.pb) * a.bt.max_blocks;
+    while (ok && next_piece()) {
+      const Piece& w = s_plan[plan % kPlan];
+      const int32_t* table = a.bt.table + static_cast<size_t>(w.b) * a.bt.max_blocks;
       // other tiles of the head read the same blocks
-      const uint64_t pol = w.pT * p.g > TM ? again : once;
+      const uint64_t pol = w.T * p.g > TM ? again : once;
       auto load = [&](const CUtensorMap* map, int blk) {
         if (!ok) return;
         const unsigned st = slot % ST;
@@ -138,7 +177,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
           return;
         }
         const int j0 = blk * BN;
-        const int live = (w.plen - j0 + rows_per - 1) / rows_per;     // boxes with tokens of the sequence
+        const int live = (w.len - j0 + rows_per - 1) / rows_per;     // boxes with tokens of the sequence
         const int n = live < boxes ? live : boxes;
         if (lane == 0) bar_expect(b_full + 8 * st, static_cast<unsigned>(n * rows_per * D * 2));
         __syncwarp();
@@ -150,7 +189,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
             flag = CONFKV_FLAG_BAD_PAGE;
             page = 0;
           }
-          const int y = (((a.layer * p.NP + page) * p.Hkv + w.ph) << p.ps_shift) + (j & (p.ps - 1));
+          const int y = (((a.layer * p.NP + page) * p.Hkv + w.h) << p.ps_shift) + (j & (p.ps - 1));
           tma_box(ring + st * M::TILE + half * M::HALF + i * rows_per * 128, map, 64 * half, y, b_full + 8 * st, pol);
         }
         ++slot;
@@ -168,6 +207,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
           if (b + 2 < w.hi) load(&mk, b + 2);
         }
       }
+      piece_done();
     }
     if (flag) atomicOr(p.err, flag);
     if (!ok)                    // no copy may land after the CTA has gone
@@ -206,7 +246,8 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
       umma_commit(b_pv + 8 * s);
       if (i & 1) release(k);
     };
-    while (ok && w.next()) {
+    while (ok && next_piece()) {
+      const Piece& w = s_plan[plan % kPlan];
       const int nb = w.hi - w.lo;
       ok = bar_wait_warp(b_q, nq & 1, &s_abort);
       ++nq;
@@ -236,6 +277,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
       if (!ok) break;
       if (mine > 0) umma_commit(b_o + 8 * s);
       slot0 += 2 * nb;
+      piece_done();
     }
     if (!ok) {
       // products in flight end before the CTA does
@@ -253,23 +295,25 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
     const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256;
     const float c = a.scale * kL2E;
     unsigned ns = 0, no = 0, slot0 = 0;
-    while (w.next()) {
+    int4 cut = make_int4(0, 0, 0, 0);                     // the unit whose first piece this CTA ends with
+    while (next_piece()) {
+      const Piece& w = s_plan[plan % kPlan];
       const int nb = w.hi - w.lo;
-      const int R = w.pT * p.g;                           // rows of the head
-      const int tile0 = w.pmt * TM;
+      const int R = w.T * p.g;                           // rows of the head
+      const int tile0 = w.mt * TM;
       // query rows into shared memory
       {
         constexpr int WD = D / 8;
         const int first = NQ == 2 ? s * 128 : 0;
         constexpr int NTH = NQ == 2 ? 128 : 256;
         const int me = NQ == 2 ? tid & 127 : tid;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = me; i < 128 * WD; i += NTH) {
           const int row = i / WD, wd = i % WD, x = tile0 + first + row;
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
           if (x < R) {
             const int t = x / p.g;
-            v = *reinterpret_cast<const uint4*>(a.q + (w.prow0 + t) * a.qs + (w.ph * p.g + x - t * p.g) * D + 8 * wd);
+            v = *reinterpret_cast<const uint4*>(a.q + (w.row0 + t) * a.qs + (w.h * p.g + x - t * p.g) * D + 8 * wd);
           }
           const uint32_t ad = swz128(base + (NQ == 2 ? s * M::TILE : 0) + (wd >> 3) * M::HALF, row, wd & 7);
           asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(ad), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -280,8 +324,8 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
       const int x = tile0 + (NQ == 2 ? s * 128 : 0) + r;  // this thread's row of the head
       const bool live = x - lane < R;                     // the warp holds rows
       const int t = x < R ? x / p.g : 0;
-      const size_t row = w.prow0 + t;
-      const int all_seen = a.bt.mask ? w.pctx : w.pctx + tile0 / p.g + 1;   // tokens that the whole unit sees
+      const size_t row = w.row0 + t;
+      const int all_seen = a.bt.mask ? w.ctx : w.ctx + tile0 / p.g + 1;   // tokens that the whole unit sees
       float m = -INFINITY, l = 0.0f;
       const int mine = NQ == 2 ? nb : (nb + 1 - s) >> 1;  // this stream's blocks
       for (int i = 0; i < 2 * mine; ++i) {
@@ -302,7 +346,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
             uint32_t v[4], z = 0u;
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(ad) : "memory");
-            const bool past = blk0 + ((y >> 3) & 127) >= w.plen;
+            const bool past = blk0 + ((y >> 3) & 127) >= w.len;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t bad = past ? 0xffffffffu : nonfinite2<BF>(v[e]);
@@ -368,7 +412,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
             if (masked) {
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                const uint32_t bits = x < R ? seen_bits(a.bt, row, t, w.pctx, w.plen, j0 + 32 * q) : 0u;
+                const uint32_t bits = x < R ? seen_bits(a.bt, row, t, w.ctx, w.len, j0 + 32 * q) : 0u;
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                   if (!(bits >> e & 1u)) sv[q][e] = 0xff800000u;
@@ -407,6 +451,12 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
         tc_fence_before();
         bar_arrive(b_p + 16 * s + 8 * (i & 1));
       }
+      const bool whole = w.pieces == 1;
+      if (tid == 0 && !whole) {
+        // all other pieces done: this one is joined as it is, without a way through memory
+        s_last = !defer && *const_cast<volatile unsigned int*>(sc.ticket + w.first_cta) == static_cast<unsigned>(w.pieces - 1);
+        __threadfence();
+      }
       if (mine > 0) {
         if (bar_wait_warp(b_o + 8 * s, no & 1, &s_abort)) tc_fence_after();
         ++no;
@@ -429,13 +479,14 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
         w1 = m1 == -INFINITY ? 0.0f : ex2f((m1 - m) * c);
         l = l0 * w0 + l1 * w1;
       }
-      const bool whole = w.pieces == 1;
+      const bool last = !whole && s_last;
+      const int own = static_cast<int>(blockIdx.x) - w.first_cta;   // which piece this is
       const bool poison = *const_cast<volatile int*>(&s_poison) != 0;
       constexpr int COLS = NQ == 1 ? D / 2 : D;           // of this thread's row
       const int col0 = NQ == 1 ? s * (D / 2) : 0;
       const int xr = NQ == 1 ? r : s * 128 + r;           // row of the unit
-      const int hq = w.ph * p.g + x - t * p.g;
-      const size_t place = (2 * static_cast<size_t>(blockIdx.x) + (w.lo == 0 ? 1 : 0)) * TM + xr;
+      const int hq = w.h * p.g + x - t * p.g;
+      const size_t place = 2 * static_cast<size_t>(blockIdx.x) + (w.lo == 0 ? 1 : 0);
       if (live) {
 #pragma unroll 1
         for (int q = 0; q < COLS; q += 32) {
@@ -453,14 +504,14 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
           }
           if (x < R) {
             if (poison) {
-              const int32_t* table = a.bt.table + static_cast<size_t>(w.pb) * a.bt.max_blocks;
+              const int32_t* table = a.bt.table + static_cast<size_t>(w.b) * a.bt.max_blocks;
               int jb = all_seen / BN * BN;
               jb = jb < w.lo * BN ? w.lo * BN : jb;
-              const int je = w.hi * BN < w.plen ? w.hi * BN : w.plen;
+              const int je = w.hi * BN < w.len ? w.hi * BN : w.len;
               for (int j = jb; j < je; ++j) {
                 const int page = table[j >> p.ps_shift];
-                if (page < 0 || page >= p.NP || !(seen_bits(a.bt, row, t, w.pctx, w.plen, j) & 1u)) continue;
-                const uint16_t* v = p.v + (((static_cast<size_t>(a.layer) * p.NP + page) * p.Hkv + w.ph) * p.ps + (j & (p.ps - 1))) * D + col0 + q;
+                if (page < 0 || page >= p.NP || !(seen_bits(a.bt, row, t, w.ctx, w.len, j) & 1u)) continue;
+                const uint16_t* v = p.v + (((static_cast<size_t>(a.layer) * p.NP + page) * p.Hkv + w.h) * p.ps + (j & (p.ps - 1))) * D + col0 + q;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                   const float z = to_f(v[i], BF);
@@ -470,18 +521,25 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
             }
             if (whole) {
               store_row<BF>(a, p, static_cast<int>(row), hq, col0 + q, y, m, l);
+            } else if (last) {
+              float jm = m, jl = l;
+              join_row<TM, D, 32, 1>(sc, w, xr, col0 + q, c, own, y, jm, jl);
+              store_row<BF>(a, p, static_cast<int>(row), hq, col0 + q, y, jm, jl);
             } else {
-              float* to_acc = sc.acc + place * D + col0 + q;
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(to_acc + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-              if (col0 + q == 0) *reinterpret_cast<float2*>(sc.ml + place * 2) = make_float2(m, l);
+                *reinterpret_cast<float4*>(acc_at<TM, D>(sc, place, xr, col0 + q + i)) =
+                    make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+              if (col0 + q == 0) *reinterpret_cast<float2*>(sc.ml + (place * TM + xr) * 2) = make_float2(m, l);
             }
           }
         }
         tc_fence_before();
       }
-      if (!whole) {
+      if (last) {
+        if (tid == 0) sc.ticket[w.first_cta] = 0u;
+        soft_sync();         // s_last and, NQ = 1, both streams' O are read before any thread goes on
+      } else if (!whole && !defer) {
         __threadfence();
         soft_sync();
         if (tid == 0) {
@@ -491,19 +549,28 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
         soft_sync();
         if (s_last) {
           __threadfence();
-          for (int i = tid; i < TM * (D / 4); i += kSoft) {
-            const int rr = i / (D / 4), ch = 4 * (i % (D / 4)), xx = tile0 + rr;
-            if (xx >= R) break;
-            float y[4], mm, ll;
-            join_row<TM>(sc, w, rr, ch, D, c, y, mm, ll);
-            const int tt = xx / p.g;
-            store_row<BF>(a, p, w.prow0 + tt, w.ph * p.g + xx - tt * p.g, ch, y, mm, ll);
+          // few rows: more threads to a row's channels
+          const int rows = R - tile0 < TM ? R - tile0 : TM;
+          const int pad = rows > 128 ? 256 : rows > 64 ? 128 : 64;
+          const int jr = tid & (pad - 1), jx = tile0 + jr;
+          constexpr int JN = 32;
+          if (jr < rows) {
+            const int jt = jx / p.g;
+#pragma unroll 1
+            for (int ch = (tid / pad) * JN; ch < D; ch += (kSoft / pad) * JN) {
+              float y[JN] = {}, jm, jl;
+              join_row<TM, D, JN, 2>(sc, w, jr, ch, c, -1, y, jm, jl);
+              store_row<BF>(a, p, w.row0 + jt, w.h * p.g + jx - jt * p.g, ch, y, jm, jl);
+            }
           }
         }
-      } else if (NQ == 1) {
-        soft_sync();         // both streams' O has been read before either goes on
+      } else if (NQ == 1 || !whole) {
+        soft_sync();
       }
+      if (defer && tid == 0 && !whole && own == 0) cut = make_int4(w.pieces, w.b, w.h, w.mt);
+      piece_done();
     }
+    if (defer && tid == 0) sc.cut[blockIdx.x] = cut;
     tc_fence_before();
   }
   __syncthreads();
@@ -514,9 +581,38 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const __grid_c
   }
 }
 
+// The cut units of a deferring launch (tiles of 128 rows), joined on all SMs:
+// blockIdx.x is the CTA that held a unit's first piece, a thread takes 8
+// channels of a row.  (8 units of 65 rows in 19 pieces each: 20 us where 8
+// CTAs join, 3 us here.)
+constexpr int kJoinThreads = 128;
+template <bool BF, int D>
+__global__ void __launch_bounds__(kJoinThreads)
+k_join(const Pool p, const AttendArgs a, const Scratch sc) {
+  pdl_wait();
+  pdl_trigger();
+  const int4 cut = sc.cut[blockIdx.x];
+  if (cut.x < 2) return;
+  Walk<128, BN, kOver> w(p, a.bt, a.rows);
+  int flag = 0;
+  w.sequence(cut.y, flag);
+  w.first_cta = blockIdx.x;
+  w.pieces = cut.x;
+  const int row = threadIdx.x, ch = 8 * blockIdx.y, x = cut.w * 128 + row;
+  if (x >= w.T * p.g) return;
+  float y[8] = {}, m, l;
+  join_row<128, D, 8, 10>(sc, w, row, ch, a.scale * kL2E, -1, y, m, l);
+  const int t = x / p.g;
+  store_row<BF>(a, p, w.row0 + t, cut.z * p.g + x - t * p.g, ch, y, m, l);
+}
+
 template <bool BF, int D, int NQ>
-cudaError_t go(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m, int ctas, cudaStream_t s) {
-  return launch_pdl(k_attend_many<BF, D, NQ>, dim3(ctas), dim3(kThreads), Many<D, NQ>::SMEM, s, p, a, sc, m.k_many, m.v_many);
+cudaError_t go(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m, int ctas, bool defer,
+               cudaStream_t s) {
+  const cudaError_t e = launch_pdl(k_attend_many<BF, D, NQ>, dim3(ctas), dim3(kThreads), Many<D, NQ>::SMEM, s, p, a, sc,
+                                   defer ? 1 : 0, m.k_many, m.v_many);
+  if (e != cudaSuccess || !defer) return e;
+  return launch_pdl(k_join<BF, D>, dim3(ctas, D / 8), dim3(kJoinThreads), 0, s, p, a, sc);
 }
 template <bool BF, int D, int NQ>
 cudaError_t set() {
@@ -526,14 +622,14 @@ cudaError_t set() {
 }  // namespace
 
 cudaError_t launch_attend_many(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m, int ctas,
-                               bool two_tiles, cudaStream_t s) {
+                               bool two_tiles, bool defer, cudaStream_t s) {
   cudaError_t e;
   if (two_tiles) {
-    if (p.bf16) e = p.d == 128 ? go<true, 128, 2>(p, a, sc, m, ctas, s) : go<true, 64, 2>(p, a, sc, m, ctas, s);
-    else e = p.d == 128 ? go<false, 128, 2>(p, a, sc, m, ctas, s) : go<false, 64, 2>(p, a, sc, m, ctas, s);
+    if (p.bf16) e = p.d == 128 ? go<true, 128, 2>(p, a, sc, m, ctas, defer, s) : go<true, 64, 2>(p, a, sc, m, ctas, defer, s);
+    else e = p.d == 128 ? go<false, 128, 2>(p, a, sc, m, ctas, defer, s) : go<false, 64, 2>(p, a, sc, m, ctas, defer, s);
   } else {
-    if (p.bf16) e = p.d == 128 ? go<true, 128, 1>(p, a, sc, m, ctas, s) : go<true, 64, 1>(p, a, sc, m, ctas, s);
-    else e = p.d == 128 ? go<false, 128, 1>(p, a, sc, m, ctas, s) : go<false, 64, 1>(p, a, sc, m, ctas, s);
+    if (p.bf16) e = p.d == 128 ? go<true, 128, 1>(p, a, sc, m, ctas, defer, s) : go<true, 64, 1>(p, a, sc, m, ctas, defer, s);
+    else e = p.d == 128 ? go<false, 128, 1>(p, a, sc, m, ctas, defer, s) : go<false, 64, 1>(p, a, sc, m, ctas, defer, s);
   }
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -132,13 +132,16 @@ cudaError_t device_ready(int dev, int* sms) {
   return cudaSuccess;
 }
 
-// [flags][tickets] (zeroed by the caller) [(maximum, sum)][accumulators]: two
+// [flags][tickets][cut units] (zeroed by the caller) [(maximum, sum)][accumulators]: two
 // places per CTA, as a CTA's share cuts at most the unit it starts in and the
 // one it ends in
 constexpr size_t kTicketsAt = 256;
 size_t scratch_rows(int sms) { return 2 * static_cast<size_t>(sms) * std::max(kFewCtasPerSm * kFewRows, kManyRows); }
 size_t scratch_bytes_of(int sms, int d) { return CONFKV_PAGED_ZEROED + scratch_rows(sms) * (2 + d) * sizeof(float); }
-bool tickets_fit(int sms) { return kTicketsAt + sizeof(unsigned int) * kFewCtasPerSm * sms <= CONFKV_PAGED_ZEROED; }
+constexpr size_t kCutAt = 8192;
+bool tickets_fit(int sms) {
+  return kTicketsAt + sizeof(unsigned int) * kFewCtasPerSm * sms <= kCutAt && kCutAt + sizeof(int4) * sms <= CONFKV_PAGED_ZEROED;
+}
 
 Batch batch_of(const confkv_paged_batch* b) {
   return Batch{b->batch, b->max_blocks, b->page_table, b->ctx_len, b->q_start, b->mask, b->mask ? b->mask_words : 0};
@@ -204,6 +207,7 @@ int confkv_paged_create(int layers, int heads, int kv_heads, int head_dim, int n
   char* at = static_cast<char*>(scratch);
   p.err = reinterpret_cast<int32_t*>(at);
   kv->scratch.ticket = reinterpret_cast<unsigned int*>(at + kTicketsAt);
+  kv->scratch.cut = reinterpret_cast<int4*>(at + kCutAt);
   kv->scratch.ml = reinterpret_cast<float*>(at + CONFKV_PAGED_ZEROED);
   kv->scratch.acc = kv->scratch.ml + 2 * scratch_rows(kv->sms);
   *out = kv;
@@ -288,7 +292,11 @@ int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int l
   // by the query rows of a sequence's KV head, on average
   const int64_t per = static_cast<int64_t>(rows) * p.g / batch->batch;
   if (per <= kFewRows) return launched(kv, launch_attend_few(p, a, kv->scratch, kv->maps, kFewCtasPerSm * kv->sms, st));
-  return launched(kv, launch_attend_many(p, a, kv->scratch, kv->maps, kv->sms, per > kManyRows, st));
+  // units of 128 rows, at most; far fewer of them than CTAs are cut into many pieces
+  // each, which a kernel of its own joins on all SMs
+  const int64_t units = p.Hkv * (static_cast<int64_t>(rows) * p.g / 128 + batch->batch);
+  const bool two = per > kManyRows;
+  return launched(kv, launch_attend_many(p, a, kv->scratch, kv->maps, kv->sms, two, !two && 4 * units <= kv->sms, st));
 }
 
 int confkv_paged_commit(confkv_paged* kv, int batch, int max_blocks, const int32_t* page_table,

@@ -24,7 +24,7 @@ constexpr int kFewCtasPerSm = 3;
 cudaError_t launch_attend_few(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
                               int ctas, cudaStream_t s);
 cudaError_t launch_attend_many(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
-                               int ctas, bool two_tiles, cudaStream_t s);
+                               int ctas, bool two_tiles, bool defer, cudaStream_t s);
 cudaError_t setup_attend_few();
 cudaError_t setup_attend_many();
 
@@ -43,9 +43,10 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, const Pool& p, in
   const size_t at = static_cast<size_t>(row) * p.Hq + hq;
   uint16_t* out = a.out + at * p.d + ch;
 #pragma unroll
-  for (int e = 0; e < N; e += 4)
-    *reinterpret_cast<uint2*>(out + e) =
-        make_uint2(pack2<BF>(x[e] * inv, x[e + 1] * inv), pack2<BF>(x[e + 2] * inv, x[e + 3] * inv));
+  for (int e = 0; e < N; e += 8)
+    *reinterpret_cast<uint4*>(out + e) =
+        make_uint4(pack2<BF>(x[e] * inv, x[e + 1] * inv), pack2<BF>(x[e + 2] * inv, x[e + 3] * inv),
+                   pack2<BF>(x[e + 4] * inv, x[e + 5] * inv), pack2<BF>(x[e + 6] * inv, x[e + 7] * inv));
   if (a.lse && ch == 0) a.lse[at] = l == 0.0f ? -INFINITY : m * a.scale + logf(l);
 }
 
@@ -56,50 +57,67 @@ __device__ __forceinline__ size_t piece_place(const W& w, int i) {
   return 2 * static_cast<size_t>(w.first_cta + i) + (i == 0 ? 1 : 0);
 }
 
-// N channels of one row joined over a unit's pieces, in their order
-template <int TM, int N, typename W>
-__device__ __forceinline__ void join_row(const Scratch& sc, const W& w, int row, int ch, int d, float c, float (&x)[N],
+// Partial accumulators lie as [place][d / 4][row][4]: both the threads of a
+// warp that hold one row each and those that join them touch whole lines.
+template <int TM, int D>
+__device__ __forceinline__ float* acc_at(const Scratch& sc, size_t place, int row, int ch) {
+  return sc.acc + (place * (D / 4) + (ch >> 2)) * (TM * 4) + 4 * row;
+}
+
+// N channels of one row joined over a unit's pieces, in their order (so that
+// the sum does not depend on who joins), U pieces' loads in flight: what this
+// costs is round trips to L2.  `own` >= 0: that piece is this thread's, in x
+// with maximum m and sum l, and is not read.
+template <int TM, int D, int N, int U, typename W>
+__device__ __forceinline__ void join_row(const Scratch& sc, const W& w, int row, int ch, float c, int own, float (&x)[N],
                                          float& m, float& l) {
-  // several pieces' loads in flight: the chain of L2 round trips is what this costs
-  constexpr int U = N > 8 ? 4 : 8;
-  m = -INFINITY;
-  l = 0.0f;
+  float z[N];
+  const float om = m, ol = l;
 #pragma unroll
-  for (int e = 0; e < N; ++e) x[e] = 0.0f;
+  for (int e = 0; e < N; ++e) {
+    z[e] = x[e];
+    x[e] = 0.0f;
+  }
+  m = own >= 0 ? om : -INFINITY;
+  l = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < w.pieces; ++i)
+    if (i != own) m = fmaxf(m, __ldcg(sc.ml + (piece_place(w, i) * TM + row) * 2));
+  if (m == -INFINITY) return;
+#pragma unroll 1
   for (int i0 = 0; i0 < w.pieces; i0 += U) {
     float2 ml[U];
     float4 v[U][N / 4];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i0 + u < w.pieces) {
-        const size_t at = piece_place(w, i0 + u) * TM + row;
-        ml[u] = __ldcg(reinterpret_cast<const float2*>(sc.ml + at * 2));
+      const int i = i0 + u;
+      if (i < w.pieces && i != own) {
+        const size_t at = piece_place(w, i);
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(sc.ml + (at * TM + row) * 2));
 #pragma unroll
-        for (int e = 0; e < N / 4; ++e) v[u][e] = __ldcg(reinterpret_cast<const float4*>(sc.acc + at * d + ch) + e);
-      } else {
-        ml[u] = make_float2(-INFINITY, 0.0f);
+        for (int e = 0; e < N / 4; ++e)
+          v[u][e] = __ldcg(reinterpret_cast<const float4*>(acc_at<TM, D>(sc, at, row, ch + 4 * e)));
       }
     }
-    float mn = m;
-#pragma unroll
-    for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
-    if (mn == -INFINITY) continue;
-    const float f0 = m == -INFINITY ? 0.0f : ex2f((m - mn) * c);
-    l *= f0;
-#pragma unroll
-    for (int e = 0; e < N; ++e) x[e] *= f0;
-    m = mn;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (ml[u].x == -INFINITY) continue;
-      const float f = ex2f((ml[u].x - m) * c);
-      l = fmaf(f, ml[u].y, l);
+      const int i = i0 + u;
+      if (i >= w.pieces) break;
+      const float mi = i == own ? om : ml[u].x;
+      if (mi == -INFINITY) continue;
+      const float f = ex2f((mi - m) * c);
+      l = fmaf(f, i == own ? ol : ml[u].y, l);
+      if (i == own) {
 #pragma unroll
-      for (int e = 0; e < N / 4; ++e) {
-        x[4 * e] = fmaf(f, v[u][e].x, x[4 * e]);
-        x[4 * e + 1] = fmaf(f, v[u][e].y, x[4 * e + 1]);
-        x[4 * e + 2] = fmaf(f, v[u][e].z, x[4 * e + 2]);
-        x[4 * e + 3] = fmaf(f, v[u][e].w, x[4 * e + 3]);
+        for (int e = 0; e < N; ++e) x[e] = fmaf(f, z[e], x[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N / 4; ++e) {
+          x[4 * e] = fmaf(f, v[u][e].x, x[4 * e]);
+          x[4 * e + 1] = fmaf(f, v[u][e].y, x[4 * e + 1]);
+          x[4 * e + 2] = fmaf(f, v[u][e].z, x[4 * e + 2]);
+          x[4 * e + 3] = fmaf(f, v[u][e].w, x[4 * e + 3]);
+        }
       }
     }
   }

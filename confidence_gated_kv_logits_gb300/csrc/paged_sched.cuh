@@ -17,14 +17,23 @@ namespace paged {
 struct Sched {          // in shared memory, filled by sched_init
   long long share;      // work per CTA
   long long cur, end;   // this CTA's range of the work
-  long long seq0;       // where sequence b's work starts
-  int b;                // sequence in which the range starts
+  // the sequence in which the range starts, and where its work does
+  long long seq0, head;  // head: work of one of its heads
+  int b, T, ctx, len, row0;
 };
 
+// 64-bit quotients of numbers that mostly fit 32 bits (a 64-bit division costs
+// some 100 cycles of a launch that may last a few thousand)
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 struct Scratch {        // of the handle: partial results of cut units
-  float* acc;           // [CTA][2][TM][d]
+  float* acc;           // [CTA][2][d / 4][TM][4]
   float* ml;            // [CTA][2][TM][2] (maximum, sum)
-  unsigned int* ticket; // [CTA]
+  unsigned int* ticket; // [CTA] of the unit whose first piece it holds: pieces done
+  int4* cut;            // [CTA] that unit for the joining kernel: pieces, sequence, head, tile
 };
 
 template <int TM, int KB, int kOverhead>
@@ -68,10 +77,10 @@ struct Walk {
   // tokens that some row of tile t may see
   __device__ __forceinline__ int tile_len(int t) const {
     if (bt.mask) return len;
-    long long last = (static_cast<long long>(t + 1) * TM - 1) / p.g + 1;   // new tokens up to the tile's last row
-    last = last > T ? T : last;
-    const long long l = ctx + last;
-    return l < len ? static_cast<int>(l) : len;
+    // new tokens up to the tile's last row (rows x heads fit 31 bits)
+    uint32_t last = (static_cast<uint32_t>(t + 1) * TM - 1) / static_cast<uint32_t>(p.g) + 1;
+    last = last > static_cast<uint32_t>(T) ? T : last;
+    return last < static_cast<uint32_t>(len - ctx) ? ctx + static_cast<int>(last) : len;
   }
   __device__ __forceinline__ int blocks(int t) const { return (tile_len(t) + KB - 1) / KB; }
   // work of one head of the sequence
@@ -87,15 +96,19 @@ struct Walk {
     cur = s.cur;
     end = s.end;
     if (cur >= end) return;
-    int flag = 0;
-    sequence(s.b, flag);
-    const long long hw = head_work();
-    h = static_cast<int>((cur - s.seq0) / hw);
-    ustart = s.seq0 + h * hw;
+    b = s.b;
+    T = s.T;
+    ctx = s.ctx;
+    len = s.len;
+    row0 = s.row0;
+    m = static_cast<int>((static_cast<long long>(T) * p.g + TM - 1) / TM);
+    h = static_cast<int>(quotient(cur - s.seq0, s.head));
+    ustart = s.seq0 + h * s.head;
     mt = 0;
-    if (bt.mask) {
+    if (m == 1) {
+    } else if (bt.mask) {
       const long long u = blocks(0) + kOverhead;
-      mt = static_cast<int>((cur - ustart) / u);
+      mt = static_cast<int>(quotient(cur - ustart, u));
       ustart += mt * u;
     } else {
       for (long long u = blocks(0) + kOverhead; cur >= ustart + u; u = blocks(mt) + kOverhead) {
@@ -104,21 +117,12 @@ struct Walk {
       }
     }
   }
+  // goes to the range's next piece; false behind the last one
   __device__ __forceinline__ bool next() {
-    while (cur < end) {
-      n = blocks(mt);
-      const long long uend = ustart + n + kOverhead;
-      const long long x1 = end < uend ? end : uend;
-      const long long a = cur - ustart - kOverhead, z = x1 - ustart - kOverhead;
-      lo = a > 0 ? static_cast<int>(a) : 0;
-      hi = z > 0 ? static_cast<int>(z) : 0;
-      first_cta = static_cast<int>((ustart + kOverhead) / share);
-      pieces = static_cast<int>((uend - 1) / share) - first_cta + 1;
-      cur = x1;
-      // the piece's place, kept while the walk moves on
-      pb = b; ph = h; pmt = mt; pT = T; pctx = ctx; plen = len; prow0 = row0; ptile = tile_len(mt);
-      if (x1 == uend) {
-        ustart = uend;
+    for (;;) {
+      if (unit_done) {
+        unit_done = false;
+        ustart += n + kOverhead;
         if (++mt == m) {
           mt = 0;
           if (++h == p.Hkv) {
@@ -130,14 +134,24 @@ struct Walk {
           }
         }
       }
+      if (cur >= end) return false;
+      n = blocks(mt);
+      const long long uend = ustart + n + kOverhead;
+      const long long x1 = end < uend ? end : uend;
+      const long long a = cur - ustart - kOverhead, z = x1 - ustart - kOverhead;
+      lo = a > 0 ? static_cast<int>(a) : 0;
+      hi = z > 0 ? static_cast<int>(z) : 0;
+      first_cta = static_cast<int>(quotient(ustart + kOverhead, share));
+      pieces = static_cast<int>(quotient(uend - 1, share)) - first_cta + 1;
+      cur = x1;
+      unit_done = x1 == uend;
       if (hi > lo) return true;
     }
-    return false;
   }
-  int pb, ph, pmt, pT, pctx, plen, prow0, ptile;
+  bool unit_done = false;
 };
 
-// Every thread of the CTA calls it (kT threads; three barriers).  s_scan holds kT / 32
+// Every thread of the CTA calls it (kT threads).  s_scan holds kT / 32
 // 64-bit words.
 template <int kT, typename W>
 __device__ __forceinline__ void sched_init(W& w, Sched* s, long long* s_scan, long long min_share) {
@@ -176,23 +190,26 @@ __device__ __forceinline__ void sched_init(W& w, Sched* s, long long* s_scan, lo
   };
   long long all;
   long long pre = scan(total, all);
-  long long share = (all + gridDim.x - 1) / gridDim.x;
+  long long share = quotient(all + gridDim.x - 1, gridDim.x);
   share = share < min_share ? min_share : share;
   const long long cur = static_cast<long long>(blockIdx.x) * share;
   if (tid == 0) {
     s->share = share;
     s->cur = cur;
     s->end = cur + share < all ? cur + share : all;
-    s->b = 0;
-    s->seq0 = 0;
   }
-  __syncthreads();
+  auto here = [&](long long at, long long x) {      // this thread's sequence (in w) is the one
+    s->b = w.b;
+    s->T = w.T;
+    s->ctx = w.ctx;
+    s->len = w.len;
+    s->row0 = w.row0;
+    s->seq0 = at;
+    s->head = quotient(x, w.p.Hkv);
+  };
   if (cur < all) {
     if (B <= kT) {
-      if (mine > 0 && cur >= pre && cur < pre + mine) {
-        s->b = tid;
-        s->seq0 = pre;
-      }
+      if (mine > 0 && cur >= pre && cur < pre + mine) here(pre, mine);
     } else {
       long long base = 0;
       for (int b0 = 0; b0 < B; b0 += kT) {
@@ -202,10 +219,7 @@ __device__ __forceinline__ void sched_init(W& w, Sched* s, long long* s_scan, lo
           x = w.T > 0 ? w.head_work() * w.p.Hkv : 0;
         }
         const long long at = base + scan(x, sum);
-        if (x > 0 && cur >= at && cur < at + x) {
-          s->b = b0 + tid;
-          s->seq0 = at;
-        }
+        if (x > 0 && cur >= at && cur < at + x) here(at, x);
         base += sum;
       }
     }
