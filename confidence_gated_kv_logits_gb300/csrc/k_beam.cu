@@ -15,10 +15,12 @@
 // maximum give the same answer.
 //
 // Precision: exponentials and their sums per thread are fp32, relative to the
-// slice's maximum (the largest terms are exact); sums over threads and slices,
-// lse and the candidates' scores are double, so candidates of different beams
-// are ordered to ~1e-8; scores are rounded to fp32 once, at the end.  Equal
+// slice's maximum (the largest terms are exact) and a power of two; sums over
+// threads and slices are whole numbers of 2^-38 (exact in any order, and off
+// the slow double pipe); lse and the candidates' scores are double, so
+// candidates of different beams are ordered to ~1e-8; scores are rounded to fp32 once, at the end.  Equal
 // scores go to the lower (beam, token).
+#include <climits>
 #include <cmath>
 
 #include "paged_internal.cuh"
@@ -33,10 +35,14 @@ constexpr int kCap = 1024;            // candidates ranked by counting
 constexpr int kMaxBeams = 32;
 constexpr float kL2E = 1.4426950408889634f;
 
+constexpr int kUnitBits = 38;          // sums are whole numbers of 2^-38
+constexpr float kUnits = 274877906944.0f;
+
+// a slice's sum of exp(z) = sum 2^(exp - kUnitBits); ~0: a NaN or +inf was
+// seen; 0: no finite logit
 struct SlicePart {
-  double sum;       // sum of exp(z - max) over the slice
-  float max;
-  int bad;          // a NaN or +inf was seen
+  unsigned long long sum;
+  long long exp;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -85,41 +91,88 @@ __device__ __forceinline__ void warp_sort(T& x) {
 }
 
 // A value that at least K of the block's values reach, from each thread's
-// largest (all threads call it): the K-th largest of the threads' maxima for
-// K <= 32, by merging the warps' sorted lanes pairwise; for more, the second
-// best of the warps' (K / 2)-th largest.  s_v: 32 values per warp.
+// largest (all threads call it, one barrier before and one behind): each warp
+// gives its T = ceil(K / 16) largest of them; the bound is the K-th largest of
+// the 16 T (K <= 32), or the smallest of the warps' T-th.  s_v: 32 values.
 template <typename T>
-__device__ __forceinline__ T block_bound(T mine, int K, T* s_v) {
+__device__ __forceinline__ T block_bound(T mine, T lowest, int K, T* s_v) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  T x = mine;
+  const int per = (K + kWarps - 1) / kWarps;
+  T x = mine, top = lowest;
+  for (int t = 0; t < per; ++t) {
+    top = x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const T y = __shfl_xor_sync(0xffffffffu, top, o);
+      top = y > top ? y : top;
+    }
+    // one lane that holds it steps back
+    const unsigned has = __ballot_sync(0xffffffffu, x == top);
+    if (lane == __ffs(has) - 1) x = lowest;
+    if (K <= 2 * kWarps && lane == 0) s_v[warp * per + t] = top;
+  }
+  if (K > 2 * kWarps && lane == 0) s_v[warp] = top;
+  __syncthreads();
+  T y = lane < (K > 2 * kWarps ? kWarps : kWarps * per) ? s_v[lane] : lowest;
+  warp_sort(y);
+  y = __shfl_sync(0xffffffffu, y, K > 2 * kWarps ? kWarps - 1 : K - 1);
+  __syncthreads();
+  return y;
+}
+
+// The K-th largest of the threads' largest itself (K <= 32; for more, the
+// second best of the warps' (K / 2)-th), for values that are each the best of
+// somewhere, so that the looser bound would keep most of them: the warps'
+// sorted lanes merged pairwise.  s_v: 32 values per warp.
+__device__ __forceinline__ unsigned long long block_bound_tight(unsigned long long x, int K, unsigned long long* s_v) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   warp_sort(x);
   s_v[warp * 32 + lane] = x;
   __syncthreads();
   if (K > 32) {
-    T w = s_v[(lane & (kWarps - 1)) * 32 + ((K + 1) >> 1) - 1];    // each warp's bound twice
+    unsigned long long w = s_v[(lane & (kWarps - 1)) * 32 + ((K + 1) >> 1) - 1];    // each warp's bound twice
     warp_sort(w);
-    w = __shfl_sync(0xffffffffu, w, 2);
-    __syncthreads();
-    return w;
+    return __shfl_sync(0xffffffffu, w, 2);
   }
 #pragma unroll
   for (int step = kWarps / 2; step > 0; step >>= 1) {
     if (warp < step) {
       // the larger of a falling and a rising list: the 32 largest, bitonic
-      const T y = s_v[(warp + step) * 32 + 31 - lane];
+      const unsigned long long y = s_v[(warp + step) * 32 + 31 - lane];
       x = x > y ? x : y;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) {
-        const T z = __shfl_xor_sync(0xffffffffu, x, d);
+        const unsigned long long z = __shfl_xor_sync(0xffffffffu, x, d);
         x = (lane & d) == 0 ? (x > z ? x : z) : (x < z ? x : z);
       }
       s_v[warp * 32 + lane] = x;
     }
     __syncthreads();
   }
-  const T r = s_v[K - 1];
-  __syncthreads();
-  return r;
+  return s_v[K - 1];
+}
+
+// e^x for x <= 0 in double, to a few 1e-15: x = n ln 2 + r and r's Taylor
+// series, summed pairwise (the double pipe is slow: few dependent steps)
+__device__ __forceinline__ double exp_neg(double x) {
+  if (x < -700.0) return 0.0;
+  const double n = rint(x * 1.4426950408889634);
+  // ln 2 as a 32-bit fraction and the rest, so that n times the first is exact
+  constexpr double kLn2Head = 2977044472.0 / 4294967296.0, kLn2Rest = -4.2009150726810846e-11;
+  const double r = fma(-n, kLn2Rest, fma(-n, kLn2Head, x));
+  const double r2 = r * r, r4 = r2 * r2;
+  const double a = fma(r, 1.0, 1.0), b = fma(r, 1.0 / 6, 0.5), c = fma(r, 1.0 / 120, 1.0 / 24),
+               d = fma(r, 1.0 / 5040, 1.0 / 720), e = fma(r, 1.0 / 362880, 1.0 / 40320),
+               f = fma(r, 1.0 / 39916800, 1.0 / 3628800);
+  const double p = fma(r2, b, a), q = fma(r2, d, c), s = fma(r2, f, e);
+  const double y = fma(r4, fma(r4, s, q), p);
+  return y * __longlong_as_double(static_cast<long long>(static_cast<int>(n) + 1023) << 52);
+}
+// ln x for x >= 1: the fp32 logarithm and one Newton step on e^y = x
+__device__ __forceinline__ double log_ge1(double x) {
+  const double y = logf(static_cast<float>(x));
+  const double d = fma(x, exp_neg(-y), -1.0);
+  return y + fma(-0.5 * d, d, d);
 }
 
 template <int DT>
@@ -154,7 +207,7 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
   constexpr int VEC = DT == CONFKV_FP32 ? 4 : 8;      // elements of a 16-byte word
   constexpr int NV = EPT / VEC;
   __shared__ Cand s_list[kCap];
-  __shared__ double s_sum[kWarps];
+  __shared__ unsigned long long s_sum[kWarps];
   __shared__ float s_f[kWarps];
   __shared__ unsigned long long s_v[kThreads];
   __shared__ Cand s_best[kWarps];
@@ -202,41 +255,63 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
       if constexpr (DT == CONFKV_FP32) return __uint_as_float(w[e]);
       else return elem<DT>(w[e >> 1], e & 1);
     };
-    float m = -INFINITY;
-    int bad = 0;
+    // largest value of a word; of all words (16-bit types two at a time; NaN is passed over)
+    auto top_of = [&](uint32_t a0, uint32_t a1) -> uint32_t {
+      uint32_t r;
+      if constexpr (DT == CONFKV_BF16) asm("max.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a0), "r"(a1));
+      else if constexpr (DT == CONFKV_FP16) asm("max.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a0), "r"(a1));
+      else r = __float_as_uint(fmaxf(__uint_as_float(a0), __uint_as_float(a1)));
+      return r;
+    };
+    auto word_top = [&](const uint4& w) { return top_of(top_of(w.x, w.y), top_of(w.z, w.w)); };
+    auto top_value = [&](uint32_t t) {
+      if constexpr (DT == CONFKV_FP32) return __uint_as_float(t);
+      else return fmaxf(elem<DT>(t, 0), elem<DT>(t, 1));
+    };
+    uint32_t mw = word_top(x[0]);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float z = value(i, e);
-        bad |= !(z < INFINITY);
-        m = fmaxf(m, z);
-      }
+    for (int i = 1; i < NV; ++i) mw = top_of(mw, word_top(x[i]));
+    const float m = top_value(mw);
     // the passes unpack the values anew instead of holding all of them as floats
     auto again = [&] {
 #pragma unroll
       for (int i = 0; i < NV; ++i) asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));
     };
     again();
-    const float bound = block_bound(m, a.K, reinterpret_cast<float*>(s_v));
     float bm = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
     if (lane == 0) s_f[warp] = bm;
-    if (bad) s_bad = 1;
-    __syncthreads();
+    const float bound = block_bound(m, -INFINITY, a.K, reinterpret_cast<float*>(s_v));    // (its barriers publish s_f)
     bm = s_f[0];
+#pragma unroll
     for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, s_f[w]);
+    // The slice's power of two: bm log2 e (the product, its rounding and the
+    // constant's) as a whole number, rounded up, and what is left (in (-1, 0]).
+    // Slices then join by shifts alone.
+    float delta;
+    long long power;
+    {
+      const float h = bm * kL2E, c0 = ceilf(h);
+      const float d = (h - c0) + fmaf(bm, 1.9259629911e-08f, fmaf(bm, kL2E, -h));
+      const float c1 = ceilf(d);
+      delta = d - c1;
+      power = static_cast<long long>(c0) + static_cast<long long>(c1);
+    }
     float sum = 0.0f;
-    if (bm > -INFINITY) {
+    if (bm > -INFINITY && bm < INFINITY) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        float part4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        // (z - max) first, which is exact for what weighs: z's product alone would lose digits
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float z = value(i, e);
-          // (z - max) exactly first: the product alone would lose the digits of large logits
-          sum += ex2((z - bm) * kL2E);
-          if (z >= bound && z > -INFINITY) {
+        for (int e = 0; e < VEC; ++e) part4[e & 3] += ex2(fmaf(value(i, e) - bm, kL2E, delta));
+        sum += (part4[0] + part4[1]) + (part4[2] + part4[3]);
+        if (top_value(word_top(x[i])) >= bound) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float z = value(i, e);
+            if (!(z >= bound && z > -INFINITY)) continue;
             const int at = atomicAdd(&s_cnt, 1);
             if (at < kCap) {
               const uint32_t v = static_cast<uint32_t>((w0 + i * kThreads + tid) * VEC - lead + e);
@@ -244,18 +319,23 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
             }
           }
         }
+      }
     }
-    double ds = sum;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
-    if (lane == 0) s_sum[warp] = ds;
+    // NaN anywhere in the slice makes its sum NaN, +inf its maximum
+    if (!(sum < INFINITY) || bm == INFINITY) s_bad = 1;
+    // the sum goes on in whole units: exact, in any order, and off the double pipe
+    const unsigned long long mine = sum < 65536.0f ? static_cast<unsigned long long>(sum * kUnits) : 0ull;   // (NaN: 0)
+    const unsigned lo = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine) & 0x7ffffffu);
+    const unsigned hi = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine >> 27));
+    if (lane == 0) s_sum[warp] = (static_cast<unsigned long long>(hi) << 27) + lo;
     __syncthreads();
     const int cnt = s_cnt;
     unsigned long long* out = cand + slice * a.K;
     if (tid == 0) {
-      double t = 0.0;
+      unsigned long long t = 0;
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) t += s_sum[w];
-      part[slice] = SlicePart{t, bm, s_bad};
+      part[slice] = SlicePart{s_bad ? ~0ull : t, power};
     }
     if (cnt <= kCap) {
       for (int i = tid; i < cnt; i += kThreads) {
@@ -301,35 +381,58 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
   __threadfence();
   if (tid == 0) ticket[b] = 0u;
 
+  // everything that the last stage reads is asked for at once
+  const int per = C * a.K, n = a.W * per;
+  constexpr int kHeld = 4;                  // candidates of a thread that stay in registers
+  unsigned long long raw[kHeld];
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    raw[u] = tid + u * kThreads < n ? __ldcg(cand + static_cast<size_t>(b) * n + tid + u * kThreads) : 0ull;
+
   // each beam's score minus lse (NaN: no candidates of its logits)
   for (int w = warp; w < a.W; w += kWarps) {
     const int r = b * a.W + w;
+    const SlicePart* pp = part + static_cast<size_t>(r) * C;
     const float sc = a.scores[r];
+    const bool done = a.finished && a.finished[r];
+    // this lane's slice (a row of more than 32 goes on below)
+    SlicePart q{0ull, LLONG_MIN};
+    auto part_of = [&](int c) {
+      const ulonglong2 v = __ldcg(reinterpret_cast<const ulonglong2*>(pp + c));
+      return SlicePart{v.x, v.x ? static_cast<long long>(v.y) : LLONG_MIN};
+    };
+    auto joined = [](const SlicePart& x, const SlicePart& y) {
+      const bool first = x.exp >= y.exp;
+      const SlicePart& big = first ? x : y;
+      const SlicePart& low = first ? y : x;
+      if (!low.sum || big.exp - low.exp > 63) return big;
+      return SlicePart{big.sum + (low.sum >> (big.exp - low.exp)), big.exp};
+    };
+    bool bad = false;
+    if (lane < C) q = part_of(lane);
     int flag = 0;
     double base = __longlong_as_double(0x7ff8000000000000ll);
     if (!(sc < INFINITY)) {
       flag = CONFKV_FLAG_NONFINITE;
-    } else if (sc > -INFINITY && !(a.finished && a.finished[r])) {
-      const SlicePart* pp = part + static_cast<size_t>(r) * C;
-      float m = -INFINITY;
-      int bad = 0;
-      for (int c = lane; c < C; c += 32) {
-        m = fmaxf(m, __ldcg(&pp[c].max));
-        bad |= __ldcg(&pp[c].bad);
+    } else if (sc > -INFINITY && !done) {
+      bad = q.sum == ~0ull;
+      for (int c = lane + 32; c < C; c += 32) {
+        const SlicePart y = part_of(c);
+        bad |= y.sum == ~0ull;
+        q = joined(q, y);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       bad = __any_sync(0xffffffffu, bad);
-      if (bad || !(m > -INFINITY)) {
-        flag = CONFKV_FLAG_NONFINITE;
-      } else {
-        double s = 0.0;
-        for (int c = lane; c < C; c += 32)
-          s += __ldcg(&pp[c].sum) * exp(static_cast<double>(__ldcg(&pp[c].max)) - static_cast<double>(m));
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        base = static_cast<double>(sc) - (static_cast<double>(m) + log(s));
+      for (int o = 16; o > 0; o >>= 1) {
+        SlicePart y;
+        y.sum = __shfl_xor_sync(0xffffffffu, q.sum, o);
+        y.exp = __shfl_xor_sync(0xffffffffu, q.exp, o);
+        q = joined(q, y);
       }
+      if (bad || !q.sum)
+        flag = CONFKV_FLAG_NONFINITE;
+      else
+        base = static_cast<double>(sc) - fma(static_cast<double>(q.exp - kUnitBits), 0.6931471805599453, log_ge1(static_cast<double>(q.sum)));
     }
     if (lane == 0) {
       s_base[w] = base;
@@ -339,14 +442,12 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
   __syncthreads();
 
   // candidate i of the sequence: slice lists, then one of each finished beam
-  const int per = C * a.K, n = a.W * per;
-  auto candidate = [&](int i) -> Cand {
+  auto candidate = [&](int i, unsigned long long k) -> Cand {
     Cand c{0, 0};
     if (i < n) {
       const int w = i / per;
       const double base = s_base[w];
       if (base == base) {
-        const unsigned long long k = __ldcg(cand + static_cast<size_t>(b) * n + i);
         if (k) {
           c.key = ordered(base + static_cast<double>(unordered(static_cast<uint32_t>(k >> 32))));
           c.tie = ~((static_cast<unsigned long long>(w) << 32) | (0xffffffffu - static_cast<uint32_t>(k)));
@@ -362,20 +463,20 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
     }
     return c;
   };
-  constexpr int kHeld = 4;                  // candidates of a thread that stay in registers
+  auto fetched = [&](int i) { return candidate(i, i < n ? __ldcg(cand + static_cast<size_t>(b) * n + i) : 0ull); };
   Cand held[kHeld];
   unsigned long long top = 0;
 #pragma unroll
   for (int u = 0; u < kHeld; ++u) {
     held[u] = Cand{0, 0};
-    if (tid + u * kThreads < n + a.W) held[u] = candidate(tid + u * kThreads);
+    if (tid + u * kThreads < n + a.W) held[u] = candidate(tid + u * kThreads, raw[u]);
     top = held[u].key > top ? held[u].key : top;
   }
   for (int i = tid + kHeld * kThreads; i < n + a.W; i += kThreads) {
-    const unsigned long long k = candidate(i).key;
+    const unsigned long long k = fetched(i).key;
     top = k > top ? k : top;
   }
-  const unsigned long long bound = block_bound(top, a.K, s_v);
+  const unsigned long long bound = block_bound_tight(top, a.K, s_v);
   auto keep = [&](const Cand& c) {
     if (c.key && c.key >= bound) {
       const int at = atomicAdd(&s_cnt, 1);
@@ -384,7 +485,7 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
   };
 #pragma unroll
   for (int u = 0; u < kHeld; ++u) keep(held[u]);
-  for (int i = tid + kHeld * kThreads; i < n + a.W; i += kThreads) keep(candidate(i));
+  for (int i = tid + kHeld * kThreads; i < n + a.W; i += kThreads) keep(fetched(i));
   __syncthreads();
   const int cnt = s_cnt;
   auto put = [&](int r, const Cand& c) {
@@ -407,7 +508,7 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
     for (int r = 0; r < a.K; ++r) {
       Cand best{0, 0};
       for (int i = tid; i < n + a.W; i += kThreads) {
-        const Cand c = candidate(i);
+        const Cand c = fetched(i);
         if (c.key && before(last, c) && before(c, best)) best = c;
       }
       last = block_best(best, s_best);
