@@ -12,10 +12,13 @@
 // than the memory.
 //
 // The work is traffic: each row is read once and written once, 16 bytes per
-// access.  One CTA takes `tpc` rows (4 where there are enough to fill the
-// GPU, else 1), computes their rot / 2 sines once into shared memory for all
-// heads, and then moves (row, head, 8-channel chunk) items, a rotated item
-// being the two chunks of eight pairs.
+// access, one CTA per row.  What a row costs besides is a chain of small reads
+// (its sequence, length, page) before anything can be stored, so every thread
+// asks for its part of the row first and the chain runs meanwhile; the row's
+// rot / 2 sines are computed once into shared memory for all heads.
+// (4 prompts' chunks, 40 + 2 x 8 heads, d = 128, bf16, 116 MB: 30.0 us with
+// four rows per CTA and loads behind the chain, 27.1 with two items of a thread
+// in flight and 5 CTAs per SM, 25.8 with one and 8.)
 #include "paged_internal.cuh"
 
 namespace confkv {
@@ -23,7 +26,7 @@ namespace paged {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTpc = 4;
+constexpr int kU = 1;             // items of a thread in flight (8 CTAs per SM hide more than 2 items in 5)
 
 template <bool BF>
 __device__ __forceinline__ void rotate8(uint4& lo, uint4& hi, const float2* cs, bool interleaved) {
@@ -50,111 +53,133 @@ __device__ __forceinline__ void rotate8(uint4& lo, uint4& hi, const float2* cs, 
   }
 }
 
+// A row's items: first the rotated chunks of the q and k heads (two 16-byte
+// accesses each), then those heads' other channels, then v (one access each).
+struct Item {
+  const uint16_t* src;
+  int to;            // channel offset in q_out's row, or in the page of k or v: head * head stride + channel
+  int second;        // channels from the first access to the second, 0: none
+  int pair;          // first of its rotated pairs
+  int dst;           // 0 q_out, 1 k, 2 v, -1 none
+};
+
 template <bool BF>
-__global__ void __launch_bounds__(kThreads)
-k_append(const Pool p, const AppendArgs a, int tpc) {
-  __shared__ float2 s_cs[kMaxTpc * 64];      // (cos, sin) per row and pair
-  __shared__ long long s_row[kMaxTpc];       // element offset of (layer, page, head 0, slot), -1: no store
-  __shared__ int s_pos[kMaxTpc];             // position
-  __shared__ int s_live[kMaxTpc];            // the row belongs to a sequence
+__global__ void __launch_bounds__(kThreads, 8)
+k_append(const Pool p, const AppendArgs a) {
+  __shared__ float2 s_cs[64];      // (cos, sin) per pair
+  __shared__ long long s_row;      // element offset of (layer, page, head 0, slot), -1: no store
+  __shared__ int s_pos, s_live;    // position; the row belongs to a sequence
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row0 = blockIdx.x * tpc;
-  if (warp < tpc) {
-    const int row = row0 + warp;
-    int b = a.bt.B;
-    if (row < a.rows) b = sequence_of(a.bt.q_start, a.bt.B, row);
-    if (lane == 0) {
-      long long off = -1;
-      int pos = 0, live = 0;
-      if (b < a.bt.B) {
-        const int first = a.bt.q_start[b], ctx = a.bt.ctx[b];
-        if (row >= first) {
-          live = 1;
-          const long long place = static_cast<long long>(ctx) + (row - first);
-          pos = a.pos ? a.pos[row] : static_cast<int>(place);
-          const long long blk = place >> p.ps_shift;
-          if (ctx < 0) {
-            atomicOr(p.err, CONFKV_FLAG_BAD_INDEX);
-          } else if (blk >= a.bt.max_blocks) {
-            atomicOr(p.err, CONFKV_FLAG_CAPACITY);
-          } else {
-            const int page = a.bt.table[static_cast<size_t>(b) * a.bt.max_blocks + blk];
-            if (page < 0 || page >= p.NP) {
-              atomicOr(p.err, CONFKV_FLAG_BAD_PAGE);
+  const int row = blockIdx.x;
+  const int half = a.rot >> 1, rc = a.rot >> 4, pc = (p.d - a.rot) >> 3, vc = p.d >> 3;
+  const int q0 = a.q ? p.Hq : 0, heads = q0 + p.Hkv;
+  const int nrot = heads * rc, nplain = heads * pc, items = nrot + nplain + p.Hkv * vc;
+  const int hs = p.ps * p.d;       // head stride in a page
+  auto item = [&](int j) {
+    Item t{nullptr, 0, 0, 0, -1};
+    if (j >= items) return t;
+    int h, c;
+    if (j < nrot) {
+      h = j / rc;
+      c = j - h * rc;
+      t.pair = 8 * c;
+      t.second = a.interleaved ? 8 : half;
+      c *= a.interleaved ? 16 : 8;
+    } else if (j < nrot + nplain) {
+      j -= nrot;
+      h = j / pc;
+      c = a.rot + 8 * (j - h * pc);
+    } else {
+      j -= nrot + nplain;
+      h = j / vc;
+      c = 8 * (j - h * vc);
+      t.src = a.v + row * a.vs + h * p.d + c;
+      t.to = h * hs + c;
+      t.dst = 2;
+      return t;
+    }
+    if (h < q0) {
+      t.src = a.q + row * a.qs + h * p.d + c;
+      t.to = h * p.d + c;
+      t.dst = 0;
+    } else {
+      h -= q0;
+      t.src = a.k + row * a.ks + h * p.d + c;
+      t.to = h * hs + c;
+      t.dst = 1;
+    }
+    return t;
+  };
+  for (int j0 = tid; j0 - tid < items; j0 += kU * kThreads) {
+    Item t[kU];
+    uint4 lo[kU], hi[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      t[u] = item(j0 + u * kThreads);
+      if (t[u].dst >= 0) {
+        lo[u] = *reinterpret_cast<const uint4*>(t[u].src);
+        if (t[u].second) hi[u] = *reinterpret_cast<const uint4*>(t[u].src + t[u].second);
+      }
+    }
+    if (j0 == tid) {               // the first time round: where the row goes, and its sines
+      if (warp == 0) {
+        const int given = a.pos ? a.pos[row] : 0;
+        const int b = sequence_of(a.bt.q_start, a.bt.B, row);
+        long long off = -1;
+        int pos = given, live = 0;
+        if (b < a.bt.B) {
+          const int first = a.bt.q_start[b], ctx = a.bt.ctx[b];
+          if (row >= first) {
+            live = 1;
+            const long long place = static_cast<long long>(ctx) + (row - first);
+            if (!a.pos) pos = static_cast<int>(place);
+            const long long blk = place >> p.ps_shift;
+            int flag = 0;
+            if (ctx < 0) {
+              flag = CONFKV_FLAG_BAD_INDEX;
+            } else if (blk >= a.bt.max_blocks) {
+              flag = CONFKV_FLAG_CAPACITY;
             } else {
-              const int slot = static_cast<int>(place & (p.ps - 1));
-              off = ((static_cast<long long>(a.layer) * p.NP + page) * p.Hkv * p.ps + slot) * p.d;
+              const int page = a.bt.table[static_cast<size_t>(b) * a.bt.max_blocks + blk];
+              if (page < 0 || page >= p.NP) flag = CONFKV_FLAG_BAD_PAGE;
+              else off = ((static_cast<long long>(a.layer) * p.NP + page) * p.Hkv * p.ps + (place & (p.ps - 1))) * p.d;
             }
+            if (flag && lane == 0) atomicOr(p.err, flag);
           }
         }
+        if (lane == 0) {
+          s_row = off;
+          s_pos = pos;
+          s_live = live;
+        }
       }
-      s_row[warp] = off;
-      s_pos[warp] = pos;
-      s_live[warp] = live;
+      __syncthreads();
+      if (!s_live) return;
+      if (tid < half) {
+        double turns = static_cast<double>(a.inv_freq[tid]) * 0.15915494309189535;   // 1 / (2 pi)
+        turns -= floor(turns);
+        const unsigned long long F = static_cast<unsigned long long>(turns * 18446744073709551616.0);
+        const unsigned long long ang = static_cast<unsigned long long>(static_cast<long long>(s_pos)) * F;
+        const int h = static_cast<int>((ang + 0x80000000ull) >> 32);   // fraction of a half turn, 2^-31 units
+        float sn, cn;
+        sincospif(static_cast<float>(h) * 4.656612873077393e-10f, &sn, &cn);
+        s_cs[tid] = make_float2(cn, sn);
+      }
+      __syncthreads();
     }
-  }
-  __syncthreads();
-  const int half = a.rot >> 1;
-  for (int i = tid; i < tpc * half; i += kThreads) {
-    const int t = i / half, c = i - t * half;
-    double turns = static_cast<double>(a.inv_freq[c]) * 0.15915494309189535;   // 1 / (2 pi)
-    turns -= floor(turns);
-    const unsigned long long F = static_cast<unsigned long long>(turns * 18446744073709551616.0);
-    const unsigned long long ang = static_cast<unsigned long long>(static_cast<long long>(s_pos[t])) * F;
-    const int h = static_cast<int>((ang + 0x80000000ull) >> 32);   // fraction of a half turn, 2^-31 units
-    float sn, cn;
-    sincospif(static_cast<float>(h) * 4.656612873077393e-10f, &sn, &cn);
-    s_cs[t * 64 + c] = make_float2(cn, sn);
-  }
-  __syncthreads();
-
-  // items of one row: rotated chunks of the q and k heads (two 16-byte
-  // accesses each), then their other channels, then v (one access each)
-  const int rc = a.rot >> 4;                       // rotated items per head
-  const int pc = (p.d - a.rot) >> 3;               // plain items per head
-  const int heads = (a.q ? p.Hq : 0) + p.Hkv;
-  const int nrot = heads * rc, npl = heads * pc, nv = p.Hkv * (p.d >> 3);
-  const int per_row = nrot + npl + nv;
-  const int q0 = a.q ? p.Hq : 0;
-  const long long hs = static_cast<long long>(p.ps) * p.d;   // head stride in a page
-  for (int i = blockIdx.y * kThreads + tid; i < tpc * per_row; i += gridDim.y * kThreads) {
-    const int t = i / per_row;
-    int j = i - t * per_row;
-    if (!s_live[t]) continue;
-    const int row = row0 + t;
-    const long long dst = s_row[t];
-    if (j < nrot) {
-      const int h = j / rc, c = j - h * rc;
-      const int c0 = a.interleaved ? 16 * c : 8 * c;
-      const int c1 = a.interleaved ? c0 + 8 : c0 + half;
-      const uint16_t* src = h < q0 ? a.q + row * a.qs + h * p.d : a.k + row * a.ks + (h - q0) * p.d;
-      uint16_t* out = h < q0 ? a.q_out + row * a.qos + h * p.d : p.k + dst + (h - q0) * hs;
-      uint4 lo = *reinterpret_cast<const uint4*>(src + c0);
-      uint4 hi = *reinterpret_cast<const uint4*>(src + c1);
-      rotate8<BF>(lo, hi, s_cs + t * 64 + 8 * c, a.interleaved);
-      if (h < q0 || dst >= 0) {
-        *reinterpret_cast<uint4*>(out + c0) = lo;
-        *reinterpret_cast<uint4*>(out + c1) = hi;
+    const long long at = s_row;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (t[u].dst < 0 || (t[u].dst > 0 && at < 0)) continue;
+      uint16_t* out = t[u].dst == 0 ? a.q_out + row * a.qos : (t[u].dst == 1 ? p.k : p.v) + at;
+      out += t[u].to;
+      if (t[u].second) {
+        rotate8<BF>(lo[u], hi[u], s_cs + t[u].pair, a.interleaved);
+        *reinterpret_cast<uint4*>(out + t[u].second) = hi[u];
       }
-    } else {
-      j -= nrot;
-      const uint16_t* src;
-      uint16_t* out;
-      bool st = dst >= 0;
-      if (j < npl) {
-        const int h = j / pc, c = a.rot + 8 * (j - h * pc);
-        src = (h < q0 ? a.q + row * a.qs + h * p.d : a.k + row * a.ks + (h - q0) * p.d) + c;
-        out = (h < q0 ? a.q_out + row * a.qos + h * p.d : p.k + dst + (h - q0) * hs) + c;
-        st = st || h < q0;
-      } else {
-        j -= npl;
-        const int h = j / (p.d >> 3), c = 8 * (j - h * (p.d >> 3));
-        src = a.v + row * a.vs + h * p.d + c;
-        out = p.v + dst + h * hs + c;
-      }
-      if (st) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(src);
+      *reinterpret_cast<uint4*>(out) = lo[u];
     }
   }
 }
@@ -162,14 +187,7 @@ k_append(const Pool p, const AppendArgs a, int tpc) {
 }  // namespace
 
 cudaError_t launch_append(const Pool& p, const AppendArgs& a, cudaStream_t s) {
-  const int tpc = a.rows >= 4 * 152 ? kMaxTpc : 1;
-  const int heads = (a.q ? p.Hq : 0) + p.Hkv;
-  const int items = tpc * (heads * ((a.rot >> 4) + ((p.d - a.rot) >> 3)) + p.Hkv * (p.d >> 3));
-  const int gx = (a.rows + tpc - 1) / tpc;
-  // few rows: their items over several CTAs, one item per thread
-  const int split = gx >= 152 ? 1 : (items + kThreads - 1) / kThreads;
-  const cudaError_t e = launch_pdl(p.bf16 ? k_append<true> : k_append<false>, dim3(gx, split),
-                                   dim3(kThreads), 0, s, p, a, tpc);
+  const cudaError_t e = launch_pdl(p.bf16 ? k_append<true> : k_append<false>, dim3(a.rows), dim3(kThreads), 0, s, p, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

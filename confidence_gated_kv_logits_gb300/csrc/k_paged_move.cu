@@ -10,16 +10,17 @@ namespace confkv {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kCommitBatch = 8;     // rows in flight per thread
+constexpr int kThreads = 256;       // of fork
+constexpr int kCommitThreads = 128; // 8 KV heads of 128 channels are 128 columns
+constexpr int kCommitBatch = 8;     // rows of K and of V in flight per thread
 constexpr int kMaxPath = 1024;      // path_cap limit (confkv_paged.h)
 
-// One CTA: sequence blockIdx.x, layer blockIdx.y / 2, K or V.  A thread owns a
-// 16-byte column of one head and moves it along the whole path, several rows
-// loaded before they are stored.  In place this is safe: the path rises, so
-// path[j] >= j, and a row that is overwritten (place j) can only be the source
-// of a move j' <= j, which has been loaded by then.
-__global__ void __launch_bounds__(kThreads)
+// One CTA: sequence blockIdx.x, layer blockIdx.y.  A thread owns a 16-byte
+// column of one head of K and of V and moves it along the whole path, several
+// rows loaded before they are stored.  In place this is safe: the path rises,
+// so path[j] >= j, and a row that is overwritten (place j) can only be the
+// source of a move j' <= j, which has been loaded by then.
+__global__ void __launch_bounds__(kCommitThreads)
 k_commit(const Pool p, const CommitArgs a) {
   __shared__ int s_src[kMaxPath], s_dst[kMaxPath];   // row numbers in the layer's head 0: page * Hkv * ps + slot
   __shared__ int s_bad;
@@ -34,7 +35,7 @@ k_commit(const Pool p, const CommitArgs a) {
   if (tid == 0) s_bad = sane ? 0 : CONFKV_FLAG_BAD_INDEX;
   __syncthreads();
   if (sane) {
-    for (int j = tid; j < n; j += kThreads) {
+    for (int j = tid; j < n; j += kCommitThreads) {
       const int x = path[j];
       const int prev = j ? path[j - 1] : -1;
       if (x <= prev) {
@@ -71,19 +72,28 @@ k_commit(const Pool p, const CommitArgs a) {
   while (first < n && s_src[first] < 0) ++first;
   if (first == n) return;
   const int cols = p.Hkv * (p.d >> 3);
-  uint16_t* base = ((blockIdx.y & 1) ? p.v : p.k) +
-                   static_cast<size_t>(blockIdx.y >> 1) * p.NP * p.Hkv * p.ps * p.d;
-  for (int c = tid; c < cols; c += kThreads) {
+  const size_t layer = static_cast<size_t>(blockIdx.y) * p.NP * p.Hkv * p.ps * p.d;
+  for (int c = tid; c < cols; c += kCommitThreads) {
     const int h = c / (p.d >> 3), x = c - h * (p.d >> 3);
-    uint16_t* col = base + static_cast<size_t>(h) * p.ps * p.d + 8 * x;
+    const size_t col = layer + static_cast<size_t>(h) * p.ps * p.d + 8 * x;
     for (int j = first; j < n; j += kCommitBatch) {
-      uint4 r[kCommitBatch];
+      uint4 k[kCommitBatch], v[kCommitBatch];
 #pragma unroll
-      for (int i = 0; i < kCommitBatch; ++i)
-        if (j + i < n) r[i] = *reinterpret_cast<const uint4*>(col + static_cast<size_t>(s_src[j + i]) * p.d);
+      for (int i = 0; i < kCommitBatch; ++i) {
+        if (j + i < n) {
+          const size_t at = col + static_cast<size_t>(s_src[j + i]) * p.d;
+          k[i] = *reinterpret_cast<const uint4*>(p.k + at);
+          v[i] = *reinterpret_cast<const uint4*>(p.v + at);
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < kCommitBatch; ++i)
-        if (j + i < n) *reinterpret_cast<uint4*>(col + static_cast<size_t>(s_dst[j + i]) * p.d) = r[i];
+      for (int i = 0; i < kCommitBatch; ++i) {
+        if (j + i < n) {
+          const size_t at = col + static_cast<size_t>(s_dst[j + i]) * p.d;
+          *reinterpret_cast<uint4*>(p.k + at) = k[i];
+          *reinterpret_cast<uint4*>(p.v + at) = v[i];
+        }
+      }
     }
   }
 }
@@ -146,7 +156,7 @@ k_fork(const Pool p, const ForkArgs a) {
 }  // namespace
 
 cudaError_t launch_commit(const Pool& p, const CommitArgs& a, cudaStream_t s) {
-  const cudaError_t e = launch_pdl(k_commit, dim3(a.B, 2 * p.L), dim3(kThreads), 0, s, p, a);
+  const cudaError_t e = launch_pdl(k_commit, dim3(a.B, p.L), dim3(kCommitThreads), 0, s, p, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -85,11 +85,10 @@ class _Device:
     def _rows(self, t, shape, name):
         """Address and row stride of a [rows, heads, head_dim] tensor whose rows are dense."""
         if t.dtype is self.dtype and t.shape == shape and t.get_device() == self._index:
-            if t.is_contiguous():
-                return t.data_ptr(), shape[1] * shape[2]
-            s = t.stride()
-            if s[2] == 1 and (s[1] == shape[2] or shape[1] == 1):
-                return t.data_ptr(), s[0] if shape[0] > 1 else shape[1] * shape[2]
+            rows, heads, d = shape
+            step, head, one = t.stride()
+            if one == 1 and (head == d or heads == 1):
+                return t.data_ptr(), step if rows > 1 else heads * d
         raise ValueError(f"{name}: want {self.dtype} {tuple(shape)} on {self.device} with dense rows, got "
                          f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
