@@ -55,6 +55,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
   __shared__ __align__(8) unsigned long long s_bar[kWarps * kStages];
   __shared__ float s_ml[kWarps][kRows][2];
   __shared__ Sched s_sched;
+  __shared__ WalkState s_walk;
   __shared__ long long s_scan[kWarps];
   __shared__ int s_abort, s_last;
 
@@ -70,51 +71,74 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
   pdl_wait();
   pdl_trigger();
 
-  Walk<kRows, F::CH, F::OVER> w(p, a.bt, a.rows);
-  sched_init<kThreads>(w, &s_sched, s_scan, 2 * kWarps);
-  w.start(s_sched);
+  // the walk stays in shared memory: its registers are the accumulators' between pieces
+  using WalkF = Walk<kRows, F::CH, F::OVER>;
+  if (a.bt.B > 32) {
+    WalkF w(p, a.bt, a.rows);
+    sched_init<kThreads>(w, &s_sched, s_scan, 2 * kWarps);
+  }
+  if (warp == 0) {
+    WalkF w(p, a.bt, a.rows);
+    if (a.bt.B > 32) {
+      w.start(s_sched);
+    } else {
+      const Sched sh = sched_warp(w, 2 * kWarps);
+      w.start(sh);
+    }
+    w.next();
+    if (lane == 0) s_walk = w;
+  }
+  __syncthreads();
+  const WalkState& w = s_walk;
   const uint64_t pol = stream_policy();
   const float c = a.scale * kL2E;
   unsigned turn = 0;                                // chunks this warp has taken so far
   const int r0 = lane >> 2, t4 = lane & 3;
 
-  while (w.next()) {
+  while (w.more) {
     const int b = w.b, h = w.h;
     const int32_t* table = a.bt.table + static_cast<size_t>(b) * a.bt.max_blocks;
     const int layer_row = (a.layer * p.NP) * p.Hkv;  // page of head h: (layer_row + page * Hkv + h) * ps
     int flag = 0;
-    auto issue = [&](int ci, unsigned k) {
-      // boxes of 16 rows (or the whole chunk, where a page holds it)
+    // boxes of 16 rows (or the whole chunk, where a page holds it); lane i asks
+    // for box i (d = 128: half i & 1 of box i / 2)
+    const int box = p.ps < F::CH ? p.ps : F::CH;
+    const int my_box = D == 128 ? lane >> 1 : lane, my_half = D == 128 ? lane & 1 : 0;
+    auto boxes = [&](int ci) {                        // those with tokens of the sequence
+      const int live = (w.len - ci * F::CH + box - 1) / box;
+      return live < F::CH / box ? live : F::CH / box;
+    };
+    // the lane's page of a chunk, read well before its boxes are asked for
+    auto page_of = [&](int ci) { return ci < w.hi && my_box < boxes(ci) ? table[(ci * F::CH + my_box * box) >> p.ps_shift] : 0; };
+    auto issue = [&](int ci, unsigned k, int page) {
       const int st = k % kStages;
       const uint32_t dst = ring + st * kChunkBytes, fb = bar + 8 * st;
-      const int j0 = ci * F::CH;
-      const int box = p.ps < F::CH ? p.ps : F::CH;
-      const int nb = F::CH / box;
-      const int live = (w.len - j0 + box - 1) / box;       // boxes with tokens of the sequence
-      const int n = live < nb ? live : nb;
+      const int n = boxes(ci);
       if (lane == 0) bar_expect(fb, static_cast<unsigned>(n * box * D * 4));
       __syncwarp();
-      if (lane < n * (D / 64)) {
-        const int i = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
-        const int j = j0 + i * box;
-        int page = table[j >> p.ps_shift];
+      if (my_box < n && lane < F::CH / box * (D / 64)) {
         if (page < 0 || page >= p.NP) {
           flag = CONFKV_FLAG_BAD_PAGE;
           page = 0;
         }
+        const int j = ci * F::CH + my_box * box;
         const int y = ((layer_row + page * p.Hkv + h) << p.ps_shift) + (j & (p.ps - 1));
-        const uint32_t o = dst + half * F::HALF + i * box * 128;
-        tma_box(o, &mk, 64 * half, y, fb, pol);
-        tma_box(o + F::KV, &mv, 64 * half, y, fb, pol);
+        const uint32_t o = dst + my_half * F::HALF + my_box * box * 128;
+        tma_box(o, &mk, 64 * my_half, y, fb, pol);
+        tma_box(o + F::KV, &mv, 64 * my_half, y, fb, pol);
       }
     };
     const int first = w.lo + warp;
     const unsigned turn0 = turn;
     unsigned issued = turn0;
     bool dead = false;
+    int pages[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) pages[i] = page_of(first + i * kWarps);
 #pragma unroll
     for (int i = 0; i < kStages; ++i)
-      if (first + i * kWarps < w.hi) issue(first + i * kWarps, issued++);
+      if (first + i * kWarps < w.hi) issue(first + i * kWarps, issued++, pages[i]);
+    int page_next = page_of(first + kStages * kWarps);
 
     // the tile's query rows as A fragments (zero behind the sequence's rows)
     const int R = w.T * p.g, base = w.mt * kRows;
@@ -277,7 +301,10 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
         }
       }
       __syncwarp();           // every lane has read the stage
-      if (ci + kStages * kWarps < w.hi) issue(ci + kStages * kWarps, issued++);
+      if (ci + kStages * kWarps < w.hi) {
+        issue(ci + kStages * kWarps, issued++, page_next);
+        page_next = page_of(ci + (kStages + 1) * kWarps);
+      }
       ++turn;
     }
     if (dead)                 // no copy may land after the CTA has gone
@@ -351,16 +378,73 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
       }
       __syncthreads();
       if (s_last) {
+        // The pieces in their order, as many at a time as the rings hold: all of a
+        // batch's words are asked for at once (a thread that walked its own words
+        // through L2 one piece after another took 3 to 6 us for 9 pieces).
         __threadfence();
-        if (rr < R) {
-          join_row<kRows, D, PER, (PER > 8 ? 2 : 5)>(sc, w, row, ch0, c, -1, x, m, l);
+        const int live = R - base < kRows ? R - base : kRows;
+        const int per_piece = live * (D / 4) + live / 2 + 1;            // 16-byte words, (maximum, sum) pairs behind
+        const int batch = kWarps * kStages * kChunkBytes / (16 * per_piece);
+        m = -INFINITY;
+        l = 0.0f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) x[e] = 0.0f;
+        for (int i0 = 0; i0 < w.pieces; i0 += batch) {
+          const int nb = w.pieces - i0 < batch ? w.pieces - i0 : batch;
+          const int words = live * (D / 4);
+          for (int it = tid; it < nb * words; it += kThreads) {
+            const int i = it / words, y = it - i * words, ch = y / live, r = y - ch * live;
+            cp_async16(ring0 + (i * per_piece + r * (D / 4) + ch) * 16, acc_at<kRows, D>(sc, piece_place(w, i0 + i), r, 4 * ch));
+          }
+          const int twos = (live + 1) / 2;                              // two rows' pairs are a word
+          for (int it = tid; it < nb * twos; it += kThreads) {
+            const int i = it / twos, r = it - i * twos;
+            cp_async16(ring0 + (i * per_piece + words + r) * 16, sc.ml + (piece_place(w, i0 + i) * kRows + 2 * r) * 2);
+          }
+          cp_async_wait();
+          __syncthreads();
+          if (row < live) {
+            float mn = m;
+            for (int i = 0; i < nb; ++i) mn = fmaxf(mn, lds_f2(ring0 + (i * per_piece + words) * 16 + row * 8).x);
+            const float f0 = m == -INFINITY ? 0.0f : ex2f((m - mn) * c);
+            l *= f0;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[e] *= f0;
+            m = mn;
+            for (int i = 0; i < nb; ++i) {
+              const float2 ml = lds_f2(ring0 + (i * per_piece + words) * 16 + row * 8);
+              if (ml.x == -INFINITY) continue;
+              const float f = ex2f((ml.x - m) * c);
+              l = fmaf(f, ml.y, l);
+#pragma unroll
+              for (int e = 0; e < PER; e += 4) {
+                float v[4];
+                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];\n"
+                             : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                             : "r"(ring0 + (i * per_piece + row * (D / 4) + (ch0 + e) / 4) * 16) : "memory");
+#pragma unroll
+                for (int y = 0; y < 4; ++y) x[e + y] = fmaf(f, v[y], x[e + y]);
+              }
+            }
+          }
+          __syncthreads();
+        }
+        if (row < live) {
           const int t = rr / p.g;
           store_row<BF, PER>(a, p, w.row0 + t, h * p.g + rr - t * p.g, ch0, x, m, l);
         }
       }
     }
     fence_async();
-    __syncthreads();          // the rings are free again
+    __syncthreads();          // the rings are free again, the piece has been read
+    if (warp == 0) {
+      WalkF on(p, a.bt, a.rows);
+      static_cast<WalkState&>(on) = s_walk;
+      on.next();
+      __syncwarp();
+      if (lane == 0) s_walk = on;
+    }
+    __syncthreads();
   }
   if (s_abort && tid == 0) atomicOr(p.err, CONFKV_FLAG_TIMEOUT);
 }

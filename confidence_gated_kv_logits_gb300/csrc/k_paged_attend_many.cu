@@ -123,9 +123,11 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
   pdl_wait();
   pdl_trigger();
   tc_fence_before();
-  {
+  if (a.bt.B > 32) {
     Walk<TM, BN, kOver> w(p, a.bt, a.rows);
     sched_init<kThreads>(w, &s_sched, s_scan, 4);
+  } else {
+    __syncthreads();          // barriers and tensor memory are there
   }
   tc_fence_after();
   const uint32_t tmem = s_tmem;
@@ -147,7 +149,12 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
     if (warp == 11) {
       // ---- the plan ----
       Walk<TM, BN, kOver> w(p, a.bt, a.rows);
-      w.start(s_sched);
+      if (a.bt.B <= 32) {
+        const Sched sh = sched_warp(w, 4);
+        w.start(sh);
+      } else {
+        w.start(s_sched);
+      }
       for (bool more = true; more; ++plan) {
         more = w.next();
         if (plan >= kPlan && !bar_wait_warp(b_read + 8 * (plan % kPlan), (plan / kPlan - 1) & 1, &s_abort)) break;

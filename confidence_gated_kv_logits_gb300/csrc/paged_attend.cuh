@@ -80,10 +80,12 @@ __device__ __forceinline__ void join_row(const Scratch& sc, const W& w, int row,
   }
   m = own >= 0 ? om : -INFINITY;
   l = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < w.pieces; ++i)
-    if (i != own) m = fmaxf(m, __ldcg(sc.ml + (piece_place(w, i) * TM + row) * 2));
-  if (m == -INFINITY) return;
+  if (w.pieces > U) {       // else the one round below brings all maxima
+#pragma unroll 8
+    for (int i = 0; i < w.pieces; ++i)
+      if (i != own) m = fmaxf(m, __ldcg(sc.ml + (piece_place(w, i) * TM + row) * 2));
+    if (m == -INFINITY) return;
+  }
 #pragma unroll 1
   for (int i0 = 0; i0 < w.pieces; i0 += U) {
     float2 ml[U];
@@ -98,6 +100,11 @@ __device__ __forceinline__ void join_row(const Scratch& sc, const W& w, int row,
         for (int e = 0; e < N / 4; ++e)
           v[u][e] = __ldcg(reinterpret_cast<const float4*>(acc_at<TM, D>(sc, at, row, ch + 4 * e)));
       }
+    }
+    if (w.pieces <= U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < w.pieces && u != own) m = fmaxf(m, ml[u].x);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {

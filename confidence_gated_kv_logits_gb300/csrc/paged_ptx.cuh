@@ -145,6 +145,18 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       : "memory");
 }
 
+// copies of single words into shared memory that take no registers on the way
+// (past L1: the words may have been written in this launch)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
 // byte address of 16-byte word `w` (0..7) of row `row` in a tile of 128-byte
 // rows under the 128-byte swizzle (tile 1024-byte aligned)
 __device__ __forceinline__ uint32_t swz128(uint32_t tile, int row, int w) {

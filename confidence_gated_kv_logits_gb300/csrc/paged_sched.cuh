@@ -14,7 +14,7 @@
 namespace confkv {
 namespace paged {
 
-struct Sched {          // in shared memory, filled by sched_init
+struct Sched {          // of one CTA: sched_warp, or for more than 32 sequences sched_init
   long long share;      // work per CTA
   long long cur, end;   // this CTA's range of the work
   // the sequence in which the range starts, and where its work does
@@ -36,11 +36,7 @@ struct Scratch {        // of the handle: partial results of cut units
   int4* cut;            // [CTA] that unit for the joining kernel: pieces, sequence, head, tile
 };
 
-template <int TM, int KB, int kOverhead>
-struct Walk {
-  const Pool& p;
-  const Batch& bt;
-  int rows;
+struct WalkState {
   long long share, cur, end, ustart;
   int b, h, mt;
   int T, ctx, len, row0, m;     // of sequence b; m = tiles per head
@@ -48,6 +44,15 @@ struct Walk {
   // a piece of a unit: blocks [lo, hi) of its n
   int lo, hi, n;
   int first_cta, pieces;        // CTAs that hold the unit's pieces
+  int unit_done;                // the walk is behind the unit's last piece
+  int more;                     // there is a piece
+};
+
+template <int TM, int KB, int kOverhead>
+struct Walk : WalkState {
+  const Pool& p;
+  const Batch& bt;
+  int rows;
 
   __device__ __forceinline__ Walk(const Pool& p_, const Batch& b_, int rows_) : p(p_), bt(b_), rows(rows_) {}
 
@@ -92,6 +97,7 @@ struct Walk {
   }
 
   __device__ __forceinline__ void start(const Sched& s) {
+    unit_done = 0;
     share = s.share;
     cur = s.cur;
     end = s.end;
@@ -121,7 +127,7 @@ struct Walk {
   __device__ __forceinline__ bool next() {
     for (;;) {
       if (unit_done) {
-        unit_done = false;
+        unit_done = 0;
         ustart += n + kOverhead;
         if (++mt == m) {
           mt = 0;
@@ -134,7 +140,10 @@ struct Walk {
           }
         }
       }
-      if (cur >= end) return false;
+      if (cur >= end) {
+        more = 0;
+        return false;
+      }
       n = blocks(mt);
       const long long uend = ustart + n + kOverhead;
       const long long x1 = end < uend ? end : uend;
@@ -145,11 +154,55 @@ struct Walk {
       pieces = static_cast<int>(quotient(uend - 1, share)) - first_cta + 1;
       cur = x1;
       unit_done = x1 == uend;
-      if (hi > lo) return true;
+      if (hi > lo) {
+        more = 1;
+        return true;
+      }
     }
   }
-  bool unit_done = false;
 };
+
+// The share of CTA `cta` of `ctas`, and the sequence that it starts in.
+template <typename W>
+__device__ __forceinline__ void sched_share(Sched* s, long long all, int cta, int ctas, long long min_share) {
+  const long long even = quotient(all + ctas - 1, ctas);
+  s->share = even < min_share ? min_share : even;
+  s->cur = static_cast<long long>(cta) * s->share;
+  s->end = s->cur + s->share < all ? s->cur + s->share : all;
+}
+
+// Up to 32 sequences: every warp works the schedule out by itself, a lane per
+// sequence, without a barrier.
+template <typename W>
+__device__ __forceinline__ Sched sched_warp(W& w, long long min_share) {
+  const int lane = threadIdx.x & 31;
+  int flag = 0;
+  long long x = 0, head = 0;
+  if (lane < w.bt.B) {
+    w.sequence(lane, flag);
+    head = w.T > 0 ? w.head_work() : 0;
+    x = head * w.p.Hkv;
+  }
+  if (flag && blockIdx.x == 0) atomicOr(w.p.err, flag);
+  long long incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  Sched s;
+  sched_share<W>(&s, __shfl_sync(0xffffffffu, incl, 31), blockIdx.x, gridDim.x, min_share);
+  const unsigned in = __ballot_sync(0xffffffffu, x > 0 && s.cur >= incl - x && s.cur < incl);
+  const int b = in ? __ffs(in) - 1 : 0;
+  s.b = b;
+  s.seq0 = __shfl_sync(0xffffffffu, incl - x, b);
+  s.head = __shfl_sync(0xffffffffu, head, b);
+  s.T = __shfl_sync(0xffffffffu, w.T, b);
+  s.ctx = __shfl_sync(0xffffffffu, w.ctx, b);
+  s.len = __shfl_sync(0xffffffffu, w.len, b);
+  s.row0 = __shfl_sync(0xffffffffu, w.row0, b);
+  return s;
+}
 
 // Every thread of the CTA calls it (kT threads).  s_scan holds kT / 32
 // 64-bit words.
@@ -190,13 +243,13 @@ __device__ __forceinline__ void sched_init(W& w, Sched* s, long long* s_scan, lo
   };
   long long all;
   long long pre = scan(total, all);
-  long long share = quotient(all + gridDim.x - 1, gridDim.x);
-  share = share < min_share ? min_share : share;
-  const long long cur = static_cast<long long>(blockIdx.x) * share;
+  Sched mine_of;
+  sched_share<W>(&mine_of, all, blockIdx.x, gridDim.x, min_share);
+  const long long cur = mine_of.cur;
   if (tid == 0) {
-    s->share = share;
+    s->share = mine_of.share;
     s->cur = cur;
-    s->end = cur + share < all ? cur + share : all;
+    s->end = mine_of.end;
   }
   auto here = [&](long long at, long long x) {      // this thread's sequence (in w) is the one
     s->b = w.b;
