@@ -15,12 +15,11 @@
 // maximum give the same answer.
 //
 // Precision: exponentials and their sums per thread are fp32, relative to the
-// slice's maximum (the largest terms are exact) and a power of two; sums over
-// threads and slices are whole numbers of 2^-38 (exact in any order, and off
-// the slow double pipe); lse and the candidates' scores are double, so
+// slice's maximum (the largest terms are exact); sums over threads and slices
+// are whole numbers of 2^-38 (exact in any order, and off the slow double
+// pipe); the slices' weights, lse and the candidates' scores are double, so
 // candidates of different beams are ordered to ~1e-8; scores are rounded to fp32 once, at the end.  Equal
 // scores go to the lower (beam, token).
-#include <climits>
 #include <cmath>
 
 #include "paged_internal.cuh"
@@ -35,14 +34,13 @@ constexpr int kCap = 1024;            // candidates ranked by counting
 constexpr int kMaxBeams = 32;
 constexpr float kL2E = 1.4426950408889634f;
 
-constexpr int kUnitBits = 38;          // sums are whole numbers of 2^-38
-constexpr float kUnits = 274877906944.0f;
+constexpr float kUnits = 274877906944.0f;     // 2^38: sums are whole numbers of 2^-38
 
-// a slice's sum of exp(z) = sum 2^(exp - kUnitBits); ~0: a NaN or +inf was
+// a slice's largest logit and sum of exp(z - max); sum ~0: a NaN or +inf was
 // seen; 0: no finite logit
 struct SlicePart {
   unsigned long long sum;
-  long long exp;
+  float max;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -286,18 +284,6 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
     bm = s_f[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, s_f[w]);
-    // The slice's power of two: bm log2 e (the product, its rounding and the
-    // constant's) as a whole number, rounded up, and what is left (in (-1, 0]).
-    // Slices then join by shifts alone.
-    float delta;
-    long long power;
-    {
-      const float h = bm * kL2E, c0 = ceilf(h);
-      const float d = (h - c0) + fmaf(bm, 1.9259629911e-08f, fmaf(bm, kL2E, -h));
-      const float c1 = ceilf(d);
-      delta = d - c1;
-      power = static_cast<long long>(c0) + static_cast<long long>(c1);
-    }
     float sum = 0.0f;
     if (bm > -INFINITY && bm < INFINITY) {
 #pragma unroll
@@ -305,7 +291,7 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
         float part4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         // (z - max) first, which is exact for what weighs: z's product alone would lose digits
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) part4[e & 3] += ex2(fmaf(value(i, e) - bm, kL2E, delta));
+        for (int e = 0; e < VEC; ++e) part4[e & 3] += ex2((value(i, e) - bm) * kL2E);
         sum += (part4[0] + part4[1]) + (part4[2] + part4[3]);
         if (top_value(word_top(x[i])) >= bound) {
 #pragma unroll
@@ -335,7 +321,7 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
       unsigned long long t = 0;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) t += s_sum[w];
-      part[slice] = SlicePart{s_bad ? ~0ull : t, power};
+      part[slice] = SlicePart{s_bad ? ~0ull : t, bm};
     }
     if (cnt <= kCap) {
       for (int i = tid; i < cnt; i += kThreads) {
@@ -395,44 +381,47 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
     const SlicePart* pp = part + static_cast<size_t>(r) * C;
     const float sc = a.scores[r];
     const bool done = a.finished && a.finished[r];
-    // this lane's slice (a row of more than 32 goes on below)
-    SlicePart q{0ull, LLONG_MIN};
+    // this lane's slices, the first of them at once
     auto part_of = [&](int c) {
       const ulonglong2 v = __ldcg(reinterpret_cast<const ulonglong2*>(pp + c));
-      return SlicePart{v.x, v.x ? static_cast<long long>(v.y) : LLONG_MIN};
+      return SlicePart{v.x, v.x ? __uint_as_float(static_cast<unsigned>(v.y)) : -INFINITY};
     };
-    auto joined = [](const SlicePart& x, const SlicePart& y) {
-      const bool first = x.exp >= y.exp;
-      const SlicePart& big = first ? x : y;
-      const SlicePart& low = first ? y : x;
-      if (!low.sum || big.exp - low.exp > 63) return big;
-      return SlicePart{big.sum + (low.sum >> (big.exp - low.exp)), big.exp};
-    };
-    bool bad = false;
+    SlicePart q{0ull, -INFINITY};
     if (lane < C) q = part_of(lane);
     int flag = 0;
     double base = __longlong_as_double(0x7ff8000000000000ll);
     if (!(sc < INFINITY)) {
       flag = CONFKV_FLAG_NONFINITE;
     } else if (sc > -INFINITY && !done) {
-      bad = q.sum == ~0ull;
+      float m = q.max;
+      bool bad = q.sum == ~0ull;
       for (int c = lane + 32; c < C; c += 32) {
         const SlicePart y = part_of(c);
+        m = fmaxf(m, y.max);
         bad |= y.sum == ~0ull;
-        q = joined(q, y);
       }
-      bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        SlicePart y;
-        y.sum = __shfl_xor_sync(0xffffffffu, q.sum, o);
-        y.exp = __shfl_xor_sync(0xffffffffu, q.exp, o);
-        q = joined(q, y);
-      }
-      if (bad || !q.sum)
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      bad = __any_sync(0xffffffffu, bad);
+      if (bad || !(m > -INFINITY)) {
         flag = CONFKV_FLAG_NONFINITE;
-      else
-        base = static_cast<double>(sc) - fma(static_cast<double>(q.exp - kUnitBits), 0.6931471805599453, log_ge1(static_cast<double>(q.sum)));
+      } else {
+        // the slices' sums relative to the row's maximum, in whole units again: the
+        // slice that holds it counts as it is, so a row of one token gives exactly 0
+        auto units = [&](const SlicePart& y) {
+          return static_cast<unsigned long long>(static_cast<double>(y.sum) *
+                                                 exp_neg(static_cast<double>(y.max) - static_cast<double>(m)));
+        };
+        unsigned long long sum = q.sum ? units(q) : 0ull;
+        for (int c = lane + 32; c < C; c += 32) {
+          const SlicePart y = part_of(c);
+          if (y.sum) sum += units(y);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        base = static_cast<double>(sc) -
+               (static_cast<double>(m) + log_ge1(static_cast<double>(sum) * (1.0 / 274877906944.0)));
+      }
     }
     if (lane == 0) {
       s_base[w] = base;

@@ -96,7 +96,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       bar_init(b_full + 8 * i, 1);
-      bar_init(b_empty + 8 * i, NQ);      // the streams that read a stage
+      bar_init(b_empty + 8 * i, 2);       // both streams give every stage back
     }
     for (int i = 0; i < 4; ++i) {
       bar_init(b_s + 8 * i, 1);
@@ -227,11 +227,27 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
     const uint32_t ts = uniform(tmem + s * 128), to = uniform(tmem + 256 + s * 128),
                    q_lo = uniform(umma_lo(base + (NQ == 2 ? s * M::TILE : 0), 16)), k_lo = uniform(umma_lo(ring, 16)),
                    v_lo = uniform(umma_lo(ring, M::HALF));
-    unsigned slot0 = 0, np = 0, nq = 0;
+    unsigned slot0 = 0, np = 0, nq = 0, seen = 0;
     bool ok = true;
+    // Slot k is there.  A stream waits for every slot in turn, its own or not:
+    // those before k that it has not waited for are the other stream's (NQ = 1)
+    // and are given back at once.  (Were they passed over, a stage whose earlier
+    // slot is still on its way would answer for the later one: a wait knows a
+    // phase by its parity alone.)
     auto full = [&](unsigned k) {
-      ok = bar_wait_warp(b_full + 8 * (k % ST), (k / ST) & 1, &s_abort);
+      while (ok && seen <= k) {
+        ok = bar_wait_warp(b_full + 8 * (seen % ST), (seen / ST) & 1, &s_abort);
+        if (ok && seen < k) bar_arrive_warp(b_empty + 8 * (seen % ST));
+        ++seen;
+      }
       return ok;
+    };
+    auto give_back = [&](unsigned end) {    // what is left of the piece is the other stream's
+      while (ok && seen < end) {
+        ok = bar_wait_warp(b_full + 8 * (seen % ST), (seen / ST) & 1, &s_abort);
+        if (ok) bar_arrive_warp(b_empty + 8 * (seen % ST));
+        ++seen;
+      }
     };
     auto release = [&](unsigned k) { umma_commit(b_empty + 8 * (k % ST)); };
     auto qk = [&](int i, unsigned k) {      // S of sub-block i = Q K^T, half i & 1 of K's stage
@@ -282,8 +298,10 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
         if (more) qk(i, v + 1);
       }
       if (!ok) break;
-      if (mine > 0) umma_commit(b_o + 8 * s);
+      umma_commit(b_o + 8 * s);             // (also where the stream has no block: it is waited for)
       slot0 += 2 * nb;
+      give_back(slot0);
+      if (!ok) break;
       piece_done();
     }
     if (!ok) {
@@ -425,6 +443,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
                   if (!(bits >> e & 1u)) sv[q][e] = 0xff800000u;
               }
             }
+            __syncwarp();
             weights(true);
           }
           const float mn = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
@@ -464,10 +483,9 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
         s_last = !defer && *const_cast<volatile unsigned int*>(sc.ticket + w.first_cta) == static_cast<unsigned>(w.pieces - 1);
         __threadfence();
       }
-      if (mine > 0) {
-        if (bar_wait_warp(b_o + 8 * s, no & 1, &s_abort)) tc_fence_after();
-        ++no;
-      }
+      // (a stream without a block too: its issuing warp may not fall a piece behind)
+      if (bar_wait_warp(b_o + 8 * s, no & 1, &s_abort)) tc_fence_after();
+      ++no;
       slot0 += 2 * nb;
       if (NQ == 1) {
         s_x[(s * 128 + r) * 2] = m;
@@ -499,6 +517,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
         for (int q = 0; q < COLS; q += 32) {
           uint32_t o[32];
           float y[32];
+          __syncwarp();
           tmem_ld32(o, to + (NQ == 1 ? 0 : s * 128) + col0 + q);
           tmem_wait_ld(o);
 #pragma unroll
