@@ -28,9 +28,9 @@ namespace confkv {
 namespace paged {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 2;
+constexpr int kStages = 3;
 constexpr int kRows = kFewRows;
 constexpr int kChunkBytes = 4 * kFewChunk;
 constexpr float kL2E = 1.4426950408889634f;
@@ -47,7 +47,7 @@ struct Few {
 };
 
 template <bool BF, int D>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 1)
 k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_constant__ CUtensorMap mk,
              const __grid_constant__ CUtensorMap mv) {
   using F = Few<D>;

@@ -289,14 +289,20 @@ int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int l
   AttendArgs a{batch_of(batch), layer, rows, static_cast<const uint16_t*>(q), q_stride, static_cast<uint16_t*>(out),
                lse, scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(p.d))};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // by the query rows of a sequence's KV head, on average
-  const int64_t per = static_cast<int64_t>(rows) * p.g / batch->batch;
+  // By the query rows of a sequence's KV head, on average (measured on GB300, us):
+  //  - up to 16 the streaming kernel (1 x 32768 tokens, 40/8 heads, d = 128: 10 rows 37
+  //    streamed, 42 with the padded tiles of 128; 20 rows 62 in two streamed tiles, 42)
+  //  - from 257 on units of two tiles, which share each K and V block, if they fill half
+  //    the GPU (8 x 8192 tokens: 385 rows 152, 194 in units of one tile; 1 x 32768 tokens,
+  //    whose 16 units do not: 260 rows 110, 87 in units of one)
+  //  - far fewer units of one tile than CTAs are cut into many pieces each, which a
+  //    kernel of its own joins on all SMs (1 x 32768 tokens, 65 rows: 58 joined by the
+  //    last CTA of each unit, 42)
+  const int64_t heads = static_cast<int64_t>(rows) * p.g, per = heads / batch->batch;
   if (per <= kFewRows) return launched(kv, launch_attend_few(p, a, kv->scratch, kv->maps, kFewCtasPerSm * kv->sms, st));
-  // units of 128 rows, at most; far fewer of them than CTAs are cut into many pieces
-  // each, which a kernel of its own joins on all SMs
-  const int64_t units = p.Hkv * (static_cast<int64_t>(rows) * p.g / 128 + batch->batch);
-  const bool two = per > kManyRows;
-  return launched(kv, launch_attend_many(p, a, kv->scratch, kv->maps, kv->sms, two, !two && 4 * units <= kv->sms, st));
+  const int64_t ones = p.Hkv * (heads / 128 + batch->batch), twos = p.Hkv * (heads / kManyRows + batch->batch);
+  const bool two = per > kManyRows && 2 * twos >= kv->sms;
+  return launched(kv, launch_attend_many(p, a, kv->scratch, kv->maps, kv->sms, two, !two && 4 * ones <= kv->sms, st));
 }
 
 int confkv_paged_commit(confkv_paged* kv, int batch, int max_blocks, const int32_t* page_table,

@@ -18,8 +18,8 @@ constexpr int kFewChunk = 2048;        // elements of K in a chunk (tokens x d)
 constexpr int kManyRows = 256;         // two tiles of 128
 constexpr int kManyBlock = 128;        // tokens of a block
 
-// CTAs of a launch: resident ones only, three per SM or one
-constexpr int kFewCtasPerSm = 3;
+// CTAs of a launch: one per SM
+constexpr int kFewCtasPerSm = 1;
 
 cudaError_t launch_attend_few(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
                               int ctas, cudaStream_t s);
@@ -42,11 +42,19 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, const Pool& p, in
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const size_t at = static_cast<size_t>(row) * p.Hq + hq;
   uint16_t* out = a.out + at * p.d + ch;
+  static_assert(N % 4 == 0, "whole 8-byte words");
+  if constexpr (N % 8 == 0) {
 #pragma unroll
-  for (int e = 0; e < N; e += 8)
-    *reinterpret_cast<uint4*>(out + e) =
-        make_uint4(pack2<BF>(x[e] * inv, x[e + 1] * inv), pack2<BF>(x[e + 2] * inv, x[e + 3] * inv),
-                   pack2<BF>(x[e + 4] * inv, x[e + 5] * inv), pack2<BF>(x[e + 6] * inv, x[e + 7] * inv));
+    for (int e = 0; e < N; e += 8)
+      *reinterpret_cast<uint4*>(out + e) =
+          make_uint4(pack2<BF>(x[e] * inv, x[e + 1] * inv), pack2<BF>(x[e + 2] * inv, x[e + 3] * inv),
+                     pack2<BF>(x[e + 4] * inv, x[e + 5] * inv), pack2<BF>(x[e + 6] * inv, x[e + 7] * inv));
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; e += 4)
+      *reinterpret_cast<uint2*>(out + e) =
+          make_uint2(pack2<BF>(x[e] * inv, x[e + 1] * inv), pack2<BF>(x[e + 2] * inv, x[e + 3] * inv));
+  }
   if (a.lse && ch == 0) a.lse[at] = l == 0.0f ? -INFINITY : m * a.scale + logf(l);
 }
 
