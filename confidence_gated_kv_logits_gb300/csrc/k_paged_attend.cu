@@ -70,6 +70,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
   fence_async();
   pdl_wait();
   pdl_trigger();
+  fence_async_global();
 
   // the walk stays in shared memory: its registers are the accumulators' between pieces
   using WalkF = Walk<kRows, F::CH, F::OVER>;

@@ -122,6 +122,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
   }
   pdl_wait();
   pdl_trigger();
+  fence_async_global();
   tc_fence_before();
   if (a.bt.B > 32) {
     Walk<TM, BN, kOver> w(p, a.bt, a.rows);

@@ -224,7 +224,8 @@ int confkv_paged_status(confkv_paged* kv, int32_t* flags) {
   int32_t f = 0;
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpy(&f, kv->pool.err, sizeof(f), cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess && f) e = cudaMemset(kv->pool.err, 0, sizeof(f));
+  // with the flags the tickets: a launch that gave up (CONFKV_FLAG_TIMEOUT) may have left some
+  if (e == cudaSuccess && f) e = cudaMemset(kv->pool.err, 0, CONFKV_PAGED_ZEROED);
   if (e == cudaSuccess && f) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return launched(kv, e);
   if (flags) *flags = f;

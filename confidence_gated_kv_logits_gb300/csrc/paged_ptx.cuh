@@ -122,6 +122,8 @@ __device__ __forceinline__ void bar_drain(uint32_t bar, unsigned parity) {
 // generic-proxy writes to shared memory become visible to the async proxy
 // (TMA, tcgen05), and the reverse order of reuse
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+// K and V rows that the kernel before stored are read here by TMA
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;\n" ::: "memory"); }
 __device__ __forceinline__ void fence_bar_init() { asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory"); }
 
 __device__ __forceinline__ uint64_t stream_policy() {

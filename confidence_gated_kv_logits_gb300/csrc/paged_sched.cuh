@@ -75,8 +75,9 @@ struct Walk : WalkState {
       if (T) flag |= CONFKV_FLAG_CAPACITY;
       l = cap;
     }
-    if (l > 0x7ffffff0ll) l = 0x7ffffff0ll;
+    if (l > 0x7fffff00ll) l = 0x7fffff00ll;         // (a block more still fits an int)
     len = static_cast<int>(l);
+    if (ctx > len) ctx = len;
     m = static_cast<int>((static_cast<long long>(T) * p.g + TM - 1) / TM);
   }
   // tokens that some row of tile t may see

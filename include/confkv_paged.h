@@ -87,7 +87,9 @@ const char* confkv_paged_last_error(const confkv_paged* kv);
 /*
  * confkv_paged_status -- synchronise the device, return the CONFKV_FLAG_*
  * bits latched since the last call in *flags (may be NULL) and clear them:
- * CONFKV_ERR_DEVICE where any was set, else CONFKV_OK.
+ * CONFKV_ERR_DEVICE where any was set, else CONFKV_OK.  CONFKV_FLAG_TIMEOUT
+ * (a wait inside an attend call gave up after 2 s) makes that call's output
+ * void; the handle is usable again after this call.
  */
 int confkv_paged_status(confkv_paged* kv, int32_t* flags);
 

@@ -247,6 +247,78 @@ def test_attend_many_sequences(pkg):
     check(c, run_attend(pkg, c), reference(c))
 
 
+@pytest.mark.parametrize("n,most,heads,kv_heads", [(40, 30, 16, 2), (500, 6, 16, 2), (700, 2, 4, 2), (33, 200, 5, 1)])
+def test_attend_more_sequences_than_lanes_or_threads(pkg, n, most, heads, kv_heads):
+    r = np.random.default_rng(n)
+    ctx = [int(x) for x in r.integers(0, 300, n)]
+    new = [int(x) for x in r.integers(0, most + 1, n)]
+    c = Case(torch.float16, heads, kv_heads, 64, 32, ctx, new, seed=n)
+    check(c, run_attend(pkg, c), reference(c))
+    bits = tree_bits(new, n)
+    check(c, run_attend(pkg, c, bits), reference(c, bits=bits))
+
+
+@pytest.mark.parametrize("heads,kv_heads,d,ctx,t", [
+    (40, 8, 128, [32768], 4), (40, 8, 128, [32768], 1), (40, 8, 128, [9000] * 4, 26), (16, 2, 64, [20000, 5], 40),
+    (40, 8, 128, [700, 3000], 400), (5, 1, 128, [100] * 30, 9)])
+def test_attend_gives_the_same_bits_launch_after_launch(pkg, heads, kv_heads, d, ctx, t):
+    c = Case(torch.bfloat16, heads, kv_heads, d, 64, ctx, [t] * len(ctx), seed=t, layers=1)
+    kv = pkg.PagedKV(c.k, c.v, heads)
+    batch = c.batch(kv)
+    first = None
+    outs = [torch.empty_like(c.q) for _ in range(4)]
+    lses = [torch.empty(c.rows, heads, device=DEV) for _ in range(4)]
+    for _ in range(40):
+        for o, l in zip(outs, lses):
+            kv.attend(0, batch, c.q, o, lse=l)
+        for o, l in zip(outs, lses):
+            n = c.starts[-1]
+            first = first or (o[:n].clone(), l[:n].clone())
+            assert torch.equal(o[:n], first[0]) and torch.equal(l[:n], first[1])
+    assert kv.status() == 0
+
+
+def test_two_handles_on_two_streams_over_the_same_pools(pkg):
+    c = Case(torch.float16, 16, 2, 64, 32, [3000, 800], [40, 3], seed=21)
+    want = reference(c)
+    side = torch.cuda.Stream()
+    a, b = pkg.PagedKV(c.k, c.v, 16), pkg.PagedKV(c.k, c.v, 16)
+    ba, bb = c.batch(a), c.batch(b)
+    one = [torch.full_like(c.q, 7) for _ in range(2)]
+    lse = [torch.full((c.rows, 16), 7.0, device=DEV) for _ in range(2)]
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        a.attend(1, ba, c.q, one[0], lse=lse[0])
+        b.attend(1, bb, c.q, one[1], lse=lse[1], stream=side)
+    torch.cuda.synchronize()
+    for i in range(2):
+        check(c, (one[i], lse[i]), want)
+
+
+def test_two_graphs_of_one_handle_in_turn(pkg):
+    c = Case(torch.bfloat16, 40, 8, 128, 64, [5000], [20], seed=22, layers=2)
+    kv = pkg.PagedKV(c.k, c.v, 40)
+    batch = c.batch(kv)
+    outs, graphs = [torch.empty_like(c.q) for _ in range(3)], []
+    kv.attend(0, batch, c.q, outs[2])
+    kv.attend(1, batch, c.q, outs[2])
+    for layer in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kv.attend(layer, batch, c.q, outs[layer])
+        graphs.append(g)
+    for _ in range(10):
+        for g in graphs:
+            g.replay()
+        kv.attend(1, batch, c.q, outs[2])
+    torch.cuda.synchronize()
+    n = c.starts[-1]
+    for layer in range(2):
+        o, _, tol, _ = reference(c, layer=layer)
+        assert ((outs[layer][:n].double() - o).abs() <= tol).all()
+    assert torch.equal(outs[1][:n], outs[2][:n])
+
+
 def test_attend_strided_rows_streams_and_repeats(pkg):
     c = Case(torch.float16, 10, 2, 128, 32, [700, 31, 0], [3, 60, 2], seed=8)
     wide = torch.full((c.rows, 16, 128), math.nan, dtype=c.dt, device=DEV)
@@ -419,6 +491,10 @@ def test_python_refusals(pkg):
               lambda: kv.batch(c.table.long(), ints([5]), ints([0, 4])), lambda: kv.batch(c.table, ints([5]), ints([0])),
               lambda: kv.batch(c.table, ints([5]), ints([0, 4]), torch.zeros(4, device=DEV)),
               lambda: kv.attend(0, kv.batch(c.table, ints([5]), ints([0, 4]), ints([[1]] * 3)), c.q, out),
+              lambda: kv.attend(0, b, c.q[:, :, :32], out), lambda: kv.commit(c.table, ints([5]), ints([[0]]), ints([1, 1]), ints([0])),
+              lambda: pkg.BeamSelect(1, 33, 100, 4), lambda: pkg.BeamSelect(1, 4, 100, 4, dtype=torch.float64),
+              lambda: pkg.BeamSelect(1, 4, 100, 4).select(torch.zeros(1, 4, 99, device=DEV), *[torch.zeros(1, 4, device=DEV)] * 2,
+                                                          ints([[0] * 4]), ints([[0] * 4])),
               lambda: pkg.PagedKV(c.k, c.v.bfloat16(), 8), lambda: pkg.PagedKV(c.k, c.v, 9),
               lambda: pkg.PagedKV(c.k.float(), c.v.float(), 8), lambda: pkg.PagedKV(c.k[:, 1:], c.v[:, 1:], 8)):
         with pytest.raises(E):
