@@ -1,20 +1,25 @@
 """Build the CONF-KV CUDA library in-tree (nvcc, sm_103a, no cmake).
 
 Each .cu file under csrc/ is compiled to an object in parallel, then linked
-into ``libconfkv.so`` next to this file.  Host code is compiled without
+into ``libconfkv.so`` next to this file; csrc/paged_py.cpp, which reads tensor
+arguments for the paged operators, becomes the Python module ``_paged_ops.so``
+(g++ with torch's own headers, linked to both).  Host code is compiled without
 floating-point contraction so the per-layer budget table is computed with
 plain IEEE double operations.
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libconfkv.so")
+OPS = os.path.join(HERE, "_paged_ops.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,6 +40,30 @@ def _stale(target, deps):
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(x) > t for x in deps)
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stderr}")
+
+
+def _ops_object(src, obj):
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=1",
+          "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
+          "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+          "-isystem", os.path.join(cuda, "include"), "-c", src, "-o", obj], f"g++ on {src}")
+
+
+def _ops_link(obj):
+    lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+    tmp = OPS + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:libconfkv.so", "-L", lib, "-ltorch_python",
+          "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"],
+         "linking _paged_ops.so")
+    os.replace(tmp, OPS)
 
 
 def build(force=False, verbose=False):
@@ -60,8 +89,14 @@ def build(force=False, verbose=False):
             print(r.stderr)
         return o
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
+    ops_src = os.path.join(CSRC, "paged_py.cpp")
+    ops_obj = os.path.join(OBJ, "paged_py.o")
+    ops = force or _stale(ops_obj, [ops_src] + hdrs)
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        extra = ex.submit(_ops_object, ops_src, ops_obj) if ops else None
         list(ex.map(compile_one, jobs))
+        if extra:
+            extra.result()
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
@@ -69,6 +104,8 @@ def build(force=False, verbose=False):
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, LIB)
+    if force or _stale(OPS, [ops_obj, LIB]):
+        _ops_link(ops_obj)
     return LIB
 
 

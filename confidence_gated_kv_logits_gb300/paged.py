@@ -8,27 +8,32 @@ is copied, converted or computed here.  As everywhere in CUDA, a tensor that
 is used on another stream than its own must stay alive until that work is
 done (``Tensor.record_stream``).
 
-The checks are written for few attribute reads per tensor: for a single token
-they and the launch are the call's whole cost.
+The per-call checks live in ``_paged_ops.so`` (csrc/paged_py.cpp): for a single
+token they and the launch are the call's whole cost.
 """
 import ctypes
 
 FP16, BF16, FP32 = 0, 1, 2
 ZEROED = 16384                      # CONFKV_PAGED_ZEROED
 torch = None                        # imported with the first handle
-_raw_stream = None
-_F32 = _I32 = None
+_ops = None
 
 
 def _load():
-    """The library; torch, on first use (importing the package needs none)."""
-    global torch, _raw_stream, _F32, _I32
+    """The library; torch and the argument checks, on first use (importing the
+    package needs neither)."""
+    global torch, _ops
     from . import load_library
-    if torch is None:
+    L = load_library()
+    if _ops is None:
         import torch as t
-        torch, _raw_stream = t, t._C._cuda_getCurrentRawStream
-        _F32, _I32 = t.float32, t.int32
-    return load_library()
+        try:
+            from . import _paged_ops
+        except ImportError as e:
+            raise ImportError(f"_paged_ops.so cannot be loaded ({e}): build it with "
+                              "confidence_gated_kv_logits_gb300.build.build()") from e
+        torch, _ops = t, _paged_ops
+    return L
 
 
 class BatchStruct(ctypes.Structure):
@@ -73,24 +78,16 @@ def _dtype_code(dtype):
 
 
 class _Device:
-    """Checks of tensor arguments against one device."""
+    """An object on one device with scratch of its own."""
 
-    def _dense(self, t, dtype, shape, name):
-        """Address of a contiguous tensor."""
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
-            raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {self.device}, got "
+    _ob = None
+
+    def _dense(self, t, shape, name):
+        """Address of a contiguous int32 tensor."""
+        if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
+            raise ValueError(f"{name}: want contiguous int32 {tuple(shape)} on {self.device}, got "
                              f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
         return t.data_ptr()
-
-    def _rows(self, t, shape, name):
-        """Address and row stride of a [rows, heads, head_dim] tensor whose rows are dense."""
-        if t.dtype is self.dtype and t.shape == shape and t.get_device() == self._index:
-            rows, heads, d = shape
-            step, head, one = t.stride()
-            if one == 1 and (head == d or heads == 1):
-                return t.data_ptr(), step if rows > 1 else heads * d
-        raise ValueError(f"{name}: want {self.dtype} {tuple(shape)} on {self.device} with dense rows, got "
-                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
     def _scratch(self, n, zeroed):
         """Device scratch, its first `zeroed` bytes zero whichever stream comes first."""
@@ -98,18 +95,13 @@ class _Device:
         self._mem[:zeroed].zero_()
         home = torch.cuda.current_stream(self.device)
         home.synchronize()
-        self._home, self._away = home.cuda_stream, False
+        self._home = home.cuda_stream
         return self._mem.data_ptr()
-
-    def _stream(self, stream):
-        s = _raw_stream(self._index) if stream is None else stream.cuda_stream
-        if s != self._home:
-            self._away = True
-        return s
 
     def _leave(self):
         # the scratch goes back to its own stream's allocator: work of others has to be done
-        if self._away:
+        ob, self._ob = self._ob, None
+        if ob is not None and _ops.release(ob):
             torch.cuda.synchronize(self.device)
 
 
@@ -156,6 +148,8 @@ class PagedKV(_Device):
         if rc:
             raise ConfKVError(rc, "confkv_paged_create failed")
         self._h = h.value
+        self._ob = _ops.make(self._h, 0, 0, self._home, heads, self.kv_heads, self.head_dim, 0, self._index,
+                             _dtype_code(self.dtype))
 
     def close(self):
         if getattr(self, "_h", None):
@@ -189,15 +183,15 @@ class PagedKV(_Device):
         if page_table.dim() != 2:
             raise ValueError("page_table: want [batch, blocks]")
         B, blocks = page_table.shape
-        s = BatchStruct(B, blocks, self._dense(page_table, _I32, (B, blocks), "page_table"),
-                        self._dense(ctx_len, _I32, (B,), "ctx_len"),
-                        self._dense(q_start, _I32, (B + 1,), "q_start"), None, 0)
-        rows = None
+        s = BatchStruct(B, blocks, self._dense(page_table, (B, blocks), "page_table"),
+                        self._dense(ctx_len, (B,), "ctx_len"),
+                        self._dense(q_start, (B + 1,), "q_start"), None, 0)
+        rows = -1
         if mask is not None:
             if mask.dim() != 2 or mask.shape[1] < 1:
                 raise ValueError("mask: want int32 [rows, words], a word per row at least")
             rows = mask.shape[0]
-            s.mask = self._dense(mask, _I32, mask.shape, "mask")
+            s.mask = self._dense(mask, mask.shape, "mask")
             s.mask_words = mask.shape[1]
         return PagedBatch(s, (page_table, ctx_len, q_start, mask), B, rows)
 
@@ -207,28 +201,7 @@ class PagedKV(_Device):
         layer `layer`, k rotated by `positions` (int32 [rows]; None: places in
         the sequence) x `inv_freq` (fp32 [rotary / 2]; None: not rotated), and
         rotates q [rows, heads, head_dim] into q_out (q itself allowed)."""
-        rows = k.shape[0]
-        shape = (rows, self.kv_heads, self.head_dim)
-        kp, ks = self._rows(k, shape, "k")
-        vp, vs = self._rows(v, shape, "v")
-        qp = op = fp = pp = None
-        qs = os_ = rotary = 0
-        if q is not None or q_out is not None:
-            if q is None or q_out is None:
-                raise ValueError("q and q_out go together")
-            shape = (rows, self.heads, self.head_dim)
-            qp, qs = self._rows(q, shape, "q")
-            op, os_ = self._rows(q_out, shape, "q_out")
-        if inv_freq is not None:
-            if inv_freq.dim() != 1:
-                raise ValueError("inv_freq: want [rotary / 2]")
-            rotary = 2 * inv_freq.shape[0]
-            fp = self._dense(inv_freq, _F32, inv_freq.shape, "inv_freq")
-        if positions is not None:
-            pp = self._dense(positions, _I32, (rows,), "positions")
-        rc = self._L.confkv_paged_append(self._h, batch._ref, layer, rows, kp, ks, vp, vs, qp, qs, op,
-                                         os_, pp, fp, rotary, 1 if interleaved else 0,
-                                         self._stream(stream))
+        rc = _ops.append(self._ob, batch._ref, layer, k, v, q, q_out, positions, inv_freq, interleaved, stream)
         if rc:
             self._check(rc)
 
@@ -236,31 +209,14 @@ class PagedKV(_Device):
         """Attention of q [rows, heads, head_dim] over layer `layer` into out
         (contiguous, same shape and type); lse fp32 [rows, heads] or None;
         scale 0: 1 / sqrt(head_dim)."""
-        rows = q.shape[0]
-        if batch.mask_rows is not None and batch.mask_rows < rows:
-            raise ValueError(f"the batch's mask has {batch.mask_rows} rows, q has {rows}")
-        shape = (rows, self.heads, self.head_dim)
-        qp, qs = self._rows(q, shape, "q")
-        op = self._dense(out, self.dtype, shape, "out")
-        lp = None if lse is None else self._dense(lse, _F32, (rows, self.heads), "lse")
-        rc = self._L.confkv_paged_attend(self._h, batch._ref, layer, rows, qp, qs, op, lp, scale,
-                                         self._stream(stream))
+        rc = _ops.attend(self._ob, batch._ref, batch.mask_rows, layer, q, out, lse, scale, stream)
         if rc:
             self._check(rc)
 
     def commit(self, page_table, ctx_len, path, path_len, new_len, stream=None):
         """Moves the accepted drafted tokens path [B, cap] (path_len [B] of them)
         behind the cached ones in every layer; new_len [B] receives ctx_len + path_len."""
-        if page_table.dim() != 2 or path.dim() != 2:
-            raise ValueError("page_table and path: want [batch, blocks] and [batch, cap]")
-        B, blocks = page_table.shape
-        cap = path.shape[1]
-        one = (B,)
-        rc = self._L.confkv_paged_commit(
-            self._h, B, blocks, self._dense(page_table, _I32, (B, blocks), "page_table"),
-            self._dense(ctx_len, _I32, one, "ctx_len"), self._dense(path, _I32, (B, cap), "path"), cap,
-            self._dense(path_len, _I32, one, "path_len"), self._dense(new_len, _I32, one, "new_len"),
-            self._stream(stream))
+        rc = _ops.commit(self._ob, page_table, ctx_len, path, path_len, new_len, stream)
         if rc:
             self._check(rc)
 
@@ -268,19 +224,7 @@ class PagedKV(_Device):
         """Reorders beams: row r of [batch x beams] takes over its parent's pages,
         the part-filled last one as a copy in tail_pages[r].  parent: int32
         [rows] or [batch, beams]."""
-        if table_in.dim() != 2:
-            raise ValueError("table_in: want [rows, blocks]")
-        n, blocks = table_in.shape
-        one = (n,)
-        if parent.dim() == 2 and parent.shape[1] == beams and parent.numel() == n:
-            pp = self._dense(parent, _I32, parent.shape, "parent")
-        else:
-            pp = self._dense(parent, _I32, one, "parent")
-        rc = self._L.confkv_paged_fork(
-            self._h, n, beams, blocks, pp, self._dense(table_in, _I32, (n, blocks), "table_in"),
-            self._dense(len_in, _I32, one, "len_in"), self._dense(tail_pages, _I32, one, "tail_pages"),
-            self._dense(table_out, _I32, (n, blocks), "table_out"), self._dense(len_out, _I32, one, "len_out"),
-            self._stream(stream))
+        rc = _ops.fork(self._ob, parent, beams, table_in, len_in, tail_pages, table_out, len_out, stream)
         if rc:
             self._check(rc)
 
@@ -292,7 +236,7 @@ class BeamSelect(_Device):
     def __init__(self, batch, beams, vocab, keep, dtype=None, device=None):
         from . import ConfKVError, ERR_INVALID_ARG
         self._L = _load()
-        self.logits_dtype = _F32 if dtype is None else dtype
+        self.logits_dtype = torch.float32 if dtype is None else dtype
         self._code = _dtype_code(self.logits_dtype)
         if self._code is None:
             raise ValueError("dtype: want float16, bfloat16 or float32")
@@ -304,8 +248,8 @@ class BeamSelect(_Device):
             device = torch.cuda.current_device()
         self._index = device if isinstance(device, int) else torch.device(device).index or 0
         self.device = torch.device("cuda", self._index)
-        self._bytes = n
-        self._ws = self._scratch(n, n)
+        ws = self._scratch(n, n)
+        self._ob = _ops.make(1, ws, n, self._home, batch, beams, vocab, keep, self._index, self._code)
 
     def __del__(self):
         try:
@@ -318,28 +262,8 @@ class BeamSelect(_Device):
         """logits [batch, beams, vocab] (rows may be strided), scores fp32
         [batch, beams]; score_out fp32, parent_out and token_out int32 [batch,
         keep]; finished bool [batch, beams]; flags_out int32 [batch, beams]."""
-        B, W, V, K = self.sizes
-        stride = V
-        if logits.dtype is not self.logits_dtype or logits.get_device() != self._index \
-                or logits.shape != (B, W, V):
-            raise ValueError(f"logits: want {self.logits_dtype} {(B, W, V)} on {self.device}, got "
-                             f"{logits.dtype} {tuple(logits.shape)} on {logits.device}")
-        if not logits.is_contiguous():
-            s = logits.stride()
-            stride = s[1] if W > 1 else s[0]
-            if s[2] != 1 or (B > 1 and s[0] != W * stride) or stride < V:
-                raise ValueError(f"logits: want evenly spaced dense rows, got strides {s}")
-        at, out = (B, W), (B, K)
-        fp = gp = None
-        if finished is not None:
-            fp = self._dense(finished, torch.uint8 if finished.dtype is torch.uint8 else torch.bool, at, "finished")
-        if flags_out is not None:
-            gp = self._dense(flags_out, _I32, at, "flags_out")
-        rc = self._L.confkv_beam_select(
-            logits.data_ptr(), self._code, stride, B, W, V, K, self._dense(scores, _F32, at, "scores"), fp,
-            pad_token, self._dense(score_out, _F32, out, "score_out"),
-            self._dense(parent_out, _I32, out, "parent_out"), self._dense(token_out, _I32, out, "token_out"),
-            gp, self._ws, self._bytes, self._index, self._stream(stream))
+        rc = _ops.select(self._ob, logits, scores, finished, pad_token, score_out, parent_out, token_out,
+                         flags_out, stream)
         if rc:
             from . import ConfKVError
             raise ConfKVError(rc, "confkv_beam_select refused its arguments" if rc == -1 else "confkv_beam_select")
