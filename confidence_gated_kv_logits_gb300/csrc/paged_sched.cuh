@@ -20,6 +20,7 @@ struct Sched {          // of one CTA: sched_warp, or for more than 32 sequences
   // the sequence in which the range starts, and where its work does
   long long seq0, head;  // head: work of one of its heads
   int b, T, ctx, len, row0;
+  int whole;             // units are not cut: each counts as 1, whatever its length
 };
 
 // 64-bit quotients of numbers that mostly fit 32 bits (a 64-bit division costs
@@ -46,6 +47,7 @@ struct WalkState {
   int first_cta, pieces;        // CTAs that hold the unit's pieces
   int unit_done;                // the walk is behind the unit's last piece
   int more;                     // there is a piece
+  int whole;                    // of Sched
 };
 
 template <int TM, int KB, int kOverhead>
@@ -97,8 +99,10 @@ struct Walk : WalkState {
     return w;
   }
 
+  __device__ __forceinline__ int cost(int t) const { return whole ? 1 : blocks(t) + kOverhead; }
   __device__ __forceinline__ void start(const Sched& s) {
     unit_done = 0;
+    whole = s.whole;
     share = s.share;
     cur = s.cur;
     end = s.end;
@@ -114,11 +118,11 @@ struct Walk : WalkState {
     mt = 0;
     if (m == 1) {
     } else if (bt.mask) {
-      const long long u = blocks(0) + kOverhead;
+      const long long u = cost(0);
       mt = static_cast<int>(quotient(cur - ustart, u));
       ustart += mt * u;
     } else {
-      for (long long u = blocks(0) + kOverhead; cur >= ustart + u; u = blocks(mt) + kOverhead) {
+      for (long long u = cost(0); cur >= ustart + u; u = cost(mt)) {
         ustart += u;
         ++mt;
       }
@@ -129,7 +133,7 @@ struct Walk : WalkState {
     for (;;) {
       if (unit_done) {
         unit_done = 0;
-        ustart += n + kOverhead;
+        ustart += whole ? 1 : n + kOverhead;
         if (++mt == m) {
           mt = 0;
           if (++h == p.Hkv) {
@@ -146,6 +150,16 @@ struct Walk : WalkState {
         return false;
       }
       n = blocks(mt);
+      if (whole) {
+        lo = 0;
+        hi = n;
+        first_cta = blockIdx.x;
+        pieces = 1;
+        ++cur;
+        unit_done = 1;
+        more = 1;
+        return true;
+      }
       const long long uend = ustart + n + kOverhead;
       const long long x1 = end < uend ? end : uend;
       const long long a = cur - ustart - kOverhead, z = x1 - ustart - kOverhead;
@@ -174,15 +188,36 @@ __device__ __forceinline__ void sched_share(Sched* s, long long all, int cta, in
 
 // Up to 32 sequences: every warp works the schedule out by itself, a lane per
 // sequence, without a barrier.
+// Where no unit has more than `uncut` blocks and each finds a CTA of its own,
+// none is cut (joining the pieces would take longer than the blocks).
 template <typename W>
-__device__ __forceinline__ Sched sched_warp(W& w, long long min_share) {
+__device__ __forceinline__ Sched sched_warp(W& w, long long min_share, int uncut) {
   const int lane = threadIdx.x & 31;
-  int flag = 0;
-  long long x = 0, head = 0;
+  int flag = 0, most = 0;
+  long long x = 0, head = 0, units = 0;
+  w.whole = 0;
   if (lane < w.bt.B) {
     w.sequence(lane, flag);
-    head = w.T > 0 ? w.head_work() : 0;
+    if (w.T > 0) {
+      head = w.head_work();
+      units = static_cast<long long>(w.m) * w.p.Hkv;
+      most = w.blocks(w.m - 1);
+    }
     x = head * w.p.Hkv;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  Sched s;
+  s.whole = 0;
+  if (most <= uncut) {
+    long long all = units;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (all <= gridDim.x) {
+      s.whole = 1;
+      min_share = 1;
+      x = units;
+      head = units ? w.m : 0;
+    }
   }
   if (flag && blockIdx.x == 0) atomicOr(w.p.err, flag);
   long long incl = x;
@@ -191,7 +226,6 @@ __device__ __forceinline__ Sched sched_warp(W& w, long long min_share) {
     const long long y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  Sched s;
   sched_share<W>(&s, __shfl_sync(0xffffffffu, incl, 31), blockIdx.x, gridDim.x, min_share);
   const unsigned in = __ballot_sync(0xffffffffu, x > 0 && s.cur >= incl - x && s.cur < incl);
   const int b = in ? __ffs(in) - 1 : 0;
@@ -260,6 +294,7 @@ __device__ __forceinline__ void sched_init(W& w, Sched* s, long long* s_scan, lo
     s->row0 = w.row0;
     s->seq0 = at;
     s->head = quotient(x, w.p.Hkv);
+    s->whole = 0;
   };
   if (cur < all) {
     if (B <= kT) {
