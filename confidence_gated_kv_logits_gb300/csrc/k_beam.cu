@@ -306,6 +306,12 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
           }
         }
       }
+    } else if (!(bm >= INFINITY)) {         // no finite logit, but perhaps a NaN (the maxima pass over it)
+      again();
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum = value(i, e) == value(i, e) ? sum : NAN;
     }
     // NaN anywhere in the slice makes its sum NaN, +inf its maximum
     if (!(sum < INFINITY) || bm == INFINITY) s_bad = 1;

@@ -669,6 +669,21 @@ def test_select_leaves_bad_rows_out(pkg):
     assert got[3].tolist() == [[N, N, N, 0], [0, 0, N, N]]
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.float16, torch.bfloat16])
+def test_select_a_nan_among_masked_tokens(pkg, dt):
+    """A NaN in a part of the vocabulary that is masked out otherwise, or wholly NaN, far from the finite logits."""
+    V = 70001
+    z = torch.full((1, 4, V), -math.inf, device=DEV)
+    z[..., :50] = torch.linspace(-1, 1, 50, device=DEV)
+    z[0, 1, V - 1] = math.nan
+    z[0, 2, 100:] = math.nan
+    z = z.to(dt)
+    scores = torch.zeros(1, 4, device=DEV)
+    got = run_select(pkg, z, scores, 6)
+    check_select(got, select_reference(z.cpu(), scores.cpu(), None, 6, 0))
+    assert got[3].tolist() == [[0, pkg.FLAG_NONFINITE, pkg.FLAG_NONFINITE, 0]]
+
+
 def test_select_strided_rows_and_replay(pkg):
     B, W, V, keep = 2, 4, 5001, 8
     wide = torch.randn(B * W, V + 13, device=DEV).to(torch.float16)
