@@ -10,16 +10,23 @@
 //
 // Best K of a block's values: the K-th largest of the threads' own maxima is
 // reached by K values at least and, on data in no particular order, by few
-// more.  Those are ranked by counting.  Should more be kept than the buffer holds (long runs of equal
-// values, or an order that follows the lanes), K rounds of a block-wide
-// maximum give the same answer.
+// more.  The 16-byte words that hold them are set aside in shared memory and
+// taken apart there by a thread per value (inside the sum's unrolled loop that
+// cost 33.5 us where it now takes 30.5: 128 rows of 201088 bf16 logits, K = 16),
+// and the values ranked by counting.  Should more be kept than the buffers hold
+// (long runs of equal values, or an order that follows the lanes), K rounds of a
+// block-wide maximum give the same answer.
+//
+// What bounds it: neither the 35 MB (5.2 us) nor the issue slots (half of the
+// SMs' active cycles) but each slice's chain (load, maximum, bound, exponentials,
+// ranking, ticket) with two CTAs per SM, and the last sequence's join behind it.
 //
 // Precision: exponentials and their sums per thread are fp32, relative to the
 // slice's maximum (the largest terms are exact); sums over threads and slices
 // are whole numbers of 2^-38 (exact in any order, and off the slow double
 // pipe); the slices' weights, lse and the candidates' scores are double, so
-// candidates of different beams are ordered to ~1e-8; scores are rounded to fp32 once, at the end.  Equal
-// scores go to the lower (beam, token).
+// candidates of different beams are ordered to ~1e-8; scores are rounded to fp32
+// once, at the end.  Equal scores go to the lower (beam, token).
 #include <cmath>
 
 #include "paged_internal.cuh"
@@ -31,6 +38,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCap = 1024;            // candidates ranked by counting
+constexpr int kWords = 512;           // words of a slice that may hold them
 constexpr int kMaxBeams = 32;
 constexpr float kL2E = 1.4426950408889634f;
 
@@ -90,12 +98,15 @@ __device__ __forceinline__ void warp_sort(T& x) {
 
 // A value that at least K of the block's values reach, from each thread's
 // largest (all threads call it, one barrier before and one behind): each warp
-// gives its T = ceil(K / 16) largest of them; the bound is the K-th largest of
-// the 16 T (K <= 32), or the smallest of the warps' T-th.  s_v: 32 values.
+// gives its T largest of them, so that there are 16 T >= K; the bound is the K-th
+// largest of these (K <= 32), or the smallest of the warps' T-th.  T = 2 from
+// K = 9 on: with K = 16 of 16 values the bound is the weakest warp's and lets
+// three times as many through (128 rows of 201088 bf16 logits, K = 16: 31.5
+// against 30.5 us).  s_v: 32 values.
 template <typename T>
 __device__ __forceinline__ T block_bound(T mine, T lowest, int K, T* s_v) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = (K + kWarps - 1) / kWarps;
+  const int per = K <= kWarps / 2 ? 1 : K <= 2 * kWarps ? 2 : (K + kWarps - 1) / kWarps;
   T x = mine, top = lowest;
   for (int t = 0; t < per; ++t) {
     top = x;
@@ -210,12 +221,14 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
   __shared__ unsigned long long s_v[kThreads];
   __shared__ Cand s_best[kWarps];
   __shared__ double s_base[kMaxBeams];
-  __shared__ int s_cnt, s_bad, s_last;
+  __shared__ int s_cnt, s_words, s_bad, s_last;
+  __shared__ uint4 s_word[kWords];
+  __shared__ int s_place[kWords];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = blockIdx.y, b = row / a.W;
   const size_t slice = static_cast<size_t>(row) * C + blockIdx.x;
-  if (tid == 0) s_cnt = s_bad = 0;
+  if (tid == 0) s_cnt = s_words = s_bad = 0;
   pdl_wait();
   pdl_trigger();
   const float score = a.scores[row];
@@ -293,16 +306,12 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
 #pragma unroll
         for (int e = 0; e < VEC; ++e) part4[e & 3] += ex2((value(i, e) - bm) * kL2E);
         sum += (part4[0] + part4[1]) + (part4[2] + part4[3]);
+        // words that hold a candidate: taken apart below, by other threads
         if (top_value(word_top(x[i])) >= bound) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float z = value(i, e);
-            if (!(z >= bound && z > -INFINITY)) continue;
-            const int at = atomicAdd(&s_cnt, 1);
-            if (at < kCap) {
-              const uint32_t v = static_cast<uint32_t>((w0 + i * kThreads + tid) * VEC - lead + e);
-              s_list[at].key = (static_cast<unsigned long long>(ordered(z)) << 32) | (0xffffffffu - v);
-            }
+          const int at = atomicAdd(&s_words, 1);
+          if (at < kWords) {
+            s_word[at] = x[i];
+            s_place[at] = i * kThreads + tid;
           }
         }
       }
@@ -321,7 +330,23 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
     const unsigned hi = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine >> 27));
     if (lane == 0) s_sum[warp] = (static_cast<unsigned long long>(hi) << 27) + lo;
     __syncthreads();
-    const int cnt = s_cnt;
+    const int words = s_words;
+    if (words <= kWords) {
+      for (int i = tid; i < words * VEC; i += kThreads) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&s_word[i / VEC]);
+        const int e = i % VEC;
+        float z;
+        if constexpr (DT == CONFKV_FP32) z = __uint_as_float(w[e]);
+        else z = elem<DT>(w[e >> 1], e & 1);
+        if (z >= bound && z > -INFINITY) {
+          const uint32_t v = static_cast<uint32_t>((w0 + s_place[i / VEC]) * VEC - lead + e);
+          const int at = atomicAdd(&s_cnt, 1);
+          if (at < kCap) s_list[at].key = (static_cast<unsigned long long>(ordered(z)) << 32) | (0xffffffffu - v);
+        }
+      }
+      __syncthreads();
+    }
+    const int cnt = words <= kWords ? s_cnt : kCap + 1;
     unsigned long long* out = cand + slice * a.K;
     if (tid == 0) {
       unsigned long long t = 0;
