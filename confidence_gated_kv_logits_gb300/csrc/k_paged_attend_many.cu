@@ -6,9 +6,12 @@
 //   O = P V (fp32, tensor memory);    out = O / sum P
 //
 // Roles of a CTA's twelve warps: two warpgroups do the softmax of a stream of
-// products each, one thread of warps 8 and 9 issues a stream's tcgen05.mma,
+// products each, warps 8 and 9 issue a stream's tcgen05.mma each (the whole warp
+// stays together and one elected lane issues, so that descriptors stay in uniform
+// registers: 544 us against 747 with a lane branched off, for the chunk below),
 // warp 10 moves K and V blocks of 128 tokens from the pages by TMA through a
-// ring of 32 KB (d = 128) or 16 KB stages.  There are two streams so that the
+// ring of 32 KB (d = 128) or 16 KB stages, warp 11 plans the CTA's pieces and
+// hands them to the others through shared memory.  There are two streams so that the
 // tensor cores work on one while the other's exponentials are taken:
 //   NQ = 2: a unit is 256 query rows, a stream takes 128 of them and all blocks;
 //   NQ = 1: a unit is 128 query rows, a stream takes every second block, and
@@ -17,9 +20,9 @@
 // A stream goes on by sub-blocks of 64 tokens with two S buffers: behind PV of
 // sub-block i comes QK of i + 2 into the same buffer, so a softmax finds its
 // next S there already.  Products of one thread complete in order: S is
-// overwritten only behind the PV that read the P in its place.  P is written over S in tensor memory (the
-// first product operand may lie there) and V is read as it lies, rows of
-// channels (MN-major), so neither is transposed.
+// overwritten only behind the PV that read the P in its place.  P is written
+// over S in tensor memory (the first product operand may lie there) and V is
+// read as it lies, rows of channels (MN-major), so neither is transposed.
 //
 // The running maximum is raised only when it grows by a factor of 2^8 or more
 // (P <= 2^8 meanwhile: exact in fp32, and fp16 P keeps more small values), so
@@ -27,13 +30,23 @@
 // cache's type.  Masks and what masked places hold: as in k_paged_attend.cu,
 // with V mended in shared memory before the product, and non-finite elements
 // added behind it to the rows that see them.
+//
+// Measured: two prompts' chunks of 2048 rows over 6144 cached tokens, 40/8 heads
+// of 128 channels, bf16, 557 us, 1079 TFLOP/s of products that count; trees of 64
+// over 8 x 8192 tokens, fp16, 147 us (320 rows a head fill 2.5 tiles of 128).
+// What bounds it is the softmax between the products: a sub-block's QK is 64 wide
+// and takes the tensor cores as long as one of 128 (its operands come from shared
+// memory), exponentials take 4 cycles a warp instruction, and each hand-over
+// between a product and a softmax costs 100 to 200 cycles.  Of a launch's cycles
+// the tensor pipe is active in 46%, the issue slots in 39%.  One stream of
+// 128-wide products with a single issuer took 577 us, streams that take turns more.
 #include "paged_attend.cuh"
 
 namespace confkv {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 384;               // three warpgroups; the last one's warps 2 and 3 only lend registers
+constexpr int kThreads = 384;               // three warpgroups
 constexpr int kSoft = 256;                  // softmax threads
 constexpr int BN = kManyBlock;
 constexpr int SB = BN / 2;                 // tokens of a sub-block
@@ -116,7 +129,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
     fence_bar_init();
     fence_async();
   }
-    if (warp == 10) {
+  if (warp == 10) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_addr(&s_tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
@@ -165,153 +178,153 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
         }
       }
     } else if (warp == 10) {
-    // ---- K and V blocks into the ring ----
-    const uint64_t once = stream_policy(), again = reuse_policy();
-    const int rows_per = p.ps < BN ? p.ps : BN;
-    const int boxes = BN / rows_per;
-    unsigned slot = 0;
-    int flag = 0;
-    bool ok = true;
-    while (ok && next_piece()) {
-      const Piece& w = s_plan[plan % kPlan];
-      const int32_t* table = a.bt.table + static_cast<size_t>(w.b) * a.bt.max_blocks;
-      // other tiles of the head read the same blocks
-      const uint64_t pol = w.T * p.g > TM ? again : once;
-      auto load = [&](const CUtensorMap* map, int blk) {
-        if (!ok) return;
-        const unsigned st = slot % ST;
-        if (slot >= ST && !bar_wait_warp(b_empty + 8 * st, (slot / ST - 1) & 1, &s_abort)) {
-          ok = false;
-          return;
-        }
-        const int j0 = blk * BN;
-        const int live = (w.len - j0 + rows_per - 1) / rows_per;     // boxes with tokens of the sequence
-        const int n = live < boxes ? live : boxes;
-        if (lane == 0) bar_expect(b_full + 8 * st, static_cast<unsigned>(n * rows_per * D * 2));
-        __syncwarp();
-        if (lane < n * (D / 64)) {
-          const int i = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
-          const int j = j0 + i * rows_per;
-          int page = table[j >> p.ps_shift];
-          if (page < 0 || page >= p.NP) {
-            flag = CONFKV_FLAG_BAD_PAGE;
-            page = 0;
+      // ---- K and V blocks into the ring ----
+      const uint64_t once = stream_policy(), again = reuse_policy();
+      const int rows_per = p.ps < BN ? p.ps : BN;
+      const int boxes = BN / rows_per;
+      unsigned slot = 0;
+      int flag = 0;
+      bool ok = true;
+      while (ok && next_piece()) {
+        const Piece& w = s_plan[plan % kPlan];
+        const int32_t* table = a.bt.table + static_cast<size_t>(w.b) * a.bt.max_blocks;
+        // other tiles of the head read the same blocks
+        const uint64_t pol = w.T * p.g > TM ? again : once;
+        auto load = [&](const CUtensorMap* map, int blk) {
+          if (!ok) return;
+          const unsigned st = slot % ST;
+          if (slot >= ST && !bar_wait_warp(b_empty + 8 * st, (slot / ST - 1) & 1, &s_abort)) {
+            ok = false;
+            return;
           }
-          const int y = (((a.layer * p.NP + page) * p.Hkv + w.h) << p.ps_shift) + (j & (p.ps - 1));
-          tma_box(ring + st * M::TILE + half * M::HALF + i * rows_per * 128, map, 64 * half, y, b_full + 8 * st, pol);
+          const int j0 = blk * BN;
+          const int live = (w.len - j0 + rows_per - 1) / rows_per;     // boxes with tokens of the sequence
+          const int n = live < boxes ? live : boxes;
+          if (lane == 0) bar_expect(b_full + 8 * st, static_cast<unsigned>(n * rows_per * D * 2));
+          __syncwarp();
+          if (lane < n * (D / 64)) {
+            const int i = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
+            const int j = j0 + i * rows_per;
+            int page = table[j >> p.ps_shift];
+            if (page < 0 || page >= p.NP) {
+              flag = CONFKV_FLAG_BAD_PAGE;
+              page = 0;
+            }
+            const int y = (((a.layer * p.NP + page) * p.Hkv + w.h) << p.ps_shift) + (j & (p.ps - 1));
+            tma_box(ring + st * M::TILE + half * M::HALF + i * rows_per * 128, map, 64 * half, y, b_full + 8 * st, pol);
+          }
+          ++slot;
+        };
+        if (NQ == 2) {
+          for (int b = w.lo; b < w.hi; ++b) {
+            load(&mk, b);
+            load(&mv, b);
+          }
+        } else {
+          load(&mk, w.lo);
+          if (w.lo + 1 < w.hi) load(&mk, w.lo + 1);
+          for (int b = w.lo; b < w.hi; ++b) {
+            load(&mv, b);
+            if (b + 2 < w.hi) load(&mk, b + 2);
+          }
         }
-        ++slot;
+        piece_done();
+      }
+      if (flag) atomicOr(p.err, flag);
+      if (!ok)                    // no copy may land after the CTA has gone
+        for (unsigned k = slot > ST ? slot - ST : 0; k < slot; ++k) bar_drain(b_full + 8 * (k % ST), (k / ST) & 1);
+    } else if (warp < 10) {
+      // ---- matrix products of one stream (the warp stays together; one elected thread issues) ----
+      constexpr uint32_t id_qk = umma_idesc(BF, 128, SB, false), id_pv = umma_idesc(BF, 128, D, true);
+      constexpr uint32_t hi = umma_hi(1024);
+      const int s = warp - 8;
+      const uint32_t ts = uniform(tmem + s * 128), to = uniform(tmem + 256 + s * 128),
+                     q_lo = uniform(umma_lo(base + (NQ == 2 ? s * M::TILE : 0), 16)), k_lo = uniform(umma_lo(ring, 16)),
+                     v_lo = uniform(umma_lo(ring, M::HALF));
+      unsigned slot0 = 0, np = 0, nq = 0, seen = 0;
+      bool ok = true;
+      // Slot k is there.  A stream waits for every slot in turn, its own or not:
+      // those before k that it has not waited for are the other stream's (NQ = 1)
+      // and are given back at once.  (Were they passed over, a stage whose earlier
+      // slot is still on its way would answer for the later one: a wait knows a
+      // phase by its parity alone.)
+      auto full = [&](unsigned k) {
+        while (ok && seen <= k) {
+          ok = bar_wait_warp(b_full + 8 * (seen % ST), (seen / ST) & 1, &s_abort);
+          if (ok && seen < k) bar_arrive_warp(b_empty + 8 * (seen % ST));
+          ++seen;
+        }
+        return ok;
       };
-      if (NQ == 2) {
-        for (int b = w.lo; b < w.hi; ++b) {
-          load(&mk, b);
-          load(&mv, b);
+      auto give_back = [&](unsigned end) {    // what is left of the piece is the other stream's
+        while (ok && seen < end) {
+          ok = bar_wait_warp(b_full + 8 * (seen % ST), (seen / ST) & 1, &s_abort);
+          if (ok) bar_arrive_warp(b_empty + 8 * (seen % ST));
+          ++seen;
         }
-      } else {
-        load(&mk, w.lo);
-        if (w.lo + 1 < w.hi) load(&mk, w.lo + 1);
-        for (int b = w.lo; b < w.hi; ++b) {
-          load(&mv, b);
-          if (b + 2 < w.hi) load(&mk, b + 2);
-        }
-      }
-      piece_done();
-    }
-    if (flag) atomicOr(p.err, flag);
-    if (!ok)                    // no copy may land after the CTA has gone
-      for (unsigned k = slot > ST ? slot - ST : 0; k < slot; ++k) bar_drain(b_full + 8 * (k % ST), (k / ST) & 1);
-  } else if (warp < 10) {
-    // ---- matrix products of one stream (the warp stays together; one elected thread issues) ----
-    constexpr uint32_t id_qk = umma_idesc(BF, 128, SB, false), id_pv = umma_idesc(BF, 128, D, true);
-    constexpr uint32_t hi = umma_hi(1024);
-    const int s = warp - 8;
-    const uint32_t ts = uniform(tmem + s * 128), to = uniform(tmem + 256 + s * 128),
-                   q_lo = uniform(umma_lo(base + (NQ == 2 ? s * M::TILE : 0), 16)), k_lo = uniform(umma_lo(ring, 16)),
-                   v_lo = uniform(umma_lo(ring, M::HALF));
-    unsigned slot0 = 0, np = 0, nq = 0, seen = 0;
-    bool ok = true;
-    // Slot k is there.  A stream waits for every slot in turn, its own or not:
-    // those before k that it has not waited for are the other stream's (NQ = 1)
-    // and are given back at once.  (Were they passed over, a stage whose earlier
-    // slot is still on its way would answer for the later one: a wait knows a
-    // phase by its parity alone.)
-    auto full = [&](unsigned k) {
-      while (ok && seen <= k) {
-        ok = bar_wait_warp(b_full + 8 * (seen % ST), (seen / ST) & 1, &s_abort);
-        if (ok && seen < k) bar_arrive_warp(b_empty + 8 * (seen % ST));
-        ++seen;
-      }
-      return ok;
-    };
-    auto give_back = [&](unsigned end) {    // what is left of the piece is the other stream's
-      while (ok && seen < end) {
-        ok = bar_wait_warp(b_full + 8 * (seen % ST), (seen / ST) & 1, &s_abort);
-        if (ok) bar_arrive_warp(b_empty + 8 * (seen % ST));
-        ++seen;
-      }
-    };
-    auto release = [&](unsigned k) { umma_commit(b_empty + 8 * (k % ST)); };
-    auto qk = [&](int i, unsigned k) {      // S of sub-block i = Q K^T, half i & 1 of K's stage
-      const uint32_t kt = uniform(k_lo + (k % ST) * (M::TILE / 16) + (i & 1) * (SB * 128 / 16));
-      const uint32_t d = uniform(ts + (i & 1) * SB);
+      };
+      auto release = [&](unsigned k) { umma_commit(b_empty + 8 * (k % ST)); };
+      auto qk = [&](int i, unsigned k) {      // S of sub-block i = Q K^T, half i & 1 of K's stage
+        const uint32_t kt = uniform(k_lo + (k % ST) * (M::TILE / 16) + (i & 1) * (SB * 128 / 16));
+        const uint32_t d = uniform(ts + (i & 1) * SB);
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        const uint32_t o = ((x >> 2) * M::HALF + (x & 3) * 32) / 16;
-        umma_ss(d, q_lo + o, hi, kt + o, hi, id_qk, x > 0);
-      }
-      umma_commit(b_s + 16 * s + 8 * (i & 1));
-      if (i & 1) release(k);
-    };
-    auto pv = [&](int i, unsigned k) {      // O += P V
-      const uint32_t vt = uniform(v_lo + (k % ST) * (M::TILE / 16) + (i & 1) * (SB * 128 / 16));
-      const uint32_t pt = uniform(ts + (i & 1) * SB);
-#pragma unroll
-      for (int x = 0; x < SB / 16; ++x) umma_ts(to, pt + x * 8, vt + x * 128, hi, id_pv, i > 0 || x > 0);
-      umma_commit(b_pv + 8 * s);
-      if (i & 1) release(k);
-    };
-    while (ok && next_piece()) {
-      const Piece& w = s_plan[plan % kPlan];
-      const int nb = w.hi - w.lo;
-      ok = bar_wait_warp(b_q, nq & 1, &s_abort);
-      ++nq;
-      if (!ok) break;
-      tc_fence_after();
-      const int mine = NQ == 2 ? nb : (nb + 1 - s) >> 1;
-      if (mine > 0) {
-        const unsigned k0 = slot0 + (NQ == 2 ? 0 : s);
-        if (!full(k0)) break;
-        qk(0, k0);
-        qk(1, k0);
-      }
-      for (int i = 0; i < 2 * mine; ++i) {
-        const unsigned v = slot0 + v_slot<NQ>(NQ == 2 ? i >> 1 : (i & ~1) + s, nb);
-        const bool more = i + 2 < 2 * mine;  // this stream's next K lies behind V
-        if (!(i & 1)) {
-          if (!full(v)) break;
-          if (more && !full(v + 1)) break;
+        for (int x = 0; x < D / 16; ++x) {
+          const uint32_t o = ((x >> 2) * M::HALF + (x & 3) * 32) / 16;
+          umma_ss(d, q_lo + o, hi, kt + o, hi, id_qk, x > 0);
         }
-        ok = bar_wait_warp(b_p + 16 * s + 8 * (i & 1), (np >> 1) & 1, &s_abort);
-        ++np;
+        umma_commit(b_s + 16 * s + 8 * (i & 1));
+        if (i & 1) release(k);
+      };
+      auto pv = [&](int i, unsigned k) {      // O += P V
+        const uint32_t vt = uniform(v_lo + (k % ST) * (M::TILE / 16) + (i & 1) * (SB * 128 / 16));
+        const uint32_t pt = uniform(ts + (i & 1) * SB);
+#pragma unroll
+        for (int x = 0; x < SB / 16; ++x) umma_ts(to, pt + x * 8, vt + x * 128, hi, id_pv, i > 0 || x > 0);
+        umma_commit(b_pv + 8 * s);
+        if (i & 1) release(k);
+      };
+      while (ok && next_piece()) {
+        const Piece& w = s_plan[plan % kPlan];
+        const int nb = w.hi - w.lo;
+        ok = bar_wait_warp(b_q, nq & 1, &s_abort);
+        ++nq;
         if (!ok) break;
         tc_fence_after();
-        pv(i, v);
-        if (more) qk(i, v + 1);
+        const int mine = NQ == 2 ? nb : (nb + 1 - s) >> 1;
+        if (mine > 0) {
+          const unsigned k0 = slot0 + (NQ == 2 ? 0 : s);
+          if (!full(k0)) break;
+          qk(0, k0);
+          qk(1, k0);
+        }
+        for (int i = 0; i < 2 * mine; ++i) {
+          const unsigned v = slot0 + v_slot<NQ>(NQ == 2 ? i >> 1 : (i & ~1) + s, nb);
+          const bool more = i + 2 < 2 * mine;  // this stream's next K lies behind V
+          if (!(i & 1)) {
+            if (!full(v)) break;
+            if (more && !full(v + 1)) break;
+          }
+          ok = bar_wait_warp(b_p + 16 * s + 8 * (i & 1), (np >> 1) & 1, &s_abort);
+          ++np;
+          if (!ok) break;
+          tc_fence_after();
+          pv(i, v);
+          if (more) qk(i, v + 1);
+        }
+        if (!ok) break;
+        umma_commit(b_o + 8 * s);             // (also where the stream has no block: it is waited for)
+        slot0 += 2 * nb;
+        give_back(slot0);
+        if (!ok) break;
+        piece_done();
       }
-      if (!ok) break;
-      umma_commit(b_o + 8 * s);             // (also where the stream has no block: it is waited for)
-      slot0 += 2 * nb;
-      give_back(slot0);
-      if (!ok) break;
-      piece_done();
+      if (!ok) {
+        // products in flight end before the CTA does
+        umma_commit(b_end + 8 * s);
+        bar_drain(b_end + 8 * s, 0);
+      }
+      __syncwarp();
     }
-    if (!ok) {
-      // products in flight end before the CTA does
-      umma_commit(b_end + 8 * s);
-      bar_drain(b_end + 8 * s, 0);
-    }
-    __syncwarp();
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
     // ---- softmax and epilogue ----

