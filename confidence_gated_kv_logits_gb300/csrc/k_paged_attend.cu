@@ -14,8 +14,11 @@
 // far below the memory's time.  Softmax statistics are fp32 per row and warp;
 // P is rounded to the cache's type (fp16 by 2^-11 of its value at most, bf16 by
 // 2^-8), which weighs as much as the output's own rounding.  Warps join through
-// shared memory, pieces of a unit that was cut (paged_sched.cuh) through the
-// handle's scratch.
+// shared memory.  A unit is spread over CTAs in one of two ways: cut into equal
+// shares (paged_sched.cuh), its pieces joined through the handle's scratch, which
+// fills the GPU whatever the lengths are; or, where all units run at once and none
+// can be long, shared by a cluster of two to eight CTAs that join it through
+// distributed shared memory (the rule and its figures: paged_api.cu).
 //
 // Long caches are bound by HBM: 32 sequences of up to 16384 tokens, 64/8 heads of
 // 64 channels (733 MB) take 121 us, 6.05 TB/s.  Short ones by the chain ctx_len ->
@@ -27,7 +30,8 @@
 // them V's rows past the end are zeroed in shared memory, and so are
 // non-finite elements (0 x NaN would reach rows that do not see them), which
 // the rows that do see them get added by hand.
-#include <cstring>
+#include <climits>
+#include <type_traits>
 
 #include "paged_attend.cuh"
 
@@ -40,9 +44,9 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
 constexpr int kRows = kFewRows;
 // Chunks of a unit that one CTA takes whole, while every unit finds a CTA of its
-// own. Cut against whole, one row: 1 x 128 tokens of 40/8 x 128 heads 11.1 against
-// 8.4 us, 8 x 700 tokens 16.7 against 13.1 us; at 1 x 1024 tokens (d 128) whole
-// units of 16 chunks a warp take 15.2 us against 12.1 cut.
+// own and no cluster shares it. Cut against whole, one row: 1 x 128 tokens of
+// 40/8 x 128 heads 11.1 against 8.4 us, 8 x 700 tokens of 12/12 x 64 13.9 against
+// 9.0; at 16 chunks a warp (1 x 1024 tokens, d 128) 12.1 against 15.2.
 constexpr int kUncut = 8 * kWarps;
 constexpr int kChunkBytes = 4 * kFewChunk;
 constexpr float kL2E = 1.4426950408889634f;
@@ -58,7 +62,9 @@ struct Few {
   static constexpr int OVER = 2 * kWarps;          // a unit's fixed cost in chunks
 };
 
-template <bool BF, int D>
+// CL > 1: the CTAs of a cluster share each of their units, which are not cut
+// otherwise, and join them through distributed shared memory.
+template <bool BF, int D, int CL>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_constant__ CUtensorMap mk,
              const __grid_constant__ CUtensorMap mv) {
@@ -69,9 +75,12 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
   __shared__ Sched s_sched;
   __shared__ WalkState s_walk;
   __shared__ long long s_scan[kWarps];
+  __shared__ float s_all[kRows][2];                 // CL > 1: the CTA's (maximum, sum) of each row
   __shared__ int s_abort, s_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int STEP = kWarps * CL;                 // a warp's next chunk
+  const int rank = CL > 1 ? blockIdx.x % CL : 0, wid = rank * kWarps + warp;
   const uint32_t ring0 = (smem_addr(s_raw) + 1023u) & ~1023u;
   const uint32_t ring = ring0 + warp * (kStages * kChunkBytes);
   const uint32_t bar = smem_addr(&s_bar[warp * kStages]);
@@ -95,7 +104,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
     if (a.bt.B > 32) {
       w.start(s_sched);
     } else {
-      const Sched sh = sched_warp(w, 2 * kWarps, kUncut);
+      const Sched sh = sched_warp(w, 2 * kWarps, CL > 1 ? -1 : kUncut, blockIdx.x / CL, gridDim.x / CL);
       w.start(sh);
     }
     w.next();
@@ -141,17 +150,17 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
         tma_box(o + F::KV, &mv, 64 * my_half, y, fb, pol);
       }
     };
-    const int first = w.lo + warp;
+    const int first = w.lo + wid;
     const unsigned turn0 = turn;
     unsigned issued = turn0;
     bool dead = false;
     int pages[kStages];
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) pages[i] = page_of(first + i * kWarps);
+    for (int i = 0; i < kStages; ++i) pages[i] = page_of(first + i * STEP);
 #pragma unroll
     for (int i = 0; i < kStages; ++i)
-      if (first + i * kWarps < w.hi) issue(first + i * kWarps, issued++, pages[i]);
-    int page_next = page_of(first + kStages * kWarps);
+      if (first + i * STEP < w.hi) issue(first + i * STEP, issued++, pages[i]);
+    int page_next = page_of(first + kStages * STEP);
 
     // the tile's query rows as A fragments (zero behind the sequence's rows)
     const int R = w.T * p.g, base = w.mt * kRows;
@@ -178,7 +187,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
       for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
     float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
 
-    for (int ci = first; ci < w.hi; ci += kWarps) {
+    for (int ci = first; ci < w.hi; ci += STEP) {
       const unsigned st = turn % kStages;
       if (!bar_wait_warp(bar + 8 * st, (turn / kStages) & 1, &s_abort)) {
         dead = true;
@@ -314,9 +323,9 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
         }
       }
       __syncwarp();           // every lane has read the stage
-      if (ci + kStages * kWarps < w.hi) {
-        issue(ci + kStages * kWarps, issued++, page_next);
-        page_next = page_of(ci + (kStages + 1) * kWarps);
+      if (ci + kStages * STEP < w.hi) {
+        issue(ci + kStages * STEP, issued++, page_next);
+        page_next = page_of(ci + (kStages + 1) * STEP);
       }
       ++turn;
     }
@@ -344,7 +353,8 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
       }
     }
     __syncthreads();
-    if (s_abort) break;       // set before the barrier or not at all
+    // set before the barrier or not at all; a cluster's CTAs leave together, below
+    if (CL == 1 && s_abort) break;
     constexpr int PER = kRows * D / kThreads;        // 16 or 8 channels of one row
     const int row = tid / (D / PER), ch0 = (tid % (D / PER)) * PER;
     const bool whole = w.pieces == 1;
@@ -370,7 +380,52 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
       }
     }
     const int rr = base + row;
-    if (whole) {
+    if constexpr (CL > 1) {
+      // the CTA's rows into its second chunk (nothing else lies there now), then
+      // each CTA joins kRows / CL of them
+      const uint32_t mine = ring0 + kChunkBytes;
+#pragma unroll
+      for (int e = 0; e < PER; e += 4)
+        asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};\n" ::"r"(mine + (row * D + ch0 + e) * 4), "f"(x[e]), "f"(x[e + 1]),
+                     "f"(x[e + 2]), "f"(x[e + 3]) : "memory");
+      if (ch0 == 0) {
+        s_all[row][0] = m;
+        s_all[row][1] = l;
+      }
+      cluster_sync();
+      bool dead_any = false;
+#pragma unroll
+      for (int i = 0; i < CL; ++i) dead_any |= ld_cluster_u32(cluster_addr(smem_addr(&s_abort), i)) != 0u;
+      const int jr = rank * (kRows / CL) + tid / (D / 4), jc = tid % (D / 4) * 4, js = base + jr;
+      if (!dead_any && tid < kRows / CL * (D / 4) && js < R) {
+        float2 ml[CL];
+        float4 v[CL];
+#pragma unroll
+        for (int i = 0; i < CL; ++i) {
+          ml[i] = ld_cluster_f2(cluster_addr(smem_addr(&s_all[jr][0]), i));
+          v[i] = ld_cluster_f4(cluster_addr(mine + (jr * D + jc) * 4, i));
+        }
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        m = -INFINITY;
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < CL; ++i) m = fmaxf(m, ml[i].x);
+#pragma unroll
+        for (int i = 0; i < CL; ++i) {
+          if (ml[i].x == -INFINITY) continue;
+          const float f = ex2f((ml[i].x - m) * c);
+          l = fmaf(f, ml[i].y, l);
+          y[0] = fmaf(f, v[i].x, y[0]);
+          y[1] = fmaf(f, v[i].y, y[1]);
+          y[2] = fmaf(f, v[i].z, y[2]);
+          y[3] = fmaf(f, v[i].w, y[3]);
+        }
+        const int t = js / p.g;
+        store_row<BF, 4>(a, p, w.row0 + t, h * p.g + js - t * p.g, jc, y, m, l);
+      }
+      cluster_sync();         // nobody leaves or goes on while its rows are read
+      if (dead_any) break;
+    } else if (whole) {
       if (rr < R) {
         const int t = rr / p.g;
         store_row<BF, PER>(a, p, w.row0 + t, h * p.g + rr - t * p.g, ch0, x, m, l);
@@ -462,28 +517,66 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
   if (s_abort && tid == 0) atomicOr(p.err, CONFKV_FLAG_TIMEOUT);
 }
 
+// f of every instance, until one fails
+template <typename F>
+cudaError_t each_few(F&& f) {
+  cudaError_t e = cudaSuccess;
+  auto of = [&](auto bf, auto d) {
+    auto one = [&](auto cl) {
+      if (e == cudaSuccess) e = f(bf, d, cl, k_attend_few<decltype(bf)::value, decltype(d)::value, decltype(cl)::value>);
+    };
+    one(std::integral_constant<int, 1>{});
+    one(std::integral_constant<int, 2>{});
+    one(std::integral_constant<int, 4>{});
+    one(std::integral_constant<int, 8>{});
+  };
+  of(std::false_type{}, std::integral_constant<int, 64>{});
+  of(std::false_type{}, std::integral_constant<int, 128>{});
+  of(std::true_type{}, std::integral_constant<int, 64>{});
+  of(std::true_type{}, std::integral_constant<int, 128>{});
+  return e;
+}
+
 }  // namespace
 
 cudaError_t launch_attend_few(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
-                              int ctas, cudaStream_t s) {
+                              int ctas, int cluster, cudaStream_t s) {
   const size_t smem = kWarps * kStages * kChunkBytes + 1024;
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem, s, p, a, sc, m.k_few, m.v_few);
-  };
-  cudaError_t e;
-  if (p.bf16) e = p.d == 128 ? go(k_attend_few<true, 128>) : go(k_attend_few<true, 64>);
-  else e = p.d == 128 ? go(k_attend_few<false, 128>) : go(k_attend_few<false, 64>);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return each_few([&](auto bf, auto d, auto cl, auto kernel) {
+    if (bf != p.bf16 || d != p.d || cl != cluster) return cudaSuccess;
+    cudaError_t e;
+    if (cl > 1) e = launch_pdl_cluster(kernel, dim3(ctas), dim3(kThreads), cl, smem, s, p, a, sc, m.k_few, m.v_few);
+    else e = launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem, s, p, a, sc, m.k_few, m.v_few);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  });
+}
+
+cudaError_t few_clusters(int size, int* fit) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kWarps * kStages * kChunkBytes + 1024;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = size;
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  *fit = INT_MAX;
+  return each_few([&](auto, auto, auto cl, auto kernel) {
+    int n = INT_MAX;
+    const cudaError_t e = cl == size ? cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) : cudaSuccess;
+    *fit = n < *fit ? n : *fit;
+    return e;
+  });
 }
 
 cudaError_t setup_attend_few() {
-  const int smem = kWarps * kStages * kChunkBytes + 1024;
-  for (const void* k : {reinterpret_cast<const void*>(k_attend_few<true, 128>), reinterpret_cast<const void*>(k_attend_few<true, 64>),
-                        reinterpret_cast<const void*>(k_attend_few<false, 128>), reinterpret_cast<const void*>(k_attend_few<false, 64>)}) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  return each_few([](auto, auto, auto, auto kernel) {
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kWarps * kStages * kChunkBytes + 1024);
+  });
 }
 
 }  // namespace paged

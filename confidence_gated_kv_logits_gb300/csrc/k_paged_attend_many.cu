@@ -164,7 +164,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
       // ---- the plan ----
       Walk<TM, BN, kOver> w(p, a.bt, a.rows);
       if (a.bt.B <= 32) {
-        const Sched sh = sched_warp(w, 4, 0);
+        const Sched sh = sched_warp(w, 4, 0, blockIdx.x, gridDim.x);
         w.start(sh);
       } else {
         w.start(s_sched);

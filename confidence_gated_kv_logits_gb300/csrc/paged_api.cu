@@ -46,13 +46,17 @@ bool rows_overlap(const void* a, int64_t sa, int64_t wa, const void* b, int64_t 
   return d < 2 * wa || d + 2 * wb > step;
 }
 
+struct Limits {         // what a device runs at once: CTAs of the big kernels, clusters of two, four and eight
+  int sms, clusters2, clusters4, clusters8;
+};
+
 }  // namespace
 
 struct confkv_paged {
   Pool pool{};
   AttendMaps maps;
   Scratch scratch{};
-  int sms = 0;
+  Limits limits = {};
   int device = 0;
   const char* msg = "ok";     // static texts only: no allocation, so nothing can throw
 };
@@ -112,24 +116,46 @@ cudaError_t encode_maps(const Pool& p, AttendMaps* m) {
   return cudaSuccess;
 }
 
-// The device's SM count and, the first time, the kernels' shared-memory limits
-// (function attributes hold per device).
-cudaError_t device_ready(int dev, int* sms) {
+// What the device runs at once and, the first time, the kernels' shared-memory
+// limits (function attributes hold per device).
+cudaError_t device_ready(int dev, Limits* limits) {
   constexpr int kDevices = 64;
   static std::mutex mu;
-  static int known[kDevices] = {};
+  static Limits known[kDevices] = {};
   std::lock_guard<std::mutex> lock(mu);
   if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
-  if (!known[dev]) {
-    int n = 0;
-    cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (!known[dev].sms) {
+    Limits n = {};
+    cudaError_t e = cudaDeviceGetAttribute(&n.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = setup_attend_few();
     if (e == cudaSuccess) e = setup_attend_many();
+    if (e == cudaSuccess) e = few_clusters(2, &n.clusters2);
+    if (e == cudaSuccess) e = few_clusters(4, &n.clusters4);
+    if (e == cudaSuccess) e = few_clusters(8, &n.clusters8);
     if (e != cudaSuccess) return e;
     known[dev] = n;
   }
-  *sms = known[dev];
+  *limits = known[dev];
   return cudaSuccess;
+}
+
+// CTAs that share a unit of the few rows' kernel as a cluster, or 1 to cut the
+// units into equal shares. A cluster joins its pieces in 1 us where tickets and
+// the scratch take 3 to 4, but holds 96 of 152 SMs at worst, so it is for units
+// that all run at once and sequences that cannot be long (a table's width is
+// what the host knows): from 9 chunks (below, one CTA does) to 16 a warp.
+// One row, us, cut against clusters: 12/12 heads of 64, 1 x 512 tokens 8.5, 7.6;
+// 1 x 2048 10.6, 8.5; 1 x 16384 18.5, 16.7; 2 x 4000 13.6, 11.1; 40/8 heads of 128,
+// 1 x 1024 12.1, 9.1; 1 x 8192 19.0, 17.0; 1 x 16384 24.9, 24.9; 4 x 2000 18.3,
+// 13.3; 8 x 4000 31.6, 27.4.  More clusters than run at once (16 of eight): 2 x 1500
+// 12.9, 18.2.
+int few_cluster(const confkv_paged& kv, int batch, int64_t units, int64_t tokens) {
+  const int64_t chunks = (tokens * kv.pool.d + kFewChunk - 1) / kFewChunk;
+  if (batch > 32 || chunks <= 8) return 1;
+  if (units <= kv.limits.clusters8) return chunks <= 16 * 64 ? 8 : 1;
+  if (units <= kv.limits.clusters4) return chunks <= 16 * 32 ? 4 : 1;
+  if (units <= kv.limits.clusters2) return chunks <= 16 * 16 ? 2 : 1;
+  return 1;
 }
 
 // [flags][tickets][cut units] (zeroed by the caller) [(maximum, sum)][accumulators]: two
@@ -197,9 +223,9 @@ int confkv_paged_create(int layers, int heads, int kv_heads, int head_dim, int n
   p.ps = page_size;
   while ((1 << p.ps_shift) < page_size) ++p.ps_shift;
   p.bf16 = dtype == CONFKV_BF16;
-  cudaError_t e = device_ready(dev, &kv->sms);
+  cudaError_t e = device_ready(dev, &kv->limits);
   if (e == cudaSuccess) e = encode_maps(p, &kv->maps);
-  if (e != cudaSuccess || !tickets_fit(kv->sms) || scratch_bytes < scratch_bytes_of(kv->sms, head_dim)) {
+  if (e != cudaSuccess || !tickets_fit(kv->limits.sms) || scratch_bytes < scratch_bytes_of(kv->limits.sms, head_dim)) {
     cudaGetLastError();
     delete kv;
     return e != cudaSuccess ? CONFKV_ERR_CUDA : CONFKV_ERR_CAPACITY;
@@ -209,7 +235,7 @@ int confkv_paged_create(int layers, int heads, int kv_heads, int head_dim, int n
   kv->scratch.ticket = reinterpret_cast<unsigned int*>(at + kTicketsAt);
   kv->scratch.cut = reinterpret_cast<int4*>(at + kCutAt);
   kv->scratch.ml = reinterpret_cast<float*>(at + CONFKV_PAGED_ZEROED);
-  kv->scratch.acc = kv->scratch.ml + 2 * scratch_rows(kv->sms);
+  kv->scratch.acc = kv->scratch.ml + 2 * scratch_rows(kv->limits.sms);
   *out = kv;
   return CONFKV_OK;
 }
@@ -300,10 +326,18 @@ int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int l
   //    kernel of its own joins on all SMs (1 x 32768 tokens, 65 rows: 58 joined by the
   //    last CTA of each unit, 42)
   const int64_t heads = static_cast<int64_t>(rows) * p.g, per = heads / batch->batch;
-  if (per <= kFewRows) return launched(kv, launch_attend_few(p, a, kv->scratch, kv->maps, kFewCtasPerSm * kv->sms, st));
+  if (per <= kFewRows) {
+    // at most (a row's heads fill one tile, or its sequence's last is part-filled)
+    const int64_t units = p.Hkv * std::min<int64_t>(static_cast<int64_t>(rows) * ((p.g + kFewRows - 1) / kFewRows),
+                                                    heads / kFewRows + batch->batch);
+    const int cl = few_cluster(*kv, batch->batch, units, static_cast<int64_t>(batch->max_blocks) * p.ps);
+    const int ctas = cl > 1 ? cl * static_cast<int>(units) : kFewCtasPerSm * kv->limits.sms;
+    return launched(kv, launch_attend_few(p, a, kv->scratch, kv->maps, ctas, cl, st));
+  }
+  const int sms = kv->limits.sms;
   const int64_t ones = p.Hkv * (heads / 128 + batch->batch), twos = p.Hkv * (heads / kManyRows + batch->batch);
-  const bool two = per > kManyRows && 2 * twos >= kv->sms;
-  return launched(kv, launch_attend_many(p, a, kv->scratch, kv->maps, kv->sms, two, !two && 4 * ones <= kv->sms, st));
+  const bool two = per > kManyRows && 2 * twos >= sms;
+  return launched(kv, launch_attend_many(p, a, kv->scratch, kv->maps, sms, two, !two && 4 * ones <= sms, st));
 }
 
 int confkv_paged_commit(confkv_paged* kv, int batch, int max_blocks, const int32_t* page_table,

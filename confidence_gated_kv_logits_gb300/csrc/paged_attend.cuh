@@ -22,10 +22,11 @@ constexpr int kManyBlock = 128;        // tokens of a block
 constexpr int kFewCtasPerSm = 1;
 
 cudaError_t launch_attend_few(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
-                              int ctas, cudaStream_t s);
+                              int ctas, int cluster, cudaStream_t s);
 cudaError_t launch_attend_many(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
                                int ctas, bool two_tiles, bool defer, cudaStream_t s);
 cudaError_t setup_attend_few();
+cudaError_t few_clusters(int size, int* fit);       // clusters of `size` CTAs that run at once
 cudaError_t setup_attend_many();
 
 // 0xffff in each half of a word whose element is NaN or infinite

@@ -189,9 +189,11 @@ __device__ __forceinline__ void sched_share(Sched* s, long long all, int cta, in
 // Up to 32 sequences: every warp works the schedule out by itself, a lane per
 // sequence, without a barrier.
 // Where no unit has more than `uncut` blocks and each finds a CTA of its own,
-// none is cut (joining the pieces would take longer than the blocks).
+// none is cut (joining the pieces would take longer than the blocks); nor is
+// any where uncut < 0.  (cta, ctas: a cluster and the clusters, if those share
+// a unit.)
 template <typename W>
-__device__ __forceinline__ Sched sched_warp(W& w, long long min_share, int uncut) {
+__device__ __forceinline__ Sched sched_warp(W& w, long long min_share, int uncut, int cta, int ctas) {
   const int lane = threadIdx.x & 31;
   int flag = 0, most = 0;
   long long x = 0, head = 0, units = 0;
@@ -208,11 +210,11 @@ __device__ __forceinline__ Sched sched_warp(W& w, long long min_share, int uncut
   most = __reduce_max_sync(0xffffffffu, most);
   Sched s;
   s.whole = 0;
-  if (most <= uncut) {
+  if (uncut < 0 || most <= uncut) {
     long long all = units;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    if (all <= gridDim.x) {
+    if (uncut < 0 || all <= ctas) {
       s.whole = 1;
       min_share = 1;
       x = units;
@@ -226,7 +228,7 @@ __device__ __forceinline__ Sched sched_warp(W& w, long long min_share, int uncut
     const long long y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  sched_share<W>(&s, __shfl_sync(0xffffffffu, incl, 31), blockIdx.x, gridDim.x, min_share);
+  sched_share<W>(&s, __shfl_sync(0xffffffffu, incl, 31), cta, ctas, min_share);
   const unsigned in = __ballot_sync(0xffffffffu, x > 0 && s.cur >= incl - x && s.cur < incl);
   const int b = in ? __ffs(in) - 1 : 0;
   s.b = b;

@@ -187,6 +187,38 @@ def test_attend_ragged_causal(pkg, dt, page, heads, kv_heads, d):
     check(c, run_attend(pkg, c), reference(c))
 
 
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("heads,kv_heads,d,ctx,new", [
+    (12, 12, 64, [2047], [1]), (40, 8, 128, [1500], [3]), (16, 1, 128, [700, 0, 5000, 1], [1, 0, 1, 1]),
+    (24, 3, 64, [1033, 64, 0, 2500], [2, 2, 2, 1]), (40, 8, 128, [900, 17, 1024, 0, 333, 128, 1, 600], [1] * 8),
+    (14, 2, 64, [600] * 33, [1] * 33)])
+def test_attend_few_rows_whatever_the_tables_width(pkg, dt, heads, kv_heads, d, ctx, new, wide):
+    """How units are shared among CTAs goes by how long a sequence can be: both ways, causal and with trees."""
+    c = Case(DT[dt], heads, kv_heads, d, 32, ctx, new, seed=len(ctx))
+    if wide:
+        c.table = torch.nn.functional.pad(c.table, (0, 4000), value=-1).contiguous()
+    first = run_attend(pkg, c)
+    check(c, first, reference(c))
+    again = run_attend(pkg, c, kv=first[2])                     # nothing depends on timing
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    bits = tree_bits(c.new, 3)
+    check(c, run_attend(pkg, c, bits), reference(c, bits=bits))
+
+
+def test_attend_few_rows_with_row_starts_that_overlap(pkg):
+    """More rows in all than the tensors have: every sequence's own are still right (here the same for both)."""
+    c = Case(torch.float16, 8, 8, 64, 16, [300, 300], [2, 2], extra_rows=0)
+    c.table[1] = c.table[0]
+    want = reference(c)
+    kv = pkg.PagedKV(c.k, c.v, c.heads)
+    out = torch.full((2, 8, 64), 7.0, dtype=c.dt, device=DEV)
+    batch = kv.batch(torch.cat([c.table[:1]] * 5), ints([300] * 5), ints([0, 2, 0, 2, 0, 2]))
+    kv.attend(1, batch, c.q[:2], out)
+    torch.cuda.synchronize()
+    assert ((out.double() - want[0][:2]).abs() <= want[2][:2]).all()
+
+
 @pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("heads,kv_heads,d", SHAPES)
 def test_attend_trees(pkg, dt, heads, kv_heads, d):
