@@ -14,11 +14,14 @@
 // The work is traffic: each row is read once and written once, 16 bytes per
 // access, one CTA per row.  What a row costs besides is a chain of small reads
 // (its sequence, length, page) before anything can be stored, so every thread
-// asks for its part of the row first and the chain runs meanwhile; the row's
-// rot / 2 sines are computed once into shared memory for all heads.
-// (4 prompts' chunks, 40 + 2 x 8 heads, d = 128, bf16, 116 MB: 30.0 us with
-// four rows per CTA and loads behind the chain, 27.1 with two items of a thread
-// in flight and 5 CTAs per SM, 25.8 with one and 8.)
+// asks for its part of the row first and the chain runs meanwhile, in the two
+// warps that take the row's sines, which lie in shared memory as the lanes read
+// them.  (4 prompts' chunks, 40 + 2 x 8 heads, d = 128, bf16, 116 MB, 17.1 us at
+// the copy rate: 30.0 us with four rows per CTA and loads behind the chain, 25.8
+// with one row and one item of a thread in flight, 22.0 with the sines read without
+// bank conflicts and one barrier instead of two; then 22.8 with two items in
+// flight and 5 CTAs per SM instead of 8, 23.5 with CTAs of 512 threads.  A row's
+// chain and the turnover of CTAs bound it: half of the issue slots are used.)
 #include "paged_internal.cuh"
 
 namespace confkv {
@@ -28,27 +31,33 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kU = 1;             // items of a thread in flight (8 CTAs per SM hide more than 2 items in 5)
 
+// Sines of a row: pairs 8c + 2i and 8c + 2i + 1 (cos, sin, cos, sin) at [i][c], so
+// that a warp's lanes, which have neighbouring c, read whole lines.
+constexpr int kChunks = 8;        // of 8 pairs: 64 pairs at most
+
 template <bool BF>
-__device__ __forceinline__ void rotate8(uint4& lo, uint4& hi, const float2* cs, bool interleaved) {
-  // half-split: lo = channels c .. c+7, hi = their partners, cs[0..7]
+__device__ __forceinline__ void rotate8(uint4& lo, uint4& hi, const float4* cs, bool interleaved) {
+  // half-split: lo = channels c .. c+7, hi = their partners, cs: their pairs
   // interleaved: lo, hi = 16 channels in order = pairs 0..7
   uint32_t* a = reinterpret_cast<uint32_t*>(&lo);
   uint32_t* b = reinterpret_cast<uint32_t*>(&hi);
   if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t& w = i < 4 ? a[i] : b[i - 4];
-      const float2 x = unpack2<BF>(w);
-      const float2 t = cs[i];
-      w = pack2<BF>(x.x * t.x - x.y * t.y, x.y * t.x + x.x * t.y);
+    for (int i = 0; i < 4; ++i) {
+      const float4 t = cs[i * kChunks];
+      uint32_t& w0 = i < 2 ? a[2 * i] : b[2 * i - 4];
+      uint32_t& w1 = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+      const float2 x = unpack2<BF>(w0), y = unpack2<BF>(w1);
+      w0 = pack2<BF>(x.x * t.x - x.y * t.y, x.y * t.x + x.x * t.y);
+      w1 = pack2<BF>(y.x * t.z - y.y * t.w, y.y * t.z + y.x * t.w);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const float4 t = cs[i * kChunks];
       const float2 x = unpack2<BF>(a[i]), y = unpack2<BF>(b[i]);
-      const float2 t = cs[2 * i], u = cs[2 * i + 1];
-      a[i] = pack2<BF>(x.x * t.x - y.x * t.y, x.y * u.x - y.y * u.y);
-      b[i] = pack2<BF>(y.x * t.x + x.x * t.y, y.y * u.x + x.y * u.y);
+      a[i] = pack2<BF>(x.x * t.x - y.x * t.y, x.y * t.z - y.y * t.w);
+      b[i] = pack2<BF>(y.x * t.x + x.x * t.y, y.y * t.z + x.y * t.w);
     }
   }
 }
@@ -59,19 +68,19 @@ struct Item {
   const uint16_t* src;
   int to;            // channel offset in q_out's row, or in the page of k or v: head * head stride + channel
   int second;        // channels from the first access to the second, 0: none
-  int pair;          // first of its rotated pairs
+  int chunk;         // its 8 rotated pairs
   int dst;           // 0 q_out, 1 k, 2 v, -1 none
 };
 
 template <bool BF>
 __global__ void __launch_bounds__(kThreads, 8)
 k_append(const Pool p, const AppendArgs a) {
-  __shared__ float2 s_cs[64];      // (cos, sin) per pair
+  __shared__ float4 s_cs[4 * kChunks];
   __shared__ long long s_row;      // element offset of (layer, page, head 0, slot), -1: no store
-  __shared__ int s_pos, s_live;    // position; the row belongs to a sequence
+  __shared__ int s_live;           // the row belongs to a sequence
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5;
   const int row = blockIdx.x;
   const int half = a.rot >> 1, rc = a.rot >> 4, pc = (p.d - a.rot) >> 3, vc = p.d >> 3;
   const int q0 = a.q ? p.Hq : 0, heads = q0 + p.Hkv;
@@ -84,7 +93,7 @@ k_append(const Pool p, const AppendArgs a) {
     if (j < nrot) {
       h = j / rc;
       c = j - h * rc;
-      t.pair = 8 * c;
+      t.chunk = c;
       t.second = a.interleaved ? 8 : half;
       c *= a.interleaved ? 16 : 8;
     } else if (j < nrot + nplain) {
@@ -124,7 +133,13 @@ k_append(const Pool p, const AppendArgs a) {
       }
     }
     if (j0 == tid) {               // the first time round: where the row goes, and its sines
-      if (warp == 0) {
+      if (warp < 2) {              // (64 pairs at most; both find the row's place)
+        unsigned long long F = 0;
+        if (tid < half) {
+          double turns = static_cast<double>(a.inv_freq[tid]) * 0.15915494309189535;   // 1 / (2 pi)
+          turns -= floor(turns);
+          F = static_cast<unsigned long long>(turns * 18446744073709551616.0);
+        }
         const int given = a.pos ? a.pos[row] : 0;
         const int b = sequence_of(a.bt.q_start, a.bt.B, row);
         long long off = -1;
@@ -146,28 +161,23 @@ k_append(const Pool p, const AppendArgs a) {
               if (page < 0 || page >= p.NP) flag = CONFKV_FLAG_BAD_PAGE;
               else off = ((static_cast<long long>(a.layer) * p.NP + page) * p.Hkv * p.ps + (place & (p.ps - 1))) * p.d;
             }
-            if (flag && lane == 0) atomicOr(p.err, flag);
+            if (flag && tid == 0) atomicOr(p.err, flag);
           }
         }
-        if (lane == 0) {
+        if (tid == 0) {
           s_row = off;
-          s_pos = pos;
           s_live = live;
+        }
+        if (tid < half) {
+          const unsigned long long ang = static_cast<unsigned long long>(static_cast<long long>(pos)) * F;
+          const int h = static_cast<int>((ang + 0x80000000ull) >> 32);   // fraction of a half turn, 2^-31 units
+          float2 t;
+          sincospif(static_cast<float>(h) * 4.656612873077393e-10f, &t.y, &t.x);
+          reinterpret_cast<float2*>(s_cs)[(((tid & 7) >> 1) * kChunks + (tid >> 3)) * 2 + (tid & 1)] = t;
         }
       }
       __syncthreads();
       if (!s_live) return;
-      if (tid < half) {
-        double turns = static_cast<double>(a.inv_freq[tid]) * 0.15915494309189535;   // 1 / (2 pi)
-        turns -= floor(turns);
-        const unsigned long long F = static_cast<unsigned long long>(turns * 18446744073709551616.0);
-        const unsigned long long ang = static_cast<unsigned long long>(static_cast<long long>(s_pos)) * F;
-        const int h = static_cast<int>((ang + 0x80000000ull) >> 32);   // fraction of a half turn, 2^-31 units
-        float sn, cn;
-        sincospif(static_cast<float>(h) * 4.656612873077393e-10f, &sn, &cn);
-        s_cs[tid] = make_float2(cn, sn);
-      }
-      __syncthreads();
     }
     const long long at = s_row;
 #pragma unroll
@@ -176,7 +186,7 @@ k_append(const Pool p, const AppendArgs a) {
       uint16_t* out = t[u].dst == 0 ? a.q_out + row * a.qos : (t[u].dst == 1 ? p.k : p.v) + at;
       out += t[u].to;
       if (t[u].second) {
-        rotate8<BF>(lo[u], hi[u], s_cs + t[u].pair, a.interleaved);
+        rotate8<BF>(lo[u], hi[u], s_cs + t[u].chunk, a.interleaved);
         *reinterpret_cast<uint4*>(out + t[u].second) = hi[u];
       }
       *reinterpret_cast<uint4*>(out) = lo[u];
