@@ -38,7 +38,7 @@
 // and takes the tensor cores as long as one of 128 (its operands come from shared
 // memory), exponentials take 4 cycles a warp instruction, and each hand-over
 // between a product and a softmax costs 100 to 200 cycles.  Of a launch's cycles
-// the tensor pipe is active in 46%, the issue slots in 39%.  One stream of
+// the tensor pipe is active in 44%, the issue slots in 39%.  One stream of
 // 128-wide products with a single issuer took 577 us, streams that take turns more.
 #include "paged_attend.cuh"
 
