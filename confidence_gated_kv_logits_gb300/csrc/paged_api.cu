@@ -409,10 +409,21 @@ int confkv_beam_select(const void* logits, int dtype, int64_t row_stride, int ba
       !aligned4(parent_out) || !aligned4(token_out) || !aligned4(flags_out) || !aligned16(workspace))
     return CONFKV_ERR_INVALID_ARG;
   if (workspace_bytes < beam_workspace(batch, beams, vocab, keep, dtype)) return CONFKV_ERR_CAPACITY;
-  const size_t no = static_cast<size_t>(batch) * keep * 4, ns = static_cast<size_t>(batch) * beams * 4;
-  // the scores are read until the last row is done: no output may lie in them
-  if (overlap(score_out, no, scores, ns) || overlap(parent_out, no, scores, ns) || overlap(token_out, no, scores, ns))
-    return CONFKV_ERR_INVALID_ARG;
+  // every input is read until the last row is done: no output may lie in one
+  struct Range {
+    const void* at;
+    size_t n;
+  };
+  const size_t rows = static_cast<size_t>(batch) * beams, no = static_cast<size_t>(batch) * keep * 4;
+  const Range in[] = {{scores, rows * 4}, {finished, finished ? rows : 0}, {workspace, workspace_bytes},
+                      {logits, ((rows - 1) * row_stride + vocab) * (elem + 1)}},
+              out[] = {{score_out, no}, {parent_out, no}, {token_out, no}, {flags_out, flags_out ? rows * 4 : 0}};
+  for (int i = 0; i < 4; ++i) {
+    for (const Range& r : in)
+      if (out[i].n && r.n && overlap(out[i].at, out[i].n, r.at, r.n)) return CONFKV_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (out[i].n && overlap(out[i].at, out[i].n, out[j].at, out[j].n)) return CONFKV_ERR_INVALID_ARG;
+  }
   const BeamArgs a{logits, dtype, row_stride, batch, beams, vocab, keep, scores, finished, pad_token, score_out,
                    parent_out, token_out, flags_out, workspace};
   DeviceGuard guard(device);

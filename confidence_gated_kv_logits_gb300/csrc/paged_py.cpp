@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <exception>
 #include <initializer_list>
 #include <new>
 
@@ -56,12 +57,17 @@ const at::Tensor* tensor(PyObject* o, const char* name) {
   return &THPVariable_Unpack(o);
 }
 
+// dense memory on the object's device that holds the values as they are
+bool plain(const Object* ob, const at::Tensor& t) {
+  return t.is_cuda() && t.layout() == at::kStrided && !t.is_nested() && !t.is_neg() && t.get_device() == ob->device;
+}
+
 // a contiguous tensor of the given type and shape on the object's device
 bool dense(const Object* ob, PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape,
            void** out) {
   const at::Tensor* t = tensor(o, name);
   if (!t) return false;
-  bool ok = t->scalar_type() == type && t->is_cuda() && t->get_device() == ob->device &&
+  bool ok = t->scalar_type() == type && plain(ob, *t) &&
             t->dim() == static_cast<int64_t>(shape.size()) && t->is_contiguous();
   if (ok) {
     int i = 0;
@@ -77,7 +83,7 @@ bool rows_of(const Object* ob, PyObject* o, const char* name, int64_t rows, int6
   const at::Tensor* t = tensor(o, name);
   if (!t) return false;
   const int64_t d = ob->sizes[2];
-  if (t->scalar_type() != type_of(ob->dtype) || !t->is_cuda() || t->get_device() != ob->device || t->dim() != 3 ||
+  if (t->scalar_type() != type_of(ob->dtype) || !plain(ob, *t) || t->dim() != 3 ||
       t->size(0) != rows || t->size(1) != heads || t->size(2) != d || t->stride(2) != 1 ||
       (heads > 1 && t->stride(1) != d))
     return wrong(name, "[rows, heads, head_dim] of the cache's type on its device, rows dense", o);
@@ -252,7 +258,7 @@ PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor* z = tensor(a[1], "logits");
   if (!z) return nullptr;
   int64_t stride = V;
-  bool ok = z->scalar_type() == type_of(ob->dtype) && z->is_cuda() && z->get_device() == ob->device && z->dim() == 3 &&
+  bool ok = z->scalar_type() == type_of(ob->dtype) && plain(ob, *z) && z->dim() == 3 &&
             z->size(0) == B && z->size(1) == W && z->size(2) == V;
   if (ok && !z->is_contiguous()) {
     stride = W > 1 ? z->stride(1) : z->stride(0);
@@ -307,7 +313,21 @@ PyObject* release(PyObject*, PyObject* o) {
   return PyBool_FromLong(away);
 }
 
-#define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f))
+// torch throws at tensors without plain memory (sparse, nested, meta): no exception
+// may pass a C entry.
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* safe(PyObject* self, PyObject* const* a, Py_ssize_t n) noexcept {
+  try {
+    return F(self, a, n);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (...) {
+    PyErr_SetString(PyExc_ValueError, "a tensor cannot be read");
+  }
+  return nullptr;
+}
+
+#define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(safe<f>))
 PyMethodDef kMethods[] = {{"append", FAST(append), METH_FASTCALL, nullptr},
                           {"attend", FAST(attend), METH_FASTCALL, nullptr},
                           {"commit", FAST(commit), METH_FASTCALL, nullptr},

@@ -109,8 +109,9 @@ class PagedBatch:
     """One step's ragged batch (``PagedKV.batch``).  It holds the tensors that
     it was made from; their contents are read by each call on the GPU."""
 
-    def __init__(self, struct, tensors, batch, mask_rows):
+    def __init__(self, struct, tensors, batch, mask_rows, index):
         self._struct = struct
+        self._index = index                 # of its tensors' device
         self._ref = ctypes.addressof(struct)
         self._tensors = tensors
         self.size = batch
@@ -193,7 +194,7 @@ class PagedKV(_Device):
             rows = mask.shape[0]
             s.mask = self._dense(mask, mask.shape, "mask")
             s.mask_words = mask.shape[1]
-        return PagedBatch(s, (page_table, ctx_len, q_start, mask), B, rows)
+        return PagedBatch(s, (page_table, ctx_len, q_start, mask), B, rows, self._index)
 
     def append(self, layer, batch, k, v, *, q=None, q_out=None, positions=None, inv_freq=None,
                interleaved=False, stream=None):
@@ -201,6 +202,8 @@ class PagedKV(_Device):
         layer `layer`, k rotated by `positions` (int32 [rows]; None: places in
         the sequence) x `inv_freq` (fp32 [rotary / 2]; None: not rotated), and
         rotates q [rows, heads, head_dim] into q_out (q itself allowed)."""
+        if batch._index != self._index:
+            raise ValueError("the batch's tensors are on another device")
         rc = _ops.append(self._ob, batch._ref, layer, k, v, q, q_out, positions, inv_freq, interleaved, stream)
         if rc:
             self._check(rc)
@@ -209,6 +212,8 @@ class PagedKV(_Device):
         """Attention of q [rows, heads, head_dim] over layer `layer` into out
         (contiguous, same shape and type); lse fp32 [rows, heads] or None;
         scale 0: 1 / sqrt(head_dim)."""
+        if batch._index != self._index:
+            raise ValueError("the batch's tensors are on another device")
         rc = _ops.attend(self._ob, batch._ref, batch.mask_rows, layer, q, out, lse, scale, stream)
         if rc:
             self._check(rc)

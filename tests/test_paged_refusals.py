@@ -68,3 +68,69 @@ def test_beam_refuses(pkg, bad):
 def test_beam_workspace_grows_with_its_sizes(pkg):
     n = lambda *a: pkg.load_library().confkv_beam_workspace(*a)  # noqa: E731
     assert 0 < n(1, 4, 50257, 8, 2) < n(16, 4, 50257, 8, 2) <= n(16, 4, 50257, 16, 2)
+
+
+def test_beam_outputs_may_not_overlap(pkg):
+    """flags_out, the outputs and finished against each other and against the scores."""
+    L = pkg.load_library()
+    a = BEAM
+    need = L.confkv_beam_workspace(a["batch"], a["beams"], a["vocab"], a["keep"], a["dtype"])
+
+    def call(so=a["so"], po=a["po"], to=a["to"], flags=1 << 25, finished=1 << 26):
+        return L.confkv_beam_select(a["logits"], a["dtype"], a["stride"], a["batch"], a["beams"], a["vocab"], a["keep"],
+                                    a["scores"], finished, a["pad"], so, po, to, flags, a["ws"], need, -1, None)
+
+    for bad in (dict(flags=a["scores"]), dict(flags=a["scores"] + 28), dict(flags=a["so"]), dict(flags=1 << 26),
+                dict(po=a["so"]), dict(to=a["po"] + 4), dict(finished=a["to"] + 8), dict(so=a["ws"] + 16),
+                dict(flags=a["ws"]), dict(so=a["logits"] + 64)):
+        assert call(**bad) == pkg.ERR_INVALID_ARG, bad
+
+
+def run_alone(code):
+    """In a process of its own, which an exception that crosses a C entry would end."""
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+
+
+def test_tensors_without_plain_memory_raise(pkg):
+    """Sparse, nested, quantised and other tensors that have no sizes, strides or address raise; nothing ends."""
+    run_alone("""
+import torch, pytest
+from confidence_gated_kv_logits_gb300 import _paged_ops as ops
+ob = ops.make(4096, 0, 0, 0, 2, 1, 64, 0, 0, 0)
+nested = torch.nested.nested_tensor([torch.zeros(2), torch.zeros(3)])
+three = torch.nested.nested_tensor([torch.zeros(2, 64), torch.zeros(3, 64)])
+sparse = torch.zeros(2, 3, dtype=torch.int32).to_sparse()
+meta = torch.zeros(2, 3, dtype=torch.int32, device="meta")
+i = torch.zeros(2, dtype=torch.int32)
+for t in (nested, sparse, meta, i, 3, None):
+    for call in (lambda: ops.commit(ob, t, i, t, i, i, None), lambda: ops.fork(ob, i, 2, t, i, i, t, i, None),
+                 lambda: ops.fork(ob, t, 2, meta, i, i, t, i, None), lambda: ops.append(ob, 0, 0, t, t, None, None, None, t, 0, None),
+                 lambda: ops.attend(ob, 0, -1, 0, t, t, t, 0.0, None)):
+        with pytest.raises((ValueError, RuntimeError, TypeError)):
+            call()
+for t in (three, nested, sparse, meta):
+    with pytest.raises((ValueError, RuntimeError, TypeError)):
+        ops.attend(ob, 0, -1, 0, t, t, None, 0.0, None)
+bs = ops.make(1, 4096, 1, 0, 1, 2, 3, 1, 0, 2)
+for t in (three, nested, sparse, meta):
+    with pytest.raises((ValueError, RuntimeError, TypeError)):
+        ops.select(bs, t, t, t, 0, t, t, t, t, None)
+ops.release(ob)
+ops.release(bs)
+""")
+
+
+def test_a_batch_of_another_device_is_refused(pkg):
+    from confidence_gated_kv_logits_gb300.paged import PagedBatch, PagedKV, _load
+    _load()
+    kv = PagedKV.__new__(PagedKV)
+    kv._h, kv._ob, kv._index = None, None, 0
+    from confidence_gated_kv_logits_gb300.paged import BatchStruct
+    batch = PagedBatch(BatchStruct(), (), 1, -1, 1)
+    with pytest.raises(ValueError, match="device"):
+        kv.append(0, batch, None, None)
+    with pytest.raises(ValueError, match="device"):
+        kv.attend(0, batch, None, None)
