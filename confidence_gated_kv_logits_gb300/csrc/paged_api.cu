@@ -312,6 +312,10 @@ int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int l
   if (!(scale >= 0.0f && std::isfinite(scale))) return fail(kv, CONFKV_ERR_INVALID_ARG, "scale must be finite and not negative");
   if (rows_overlap(q, q_stride, wq, out, wq, wq, rows))
     return fail(kv, CONFKV_ERR_INVALID_ARG, "out overlaps q");
+  const size_t nr = static_cast<size_t>(rows);
+  if (lse && (overlap(lse, nr * p.Hq * 4, out, nr * wq * 2) ||
+              overlap(lse, nr * p.Hq * 4, q, ((nr - 1) * q_stride + wq) * 2)))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "lse overlaps q or out");
   DeviceGuard guard(kv->device);
   AttendArgs a{batch_of(batch), layer, rows, static_cast<const uint16_t*>(q), q_stride, static_cast<uint16_t*>(out),
                lse, scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(p.d))};

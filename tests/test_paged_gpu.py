@@ -502,6 +502,40 @@ def test_append_in_place_q_and_places_as_positions(pkg):
     assert torch.equal(q[7:], c.q[7:])
 
 
+@pytest.mark.parametrize("new", [[1, 3], [40, 200]])
+def test_pages_behind_two_to_the_31_elements(pkg, new):
+    """Offsets that do not fit 32 bits: three layers of 2^30 elements each, the work in the last one."""
+    c = Case(torch.float16, 4, 2, 64, 256, [300, 1000], new, layers=3, spare=2 ** 15 - 20, seed=31)
+    assert c.k.numel() > 2 ** 31 and c.k[:2].numel() * 2 > 2 ** 31
+    kv = pkg.PagedKV(c.k, c.v, 4)
+    n = c.starts[-1]
+    k, v = c.randn(c.rows, 2, 64), c.randn(c.rows, 2, 64)
+    kv.append(2, c.batch(kv), k, v)
+    torch.cuda.synchronize()
+    assert torch.equal(torch.cat([c.get(c.k, 2, b, a + t)[a:] for b, (a, t) in enumerate(zip(c.ctx, new))]), k[:n])
+    check(c, run_attend(pkg, c, layer=2, kv=kv), reference(c, layer=2))
+    path, new_len = ints([[new[0] - 1], [new[1] - 1]]), ints([0, 0])
+    kv.commit(c.table, ints(c.ctx), path, ints([1, 1]), new_len)
+    tails = ints(c.spare[:2])
+    out, lens = torch.full_like(c.table, -1), ints([0, 0])
+    kv.fork(ints([1, 0]), 2, c.table, new_len, tails, out, lens)
+    torch.cuda.synchronize()
+    assert kv.status() == 0 and lens.tolist() == [1001, 301]
+    for b in range(2):
+        assert torch.equal(c.get(c.v, 2, b, c.ctx[b] + 1)[-1], v[c.starts[b] + new[b] - 1])
+        fill = c.ctx[b] % 256 + 1
+        assert torch.equal(c.k[2, tails[1 - b], :, :fill], c.k[2, c.table[b, c.ctx[b] // 256], :, :fill])
+
+
+def test_attend_lse_may_not_overlap(pkg):
+    c = Case(torch.float16, 8, 2, 64, 16, [5], [4], extra_rows=0)
+    kv = pkg.PagedKV(c.k, c.v, 8)
+    out = torch.empty_like(c.q)
+    for t in (out, c.q):
+        with pytest.raises(pkg.ConfKVError):
+            kv.attend(0, c.batch(kv), c.q, out, lse=t.view(torch.float32).flatten()[:32].view(4, 8))
+
+
 def test_python_refusals(pkg):
     c = Case(torch.float16, 8, 2, 64, 16, [5], [4], extra_rows=0)
     kv = pkg.PagedKV(c.k, c.v, 8)
