@@ -406,57 +406,89 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
   for (int u = 0; u < kHeld; ++u)
     raw[u] = tid + u * kThreads < n ? __ldcg(cand + static_cast<size_t>(b) * n + tid + u * kThreads) : 0ull;
 
-  // each beam's score minus lse (NaN: no candidates of its logits)
-  for (int w = warp; w < a.W; w += kWarps) {
+  // Each beam's score minus lse (NaN: no candidates of its logits).  The slices'
+  // sums relative to the row's maximum are whole units again, exact in any order;
+  // the slice that holds it counts as it is, so a row of one token gives exactly 0.
+  const SlicePart* pp = part + static_cast<size_t>(b) * a.W * C;
+  auto part_of = [&](int i) {
+    const ulonglong2 v = __ldcg(reinterpret_cast<const ulonglong2*>(pp + i));
+    return SlicePart{v.x, v.x ? __uint_as_float(static_cast<unsigned>(v.y)) : -INFINITY};
+  };
+  auto units = [&](const SlicePart& y, float m) {
+    return static_cast<unsigned long long>(static_cast<double>(y.sum) *
+                                           exp_neg(static_cast<double>(y.max) - static_cast<double>(m)));
+  };
+  // of beam w, whose slices' maximum and sum are given
+  auto finish = [&](int w, float m, bool bad, unsigned long long sum) {
     const int r = b * a.W + w;
-    const SlicePart* pp = part + static_cast<size_t>(r) * C;
     const float sc = a.scores[r];
     const bool done = a.finished && a.finished[r];
-    // this lane's slices, the first of them at once
-    auto part_of = [&](int c) {
-      const ulonglong2 v = __ldcg(reinterpret_cast<const ulonglong2*>(pp + c));
-      return SlicePart{v.x, v.x ? __uint_as_float(static_cast<unsigned>(v.y)) : -INFINITY};
-    };
-    SlicePart q{0ull, -INFINITY};
-    if (lane < C) q = part_of(lane);
     int flag = 0;
     double base = __longlong_as_double(0x7ff8000000000000ll);
     if (!(sc < INFINITY)) {
       flag = CONFKV_FLAG_NONFINITE;
     } else if (sc > -INFINITY && !done) {
-      float m = q.max;
-      bool bad = q.sum == ~0ull;
-      for (int c = lane + 32; c < C; c += 32) {
-        const SlicePart y = part_of(c);
+      if (bad || !(m > -INFINITY)) flag = CONFKV_FLAG_NONFINITE;
+      else base = static_cast<double>(sc) -
+                  (static_cast<double>(m) + log_ge1(static_cast<double>(sum) * (1.0 / 274877906944.0)));
+    }
+    s_base[w] = base;
+    if (a.flags_out) a.flags_out[r] = flag;
+  };
+  const int pairs = a.W * C;
+  if (pairs <= kThreads) {
+    // a thread per slice, then one per beam: few warps come to the double pipe (2
+    // results a cycle: with a warp per beam, four of them, this took a quarter of
+    // the call for 4 beams of 50257)
+    float* s_top = reinterpret_cast<float*>(s_list);
+    SlicePart q{0ull, -INFINITY};
+    if (tid < pairs) {
+      q = part_of(tid);
+      s_top[tid] = q.sum == ~0ull ? NAN : q.max;
+    }
+    __syncthreads();
+    auto top_of_beam = [&](int w, bool& bad) {
+      float m = -INFINITY;
+      for (int c = 0; c < C; ++c) {
+        const float y = s_top[w * C + c];
+        bad |= y != y;
+        m = fmaxf(m, y);
+      }
+      return m;
+    };
+    if (tid < pairs) {
+      bool bad = false;
+      const float m = top_of_beam(tid / C, bad);
+      s_v[tid] = q.sum && !bad ? units(q, m) : 0ull;
+    }
+    __syncthreads();
+    if (tid < a.W) {
+      bool bad = false;
+      const float m = top_of_beam(tid, bad);
+      unsigned long long sum = 0;
+      for (int c = 0; c < C; ++c) sum += s_v[tid * C + c];
+      finish(tid, m, bad, sum);
+    }
+  } else {
+    for (int w = warp; w < a.W; w += kWarps) {        // a warp per beam, its lanes over the slices
+      float m = -INFINITY;
+      bool bad = false;
+      for (int c = lane; c < C; c += 32) {
+        const SlicePart y = part_of(w * C + c);
         m = fmaxf(m, y.max);
         bad |= y.sum == ~0ull;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       bad = __any_sync(0xffffffffu, bad);
-      if (bad || !(m > -INFINITY)) {
-        flag = CONFKV_FLAG_NONFINITE;
-      } else {
-        // the slices' sums relative to the row's maximum, in whole units again: the
-        // slice that holds it counts as it is, so a row of one token gives exactly 0
-        auto units = [&](const SlicePart& y) {
-          return static_cast<unsigned long long>(static_cast<double>(y.sum) *
-                                                 exp_neg(static_cast<double>(y.max) - static_cast<double>(m)));
-        };
-        unsigned long long sum = q.sum ? units(q) : 0ull;
-        for (int c = lane + 32; c < C; c += 32) {
-          const SlicePart y = part_of(c);
-          if (y.sum) sum += units(y);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        base = static_cast<double>(sc) -
-               (static_cast<double>(m) + log_ge1(static_cast<double>(sum) * (1.0 / 274877906944.0)));
+      unsigned long long sum = 0;
+      for (int c = lane; c < C; c += 32) {
+        const SlicePart y = part_of(w * C + c);
+        if (y.sum && !bad) sum += units(y, m);
       }
-    }
-    if (lane == 0) {
-      s_base[w] = base;
-      if (a.flags_out) a.flags_out[r] = flag;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) finish(w, m, bad, sum);
     }
   }
   __syncthreads();
