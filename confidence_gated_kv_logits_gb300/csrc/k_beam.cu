@@ -24,9 +24,9 @@
 // Precision: exponentials and their sums per thread are fp32, relative to the
 // slice's maximum (the largest terms are exact); sums over threads and slices
 // are whole numbers of 2^-38 (exact in any order, and off the slow double
-// pipe); the slices' weights, lse and the candidates' scores are double, so
-// candidates of different beams are ordered to ~1e-8; scores are rounded to fp32
-// once, at the end.  Equal scores go to the lower (beam, token).
+// pipe); the slices' weights and lse are 64-bit whole numbers and double, the
+// candidates' scores double, so candidates of different beams are ordered to ~1e-8;
+// scores are rounded to fp32 once, at the end.  Equal scores go to the lower (beam, token).
 #include <cmath>
 
 #include "paged_internal.cuh"
@@ -133,13 +133,13 @@ __device__ __forceinline__ T block_bound(T mine, T lowest, int K, T* s_v) {
 // second best of the warps' (K / 2)-th), for values that are each the best of
 // somewhere, so that the looser bound would keep most of them: the warps'
 // sorted lanes merged pairwise.  s_v: 32 values per warp.
-__device__ __forceinline__ unsigned long long block_bound_tight(unsigned long long x, int K, unsigned long long* s_v) {
+__device__ __forceinline__ uint32_t block_bound_tight(uint32_t x, int K, uint32_t* s_v) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   warp_sort(x);
   s_v[warp * 32 + lane] = x;
   __syncthreads();
   if (K > 32) {
-    unsigned long long w = s_v[(lane & (kWarps - 1)) * 32 + ((K + 1) >> 1) - 1];    // each warp's bound twice
+    uint32_t w = s_v[(lane & (kWarps - 1)) * 32 + ((K + 1) >> 1) - 1];    // each warp's bound twice
     warp_sort(w);
     return __shfl_sync(0xffffffffu, w, 2);
   }
@@ -147,11 +147,11 @@ __device__ __forceinline__ unsigned long long block_bound_tight(unsigned long lo
   for (int step = kWarps / 2; step > 0; step >>= 1) {
     if (warp < step) {
       // the larger of a falling and a rising list: the 32 largest, bitonic
-      const unsigned long long y = s_v[(warp + step) * 32 + 31 - lane];
+      const uint32_t y = s_v[(warp + step) * 32 + 31 - lane];
       x = x > y ? x : y;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) {
-        const unsigned long long z = __shfl_xor_sync(0xffffffffu, x, d);
+        const uint32_t z = __shfl_xor_sync(0xffffffffu, x, d);
         x = (lane & d) == 0 ? (x > z ? x : z) : (x < z ? x : z);
       }
       s_v[warp * 32 + lane] = x;
@@ -161,27 +161,54 @@ __device__ __forceinline__ unsigned long long block_bound_tight(unsigned long lo
   return s_v[K - 1];
 }
 
-// e^x for x <= 0 in double, to a few 1e-15: x = n ln 2 + r and r's Taylor
-// series, summed pairwise (the double pipe is slow: few dependent steps)
-__device__ __forceinline__ double exp_neg(double x) {
-  if (x < -700.0) return 0.0;
-  const double n = rint(x * 1.4426950408889634);
-  // ln 2 as a 32-bit fraction and the rest, so that n times the first is exact
-  constexpr double kLn2Head = 2977044472.0 / 4294967296.0, kLn2Rest = -4.2009150726810846e-11;
-  const double r = fma(-n, kLn2Rest, fma(-n, kLn2Head, x));
-  const double r2 = r * r, r4 = r2 * r2;
-  const double a = fma(r, 1.0, 1.0), b = fma(r, 1.0 / 6, 0.5), c = fma(r, 1.0 / 120, 1.0 / 24),
-               d = fma(r, 1.0 / 5040, 1.0 / 720), e = fma(r, 1.0 / 362880, 1.0 / 40320),
-               f = fma(r, 1.0 / 39916800, 1.0 / 3628800);
-  const double p = fma(r2, b, a), q = fma(r2, d, c), s = fma(r2, f, e);
-  const double y = fma(r4, fma(r4, s, q), p);
-  return y * __longlong_as_double(static_cast<long long>(static_cast<int>(n) + 1023) << 52);
+// Powers of two in whole numbers, to a few 2^-60: the double pipe takes some 65
+// cycles per dependent step, a 64-bit product 30.
+__host__ __device__ constexpr unsigned long long inverse_factorial(int k) {      // 2^64 / k!
+  unsigned long long f = 1;
+  for (int i = 2; i <= k; ++i) f *= i;
+  return ~0ull / f;
 }
-// ln x for x >= 1: the fp32 logarithm and one Newton step on e^y = x
-__device__ __forceinline__ double log_ge1(double x) {
-  const double y = logf(static_cast<float>(x));
-  const double d = fma(x, exp_neg(-y), -1.0);
-  return y + fma(-0.5 * d, d, d);
+// 2^(f / 2^64) in units of 2^-63: e^r = 1 + r + r^2 (1/2! + r/3! + ..) with r =
+// f ln 2 < 0.7 (up to r^17 / 17!, the even and the odd terms side by side)
+__device__ __forceinline__ unsigned long long exp2_fraction(unsigned long long f) {
+  const unsigned long long r = __umul64hi(f, 12786308645202655660ull);      // ln 2 * 2^64
+  const unsigned long long r2 = __umul64hi(r, r);
+  unsigned long long even = inverse_factorial(16), odd = inverse_factorial(17);
+#pragma unroll
+  for (int k = 14; k >= 2; k -= 2) {
+    even = __umul64hi(even, r2) + inverse_factorial(k);
+    odd = __umul64hi(odd, r2) + inverse_factorial(k + 1);
+  }
+  const unsigned long long s = even + __umul64hi(odd, r);
+  return (1ull << 63) + ((r + __umul64hi(r2, s)) >> 1);
+}
+// 2^-a, 0 <= a < 1000, as fraction * 2^(n - 63)
+struct Power {
+  unsigned long long fraction;
+  int n;
+};
+__device__ __forceinline__ Power exp2_neg(double a) {
+  const long long t = -static_cast<long long>(a * 9007199254740992.0);      // 2^53
+  return Power{exp2_fraction(static_cast<unsigned long long>(t) << 11), static_cast<int>(t >> 53)};
+}
+constexpr double kLog2E = 1.4426950408889634;
+// sum * e^x, x <= 0, rounded down; sum < 2^63
+__device__ __forceinline__ unsigned long long scaled(unsigned long long sum, double x) {
+  const double a = -x * kLog2E;
+  if (!(a < 64.0)) return 0ull;
+  const Power p = exp2_neg(a);
+  return __umul64hi(sum << 1, p.fraction) >> -p.n;
+}
+// ln (sum / 2^38), sum >= 2^38: the fp32 logarithm y and one Newton step on e^y,
+// for which sum * e^-y / 2^38 - 1 is taken in whole numbers (0 for sum = 2^38)
+__device__ __forceinline__ double log_units(unsigned long long sum) {
+  const float y = logf(static_cast<float>(sum) * (1.0f / kUnits));
+  const Power p = exp2_neg(static_cast<double>(y) * kLog2E);
+  const int s = __clzll(sum), k = 37 + s - p.n;             // one lies at 2^k
+  const unsigned long long one = k < 64 ? 1ull << k : 0ull;
+  const double d = static_cast<double>(static_cast<long long>(__umul64hi(sum << s, p.fraction) - one)) *
+                   __longlong_as_double(static_cast<long long>(1023 - k) << 52);
+  return static_cast<double>(y) + fma(-0.5 * d, d, d);
 }
 
 template <int DT>
@@ -415,14 +442,11 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
     return SlicePart{v.x, v.x ? __uint_as_float(static_cast<unsigned>(v.y)) : -INFINITY};
   };
   auto units = [&](const SlicePart& y, float m) {
-    return static_cast<unsigned long long>(static_cast<double>(y.sum) *
-                                           exp_neg(static_cast<double>(y.max) - static_cast<double>(m)));
+    return scaled(y.sum, static_cast<double>(y.max) - static_cast<double>(m));
   };
   // of beam w, whose slices' maximum and sum are given
-  auto finish = [&](int w, float m, bool bad, unsigned long long sum) {
+  auto finish = [&](int w, float sc, bool done, float m, bool bad, unsigned long long sum) {
     const int r = b * a.W + w;
-    const float sc = a.scores[r];
-    const bool done = a.finished && a.finished[r];
     int flag = 0;
     double base = __longlong_as_double(0x7ff8000000000000ll);
     if (!(sc < INFINITY)) {
@@ -430,7 +454,7 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
     } else if (sc > -INFINITY && !done) {
       if (bad || !(m > -INFINITY)) flag = CONFKV_FLAG_NONFINITE;
       else base = static_cast<double>(sc) -
-                  (static_cast<double>(m) + log_ge1(static_cast<double>(sum) * (1.0 / 274877906944.0)));
+                  (static_cast<double>(m) + log_units(sum));
     }
     s_base[w] = base;
     if (a.flags_out) a.flags_out[r] = flag;
@@ -441,6 +465,8 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
     // results a cycle: with a warp per beam, four of them, this took a quarter of
     // the call for 4 beams of 50257)
     float* s_top = reinterpret_cast<float*>(s_list);
+    const float sc = tid < a.W ? a.scores[b * a.W + tid] : 0.0f;     // (asked for ahead)
+    const bool done = tid < a.W && a.finished && a.finished[b * a.W + tid];
     SlicePart q{0ull, -INFINITY};
     if (tid < pairs) {
       q = part_of(tid);
@@ -467,7 +493,7 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
       const float m = top_of_beam(tid, bad);
       unsigned long long sum = 0;
       for (int c = 0; c < C; ++c) sum += s_v[tid * C + c];
-      finish(tid, m, bad, sum);
+      finish(tid, sc, done, m, bad, sum);
     }
   } else {
     for (int w = warp; w < a.W; w += kWarps) {        // a warp per beam, its lanes over the slices
@@ -488,7 +514,8 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) finish(w, m, bad, sum);
+      const int r = b * a.W + w;
+      if (lane == 0) finish(w, a.scores[r], a.finished && a.finished[r], m, bad, sum);
     }
   }
   __syncthreads();
@@ -517,20 +544,21 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
   };
   auto fetched = [&](int i) { return candidate(i, i < n ? __ldcg(cand + static_cast<size_t>(b) * n + i) : 0ull); };
   Cand held[kHeld];
-  unsigned long long top = 0;
+  uint32_t top = 0;           // the scores' upper halves bound them well enough (and sort twice as fast)
 #pragma unroll
   for (int u = 0; u < kHeld; ++u) {
     held[u] = Cand{0, 0};
     if (tid + u * kThreads < n + a.W) held[u] = candidate(tid + u * kThreads, raw[u]);
-    top = held[u].key > top ? held[u].key : top;
-  }
-  for (int i = tid + kHeld * kThreads; i < n + a.W; i += kThreads) {
-    const unsigned long long k = fetched(i).key;
+    const uint32_t k = static_cast<uint32_t>(held[u].key >> 32);
     top = k > top ? k : top;
   }
-  const unsigned long long bound = block_bound_tight(top, a.K, s_v);
+  for (int i = tid + kHeld * kThreads; i < n + a.W; i += kThreads) {
+    const uint32_t k = static_cast<uint32_t>(fetched(i).key >> 32);
+    top = k > top ? k : top;
+  }
+  const uint32_t bound = block_bound_tight(top, a.K, reinterpret_cast<uint32_t*>(s_v));
   auto keep = [&](const Cand& c) {
-    if (c.key && c.key >= bound) {
+    if (c.key && (c.key >> 32) >= bound) {
       const int at = atomicAdd(&s_cnt, 1);
       if (at < kCap) s_list[at] = c;
     }
