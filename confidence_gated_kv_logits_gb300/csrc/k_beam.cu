@@ -65,7 +65,8 @@ __device__ __forceinline__ float unordered(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
 }
 __device__ __forceinline__ unsigned long long ordered(double x) {
-  const unsigned long long u = __double_as_longlong(x + 0.0);
+  unsigned long long u = __double_as_longlong(x);
+  u = u << 1 ? u : 0ull;
   return u ^ (static_cast<unsigned long long>(static_cast<long long>(u) >> 63) | 0x8000000000000000ull);
 }
 __device__ __forceinline__ double unordered(unsigned long long u) {
@@ -122,11 +123,19 @@ __device__ __forceinline__ T block_bound(T mine, T lowest, int K, T* s_v) {
   }
   if (K > 2 * kWarps && lane == 0) s_v[warp] = top;
   __syncthreads();
-  T y = lane < (K > 2 * kWarps ? kWarps : kWarps * per) ? s_v[lane] : lowest;
-  warp_sort(y);
-  y = __shfl_sync(0xffffffffu, y, K > 2 * kWarps ? kWarps - 1 : K - 1);
+  // the one of the wanted rank, by counting what lies before each (a sort by
+  // shuffles takes ten times as long)
+  const int values = K > 2 * kWarps ? kWarps : kWarps * per;
+  const T y = s_v[lane < values ? lane : 0];
+  int rank = lane < values ? 0 : 32;
+#pragma unroll 16
+  for (int i = 0; i < values; ++i) {
+    const T z = s_v[i];
+    rank += z > y || (z == y && i < lane) ? 1 : 0;
+  }
+  const unsigned at = __ballot_sync(0xffffffffu, rank == (K > 2 * kWarps ? kWarps : K) - 1);
   __syncthreads();
-  return y;
+  return __shfl_sync(0xffffffffu, y, at ? __ffs(at) - 1 : 0);     // (none: NaN among them, the row is left out)
 }
 
 // The K-th largest of the threads' largest itself (K <= 32; for more, the
@@ -191,6 +200,7 @@ __device__ __forceinline__ Power exp2_neg(double a) {
   const long long t = -static_cast<long long>(a * 9007199254740992.0);      // 2^53
   return Power{exp2_fraction(static_cast<unsigned long long>(t) << 11), static_cast<int>(t >> 53)};
 }
+constexpr long long kNone = 0x7ff8000000000000ll;            // a NaN: the beam has no candidates of its logits
 constexpr double kLog2E = 1.4426950408889634;
 // sum * e^x, x <= 0, rounded down; sum < 2^63
 __device__ __forceinline__ unsigned long long scaled(unsigned long long sum, double x) {
@@ -448,7 +458,7 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
   auto finish = [&](int w, float sc, bool done, float m, bool bad, unsigned long long sum) {
     const int r = b * a.W + w;
     int flag = 0;
-    double base = __longlong_as_double(0x7ff8000000000000ll);
+    double base = __longlong_as_double(kNone);
     if (!(sc < INFINITY)) {
       flag = CONFKV_FLAG_NONFINITE;
     } else if (sc > -INFINITY && !done) {
@@ -526,7 +536,7 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
     if (i < n) {
       const int w = i / per;
       const double base = s_base[w];
-      if (base == base) {
+      if (__double_as_longlong(base) != kNone) {
         if (k) {
           c.key = ordered(base + static_cast<double>(unordered(static_cast<uint32_t>(k >> 32))));
           c.tie = ~((static_cast<unsigned long long>(w) << 32) | (0xffffffffu - static_cast<uint32_t>(k)));
