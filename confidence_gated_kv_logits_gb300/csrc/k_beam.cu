@@ -11,13 +11,14 @@
 // Best K of a block's values: the K-th largest of the threads' own maxima is
 // reached by K values at least and, on data in no particular order, by few
 // more.  The 16-byte words that hold them are set aside in shared memory and
-// taken apart there by a thread per value (inside the sum's unrolled loop that
-// cost 33.5 us where it now takes 30.5: 128 rows of 201088 bf16 logits, K = 16),
-// and the values ranked by counting.  Should more be kept than the buffers hold
+// taken apart there by a thread per value (33.5 -> 30.5 us against picking them
+// up inside the sum's unrolled loop: 128 rows of 201088 bf16 logits, K = 16), and
+// the values ranked by counting.  Should more be kept than the buffers hold
 // (long runs of equal values, or an order that follows the lanes), K rounds of a
 // block-wide maximum give the same answer.
 //
-// What bounds it: neither the 35 MB (5.2 us) nor the issue slots (half of the
+// That takes 26.4 us now, 4 rows of 50257 fp32 logits 9.1.  What bounds it:
+// neither the 35 MB (5.2 us) nor the issue slots (half of the
 // SMs' active cycles) but each slice's chain (load, maximum, bound, exponentials,
 // ranking, ticket) with two CTAs per SM, and the last sequence's join behind it.
 //
@@ -424,15 +425,13 @@ k_beam_select(const BeamArgs a, int C, SlicePart* part, unsigned long long* cand
     }
   }
   // the sequence's last CTA goes on
-  __threadfence();
   __syncthreads();
   if (tid == 0) {
-    s_last = atomicAdd(&ticket[b], 1u) == static_cast<unsigned>(C * a.W - 1);
+    s_last = take_ticket(&ticket[b]) == static_cast<unsigned>(C * a.W - 1);
     s_cnt = 0;
   }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
   if (tid == 0) ticket[b] = 0u;
 
   // everything that the last stage reads is asked for at once

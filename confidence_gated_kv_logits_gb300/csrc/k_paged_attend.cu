@@ -438,10 +438,9 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
           *reinterpret_cast<float4*>(acc_at<kRows, D>(sc, at, row, ch0 + e)) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         if (ch0 == 0) *reinterpret_cast<float2*>(sc.ml + (at * kRows + row) * 2) = make_float2(m, l);
       }
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
-        s_last = atomicAdd(sc.ticket + w.first_cta, 1u) == static_cast<unsigned>(w.pieces - 1);
+        s_last = take_ticket(sc.ticket + w.first_cta) == static_cast<unsigned>(w.pieces - 1);
         if (s_last) sc.ticket[w.first_cta] = 0u;
       }
       __syncthreads();
@@ -449,7 +448,6 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
         // The pieces in their order, as many at a time as the rings hold: all of a
         // batch's words are asked for at once (a thread that walked its own words
         // through L2 one piece after another took 3 to 6 us for 9 pieces).
-        __threadfence();
         const int live = R - base < kRows ? R - base : kRows;
         const int per_piece = live * (D / 4) + live / 2 + 1;            // 16-byte words, (maximum, sum) pairs behind
         const int batch = kWarps * kStages * kChunkBytes / (16 * per_piece);

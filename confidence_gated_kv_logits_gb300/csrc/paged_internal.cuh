@@ -129,6 +129,16 @@ __device__ __forceinline__ int sequence_of(const int32_t* q_start, int B, int ro
   return __reduce_add_sync(0xffffffffu, n);
 }
 
+// Takes a ticket: behind a barrier of the CTA one thread's call orders what all of
+// its threads wrote before what the CTAs that take later tickets read (after a
+// barrier of their own).  A fence of every thread on both sides costs 0.3 to
+// 0.6 us more.
+__device__ __forceinline__ unsigned take_ticket(unsigned* ticket) {
+  unsigned n;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;\n" : "=r"(n) : "l"(ticket) : "memory");
+  return n;
+}
+
 // launch_pdl, the grid in clusters of `cluster` CTAs
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, int cluster, size_t smem, cudaStream_t s,
