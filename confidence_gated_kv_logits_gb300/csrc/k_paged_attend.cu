@@ -21,7 +21,7 @@
 // distributed shared memory (the rule and its figures: paged_api.cu).
 //
 // Long caches are bound by HBM: 32 sequences of up to 16384 tokens, 64/8 heads of
-// 64 channels (733 MB) take 121 us, 6.05 TB/s.  Short ones by the chain ctx_len ->
+// 64 channels (733 MB) take 119 us, 6.15 TB/s.  Short ones by the chain ctx_len ->
 // page number -> tile -> product -> join.  Eight warps with rings of three chunks,
 // one CTA per SM (192 KB in flight), against three CTAs of four warps with rings
 // of two: 35 against 49 us for 1 x 32768 tokens of 40/8 x 128 heads.

@@ -32,7 +32,7 @@
 // added behind it to the rows that see them.
 //
 // Measured: two prompts' chunks of 2048 rows over 6144 cached tokens, 40/8 heads
-// of 128 channels, bf16, 557 us, 1079 TFLOP/s of products that count; trees of 64
+// of 128 channels, bf16, 560 us, 1074 TFLOP/s of products that count; trees of 64
 // over 8 x 8192 tokens, fp16, 147 us (320 rows a head fill 2.5 tiles of 128).
 // What bounds it is the softmax between the products: a sub-block's QK is 64 wide
 // and takes the tensor cores as long as one of 128 (its operands come from shared

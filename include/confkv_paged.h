@@ -103,7 +103,10 @@ int confkv_paged_status(confkv_paged* kv, int32_t* flags);
  */
 typedef struct confkv_paged_batch {
   int32_t batch;               /* sequences B, 1 .. 65536 */
-  int32_t max_blocks;          /* entries of a page-table row */
+  int32_t max_blocks;          /* entries of a page-table row (a bound on the
+                                  lengths: attend shares few rows' work among
+                                  CTAs by it, so a row no wider than needed
+                                  makes short calls faster) */
   const int32_t* page_table;   /* [B][max_blocks]; entries past a sequence's
                                   last page are not read */
   const int32_t* ctx_len;      /* [B] tokens cached before the new ones (0 allowed) */
