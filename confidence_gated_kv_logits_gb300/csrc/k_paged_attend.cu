@@ -365,10 +365,10 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
     for (int e = 0; e < PER; ++e) x[e] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-      const float mi = s_ml[i][row][0];
-      if (mi == -INFINITY) continue;
-      const float f = ex2f((mi - m) * c);
-      l += f * s_ml[i][row][1];
+      const float li = s_ml[i][row][1];
+      if (li == 0.0f) continue;                       // nothing seen (scores that are all NaN leave m at -inf, l NaN)
+      const float f = ex2f((s_ml[i][row][0] - m) * c);
+      l += f * li;
       const uint32_t src = ring0 + i * (kStages * kChunkBytes) + (row * D + ch0) * 4;
 #pragma unroll
       for (int e = 0; e < PER; e += 4) {
@@ -412,7 +412,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
         for (int i = 0; i < CL; ++i) m = fmaxf(m, ml[i].x);
 #pragma unroll
         for (int i = 0; i < CL; ++i) {
-          if (ml[i].x == -INFINITY) continue;
+          if (ml[i].y == 0.0f) continue;
           const float f = ex2f((ml[i].x - m) * c);
           l = fmaf(f, ml[i].y, l);
           y[0] = fmaf(f, v[i].x, y[0]);
@@ -479,7 +479,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
             m = mn;
             for (int i = 0; i < nb; ++i) {
               const float2 ml = lds_f2(ring0 + (i * per_piece + words) * 16 + row * 8);
-              if (ml.x == -INFINITY) continue;
+              if (ml.y == 0.0f) continue;
               const float f = ex2f((ml.x - m) * c);
               l = fmaf(f, ml.y, l);
 #pragma unroll

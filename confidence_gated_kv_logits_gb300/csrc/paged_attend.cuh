@@ -75,7 +75,9 @@ __device__ __forceinline__ float* acc_at(const Scratch& sc, size_t place, int ro
 
 // N channels of one row joined over a unit's pieces, in their order (so that
 // the sum does not depend on who joins), U pieces' loads in flight: what this
-// costs is round trips to L2.  `own` >= 0: that piece is this thread's, in x
+// costs is round trips to L2.  A piece in which the row saw nothing has the sum
+// 0 and is left out; one whose scores were all NaN has the maximum -inf too, but
+// the sum NaN, which has to reach the row.  `own` >= 0: that piece is this thread's, in x
 // with maximum m and sum l, and is not read.
 template <int TM, int D, int N, int U, typename W>
 __device__ __forceinline__ void join_row(const Scratch& sc, const W& w, int row, int ch, float c, int own, float (&x)[N],
@@ -93,7 +95,6 @@ __device__ __forceinline__ void join_row(const Scratch& sc, const W& w, int row,
 #pragma unroll 8
     for (int i = 0; i < w.pieces; ++i)
       if (i != own) m = fmaxf(m, __ldcg(sc.ml + (piece_place(w, i) * TM + row) * 2));
-    if (m == -INFINITY) return;
   }
 #pragma unroll 1
   for (int i0 = 0; i0 < w.pieces; i0 += U) {
@@ -119,10 +120,10 @@ __device__ __forceinline__ void join_row(const Scratch& sc, const W& w, int row,
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u;
       if (i >= w.pieces) break;
-      const float mi = i == own ? om : ml[u].x;
-      if (mi == -INFINITY) continue;
-      const float f = ex2f((mi - m) * c);
-      l = fmaf(f, i == own ? ol : ml[u].y, l);
+      const float li = i == own ? ol : ml[u].y;
+      if (li == 0.0f) continue;
+      const float f = ex2f(((i == own ? om : ml[u].x) - m) * c);
+      l = fmaf(f, li, l);
       if (i == own) {
 #pragma unroll
         for (int e = 0; e < N; ++e) x[e] = fmaf(f, z[e], x[e]);

@@ -153,7 +153,8 @@ int confkv_paged_append(confkv_paged* kv, const confkv_paged_batch* batch, int l
  *   lse: fp32 [rows][heads] ln sum exp(scale q k), or NULL
  *   scale: 0 means 1 / sqrt(head_dim); else positive
  * A row that sees nothing (no cached token and an empty mask) gives 0 and
- * lse -inf.  What masked places and places past a sequence's end hold (NaN,
+ * lse -inf; one whose query or a key that it sees is NaN gives NaN in both.
+ * What masked places and places past a sequence's end hold (NaN,
  * infinities) does not matter.  Results do not depend on what else is in the
  * batch's other calls, and are the same on every run.
  */

@@ -1,0 +1,121 @@
+"""Paged-cache and beam operators where values or metadata are at the edge of what they take: NaN and infinities that a
+row does see, page tables that are wrong or too narrow, a workspace that calls of several sizes share.
+
+Tolerances are those of test_paged_gpu.py (stated there), here for any set of visible tokens."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from tests.test_paged_gpu import DEV, DT, U, Case, check_select, ints, mask_words, reference, run_attend, select_reference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    import confidence_gated_kv_logits_gb300 as pkg
+    pkg.load_library()
+    return pkg
+
+
+# (heads, kv_heads, d, ctx, new, widened table): how attend shares the work out
+FORMS = {
+    "few, a cluster a unit": (12, 12, 64, [2047], [1], False),
+    "few, whole units": (40, 8, 128, [50] * 4, [1] * 4, False),
+    "few, cut units": (12, 12, 64, [9000], [1], True),
+    "few, over 32 sequences": (14, 2, 64, [600] * 33, [1] * 33, False),
+    "many, joined on all SMs": (40, 8, 128, [1500, 0], [13, 9], False),
+    "many, joined by the last piece": (8, 2, 64, [40] * 60, [20] * 60, False),
+    "many, tile pairs": (40, 8, 128, [300] * 5, [400] * 5, False),
+}
+
+
+def case_of(name, dt, seed=1, **kw):
+    heads, kv_heads, d, ctx, new, wide = FORMS[name]
+    c = Case(dt, heads, kv_heads, d, 32, ctx, new, seed=seed, **kw)
+    if wide:
+        c.table = torch.nn.functional.pad(c.table, (0, 4000), value=-1).contiguous()
+    return c
+
+
+def exact(c, vis, layer=1):
+    """out, lse and their tolerances (test_paged_gpu.py's) with vis[b] [t, n] the tokens that are seen; a sequence's
+    first n tokens lie in its pages."""
+    u, g, scale = U[c.dt], c.heads // c.H, c.d ** -0.5
+    outs, lses, tols, tol_ls = [], [], [], []
+    for b, t in enumerate(c.new):
+        if not t:
+            continue
+        seen, n, at = vis[b].to(DEV), vis[b].shape[1], c.starts[b]
+        K, V = (x.double().nan_to_num(0, 0, 0).repeat_interleave(g, 1) for x in (c.get(c.k, layer, b, n), c.get(c.v, layer, b, n)))
+        q = c.q[at:at + t].double()
+        z = torch.einsum("thd,nhd->thn", q, K) * scale
+        z = torch.where(seen[:, None], z, -math.inf)
+        m = z.amax(2, keepdim=True)
+        p = (z - torch.where(m == -math.inf, 0, m)).exp()
+        l = p.sum(2, keepdim=True)
+        p = p / torch.where(l == 0, 1, l)
+        o, A = torch.einsum("thn,nhd->thd", p, V), torch.einsum("thn,nhd->thd", p, V.abs())
+        size = torch.where(seen[:, None], torch.einsum("thd,nhd->thn", q.abs(), K.abs()), 0).amax(2)
+        ds = (c.d + 4) * 2.0 ** -23 * scale * size
+        e = u * o.abs() + (u + 2 * ds[..., None] + n * 2.0 ** -23) * A
+        if c.dt is torch.float16:
+            e = e + n * 2.0 ** -25 * V.abs().amax()
+        lse = (m + l.log())[..., 0]
+        outs.append(o), lses.append(lse), tols.append(e)
+        tol_ls.append(ds + n * 2.0 ** -23 + 2.0 ** -22 * (1 + lse.abs()))
+    return [torch.cat(x) for x in (outs, lses, tols, tol_ls)]
+
+
+def causal(c, cap=None):
+    return [torch.ones(t, a + t, dtype=torch.bool).tril(a)[:, :cap] for a, t in zip(c.ctx, c.new)]
+
+
+def compare(c, got, want, lost=None):
+    """lost [rows, heads]: rows that have to be NaN; the others have to be within the tolerance."""
+    n = c.starts[-1]
+    out, lse = got[0][:n].double(), got[1][:n].double()
+    o, l, tol, tol_l = want
+    lost = torch.zeros(n, c.heads, dtype=torch.bool, device=DEV) if lost is None else lost
+    assert torch.isnan(out[lost]).all() and torch.isnan(lse[lost]).all()
+    assert ((out - o).abs()[~lost] <= tol[~lost]).all()
+    dead = l == -math.inf
+    assert torch.equal((lse == -math.inf)[~lost], dead[~lost])
+    live = ~lost & ~dead
+    assert ((lse - l).abs()[live] <= tol_l[live]).all()
+    assert (got[0][n:] == 7).all() and (got[1][n:] == 7).all()
+
+
+# --------------------------------------------------------------------------- NaN that a row sees
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("form", list(FORMS))
+def test_attend_a_nan_query_gives_nan(pkg, form, dt):
+    c = case_of(form, DT[dt])
+    want = reference(c)
+    n = c.starts[-1]
+    lost = torch.zeros(n, c.heads, dtype=torch.bool, device=DEV)
+    lost[0, 0] = lost[n - 1, c.heads - 1] = lost[n // 2, c.heads // 2] = True
+    q = c.q.clone()
+    q[:n][lost] = torch.where(torch.arange(c.d, device=DEV) == 3, math.nan, q[:n][lost].float()).to(c.dt)
+    compare(c, run_attend(pkg, c, q=q), want, lost)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("form", list(FORMS))
+def test_attend_nan_keys_reach_every_row_that_sees_them(pkg, form, dt):
+    """Keys that are all NaN over a stretch of tokens that begins and ends with the tiles, so that some warps and pieces
+    hold nothing else and none holds both."""
+    c = case_of(form, DT[dt])
+    want = exact(c, causal(c))
+    b = 0
+    n = c.ctx[b] + c.new[b]
+    lo, hi = (n // 3 // 128 * 128, n // 2 // 128 * 128 + 128) if n > 500 else (16, 32)
+    at = torch.arange(lo, hi, device=DEV)
+    h = c.H - 1
+    c.k[:, c.table[b].long()[at // c.page], h, at % c.page] = math.nan
+    lost = torch.zeros(c.starts[-1], c.heads, dtype=torch.bool, device=DEV)
+    first = c.starts[b] + max(0, lo - c.ctx[b])             # causal: the rows from token lo on
+    lost[first:c.starts[b] + c.new[b], h * c.heads // c.H:] = True
+    compare(c, run_attend(pkg, c), want, lost)
