@@ -211,7 +211,9 @@ int run_attention(confkv_ctx* c, const __half* q, float* out, cudaStream_t s, in
                   int splits, const StepParams* fused = nullptr, bool defer_mass = false,
                   int layer_call = 0) {
   AttnParams ap{};
-  ap.q_late = layer_call != 0 ? 1 : 0;
+  // without a confidence kernel nothing has waited for q's producer before this
+  // launch starts: the selection triggers ahead of its own wait
+  ap.q_late = layer_call != 0 || !uses_confidence(c) ? 1 : 0;
   ap.early = layer_call == 2 ? 1 : 0;
   if (fused) {
     ap.k_new = fused->k_new;

@@ -48,11 +48,14 @@ __device__ __forceinline__ void l2_discard_line(const void* p) {
 // confidence kernel triggers right after its own wait and the attention after
 // its main loop; the selection and append kernels trigger at their start,
 // which is safe because the attention reads nothing but its caller's queries
-// before its wait.  The selection reads the previous step's state before its
-// own wait: its predecessor is the confidence kernel (which has waited for
-// the previous attention) or, under the WINDOW policy, the previous step's
-// attention, whose trigger comes after every read of the cache data the
-// selection moves.
+// before its wait, and those only where the confidence kernel has waited for
+// their producer (not under the WINDOW policy, nor in per-layer steps: the
+// producer may be a kernel that lets its dependents start early, as
+// confkv_paged_append does).  The selection reads the previous step's state
+// before its own wait: its predecessor is the confidence kernel (which has
+// waited for the previous attention) or, under the WINDOW policy, the previous
+// step's attention, whose trigger comes after every read of the cache data the
+// selection moves, or a kernel that has waited for that attention.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -162,12 +165,13 @@ struct AttnParams {
   int32_t* kept_count;
   // Per-layer calls: the caller's q, k_new and v_new may come from the kernel
   // right before this launch, so they are read only after the dependency
-  // wait (q_late = 1).  A layer launch that is not the step's first may also
-  // read its own layer's cache (region sizes, reserved slot, tiles) before
-  // the wait (early = 1, tensor-core TMA path): that cache is written only by
-  // the step's selection, which is complete by then -- the step's first
-  // layer launch passes its own wait (the selection done) before it
-  // triggers, and every later launch in the stream starts after that trigger.
+  // wait (q_late = 1; the same for q of whole steps without a confidence
+  // kernel).  A layer launch that is not the step's first may also read its own
+  // layer's cache (region sizes, reserved slot, tiles) before the wait (early =
+  // 1, tensor-core TMA path): that cache is written only by the step's
+  // selection, which is complete by then -- the step's first layer launch passes
+  // its own wait (the selection done) before it triggers, and every later launch
+  // in the stream starts after that trigger.
   int q_late;
   int early;
 };

@@ -544,12 +544,13 @@ k_attn_mma(Cache c, AttnParams ap, const __grid_constant__ TmaMaps tm) {
     n16 = __ldcg(c.n16 + lb);
     hn = __ldcg(c.new_slot + lb);
   } else {
-    // whole steps: q's producer precedes the step's first kernel, which waits
-    // for it before it triggers, so q is complete when this grid starts
-    if (!PL || !ap.q_late) load_q();
+    // whole steps: q's producer precedes the confidence kernel, which waits for
+    // it before it triggers, so q is complete when this grid starts (without a
+    // confidence kernel, and in per-layer steps, q is read behind the wait)
+    if (ap.q_late) pdl_wait();
+    load_q();
     // everything below reads the selection kernel's results
     pdl_wait();
-    if (PL && ap.q_late) load_q();
     scale_q_channels();
     // Speculative first tile (TMA, one split, whole steps): warp w's first
     // chunk is chunk w, an INT8 chunk whenever the unit holds more than w INT8

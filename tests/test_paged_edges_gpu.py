@@ -119,3 +119,38 @@ def test_attend_nan_keys_reach_every_row_that_sees_them(pkg, form, dt):
     first = c.starts[b] + max(0, lo - c.ctx[b])             # causal: the rows from token lo on
     lost[first:c.starts[b] + c.new[b], h * c.heads // c.H:] = True
     compare(c, run_attend(pkg, c), want, lost)
+
+
+# --------------------------------------------------------------------------- with the decode step
+@pytest.mark.parametrize("tma", [0, -1])
+def test_a_window_step_takes_queries_that_append_rotated_right_before_it(pkg, tma):
+    """append(q_out=q) and a WINDOW step on q, one behind the other on a stream, give what they give with a wait
+    between them."""
+    L, B, Hq, H, d, T, page = 24, 16, 32, 8, 128, 96, 64
+    g = torch.Generator(device=DEV).manual_seed(11)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).half()  # noqa: E731
+    k, v = r(L, B, H, T, d), r(L, B, H, T, d)
+    steps = []
+    for _ in range(2):
+        s = pkg.ConfKV(L, Hq, H, d, 64, 64, 0.5, 4, 32, 0.9, batch=B, vocab=100, max_context=T, policy=pkg.POLICY_WINDOW, attn_tma=tma)
+        s.prefill(k, v, T)
+        steps.append(s)
+    rows = L * B
+    kp, vp = (torch.zeros(1, rows // page + 1, H, page, d, dtype=torch.float16, device=DEV) for _ in range(2))
+    kv = pkg.PagedKV(kp, vp, Hq)
+    batch = kv.batch(ints([list(range(rows // page + 1))]), ints([0]), ints([0, rows]))
+    inv = torch.rand(d // 2, generator=g, device=DEV)
+    q = [torch.zeros(rows, Hq, d, dtype=torch.float16, device=DEV) for _ in range(2)]
+    out = [torch.zeros(L, B, Hq, d, device=DEV) for _ in range(2)]
+    for i in range(12):
+        src, kn, vn = r(rows, Hq, d), r(rows, H, d), r(rows, H, d)
+        for j, s in enumerate(steps):
+            q[j].zero_()
+            torch.cuda.synchronize()
+            kv.append(0, batch, kn, vn, q=src, q_out=q[j], inv_freq=inv)
+            if j:
+                torch.cuda.synchronize()
+            s.step(None, q[j], kn, vn, out[j])
+            torch.cuda.synchronize()
+        assert torch.equal(q[0], q[1]) and torch.equal(out[0], out[1]), i
+    assert kv.status() == 0
