@@ -80,7 +80,21 @@ struct Piece {
 constexpr int kPlan = 8;                 // pieces in the ring
 constexpr int kReaders = 11;             // warps that read it
 
+// The softmax warps among themselves.  These barriers have no limit, so all eight
+// warps have to come: whether they go on with a piece is decided by all of them
+// together (soft_any), and what follows up to the next decision holds no wait.
+// (Did each decide by itself, one could see that another warp has given up where
+// the next still finds what it waits for and goes on to a barrier alone.)
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool mine) {
+  unsigned any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 2, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(any)
+      : "r"(static_cast<unsigned>(mine))
+      : "memory");
+  return any != 0;
+}
 
 template <bool BF, int D, int NQ>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -96,7 +110,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
   __shared__ long long s_scan[kThreads / 32];
   __shared__ float s_x[NQ == 1 ? 2 * 128 * 2 : 1];          // NQ = 1: the streams' (maximum, sum)
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_dead, s_last, s_poison;
+  __shared__ int s_abort, s_last, s_poison;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_addr(s_raw) + 1023u) & ~1023u;
@@ -125,7 +139,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
       bar_init(b_plan + 8 * i, 1);
       bar_init(b_read + 8 * i, kReaders);
     }
-    s_abort = s_dead = s_poison = 0;
+    s_abort = s_poison = 0;
     fence_bar_init();
     fence_async();
   }
@@ -335,7 +349,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
     const float c = a.scale * kL2E;
     unsigned ns = 0, no = 0, slot0 = 0;
     int4 cut = make_int4(0, 0, 0, 0);                     // the unit whose first piece this CTA ends with
-    while (next_piece()) {
+    while (!soft_any(!next_piece())) {
       const Piece& w = s_plan[plan % kPlan];
       const int nb = w.hi - w.lo;
       const int R = w.T * p.g;                           // rows of the head
@@ -506,9 +520,8 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
         s_x[(s * 128 + r) * 2 + 1] = l;
         tc_fence_before();
       }
-      if (tid == 0) s_dead = s_abort;
-      soft_sync();
-      if (s_dead) break;
+      // (a thread that gave up a wait has set s_abort itself)
+      if (soft_any(*const_cast<volatile int*>(&s_abort) != 0)) break;
       tc_fence_after();
       float w0 = 1.0f, w1 = 0.0f;                         // NQ = 1: the streams' weights
       if (NQ == 1) {
