@@ -636,10 +636,15 @@ cudaError_t launch_dt(const BeamArgs& a, int C, SlicePart* part, unsigned long l
 
 }  // namespace
 
-// [tickets: batch][parts: rows x slices][candidates: rows x slices x K]
+// [tickets][parts: rows x slices][candidates: rows x slices x K].  The tickets,
+// which every call leaves zero, have a place of their own whatever a call's
+// sizes are (one for each sequence that a call can have): calls of several sizes
+// may share a workspace.
+constexpr size_t kTicketBytes = sizeof(unsigned int) * 65536;
+
 size_t beam_workspace(int B, int W, int V, int K, int dtype) {
   const size_t n = static_cast<size_t>(B) * W * beam_slices(static_cast<long long>(B) * W, V, dtype);
-  return round256(sizeof(unsigned int) * B) + round256(sizeof(SlicePart) * n) + sizeof(unsigned long long) * n * K;
+  return kTicketBytes + round256(sizeof(SlicePart) * n) + sizeof(unsigned long long) * n * K;
 }
 
 cudaError_t launch_beam(const BeamArgs& a, cudaStream_t s) {
@@ -647,7 +652,7 @@ cudaError_t launch_beam(const BeamArgs& a, cudaStream_t s) {
   const size_t n = static_cast<size_t>(a.B) * a.W * C;
   char* w = static_cast<char*>(a.ws);
   unsigned int* ticket = reinterpret_cast<unsigned int*>(w);
-  w += round256(sizeof(unsigned int) * a.B);
+  w += kTicketBytes;
   SlicePart* part = reinterpret_cast<SlicePart*>(w);
   w += round256(sizeof(SlicePart) * n);
   unsigned long long* cand = reinterpret_cast<unsigned long long*>(w);

@@ -196,7 +196,8 @@ int confkv_paged_fork(confkv_paged* kv, int rows, int beams, int max_blocks, con
 /*
  * confkv_beam_workspace -- bytes of device scratch for confkv_beam_select (0
  * for sizes that it refuses).  The caller zeroes it once; every call leaves
- * it ready for the next.  Calls that share it must be ordered.
+ * it ready for the next, whatever sizes both have.  Calls that share it must be
+ * ordered, and it must be large enough for each.
  */
 size_t confkv_beam_workspace(int batch, int beams, int vocab, int keep, int dtype);
 

@@ -121,6 +121,26 @@ def test_attend_nan_keys_reach_every_row_that_sees_them(pkg, form, dt):
     compare(c, run_attend(pkg, c), want, lost)
 
 
+# --------------------------------------------------------------------------- one workspace for calls of several sizes
+def test_select_one_workspace_for_every_size(pkg):
+    """Zeroed once, made for the largest call, used by smaller and larger ones in turn (C ABI)."""
+    L = pkg.load_library()
+    sizes = [(3, 2, 700, 4, torch.float32), (100, 3, 500, 5, torch.float32), (3, 2, 700, 4, torch.float32), (1, 4, 50257, 8, torch.bfloat16),
+             (700, 1, 40, 3, torch.float16), (2, 32, 9000, 64, torch.float32), (100, 3, 500, 5, torch.float32)]
+    code = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+    ws = torch.zeros(max(L.confkv_beam_workspace(B, W, V, K, code[t]) for B, W, V, K, t in sizes), dtype=torch.uint8, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    for B, W, V, K, dt in sizes:
+        z = (3 * torch.randn(B, W, V, generator=g, device=DEV)).to(dt)
+        scores = -torch.rand(B, W, generator=g, device=DEV)
+        so, po, to = torch.full((B, K), 7.0, device=DEV), *(torch.full((B, K), 7, dtype=torch.int32, device=DEV) for _ in range(2))
+        rc = L.confkv_beam_select(z.data_ptr(), code[dt], V, B, W, V, K, scores.data_ptr(), None, 0, so.data_ptr(), po.data_ptr(),
+                                  to.data_ptr(), None, ws.data_ptr(), ws.numel(), -1, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        torch.cuda.synchronize()
+        assert rc == 0
+        check_select((so, po, to), select_reference(z.cpu(), scores.cpu(), None, K, 0))
+
+
 # --------------------------------------------------------------------------- with the decode step
 @pytest.mark.parametrize("tma", [0, -1])
 def test_a_window_step_takes_queries_that_append_rotated_right_before_it(pkg, tma):
