@@ -178,8 +178,8 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
         qf[k][3] = rb < R ? *reinterpret_cast<const uint32_t*>(qb + 16 * k + 8) : 0u;
       }
     }
-    // tokens that every row of the tile sees
-    const int all_seen = a.bt.mask ? w.ctx : w.ctx + base / p.g + 1;
+    // tokens that every row of the tile sees (a sequence may be longer than its table)
+    const int all_seen = a.bt.mask ? w.ctx : min(w.ctx + base / p.g + 1, w.len);
     float o[F::OT][4];
 #pragma unroll
     for (int i = 0; i < F::OT; ++i)

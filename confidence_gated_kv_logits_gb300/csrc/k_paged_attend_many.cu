@@ -378,7 +378,8 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
       const bool live = x - lane < R;                     // the warp holds rows
       const int t = x < R ? x / p.g : 0;
       const size_t row = w.row0 + t;
-      const int all_seen = a.bt.mask ? w.ctx : w.ctx + tile0 / p.g + 1;   // tokens that the whole unit sees
+      // tokens that the whole unit sees (a sequence may be longer than its table)
+      const int all_seen = a.bt.mask ? w.ctx : min(w.ctx + tile0 / p.g + 1, w.len);
       float m = -INFINITY, l = 0.0f;
       const int mine = NQ == 2 ? nb : (nb + 1 - s) >> 1;  // this stream's blocks
       for (int i = 0; i < 2 * mine; ++i) {

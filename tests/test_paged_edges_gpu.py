@@ -121,6 +121,29 @@ def test_attend_nan_keys_reach_every_row_that_sees_them(pkg, form, dt):
     compare(c, run_attend(pkg, c), want, lost)
 
 
+# --------------------------------------------------------------------------- page tables that are wrong
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("heads,kv_heads,d,ctx,new,blocks", [
+    (4, 4, 64, 30, 9, 1), (4, 4, 64, 40, 9, 3), (10, 2, 128, 20, 400, 3), (8, 1, 64, 100, 300, 9), (10, 2, 128, 90, 1500, 7),
+    (40, 8, 128, 0, 700, 5), (2, 2, 64, 500, 3, 1)])
+def test_attend_rows_past_the_page_table(pkg, heads, kv_heads, d, ctx, new, blocks, dt):
+    """A sequence longer than its table: rows see its tokens as far as the table goes, the flag says so."""
+    c = Case(DT[dt], heads, kv_heads, d, 16, [ctx, 50], [new, 2], seed=blocks)
+    cap = 16 * blocks
+    n = min(cap, ctx + new)
+    vis = [v[:, :cap] for v in causal(c)]
+    want = exact(c, vis)
+    kv = pkg.PagedKV(c.k, c.v, heads)
+    batch = kv.batch(c.table[:, :blocks].contiguous(), ints(c.ctx), ints(c.starts))
+    got = run_attend(pkg, c, kv=kv, batch=batch)
+    assert kv.status(check=False) == pkg.FLAG_CAPACITY
+    compare(c, got, want)
+    for _ in range(3):
+        again = run_attend(pkg, c, kv=kv, batch=batch)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    assert n == vis[0].shape[1] and kv.status(check=False) == pkg.FLAG_CAPACITY
+
+
 # --------------------------------------------------------------------------- one workspace for calls of several sizes
 def test_select_one_workspace_for_every_size(pkg):
     """Zeroed once, made for the largest call, used by smaller and larger ones in turn (C ABI)."""
