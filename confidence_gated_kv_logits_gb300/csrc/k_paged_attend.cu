@@ -139,12 +139,10 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
       if (lane == 0) bar_expect(fb, static_cast<unsigned>(n * box * D * 4));
       __syncwarp();
       if (my_box < n && lane < F::CH / box * (D / 64)) {
-        if (page < 0 || page >= p.NP) {
-          flag = CONFKV_FLAG_BAD_PAGE;
-          page = 0;
-        }
+        const bool none = static_cast<unsigned>(page) >= static_cast<unsigned>(p.NP);
+        if (none) flag = CONFKV_FLAG_BAD_PAGE;
         const int j = ci * F::CH + my_box * box;
-        const int y = ((layer_row + page * p.Hkv + h) << p.ps_shift) + (j & (p.ps - 1));
+        const int y = none ? kNoRows : ((layer_row + page * p.Hkv + h) << p.ps_shift) + (j & (p.ps - 1));
         const uint32_t o = dst + my_half * F::HALF + my_box * box * 128;
         tma_box(o, &mk, 64 * my_half, y, fb, pol);
         tma_box(o + F::KV, &mv, 64 * my_half, y, fb, pol);

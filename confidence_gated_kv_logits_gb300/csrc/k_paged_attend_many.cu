@@ -219,12 +219,10 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
           if (lane < n * (D / 64)) {
             const int i = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
             const int j = j0 + i * rows_per;
-            int page = table[j >> p.ps_shift];
-            if (page < 0 || page >= p.NP) {
-              flag = CONFKV_FLAG_BAD_PAGE;
-              page = 0;
-            }
-            const int y = (((a.layer * p.NP + page) * p.Hkv + w.h) << p.ps_shift) + (j & (p.ps - 1));
+            const int page = table[j >> p.ps_shift];
+            const bool none = static_cast<unsigned>(page) >= static_cast<unsigned>(p.NP);
+            if (none) flag = CONFKV_FLAG_BAD_PAGE;
+            const int y = none ? kNoRows : (((a.layer * p.NP + page) * p.Hkv + w.h) << p.ps_shift) + (j & (p.ps - 1));
             tma_box(ring + st * M::TILE + half * M::HALF + i * rows_per * 128, map, 64 * half, y, b_full + 8 * st, pol);
           }
           ++slot;

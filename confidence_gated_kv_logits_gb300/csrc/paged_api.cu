@@ -86,6 +86,7 @@ const char* check_batch(const confkv_paged_batch* b, bool masked) {
 
 // Tensor maps of both pools for both kernels: rows of d elements in boxes of 64
 // channels (128 bytes, swizzled) x as many rows as a page and the kernel's tile share.
+// Rows outside the pool (kNoRows) read as NaN from K's maps and as zero from V's.
 cudaError_t encode_maps(const Pool& p, AttendMaps* m) {
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult q;
@@ -105,12 +106,16 @@ cudaError_t encode_maps(const Pool& p, AttendMaps* m) {
     CUtensorMap* map;
     uint16_t* pool;
     int rows;
-  } const all[] = {{&m->k_few, p.k, few}, {&m->v_few, p.v, few}, {&m->k_many, p.k, many}, {&m->v_many, p.v, many}};
+    CUtensorMapFloatOOBfill outside;
+  } const all[] = {{&m->k_few, p.k, few, CU_TENSOR_MAP_FLOAT_OOB_FILL_NAN_REQUEST_ZERO_FMA},
+                   {&m->v_few, p.v, few, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE},
+                   {&m->k_many, p.k, many, CU_TENSOR_MAP_FLOAT_OOB_FILL_NAN_REQUEST_ZERO_FMA},
+                   {&m->v_many, p.v, many, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE}};
   for (const auto& x : all) {
     const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(x.rows)};
     if (enc(x.map, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x.pool, dims,
             strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, x.outside) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
   return cudaSuccess;

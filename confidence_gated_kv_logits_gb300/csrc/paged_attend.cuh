@@ -18,6 +18,11 @@ constexpr int kFewChunk = 2048;        // elements of K in a chunk (tokens x d)
 constexpr int kManyRows = 256;         // two tiles of 128
 constexpr int kManyBlock = 128;        // tokens of a block
 
+// Where the boxes of a page that is not in the pool are asked for: rows before the
+// pool.  TMA gives NaN for K there and zeroes for V, so that the scores of such a
+// page's tokens, and with them the rows that see one, are NaN.
+constexpr int kNoRows = -kManyBlock;
+
 // CTAs of a launch: one per SM
 constexpr int kFewCtasPerSm = 1;
 

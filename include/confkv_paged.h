@@ -156,8 +156,10 @@ int confkv_paged_append(confkv_paged* kv, const confkv_paged_batch* batch, int l
  * lse -inf; one whose query or a key that it sees is NaN gives NaN in both.
  * What masked places and places past a sequence's end hold (NaN,
  * infinities) does not matter.  A sequence that is longer than its page table
- * ends where the table does (CONFKV_FLAG_CAPACITY).  Results do not depend on
- * what else is in the batch's other calls, and are the same on every run.
+ * ends where the table does (CONFKV_FLAG_CAPACITY); a row that sees a token of a
+ * page outside the pool gives NaN in both (CONFKV_FLAG_BAD_PAGE).  Results do not
+ * depend on what else is in the batch's other calls, and are the same on every
+ * run.
  */
 int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int layer, int rows,
                         const void* q, int64_t q_stride, void* out, float* lse, float scale,

@@ -8,7 +8,7 @@ import math
 import pytest
 import torch
 
-from tests.test_paged_gpu import DEV, DT, U, Case, check_select, ints, mask_words, reference, run_attend, select_reference
+from tests.test_paged_gpu import DEV, DT, U, Case, check, check_select, ints, mask_words, reference, run_attend, select_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -122,6 +122,49 @@ def test_attend_nan_keys_reach_every_row_that_sees_them(pkg, form, dt):
 
 
 # --------------------------------------------------------------------------- page tables that are wrong
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("bad", [-1, 1 << 30])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_attend_a_bad_page_voids_the_rows_that_see_it(pkg, form, bad, dt):
+    """The second page of every other sequence is none: NaN for the rows that see it, whatever page 0 holds."""
+    c = case_of(form, DT[dt])
+    vis = causal(c)
+    want = exact(c, vis)
+    lost = torch.zeros(c.starts[-1], c.heads, dtype=torch.bool, device=DEV)
+    table = c.table.clone()
+    for b, v in enumerate(vis):
+        if b % 2 == 0 and v.shape[1] > c.page:
+            table[b, 1] = bad
+            lost[c.starts[b]:c.starts[b + 1]] = v[:, c.page:2 * c.page].any(1).to(DEV)[:, None]
+    assert lost.any()
+    kv = pkg.PagedKV(c.k, c.v, c.heads)
+    got = run_attend(pkg, c, kv=kv, batch=kv.batch(table, ints(c.ctx), ints(c.starts)))
+    assert kv.status(check=False) == pkg.FLAG_BAD_PAGE
+    compare(c, got, want, lost)
+    check(c, run_attend(pkg, c, kv=kv), reference(c))       # nothing stays behind
+    assert kv.status() == 0
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("new,d", [(1, 64), (3, 128), (90, 64), (700, 128)])
+def test_attend_a_tree_over_bad_pages(pkg, new, d, dt):
+    """Masks and bad pages of drafts together, small pages: rows that do not see their tokens are right."""
+    c = Case(DT[dt], 6, 2, d, 16, [80, 80], [new, new], seed=new)
+    bits = [1 << i | 1 << i // 2 | 1 for i in range(new)]
+    vis = torch.ones(new, 80 + new, dtype=torch.bool)
+    vis[:, 80:] = torch.tensor([[bool(x >> j & 1) for j in range(new)] for x in bits]).view(new, new)
+    table, last = c.table.clone(), (80 + new - 1) // 16
+    lost = torch.zeros(2 * new, 6, dtype=torch.bool, device=DEV)
+    for blk in {last, min(last, max(6, last // 2))}:
+        table[0, blk] = c.k.shape[1]
+        lost[:new] |= vis[:, 16 * blk:16 * blk + 16].any(1).to(DEV)[:, None]
+    kv = pkg.PagedKV(c.k, c.v, c.heads)
+    mask = mask_words(2 * bits + [0] * (c.rows - 2 * new), -(-new // 32))
+    got = run_attend(pkg, c, kv=kv, batch=kv.batch(table, ints(c.ctx), ints(c.starts), mask))
+    assert kv.status(check=False) == pkg.FLAG_BAD_PAGE and lost.any() and not lost.all()
+    compare(c, got, exact(c, [vis, vis]), lost)
+
+
 @pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("heads,kv_heads,d,ctx,new,blocks", [
     (4, 4, 64, 30, 9, 1), (4, 4, 64, 40, 9, 3), (10, 2, 128, 20, 400, 3), (8, 1, 64, 100, 300, 9), (10, 2, 128, 90, 1500, 7),
