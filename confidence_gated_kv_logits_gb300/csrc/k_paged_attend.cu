@@ -280,8 +280,9 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
       xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
       if (__any_sync(0xffffffffu, xa > ma || xb > mb)) {
         const float na = fmaxf(ma, xa), nb = fmaxf(mb, xb);
-        const float fa = ma == -INFINITY ? 0.0f : ex2f((ma - na) * c);
-        const float fb = mb == -INFINITY ? 0.0f : ex2f((mb - nb) * c);
+        // (nothing seen before: all sums are 0 but for infinities added by hand above, which stay)
+        const float fa = ma == -INFINITY ? 1.0f : ex2f((ma - na) * c);
+        const float fb = mb == -INFINITY ? 1.0f : ex2f((mb - nb) * c);
         if (turn != turn0) {
 #pragma unroll
           for (int i = 0; i < F::OT; ++i) {

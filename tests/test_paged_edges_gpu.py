@@ -121,6 +121,29 @@ def test_attend_nan_keys_reach_every_row_that_sees_them(pkg, form, dt):
     compare(c, run_attend(pkg, c), want, lost)
 
 
+# --------------------------------------------------------------------------- infinities that a row sees
+@pytest.mark.parametrize("dt", list(DT))
+def test_attend_an_infinite_value_behind_tiles_that_the_row_does_not_see(pkg, dt):
+    """Row 200 sees drafts 140 and 145 alone; draft 140's V is infinite in some channels."""
+    c = Case(DT[dt], 2, 2, 128, 32, [0] * 32, [300] + [1] * 31, seed=9)
+    bits = [(1 << i + 1) - 1 for i in range(300)] + [1] * 31
+    bits[200] = 1 << 140 | 1 << 145
+    for i in range(140, 300):
+        if i != 200:
+            bits[i] &= ~(1 << 140)
+    pg, s = int(c.table[0, 140 // 32]), 140 % 32
+    vis = [torch.tensor([[x >> j & 1 for j in range(t)] for x in bits[a:a + t]], dtype=torch.bool) for a, t in zip(c.starts, c.new)]
+    c.v[:, pg, :, s, ::3] = math.inf
+    c.v[:, pg, :, s, 1::3] = -math.inf
+    want = exact(c, vis)                                    # (with zeroes in the place of the infinities)
+    got = run_attend(pkg, c, bits)
+    assert (got[0][200, :, ::3] == math.inf).all() and (got[0][200, :, 1::3] == -math.inf).all()
+    rest = got[0].clone()
+    rest[200, :, ::3] = rest[200, :, 1::3] = 0
+    want[0][200, :, ::3] = want[0][200, :, 1::3] = 0
+    compare(c, (rest, got[1]), want)
+
+
 # --------------------------------------------------------------------------- page tables that are wrong
 @pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("bad", [-1, 1 << 30])
