@@ -3,7 +3,9 @@
 Each .cu file under csrc/ is compiled to an object in parallel, then linked
 into ``libconfkv.so`` next to this file; csrc/paged_py.cpp, which reads tensor
 arguments for the paged operators, becomes the Python module ``_paged_ops.so``
-(g++ with torch's own headers, linked to both).  Host code is compiled without
+(g++ with torch's own headers, linked to both).  The library needs neither Python's
+headers nor torch: it is linked first, and without torch the module is left out
+(the binding then says so when it is used).  Host code is compiled without
 floating-point contraction so the per-layer budget table is computed with
 plain IEEE double operations.
 """
@@ -13,6 +15,7 @@ import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -48,17 +51,37 @@ def _run(cmd, what):
         raise RuntimeError(f"{what} failed:\n{r.stderr}")
 
 
-def _ops_object(src, obj):
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+def _torch():
+    """torch's folder, None without torch."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _ops_against(torch):
+    """What the module is built against: it is built anew when this changes."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return "\n".join([sys.version, sysconfig.get_paths()["include"], torch, f.read()])
+
+
+def _ops_object(src, obj, torch):
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=1",
           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
           "-isystem", os.path.join(cuda, "include"), "-c", src, "-o", obj], f"g++ on {src}")
+    with open(obj + ".against", "w") as f:
+        f.write(_ops_against(torch))
 
 
-def _ops_link(obj):
-    lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+def _ops_stale(src, obj, hdrs, torch):
+    if _stale(obj, [src] + hdrs) or not os.path.exists(obj + ".against"):
+        return True
+    with open(obj + ".against") as f:
+        return f.read() != _ops_against(torch)
+
+
+def _ops_link(obj, torch):
+    lib = os.path.join(torch, "lib")
     tmp = OPS + f".tmp{os.getpid()}"
     _run(["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:libconfkv.so", "-L", lib, "-ltorch_python",
           "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"],
@@ -91,12 +114,11 @@ def build(force=False, verbose=False):
 
     ops_src = os.path.join(CSRC, "paged_py.cpp")
     ops_obj = os.path.join(OBJ, "paged_py.o")
-    ops = force or _stale(ops_obj, [ops_src] + hdrs)
+    torch = _torch()
+    ops = torch and (force or _ops_stale(ops_src, ops_obj, hdrs, torch))
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
-        extra = ex.submit(_ops_object, ops_src, ops_obj) if ops else None
+        extra = ex.submit(_ops_object, ops_src, ops_obj, torch) if ops else None
         list(ex.map(compile_one, jobs))
-        if extra:
-            extra.result()
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
@@ -104,11 +126,12 @@ def build(force=False, verbose=False):
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, LIB)
-    if force or _stale(OPS, [ops_obj, LIB]):
-        _ops_link(ops_obj)
+    if extra:
+        extra.result()
+    if torch and (force or _stale(OPS, [ops_obj, LIB])):
+        _ops_link(ops_obj, torch)
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True))

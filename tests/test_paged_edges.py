@@ -2,6 +2,8 @@
 import os
 import re
 
+import pytest
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -22,3 +24,53 @@ def test_softmax_warps_leave_their_loop_together():
     before, after = body.split(leave[0])
     assert "bar_wait" in before and "soft_sync" not in before
     assert "bar_wait" not in after and "next_piece" not in after
+
+
+# --------------------------------------------------------------------------- the build
+@pytest.fixture
+def builder(monkeypatch, tmp_path):
+    """The build with its objects in place and its two results elsewhere; `ran` gets the commands that it runs."""
+    from confidence_gated_kv_logits_gb300 import build as B
+    B.build()
+    B.ran = []
+    monkeypatch.setattr(B, "LIB", str(tmp_path / "libconfkv.so"))
+    monkeypatch.setattr(B, "OPS", str(tmp_path / "_paged_ops.so"))
+
+    def link_library(cmd, **kw):
+        B.ran.append("library")
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return type("Done", (), {"returncode": 0, "stderr": ""})
+
+    monkeypatch.setattr(B.subprocess, "run", link_library)
+    monkeypatch.setattr(B, "_run", lambda cmd, what: (B.ran.append("module"), open(cmd[cmd.index("-o") + 1], "w").close()))
+    return B
+
+
+def test_the_library_is_built_without_torch(builder, monkeypatch):
+    monkeypatch.setattr(builder.importlib.util, "find_spec", lambda name: None)
+    assert os.path.exists(builder.build()) and builder.ran == ["library"]
+    assert not os.path.exists(builder.OPS)
+
+
+def test_the_library_is_linked_where_the_module_does_not_compile(builder, monkeypatch):
+    def broken(*a):
+        raise RuntimeError("g++ found no Python.h")
+
+    monkeypatch.setattr(builder, "_ops_object", broken)
+    monkeypatch.setattr(builder, "_ops_stale", lambda *a: True, raising=False)
+    monkeypatch.setattr(builder, "_stale", lambda target, deps: not os.path.exists(target) or target.endswith("paged_py.o"))
+    with pytest.raises(RuntimeError, match="Python.h"):
+        builder.build()
+    assert os.path.exists(builder.LIB) and not os.path.exists(builder.OPS)
+
+
+def test_the_module_is_built_anew_for_another_torch(builder, monkeypatch, tmp_path):
+    torch = builder._torch()
+    src, obj = str(tmp_path / "a.cpp"), str(tmp_path / "a.o")
+    open(src, "w").close()
+    builder._ops_object(src, obj, torch)
+    assert builder.ran == ["module"] and not builder._ops_stale(src, obj, [], torch)
+    other = tmp_path / "torch"
+    other.mkdir()
+    (other / "version.py").write_text("__version__ = '0'")
+    assert builder._ops_stale(src, obj, [], str(other))
