@@ -191,7 +191,14 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int mask_rows, layer;
   int64_t rows, qs;
   void *q, *out, *lse = nullptr, *s;
-  if (!ready(ob) || !integer(a[2], &mask_rows) || !integer(a[3], &layer) || !rows_count(a[4], "q", &rows) ||
+  if (!ready(ob)) return nullptr;
+  const double scale = PyFloat_AsDouble(a[7]);
+  if (scale == -1.0 && PyErr_Occurred()) return nullptr;
+  if (scale != 0.0 && static_cast<float>(scale) == 0.0f) {      // 0 would mean the default
+    PyErr_SetString(PyExc_ValueError, "scale is zero in 32 bits");
+    return nullptr;
+  }
+  if (!integer(a[2], &mask_rows) || !integer(a[3], &layer) || !rows_count(a[4], "q", &rows) ||
       !rows_of(ob, a[4], "q", rows, ob->sizes[0], &q, &qs) ||
       !dense(ob, a[5], "out", type_of(ob->dtype), {rows, ob->sizes[0], ob->sizes[2]}, &out))
     return nullptr;
@@ -200,8 +207,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return nullptr;
   }
   if (a[6] != Py_None && !dense(ob, a[6], "lse", at::kFloat, {rows, ob->sizes[0]}, &lse)) return nullptr;
-  const double scale = PyFloat_AsDouble(a[7]);
-  if ((scale == -1.0 && PyErr_Occurred()) || !stream_of(ob, a[8], &s)) return nullptr;
+  if (!stream_of(ob, a[8], &s)) return nullptr;
   return PyLong_FromLong(confkv_paged_attend(ob->kv, batch, layer, static_cast<int>(rows), q, qs, out,
                                              static_cast<float*>(lse), static_cast<float>(scale), s));
 }

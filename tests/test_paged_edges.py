@@ -26,6 +26,30 @@ def test_softmax_warps_leave_their_loop_together():
     assert "bar_wait" not in after and "next_piece" not in after
 
 
+# --------------------------------------------------------------------------- the binding
+@pytest.fixture(scope="module")
+def pkg():
+    from confidence_gated_kv_logits_gb300 import build as B
+    B.build()
+    import confidence_gated_kv_logits_gb300 as pkg
+    from confidence_gated_kv_logits_gb300.paged import _load
+    _load()
+    return pkg
+
+
+def test_a_scale_that_is_zero_in_32_bits_is_refused(pkg):
+    """It would mean the default."""
+    import torch
+    from confidence_gated_kv_logits_gb300 import _paged_ops as ops
+    ob = ops.make(4096, 0, 0, 0, 2, 1, 64, 0, -1, 0)
+    # (the tensors are on the CPU: any other scale is refused for that)
+    with pytest.raises(ValueError, match="q: want"):
+        ops.attend(ob, 0, -1, 0, torch.zeros(1, 2, 64).half(), torch.zeros(1, 2, 64).half(), None, 1.0, None)
+    with pytest.raises(ValueError, match="scale"):
+        ops.attend(ob, 0, -1, 0, torch.zeros(1, 2, 64).half(), torch.zeros(1, 2, 64).half(), None, 1e-60, None)
+    ops.release(ob)
+
+
 # --------------------------------------------------------------------------- the build
 @pytest.fixture
 def builder(monkeypatch, tmp_path):
