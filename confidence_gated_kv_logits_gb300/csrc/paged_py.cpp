@@ -147,7 +147,7 @@ bool count(Py_ssize_t n, Py_ssize_t want) {
 }
 bool ready(const Object* ob) {
   if (ob && ob->kv) return true;
-  if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "the handle is closed");
+  PyErr_SetString(PyExc_ValueError, "the handle is closed");    // (in the place of what reading None raised)
   return false;
 }
 

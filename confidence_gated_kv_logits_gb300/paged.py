@@ -172,6 +172,8 @@ class PagedKV(_Device):
     def status(self, check=True):
         """The FLAG_* bits that the GPU has latched since the last call
         (synchronises); raises if there are any unless ``check`` is false."""
+        if not self._h:
+            raise ValueError("the handle is closed")
         f = ctypes.c_int32()
         rc = self._L.confkv_paged_status(self._h, ctypes.byref(f))
         if check:

@@ -50,6 +50,19 @@ def test_a_scale_that_is_zero_in_32_bits_is_refused(pkg):
     ops.release(ob)
 
 
+def test_a_closed_handle_says_so(pkg):
+    """Every call, status without its check among them (which answered 0: no flags)."""
+    from confidence_gated_kv_logits_gb300.paged import BatchStruct, PagedBatch
+    kv = pkg.PagedKV.__new__(pkg.PagedKV)
+    kv._L, kv._h, kv._ob, kv._index = pkg.load_library(), None, None, 0
+    batch = PagedBatch(BatchStruct(), (), 1, -1, 0)
+    for call in (lambda: kv.append(0, batch, None, None), lambda: kv.attend(0, batch, None, None), lambda: kv.commit(*[None] * 5),
+                 lambda: kv.fork(*[None] * 7), lambda: kv.status(), lambda: kv.status(check=False)):
+        with pytest.raises(ValueError, match="closed"):
+            call()
+    kv.close()
+
+
 # --------------------------------------------------------------------------- the build
 @pytest.fixture
 def builder(monkeypatch, tmp_path):
