@@ -251,9 +251,12 @@ class BeamSelect(_Device):
         n = self._L.confkv_beam_workspace(batch, beams, vocab, keep, self._code)
         if not n:
             raise ConfKVError(ERR_INVALID_ARG, f"beam sizes {self.sizes} are not supported")
-        if device is None:
-            device = torch.cuda.current_device()
-        self._index = device if isinstance(device, int) else torch.device(device).index or 0
+        if device is not None and not isinstance(device, int):
+            device = torch.device(device)
+            if device.type != "cuda":
+                raise ValueError(f"device: want a CUDA device, got {device}")
+            device = device.index                # ("cuda" alone: the current one)
+        self._index = torch.cuda.current_device() if device is None else device
         self.device = torch.device("cuda", self._index)
         ws = self._scratch(n, n)
         self._ob = _ops.make(1, ws, n, self._home, batch, beams, vocab, keep, self._index, self._code)

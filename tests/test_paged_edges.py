@@ -63,6 +63,23 @@ def test_a_closed_handle_says_so(pkg):
     kv.close()
 
 
+def test_beam_select_on_the_device_that_was_named(pkg, monkeypatch):
+    import torch
+    from confidence_gated_kv_logits_gb300 import paged
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+
+    def scratch(self, n, zeroed):
+        self._home = 0
+        return 4096
+
+    monkeypatch.setattr(paged.BeamSelect, "_scratch", scratch)
+    for device, index in ((None, 3), ("cuda", 3), (torch.device("cuda"), 3), ("cuda:1", 1), (torch.device("cuda", 0), 0), (2, 2), (0, 0)):
+        assert pkg.BeamSelect(1, 2, 100, 4, device=device).device == torch.device("cuda", index)
+    for device in ("cpu", torch.device("meta")):
+        with pytest.raises(ValueError, match="CUDA"):
+            pkg.BeamSelect(1, 2, 100, 4, device=device)
+
+
 # --------------------------------------------------------------------------- the build
 @pytest.fixture
 def builder(monkeypatch, tmp_path):
