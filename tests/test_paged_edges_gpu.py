@@ -8,7 +8,7 @@ import math
 import pytest
 import torch
 
-from tests.test_paged_gpu import DEV, DT, U, Case, check, check_select, ints, mask_words, reference, run_attend, select_reference
+from tests.test_paged_gpu import DEV, DT, U, Case, check, check_select, ints, mask_words, reference, run_attend, run_select, select_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -228,6 +228,62 @@ def test_select_one_workspace_for_every_size(pkg):
         torch.cuda.synchronize()
         assert rc == 0
         check_select((so, po, to), select_reference(z.cpu(), scores.cpu(), None, K, 0))
+
+
+# --------------------------------------------------------------------------- how far scores may be off
+def spread(kind, V, g):
+    if kind == "flat":
+        return torch.zeros(V, device=DEV)
+    if kind == "peak":                                      # one token over a flat tail
+        z = torch.full((V,), -12.0, device=DEV)
+        z[V // 3] = 0
+        return z
+    return {"narrow": 1.0, "wide": 4.0}[kind] * torch.randn(V, generator=g, device=DEV)
+
+
+def lse_bound(z):
+    """The selection's lse against 64 bits.  A term e^d, d = z - max, is off by 2^-22 (ex2.approx) and by |d| (2^-24 + 2^-24 +
+    2^-26) of its value (d and its product with log2 e rounded, log2 e's own rounding); the weighted mean of |d| is max -
+    sum p z.  A thread adds its terms (64 at most) in 11 rounded steps of 2^-24; what is cut off at 2^-38 a thread is below
+    2^-26 of the sum, which is 1 at least (where threads take 8 terms each, so that there are up to 2^15 of them, below
+    2^-23, but the steps are 6); the logarithm's Newton step adds less than 2^-40: 12 2^-24 covers both."""
+    z = z.double()
+    lse = torch.logsumexp(z, 0)
+    return lse, 2.0 ** -22 + float(z.max() - (torch.softmax(z, 0) * z).sum()) * 2.25 * 2.0 ** -24 + 12 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("V", [50257, 201088])
+@pytest.mark.parametrize("kind", ["flat", "peak", "narrow", "wide"])
+def test_select_scores_are_as_good_as_stated(pkg, kind, V, dt):
+    """score = scores[w] + z - lse near 0, so that its rounding to 32 bits does not hide the error of lse."""
+    z = spread(kind, V, torch.Generator(device=DEV).manual_seed(V)).to(dt)
+    lse, bound = lse_bound(z)
+    start = (lse - z.double().max()).float()
+    so, po, to, _, _ = run_select(pkg, z.view(1, 1, V), start.view(1, 1), 1)
+    want = start.double() + z.double().max() - lse
+    assert int(to) == int(z.float().argmax()) and abs(float(so) - float(want)) <= bound + 2.0 ** -24 * abs(float(want))
+
+
+@pytest.mark.parametrize("V", [50257, 201088])
+@pytest.mark.parametrize("kinds", [("flat", "peak"), ("peak", "wide"), ("narrow", "flat"), ("wide", "narrow")])
+def test_select_orders_beams_that_differ_by_more_than_the_bound(pkg, kinds, V):
+    g = torch.Generator(device=DEV).manual_seed(V)
+    z = torch.stack([spread(k, V, g) for k in kinds])
+    (la, ba), (lb, bb) = (lse_bound(x) for x in z)
+    for sign in (1, -1):
+        # the second beam's best, ahead of or behind the first's by a little more than both may be off
+        best = [float(z[0].double().max() - la), float(z[1].double().max() - lb)]
+        gap = 1.1 * (ba + bb)
+        first = torch.tensor(-best[0], dtype=torch.float64).float()
+        second = torch.tensor(float(first) + best[0] - best[1] + sign * gap, dtype=torch.float64).float()
+        real = float(second) + best[1] - (float(first) + best[0])
+        if abs(real) <= ba + bb:                            # the score's own 32 bits are coarser
+            second = torch.nextafter(second, torch.tensor(sign * math.inf))
+            real = float(second) + best[1] - (float(first) + best[0])
+        assert sign * real > ba + bb
+        so, po, _, _, _ = run_select(pkg, z.view(1, 2, V), torch.stack([first, second]).view(1, 2).to(DEV), 1)
+        assert int(po) == (1 if sign > 0 else 0)
 
 
 # --------------------------------------------------------------------------- with the decode step
