@@ -297,13 +297,15 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
         ma = na;
         mb = nb;
       }
-      const float ca = ma == -INFINITY ? 0.0f : ma * c, cb = mb == -INFINITY ? 0.0f : mb * c;
+      // the difference first: it is exact near the maximum, however large both are
+      // (s c - max c by one fma is off by max c's rounding, a factor of 2^128 for scores of 2^31)
+      const float sa = ma == -INFINITY ? 0.0f : ma, sb = mb == -INFINITY ? 0.0f : mb;
 #pragma unroll
       for (int i = 0; i < F::NT; ++i) {
-        s[i][0] = ex2f(fmaf(s[i][0], c, -ca));
-        s[i][1] = ex2f(fmaf(s[i][1], c, -ca));
-        s[i][2] = ex2f(fmaf(s[i][2], c, -cb));
-        s[i][3] = ex2f(fmaf(s[i][3], c, -cb));
+        s[i][0] = ex2f((s[i][0] - sa) * c);
+        s[i][1] = ex2f((s[i][1] - sa) * c);
+        s[i][2] = ex2f((s[i][2] - sb) * c);
+        s[i][3] = ex2f((s[i][3] - sb) * c);
         la += s[i][0] + s[i][1];
         lb += s[i][2] + s[i][3];
       }

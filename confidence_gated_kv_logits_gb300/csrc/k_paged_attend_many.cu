@@ -52,6 +52,9 @@ constexpr int BN = kManyBlock;
 constexpr int SB = BN / 2;                 // tokens of a sub-block
 constexpr float kL2E = 1.4426950408889634f;
 constexpr float kRaise = 8.0f;              // log2 of the growth that rescales
+// From here on (in units of log2) the rounding of the maximum's product with c, 2^-24
+// of it, counts: s c - max c is taken as (s - max) c and the maximum always raised.
+constexpr float kHuge = 65536.0f;
 constexpr int kOver = 2;                    // a unit's fixed cost in blocks
 
 template <int D, int NQ>
@@ -423,13 +426,16 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
           // 64 weights in groups of eight, the groups' steps interleaved (written
           // in order: the schedule is otherwise one pipe after another)
           float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+          // one fma at first; taken again, the difference first, which is exact near
+          // the maximum however large both are (kHuge)
+          auto arg = [&](float x, bool first) { return first ? fma_o(x, c, -mc) : mul_o(x - mc, c); };
           auto weights = [&](bool top) {
             uint32_t pk[2][16];
             float z[2][8];
             uint64_t e[2][4];
             auto sval = [&](int k) { return __uint_as_float(sv[k >> 5][k & 31]); };
 #pragma unroll
-            for (int y = 0; y < 8; ++y) z[0][y] = fma_o(sval(y), c, -mc);
+            for (int y = 0; y < 8; ++y) z[0][y] = arg(sval(y), top);
 #pragma unroll
             for (int g = 0; g <= 8; ++g) {
 #pragma unroll
@@ -437,8 +443,8 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
                 if (g < 8) {
                   const float e0 = ex2_o(z[g & 1][2 * y]);
                   if (g < 7) {
-                    z[(g + 1) & 1][2 * y] = fma_o(sval(8 * g + 8 + 2 * y), c, -mc);
-                    z[(g + 1) & 1][2 * y + 1] = fma_o(sval(8 * g + 9 + 2 * y), c, -mc);
+                    z[(g + 1) & 1][2 * y] = arg(sval(8 * g + 8 + 2 * y), top);
+                    z[(g + 1) & 1][2 * y + 1] = arg(sval(8 * g + 9 + 2 * y), top);
                   }
                   const float e1 = ex2_o(z[g & 1][2 * y + 1]);
                   if (top) mx[y] = max3_o(mx[y], sval(8 * g + 2 * y), sval(8 * g + 2 * y + 1));
@@ -474,12 +480,12 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
             weights(true);
           }
           const float mn = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-          const bool raise = (m == -INFINITY) ? mn > -INFINITY : (mn - m) * c > kRaise;
+          const bool raise = (m == -INFINITY) ? mn > -INFINITY : (mn - m) * c > kRaise || fabsf(mc) > kHuge;
           if (__any_sync(0xffffffffu, raise)) {
             const float f = m == -INFINITY ? 0.0f : ex2f((m - mn) * c);
             m = mn;
             l *= f;
-            mc = m == -INFINITY ? 0.0f : m * c;
+            mc = m == -INFINITY ? 0.0f : m;
             tmem_wait_st();                   // the first P before its replacement
             if (i > 0) {
               // the product before this one has to be in O

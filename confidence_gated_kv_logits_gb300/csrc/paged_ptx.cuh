@@ -56,6 +56,11 @@ __device__ __forceinline__ float fma_o(float a, float b, float c) {
   asm volatile("fma.rn.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
+__device__ __forceinline__ float mul_o(float a, float b) {
+  float y;
+  asm volatile("mul.rn.f32 %0, %1, %2;\n" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 __device__ __forceinline__ uint64_t add2_o(uint64_t a, uint64_t b) {
   uint64_t r;
   asm volatile("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));

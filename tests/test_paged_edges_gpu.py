@@ -144,6 +144,33 @@ def test_attend_an_infinite_value_behind_tiles_that_the_row_does_not_see(pkg, dt
     compare(c, (rest, got[1]), want)
 
 
+# --------------------------------------------------------------------------- scores far beyond what 32 bits tell apart
+@pytest.mark.parametrize("dt,most", [("fp16", 6e4), ("bf16", 6e4), ("bf16", 1e17)])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_attend_huge_scores_leave_the_largest(pkg, form, dt, most):
+    """Queries of `most` in every channel and keys that rise from 0 to it: a score is 1e10 and more, the next lower one a
+    hundredth of it away or further, so that one token's weight is 1 and the others' are 0, as in 64 bits."""
+    c = case_of(form, DT[dt])
+    for b, (a, t) in enumerate(zip(c.ctx, c.new)):
+        size = torch.zeros(a + t, dtype=torch.float64)
+        size[:] = -most * torch.arange(1, a + t + 1) / (a + t) * 0.5
+        size[0] = 0.5 * most
+        if a > 2:
+            size[a // 2] = most                             # seen by every row
+        k = size.to(c.dt).to(DEV)[None, :, None, None].expand(c.layers, -1, c.H, c.d)
+        at = torch.arange(a + t, device=DEV)
+        c.k[:, c.table[b].long()[at // c.page], :, at % c.page] = k.permute(1, 0, 2, 3)
+    c.q[:] = most
+    got = run_attend(pkg, c)
+    g = c.heads // c.H
+    for b, (a, t) in enumerate(zip(c.ctx, c.new)):
+        j = a // 2 if a > 2 else 0
+        v = c.get(c.v, 1, b, a + t)[j].repeat_interleave(g, 0)
+        assert torch.equal(got[0][c.starts[b]:c.starts[b + 1]], v[None].expand(t, -1, -1))
+        z = float(torch.tensor(most, dtype=c.dt)) * float(c.k[1, c.table[b].long()[j // c.page], 0, j % c.page, 0]) * c.d ** 0.5
+        assert torch.allclose(got[1][c.starts[b]:c.starts[b + 1]].double(), torch.tensor(z, dtype=torch.float64, device=DEV), rtol=(c.d + 4) * 2.0 ** -23, atol=0)
+
+
 # --------------------------------------------------------------------------- page tables that are wrong
 @pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("bad", [-1, 1 << 30])
