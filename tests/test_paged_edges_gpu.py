@@ -313,6 +313,110 @@ def test_select_orders_beams_that_differ_by_more_than_the_bound(pkg, kinds, V):
         assert int(po) == (1 if sign > 0 else 0)
 
 
+# --------------------------------------------------------------------------- the largest and the oddest sizes
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("new", [[1, 0, 2], [40, 70, 0]])
+def test_rows_before_the_first_sequence_are_left_as_they_were(pkg, new, dt):
+    c = Case(DT[dt], 8, 2, 64, 16, [20, 33, 64], new, seed=5)
+    n, lead = c.starts[-1], 5
+    q = torch.cat([c.randn(lead, 8, 64), c.q])
+    want = reference(c)
+    kv = pkg.PagedKV(c.k, c.v, 8)
+    batch = kv.batch(c.table, ints(c.ctx), ints([lead + x for x in c.starts]))
+    out, lse = torch.full_like(q, 7), torch.full(q.shape[:2], 7.0, device=DEV)
+    kv.attend(1, batch, q, out, lse=lse)
+    assert (out[:lead] == 7).all() and (lse[:lead] == 7).all()
+    check(c, (out[lead:], lse[lead:]), want)
+    k, v, q_out, k0 = c.randn(lead + c.rows, 2, 64), c.randn(lead + c.rows, 2, 64), torch.full_like(q, 7), c.k.clone()
+    kv.append(0, batch, k, v, q=q, q_out=q_out)
+    assert torch.equal(q_out[lead:lead + n], q[lead:lead + n]) and (q_out[:lead] == 7).all() and (q_out[lead + n:] == 7).all()
+    for b, (a, t) in enumerate(zip(c.ctx, new)):
+        assert torch.equal(c.get(c.k, 0, b, a + t)[a:], k[lead + c.starts[b]:lead + c.starts[b + 1]])
+        c.put(b, a, k0[:, c.table[b].long()[torch.arange(a, a + t, device=DEV) // 16], :, torch.arange(a, a + t, device=DEV) % 16].transpose(0, 1), c.get(c.v, 1, b, a + t)[None, a:].expand(2, -1, -1, -1))
+    assert torch.equal(c.k.view(torch.int16), k0.view(torch.int16))         # nothing else was written
+    assert kv.status() == 0
+
+
+@pytest.mark.parametrize("t", [40, 70])
+def test_drafts_past_the_masks_words_are_seen_by_no_row(pkg, t):
+    c = Case(torch.float16, 6, 2, 64, 16, [10], [t], seed=t)
+    bits = [(1 << t) - 1] * t
+    kv = pkg.PagedKV(c.k, c.v, 6)
+    vis = torch.ones(t, 10 + t, dtype=torch.bool)
+    vis[:, 10 + 32:] = False
+    mask = mask_words([x & 0xFFFFFFFF for x in bits] + [0] * 3, 1)
+    got = run_attend(pkg, c, kv=kv, batch=kv.batch(c.table, ints(c.ctx), ints(c.starts), mask))
+    compare(c, got, exact(c, [vis]))
+
+
+def test_the_most_sequences(pkg):
+    """65536 sequences of up to 40 tokens: append and attend."""
+    B, H, heads, d, page = 65536, 1, 2, 64, 16
+    g = torch.Generator(device=DEV).manual_seed(2)
+    ctx = torch.randint(0, 40, (B,), generator=g, device=DEV, dtype=torch.int32)
+    table = torch.randperm(B * 3, generator=g, device=DEV).to(torch.int32).view(B, 3)
+    pool = lambda: torch.randn(1, B * 3, H, page, d, generator=g, device=DEV).half()  # noqa: E731
+    k, v = pool(), pool()
+    kv = pkg.PagedKV(k, v, heads)
+    qkv = torch.randn(B, heads + 2 * H, d, generator=g, device=DEV).half()
+    batch = kv.batch(table, ctx, torch.arange(B + 1, dtype=torch.int32, device=DEV))
+    kv.append(0, batch, qkv[:, heads:heads + H], qkv[:, heads + H:])
+    out = torch.empty(B, heads, d, dtype=torch.float16, device=DEV)
+    kv.attend(0, batch, qkv[:, :heads], out)
+    assert kv.status() == 0
+    K, V = (x[0][table.long()].transpose(1, 2).reshape(B, 3 * page, d) for x in (k, v))
+    row = torch.arange(B, device=DEV)
+    assert torch.equal(K[row, ctx.long()], qkv[:, heads]) and torch.equal(V[row, ctx.long()], qkv[:, heads + 1])
+    z = torch.einsum("bhd,bnd->bhn", qkv[:, :heads].double(), K.double()) * d ** -0.5
+    z = torch.where(torch.arange(3 * page, device=DEV) <= ctx[:, None, None], z, -math.inf)
+    p = torch.softmax(z, 2)
+    o, A = torch.einsum("bhn,bnd->bhd", p, V.double()), torch.einsum("bhn,bnd->bhd", p, V.double().abs())
+    ds = (d + 4) * 2.0 ** -23 * d ** -0.5 * float((qkv[:, :heads].double().abs().sum(2).amax() * K.double().abs().amax()))
+    u = U[torch.float16]
+    assert ((out.double() - o).abs() <= u * o.abs() + (u + 2 * ds + 48 * 2.0 ** -23) * A + 48 * 2.0 ** -25 * float(V.abs().amax())).all()
+
+
+def test_commit_of_the_longest_path(pkg):
+    """1000 of 2000 drafts, kept through pages in no order; another sequence's path of 1024 that stays where it is."""
+    c = Case(torch.float16, 2, 2, 64, 16, [5, 16], [2000, 1024], layers=2, seed=8)
+    g = torch.Generator().manual_seed(1)
+    path = torch.randperm(2000, generator=g)[:1000].sort().values.to(torch.int32)
+    want = [x.clone() for x in (c.k, c.v)]
+    to = torch.arange(5, 1005, device=DEV)
+    for pool, w in zip((c.k, c.v), want):
+        at = path.to(DEV).long() + 5
+        w[:, c.table[0].long()[to // 16], :, to % 16] = pool[:, c.table[0].long()[at // 16], :, at % 16]
+    paths = torch.full((2, 1024), -1, dtype=torch.int32)
+    paths[0, :1000] = path
+    paths[1] = torch.arange(1024)
+    kv = pkg.PagedKV(c.k, c.v, 2)
+    new_len = ints([0, 0])
+    kv.commit(c.table, ints(c.ctx), paths.to(DEV), ints([1000, 1024]), new_len)
+    assert kv.status() == 0 and new_len.tolist() == [1005, 1040]
+    assert torch.equal(c.k.view(torch.int16), want[0].view(torch.int16)) and torch.equal(c.v.view(torch.int16), want[1].view(torch.int16))
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,W,V,keep", [(1, 1, 1 << 24, 64), (1, 32, 300000, 64), (65535, 1, 2, 1), (2047, 32, 5, 64)])
+def test_select_the_largest_sizes(pkg, B, W, V, keep, dt):
+    """Distinct logits and scores, so that the order is the definition's (with no pair nearer than the stated precision)."""
+    g = torch.Generator(device=DEV).manual_seed(V)
+    z = (2 * torch.randn(B, W, V, generator=g, device=DEV)).to(dt)
+    scores = -torch.rand(B, W, generator=g, device=DEV)
+    so, po, to, fl, _ = run_select(pkg, z, scores, keep)
+    x = z.double()
+    total = scores.double()[..., None] + x - torch.logsumexp(x, 2, keepdim=True)
+    best, at = total.view(B, -1).topk(min(keep, W * V), dim=1)
+    n = best.shape[1]
+    assert ((so[:, :n].double() - best).abs() <= 2.0 ** -18 + 2.0 ** -24 * best.abs()).all() and not fl.any()
+    # what was chosen has the score that the definition gives it, and is chosen once
+    flat = po[:, :n].long() * V + to[:, :n]
+    assert ((total.view(B, -1).gather(1, flat) - best).abs() <= 2.0 ** -18).all()
+    assert (flat.sort(1).values.diff(dim=1) > 0).all()
+    if n < keep:
+        assert (so[:, n:] == -math.inf).all() and (po[:, n:] == -1).all() and (to[:, n:] == -1).all()
+
+
 # --------------------------------------------------------------------------- with the decode step
 @pytest.mark.parametrize("tma", [0, -1])
 def test_a_window_step_takes_queries_that_append_rotated_right_before_it(pkg, tma):
