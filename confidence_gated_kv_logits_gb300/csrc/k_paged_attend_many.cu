@@ -53,7 +53,10 @@ constexpr int SB = BN / 2;                 // tokens of a sub-block
 constexpr float kL2E = 1.4426950408889634f;
 constexpr float kRaise = 8.0f;              // log2 of the growth that rescales
 // From here on (in units of log2) the rounding of the maximum's product with c, 2^-24
-// of it, counts: s c - max c is taken as (s - max) c and the maximum always raised.
+// of it, counts: s c - max c is taken as (s - max) c and the maximum always raised
+// (nearer ones are raised the earlier the larger they are).  One fma: with a second
+// comparison the prompt chunk below takes 565 us instead of 540, the trees 146
+// instead of 142.6.
 constexpr float kHuge = 65536.0f;
 constexpr int kOver = 2;                    // a unit's fixed cost in blocks
 
@@ -480,7 +483,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
             weights(true);
           }
           const float mn = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-          const bool raise = (m == -INFINITY) ? mn > -INFINITY : (mn - m) * c > kRaise || fabsf(mc) > kHuge;
+          const bool raise = (m == -INFINITY) ? mn > -INFINITY : fmaf(fabsf(mc), kRaise / kHuge, (mn - m) * c) > kRaise;
           if (__any_sync(0xffffffffu, raise)) {
             const float f = m == -INFINITY ? 0.0f : ex2f((m - mn) * c);
             m = mn;
