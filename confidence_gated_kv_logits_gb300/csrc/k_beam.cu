@@ -17,10 +17,11 @@
 // (long runs of equal values, or an order that follows the lanes), K rounds of a
 // block-wide maximum give the same answer.
 //
-// That takes 26.4 us now, 4 rows of 50257 fp32 logits 9.1.  What bounds it:
-// neither the 35 MB (5.2 us) nor the issue slots (half of the
-// SMs' active cycles) but each slice's chain (load, maximum, bound, exponentials,
-// ranking, ticket) with two CTAs per SM, and the last sequence's join behind it.
+// That takes 26.2 us now, 4 rows of 50257 fp32 logits 8.6.  What bounds it:
+// neither the 35 MB (5.2 us) nor the issue slots (55% of the SMs' active cycles)
+// but each slice's chain (load, maximum, bound, exponentials, ranking, ticket, with
+// barriers between) in 896 CTAs, two per SM and so three waves, and the last
+// sequence's join behind it: the SMs are active in 58% of the launch.
 //
 // Precision: exponentials and their sums per thread are fp32, relative to the
 // slice's maximum (the largest terms are exact); sums over threads and slices

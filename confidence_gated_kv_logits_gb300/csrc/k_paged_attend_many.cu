@@ -32,13 +32,13 @@
 // added behind it to the rows that see them.
 //
 // Measured: two prompts' chunks of 2048 rows over 6144 cached tokens, 40/8 heads
-// of 128 channels, bf16, 560 us, 1074 TFLOP/s of products that count; trees of 64
-// over 8 x 8192 tokens, fp16, 147 us (320 rows a head fill 2.5 tiles of 128).
+// of 128 channels, bf16, 541 us, 1110 TFLOP/s of products that count; trees of 64
+// over 8 x 8192 tokens, fp16, 143 us (320 rows a head fill 2.5 tiles of 128).
 // What bounds it is the softmax between the products: a sub-block's QK is 64 wide
 // and takes the tensor cores as long as one of 128 (its operands come from shared
 // memory), exponentials take 4 cycles a warp instruction, and each hand-over
 // between a product and a softmax costs 100 to 200 cycles.  Of a launch's cycles
-// the tensor pipe is active in 44%, the issue slots in 39%.  One stream of
+// the tensor pipe is active in 45%, the issue slots in 41%.  One stream of
 // 128-wide products with a single issuer took 577 us, streams that take turns more.
 #include "paged_attend.cuh"
 

@@ -331,6 +331,10 @@ int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int l
   //  - from 257 on units of two tiles, which share each K and V block, if they fill half
   //    the GPU (8 x 8192 tokens: 385 rows 152, 194 in units of one tile; 1 x 32768 tokens,
   //    whose 16 units do not: 260 rows 110, 87 in units of one)
+  //  - one kernel for the whole batch, so that chunks beside single tokens go with the
+  //    average: 128 rows over 2048 tokens and 64 x 1 row over 2048 (40/8 heads, d =
+  //    128) take 135 together, 32 and 88 in a call each; 512 rows over 2048 and 255 x 1
+  //    row 504, 62 and 310
   //  - far fewer units of one tile than CTAs are cut into many pieces each, which a
   //    kernel of its own joins on all SMs (1 x 32768 tokens, 65 rows: 58 joined by the
   //    last CTA of each unit, 42)

@@ -19,7 +19,8 @@
  *     are found on the host before any work is enqueued.  What only the GPU
  *     can see (a page number outside the pool, a length past the page table,
  *     a path that is none) is skipped there without any access out of range
- *     and latched as CONFKV_FLAG_* bits, which confkv_paged_status returns.
+ *     (what attend gives for such rows is said there) and latched as
+ *     CONFKV_FLAG_* bits, which confkv_paged_status returns.
  *   - No call allocates device memory or, but for status, synchronises the
  *     host, so all but create, free and status can be captured in CUDA graphs.
  *   - A cache handle holds the attention's scratch, memory of the caller: the
@@ -136,7 +137,8 @@ typedef struct confkv_paged_batch {
  *         where interleaved is 1.  rotary_dim % 16 == 0, <= head_dim.
  * Pointers 16-byte aligned, strides multiples of 8.  The angle is reduced in
  * 64-bit fixed point, so far positions lose nothing; the rotation is fp32,
- * rounded once.
+ * rounded once.  A row finds its sequence by reading q_start: work in rows x batch
+ * / 32 words, which shows from some thousands of sequences on.
  */
 int confkv_paged_append(confkv_paged* kv, const confkv_paged_batch* batch, int layer, int rows,
                         const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -160,6 +162,12 @@ int confkv_paged_append(confkv_paged* kv, const confkv_paged_batch* batch, int l
  * page outside the pool gives NaN in both (CONFKV_FLAG_BAD_PAGE).  Results do not
  * depend on what else is in the batch's other calls, and are the same on every
  * run.
+ * Scores, their maxima and sums, and the outputs' sums are 32-bit; the weights
+ * exp(score - max) are rounded once to the cache's type before they meet v, the
+ * outputs once (relative errors 2^-11 each for fp16, 2^-8 for bf16).
+ * One kernel takes the whole batch, chosen by its average of new rows: prompts'
+ * chunks beside many single tokens can take up to 1.6 times what a call for each
+ * takes.
  */
 int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int layer, int rows,
                         const void* q, int64_t q_stride, void* out, float* lse, float scale,
