@@ -81,6 +81,7 @@ class _Device:
     """An object on one device with scratch of its own."""
 
     _ob = None
+    _parked = []                        # scratch of handles that ended inside a capture
 
     def _dense(self, t, shape, name):
         """Address of a contiguous int32 tensor."""
@@ -91,6 +92,9 @@ class _Device:
 
     def _scratch(self, n, zeroed):
         """Device scratch, its first `zeroed` bytes zero whichever stream comes first."""
+        while self._parked:
+            torch.cuda.synchronize(self._parked[-1].device)
+            self._parked.pop()
         self._mem = torch.empty(n, dtype=torch.uint8, device=self.device)
         self._mem[:zeroed].zero_()
         home = torch.cuda.current_stream(self.device)
@@ -100,9 +104,13 @@ class _Device:
 
     def _leave(self):
         # the scratch goes back to its own stream's allocator: work of others has to be done
+        # (waiting for it would break a capture that runs: kept until the next handle is made)
         ob, self._ob = self._ob, None
         if ob is not None and _ops.release(ob):
-            torch.cuda.synchronize(self.device)
+            if torch.cuda.is_current_stream_capturing():
+                self._parked.append(self._mem)
+            else:
+                torch.cuda.synchronize(self.device)
 
 
 class PagedBatch:

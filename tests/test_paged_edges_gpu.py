@@ -417,6 +417,33 @@ def test_select_the_largest_sizes(pkg, B, W, V, keep, dt):
         assert (so[:, n:] == -math.inf).all() and (po[:, n:] == -1).all() and (to[:, n:] == -1).all()
 
 
+# --------------------------------------------------------------------------- handles that end
+def test_a_handle_that_ends_inside_a_capture_leaves_it_whole(pkg):
+    """One that ran on another stream than its own waits for the device when it ends, which no capture allows."""
+    c = Case(torch.float16, 8, 2, 64, 16, [100, 9], [3, 1], seed=4)
+    want = reference(c)
+    side = torch.cuda.Stream()
+    kv, old = (pkg.PagedKV(c.k, c.v, 8) for _ in range(2))
+    batch = c.batch(kv)
+    out, lse = torch.full_like(c.q, 7), torch.full(c.q.shape[:2], 7.0, device=DEV)
+    run_attend(pkg, c, kv=old, stream=side)
+    kv.attend(1, batch, c.q, out, lse=lse)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kv.attend(1, batch, c.q, out, lse=lse)
+        old.close()
+        del old
+        kv.attend(1, batch, c.q, out, lse=lse)
+    out.fill_(7), lse.fill_(7)
+    g.replay()
+    torch.cuda.synchronize()
+    check(c, (out, lse), want)
+    assert len(kv._parked) == 1
+    pkg.PagedKV(c.k, c.v, 8)
+    assert not kv._parked and kv.status() == 0
+
+
 # --------------------------------------------------------------------------- with the decode step
 @pytest.mark.parametrize("tma", [0, -1])
 def test_a_window_step_takes_queries_that_append_rotated_right_before_it(pkg, tma):
