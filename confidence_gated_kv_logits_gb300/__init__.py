@@ -41,7 +41,8 @@ EXPORTS = ("confkv_create", "confkv_prefill", "confkv_step", "confkv_step_host",
            "confkv_attention_path", "confkv_selftest_bounded_wait",
            "confkv_read_channel_exponents",
            "confkv_paged_scratch", "confkv_paged_create", "confkv_paged_free", "confkv_paged_last_error",
-           "confkv_paged_status", "confkv_paged_append", "confkv_paged_attend",
+           "confkv_paged_status", "confkv_paged_append", "confkv_paged_append_normed", "confkv_paged_attend",
+           "confkv_paged_partial", "confkv_paged_attend_shared", "confkv_paged_weigh", "confkv_paged_evict",
            "confkv_paged_commit", "confkv_paged_fork", "confkv_beam_workspace",
            "confkv_beam_select")
 
@@ -334,4 +335,4 @@ class ConfKV:
         return {p.names[i].decode(): (p.launches[i], p.total_ms[i]) for i in range(p.n_kernels)}
 
 
-from .paged import BeamSelect, PagedBatch, PagedKV  # noqa: E402
+from .paged import BeamSelect, PagedBatch, PagedKV, SharedPrefix  # noqa: E402

@@ -64,7 +64,7 @@ struct Few {
 
 // CL > 1: the CTAs of a cluster share each of their units, which are not cut
 // otherwise, and join them through distributed shared memory.
-template <bool BF, int D, int CL>
+template <bool BF, int D, int CL, bool SH>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_constant__ CUtensorMap mk,
              const __grid_constant__ CUtensorMap mv) {
@@ -94,7 +94,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
   fence_async_global();
 
   // the walk stays in shared memory: its registers are the accumulators' between pieces
-  using WalkF = Walk<kRows, F::CH, F::OVER>;
+  using WalkF = Walk<kRows, F::CH, F::OVER, SH>;
   if (a.bt.B > 32) {
     WalkF w(p, a.bt, a.rows);
     sched_init<kThreads>(w, &s_sched, s_scan, 2 * kWarps);
@@ -118,8 +118,8 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
   const int r0 = lane >> 2, t4 = lane & 3;
 
   while (w.more) {
-    const int b = w.b, h = w.h;
-    const int32_t* table = a.bt.table + static_cast<size_t>(b) * a.bt.max_blocks;
+    const int h = w.h;
+    const int32_t* table = a.bt.table + static_cast<size_t>(SH ? w.tb : w.b) * a.bt.max_blocks;
     const int layer_row = (a.layer * p.NP) * p.Hkv;  // page of head h: (layer_row + page * Hkv + h) * ps
     int flag = 0;
     // boxes of 16 rows (or the whole chunk, where a page holds it); lane i asks
@@ -422,17 +422,17 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
           y[3] = fmaf(f, v[i].w, y[3]);
         }
         const int t = js / p.g;
-        store_row<BF, 4>(a, p, w.row0 + t, h * p.g + js - t * p.g, jc, y, m, l);
+        store_row<BF, SH, 4>(a, p, w.row0 + t, h * p.g + js - t * p.g, jc, y, m, l, SH && w.pre);
       }
       cluster_sync();         // nobody leaves or goes on while its rows are read
       if (dead_any) break;
     } else if (whole) {
       if (rr < R) {
         const int t = rr / p.g;
-        store_row<BF, PER>(a, p, w.row0 + t, h * p.g + rr - t * p.g, ch0, x, m, l);
+        store_row<BF, SH, PER>(a, p, w.row0 + t, h * p.g + rr - t * p.g, ch0, x, m, l, SH && w.pre);
       }
     } else {
-      const size_t at = 2 * static_cast<size_t>(blockIdx.x) + (w.lo == 0 ? 1 : 0);
+      const size_t at = 2 * static_cast<size_t>(blockIdx.x) + (w.lo == (SH ? w.pre / F::CH : 0) ? 1 : 0);
       if (rr < R) {
 #pragma unroll
         for (int e = 0; e < PER; e += 4)
@@ -498,7 +498,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
         }
         if (row < live) {
           const int t = rr / p.g;
-          store_row<BF, PER>(a, p, w.row0 + t, h * p.g + rr - t * p.g, ch0, x, m, l);
+          store_row<BF, SH, PER>(a, p, w.row0 + t, h * p.g + rr - t * p.g, ch0, x, m, l, SH && w.pre);
         }
       }
     }
@@ -521,13 +521,18 @@ template <typename F>
 cudaError_t each_few(F&& f) {
   cudaError_t e = cudaSuccess;
   auto of = [&](auto bf, auto d) {
-    auto one = [&](auto cl) {
-      if (e == cudaSuccess) e = f(bf, d, cl, k_attend_few<decltype(bf)::value, decltype(d)::value, decltype(cl)::value>);
+    auto one = [&](auto cl, auto sh) {
+      if (e == cudaSuccess)
+        e = f(bf, d, cl, sh, k_attend_few<decltype(bf)::value, decltype(d)::value, decltype(cl)::value, decltype(sh)::value>);
     };
-    one(std::integral_constant<int, 1>{});
-    one(std::integral_constant<int, 2>{});
-    one(std::integral_constant<int, 4>{});
-    one(std::integral_constant<int, 8>{});
+    auto both = [&](auto cl) {
+      one(cl, std::false_type{});
+      one(cl, std::true_type{});
+    };
+    both(std::integral_constant<int, 1>{});
+    both(std::integral_constant<int, 2>{});
+    both(std::integral_constant<int, 4>{});
+    both(std::integral_constant<int, 8>{});
   };
   of(std::false_type{}, std::integral_constant<int, 64>{});
   of(std::false_type{}, std::integral_constant<int, 128>{});
@@ -541,8 +546,8 @@ cudaError_t each_few(F&& f) {
 cudaError_t launch_attend_few(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
                               int ctas, int cluster, cudaStream_t s) {
   const size_t smem = kWarps * kStages * kChunkBytes + 1024;
-  return each_few([&](auto bf, auto d, auto cl, auto kernel) {
-    if (bf != p.bf16 || d != p.d || cl != cluster) return cudaSuccess;
+  return each_few([&](auto bf, auto d, auto cl, auto sh, auto kernel) {
+    if (bf != p.bf16 || d != p.d || cl != cluster || sh != (a.bt.phase != 0)) return cudaSuccess;
     cudaError_t e;
     if (cl > 1) e = launch_pdl_cluster(kernel, dim3(ctas), dim3(kThreads), cl, smem, s, p, a, sc, m.k_few, m.v_few);
     else e = launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem, s, p, a, sc, m.k_few, m.v_few);
@@ -563,7 +568,7 @@ cudaError_t few_clusters(int size, int* fit) {
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   *fit = INT_MAX;
-  return each_few([&](auto, auto, auto cl, auto kernel) {
+  return each_few([&](auto, auto, auto cl, auto, auto kernel) {
     int n = INT_MAX;
     const cudaError_t e = cl == size ? cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) : cudaSuccess;
     *fit = n < *fit ? n : *fit;
@@ -572,7 +577,7 @@ cudaError_t few_clusters(int size, int* fit) {
 }
 
 cudaError_t setup_attend_few() {
-  return each_few([](auto, auto, auto, auto kernel) {
+  return each_few([](auto, auto, auto, auto, auto kernel) {
     return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kWarps * kStages * kChunkBytes + 1024);
   });

@@ -82,6 +82,7 @@ __device__ __forceinline__ unsigned v_slot(int b, int n) {
 struct Piece {
   int more;                              // 0: the CTA's share ends here
   int b, h, mt, T, ctx, len, row0, lo, hi, pieces, first_cta;
+  int tb, pre;                           // SH: as in WalkState
 };
 constexpr int kPlan = 8;                 // pieces in the ring
 constexpr int kReaders = 11;             // warps that read it
@@ -102,7 +103,7 @@ __device__ __forceinline__ bool soft_any(bool mine) {
   return any != 0;
 }
 
-template <bool BF, int D, int NQ>
+template <bool BF, int D, int NQ, bool SH>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defer, const __grid_constant__ CUtensorMap mk,
               const __grid_constant__ CUtensorMap mv) {
@@ -158,7 +159,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
   fence_async_global();
   tc_fence_before();
   if (a.bt.B > 32) {
-    Walk<TM, BN, kOver> w(p, a.bt, a.rows);
+    Walk<TM, BN, kOver, SH> w(p, a.bt, a.rows);
     sched_init<kThreads>(w, &s_sched, s_scan, 4);
   } else {
     __syncthreads();          // barriers and tensor memory are there
@@ -182,7 +183,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
     if (warp == 11) {
       // ---- the plan ----
-      Walk<TM, BN, kOver> w(p, a.bt, a.rows);
+      Walk<TM, BN, kOver, SH> w(p, a.bt, a.rows);
       if (a.bt.B <= 32) {
         const Sched sh = sched_warp(w, 4, 0, blockIdx.x, gridDim.x);
         w.start(sh);
@@ -193,7 +194,8 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
         more = w.next();
         if (plan >= kPlan && !bar_wait_warp(b_read + 8 * (plan % kPlan), (plan / kPlan - 1) & 1, &s_abort)) break;
         if (lane == 0) {
-          s_plan[plan % kPlan] = Piece{more, w.b, w.h, w.mt, w.T, w.ctx, w.len, w.row0, w.lo, w.hi, w.pieces, w.first_cta};
+          s_plan[plan % kPlan] = Piece{more, w.b, w.h, w.mt, w.T, w.ctx, w.len, w.row0, w.lo, w.hi, w.pieces, w.first_cta,
+                                     SH ? w.tb : 0, SH ? w.pre : 0};
           bar_arrive(b_plan + 8 * (plan % kPlan));
         }
       }
@@ -207,7 +209,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
       bool ok = true;
       while (ok && next_piece()) {
         const Piece& w = s_plan[plan % kPlan];
-        const int32_t* table = a.bt.table + static_cast<size_t>(w.b) * a.bt.max_blocks;
+        const int32_t* table = a.bt.table + static_cast<size_t>(SH ? w.tb : w.b) * a.bt.max_blocks;
         // other tiles of the head read the same blocks
         const uint64_t pol = w.T * p.g > TM ? again : once;
         auto load = [&](const CUtensorMap* map, int blk) {
@@ -546,7 +548,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
       const int col0 = NQ == 1 ? s * (D / 2) : 0;
       const int xr = NQ == 1 ? r : s * 128 + r;           // row of the unit
       const int hq = w.h * p.g + x - t * p.g;
-      const size_t place = 2 * static_cast<size_t>(blockIdx.x) + (w.lo == 0 ? 1 : 0);
+      const size_t place = 2 * static_cast<size_t>(blockIdx.x) + (w.lo == (SH ? w.pre / BN : 0) ? 1 : 0);
       if (live) {
 #pragma unroll 1
         for (int q = 0; q < COLS; q += 32) {
@@ -565,7 +567,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
           }
           if (x < R) {
             if (poison) {
-              const int32_t* table = a.bt.table + static_cast<size_t>(w.b) * a.bt.max_blocks;
+              const int32_t* table = a.bt.table + static_cast<size_t>(SH ? w.tb : w.b) * a.bt.max_blocks;
               int jb = all_seen / BN * BN;
               jb = jb < w.lo * BN ? w.lo * BN : jb;
               const int je = w.hi * BN < w.len ? w.hi * BN : w.len;
@@ -581,11 +583,11 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
               }
             }
             if (whole) {
-              store_row<BF>(a, p, static_cast<int>(row), hq, col0 + q, y, m, l);
+              store_row<BF, SH>(a, p, static_cast<int>(row), hq, col0 + q, y, m, l, SH && w.pre);
             } else if (last) {
               float jm = m, jl = l;
               join_row<TM, D, 32, 1>(sc, w, xr, col0 + q, c, own, y, jm, jl);
-              store_row<BF>(a, p, static_cast<int>(row), hq, col0 + q, y, jm, jl);
+              store_row<BF, SH>(a, p, static_cast<int>(row), hq, col0 + q, y, jm, jl, SH && w.pre);
             } else {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
@@ -621,7 +623,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
             for (int ch = (tid / pad) * JN; ch < D; ch += (kSoft / pad) * JN) {
               float y[JN] = {}, jm, jl;
               join_row<TM, D, JN, 2>(sc, w, jr, ch, c, -1, y, jm, jl);
-              store_row<BF>(a, p, w.row0 + jt, w.h * p.g + jx - jt * p.g, ch, y, jm, jl);
+              store_row<BF, SH>(a, p, w.row0 + jt, w.h * p.g + jx - jt * p.g, ch, y, jm, jl, SH && w.pre);
             }
           }
         }
@@ -647,14 +649,14 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
 // channels of a row.  (8 units of 65 rows in 19 pieces each: 20 us where 8
 // CTAs join, 3 us here.)
 constexpr int kJoinThreads = 128;
-template <bool BF, int D>
+template <bool BF, int D, bool SH>
 __global__ void __launch_bounds__(kJoinThreads)
 k_join(const Pool p, const AttendArgs a, const Scratch sc) {
   pdl_wait();
   pdl_trigger();
   const int4 cut = sc.cut[blockIdx.x];
   if (cut.x < 2) return;
-  Walk<128, BN, kOver> w(p, a.bt, a.rows);
+  Walk<128, BN, kOver, SH> w(p, a.bt, a.rows);
   int flag = 0;
   w.sequence(cut.y, flag);
   w.first_cta = blockIdx.x;
@@ -664,34 +666,42 @@ k_join(const Pool p, const AttendArgs a, const Scratch sc) {
   float y[8] = {}, m, l;
   join_row<128, D, 8, 10>(sc, w, row, ch, a.scale * kL2E, -1, y, m, l);
   const int t = x / p.g;
-  store_row<BF>(a, p, w.row0 + t, cut.z * p.g + x - t * p.g, ch, y, m, l);
+  store_row<BF, SH>(a, p, w.row0 + t, cut.z * p.g + x - t * p.g, ch, y, m, l, SH && w.pre);
 }
 
-template <bool BF, int D, int NQ>
+template <bool BF, int D, int NQ, bool SH>
 cudaError_t go(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m, int ctas, bool defer,
                cudaStream_t s) {
-  const cudaError_t e = launch_pdl(k_attend_many<BF, D, NQ>, dim3(ctas), dim3(kThreads), Many<D, NQ>::SMEM, s, p, a, sc,
+  const cudaError_t e = launch_pdl(k_attend_many<BF, D, NQ, SH>, dim3(ctas), dim3(kThreads), Many<D, NQ>::SMEM, s, p, a, sc,
                                    defer ? 1 : 0, m.k_many, m.v_many);
   if (e != cudaSuccess || !defer) return e;
-  return launch_pdl(k_join<BF, D>, dim3(ctas, D / 8), dim3(kJoinThreads), 0, s, p, a, sc);
+  return launch_pdl(k_join<BF, D, SH>, dim3(ctas, D / 8), dim3(kJoinThreads), 0, s, p, a, sc);
 }
 template <bool BF, int D, int NQ>
 cudaError_t set() {
-  return cudaFuncSetAttribute(k_attend_many<BF, D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, Many<D, NQ>::SMEM);
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_attend_many<BF, D, NQ, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Many<D, NQ>::SMEM);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(k_attend_many<BF, D, NQ, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Many<D, NQ>::SMEM);
+}
+
+template <bool SH>
+cudaError_t launch_of(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m, int ctas, bool two_tiles,
+                      bool defer, cudaStream_t s) {
+  if (two_tiles) {
+    if (p.bf16) return p.d == 128 ? go<true, 128, 2, SH>(p, a, sc, m, ctas, defer, s) : go<true, 64, 2, SH>(p, a, sc, m, ctas, defer, s);
+    return p.d == 128 ? go<false, 128, 2, SH>(p, a, sc, m, ctas, defer, s) : go<false, 64, 2, SH>(p, a, sc, m, ctas, defer, s);
+  }
+  if (p.bf16) return p.d == 128 ? go<true, 128, 1, SH>(p, a, sc, m, ctas, defer, s) : go<true, 64, 1, SH>(p, a, sc, m, ctas, defer, s);
+  return p.d == 128 ? go<false, 128, 1, SH>(p, a, sc, m, ctas, defer, s) : go<false, 64, 1, SH>(p, a, sc, m, ctas, defer, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attend_many(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m, int ctas,
                                bool two_tiles, bool defer, cudaStream_t s) {
-  cudaError_t e;
-  if (two_tiles) {
-    if (p.bf16) e = p.d == 128 ? go<true, 128, 2>(p, a, sc, m, ctas, defer, s) : go<true, 64, 2>(p, a, sc, m, ctas, defer, s);
-    else e = p.d == 128 ? go<false, 128, 2>(p, a, sc, m, ctas, defer, s) : go<false, 64, 2>(p, a, sc, m, ctas, defer, s);
-  } else {
-    if (p.bf16) e = p.d == 128 ? go<true, 128, 1>(p, a, sc, m, ctas, defer, s) : go<true, 64, 1>(p, a, sc, m, ctas, defer, s);
-    else e = p.d == 128 ? go<false, 128, 1>(p, a, sc, m, ctas, defer, s) : go<false, 64, 1>(p, a, sc, m, ctas, defer, s);
-  }
+  const cudaError_t e = a.bt.phase ? launch_of<true>(p, a, sc, m, ctas, two_tiles, defer, s)
+                                   : launch_of<false>(p, a, sc, m, ctas, two_tiles, defer, s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

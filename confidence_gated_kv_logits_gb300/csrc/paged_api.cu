@@ -134,6 +134,7 @@ cudaError_t device_ready(int dev, Limits* limits) {
     cudaError_t e = cudaDeviceGetAttribute(&n.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = setup_attend_few();
     if (e == cudaSuccess) e = setup_attend_many();
+    if (e == cudaSuccess) e = setup_evict();
     if (e == cudaSuccess) e = few_clusters(2, &n.clusters2);
     if (e == cudaSuccess) e = few_clusters(4, &n.clusters4);
     if (e == cudaSuccess) e = few_clusters(8, &n.clusters8);
@@ -175,8 +176,108 @@ bool tickets_fit(int sms) {
 }
 
 Batch batch_of(const confkv_paged_batch* b) {
-  return Batch{b->batch, b->max_blocks, b->page_table, b->ctx_len, b->q_start, b->mask, b->mask ? b->mask_words : 0};
+  return Batch{b->batch, b->max_blocks, b->page_table, b->ctx_len, b->q_start, b->mask, b->mask ? b->mask_words : 0,
+               0, 0, b->batch, nullptr, nullptr};
 }
+
+// The checks that both appends share; null and *a filled where there is nothing to refuse.
+const char* append_args(const Pool& p, const confkv_paged_batch* batch, int layer, int rows, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                        const int32_t* positions, const float* inv_freq, int rotary_dim, int interleaved, AppendArgs* a) {
+  if (const char* m = check_batch(batch, false)) return m;
+  if (layer < 0 || layer >= p.L) return "no such layer";
+  if (rows < 0) return "rows < 0";
+  if (rows == 0) return nullptr;
+  if (!k || !v) return "null k or v";
+  if ((q == nullptr) != (q_out == nullptr)) return "q and q_out go together";
+  const int64_t wk = static_cast<int64_t>(p.Hkv) * p.d, wq = static_cast<int64_t>(p.Hq) * p.d;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out)) return "k, v, q and q_out must be 16-byte aligned";
+  if (!good_stride(k_stride, wk) || !good_stride(v_stride, wk) ||
+      (q && (!good_stride(q_stride, wq) || !good_stride(q_out_stride, wq))))
+    return "a row stride is below the row's width or no multiple of 8";
+  if (!inv_freq) rotary_dim = 0;
+  else if (rotary_dim < 16 || rotary_dim % 16 || rotary_dim > p.d) return "rotary_dim must be a multiple of 16 up to head_dim";
+  if (interleaved < 0 || interleaved > 1) return "interleaved must be 0 or 1";
+  if (!aligned4(positions) || !aligned4(inv_freq)) return "positions and inv_freq must be 4-byte aligned";
+  if (q && !(q == q_out && q_stride == q_out_stride) && rows_overlap(q, q_stride, wq, q_out, q_out_stride, wq, rows))
+    return "q_out overlaps q and is not q itself";
+  if (q && (rows_overlap(k, k_stride, wk, q_out, q_out_stride, wq, rows) ||
+            rows_overlap(v, v_stride, wk, q_out, q_out_stride, wq, rows)))
+    return "q_out overlaps k or v";
+  *a = AppendArgs{};
+  a->bt = batch_of(batch);
+  a->layer = layer;
+  a->rows = rows;
+  a->k = static_cast<const uint16_t*>(k);
+  a->v = static_cast<const uint16_t*>(v);
+  a->q = static_cast<const uint16_t*>(q);
+  a->q_out = static_cast<uint16_t*>(q_out);
+  a->ks = k_stride;
+  a->vs = v_stride;
+  a->qs = q_stride;
+  a->qos = q_out_stride;
+  a->pos = positions;
+  a->inv_freq = inv_freq;
+  a->rot = rotary_dim;
+  a->interleaved = interleaved;
+  return nullptr;
+}
+
+// The checks that both attends share; null and *a filled where there is nothing to refuse.
+const char* attend_args(const Pool& p, const confkv_paged_batch* batch, int layer, int rows, const void* q, int64_t q_stride,
+                        void* out, float* lse, float scale, AttendArgs* a) {
+  if (const char* m = check_batch(batch, true)) return m;
+  if (layer < 0 || layer >= p.L) return "no such layer";
+  if (rows < 0) return "rows < 0";
+  if (static_cast<int64_t>(rows) * p.Hq >= (1ll << 31)) return "rows x heads must be below 2^31";
+  if (rows == 0) return nullptr;
+  if (!q || !out) return "null q or out";
+  const int64_t wq = static_cast<int64_t>(p.Hq) * p.d;
+  if (!aligned16(q) || !aligned16(out) || !aligned4(lse)) return "q and out must be 16-byte aligned, lse 4-byte";
+  if (!good_stride(q_stride, wq)) return "q_stride is below the row's width or no multiple of 8";
+  if (!(scale >= 0.0f && std::isfinite(scale))) return "scale must be finite and not negative";
+  if (rows_overlap(q, q_stride, wq, out, wq, wq, rows)) return "out overlaps q";
+  const size_t nr = static_cast<size_t>(rows);
+  if (lse && (overlap(lse, nr * p.Hq * 4, out, nr * wq * 2) || overlap(lse, nr * p.Hq * 4, q, ((nr - 1) * q_stride + wq) * 2)))
+    return "lse overlaps q or out";
+  *a = AttendArgs{batch_of(batch), layer, rows, static_cast<const uint16_t*>(q), q_stride, static_cast<uint16_t*>(out), lse,
+                  scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(p.d)), nullptr, nullptr};
+  return nullptr;
+}
+
+// Launches the attention of `batch` sequences (groups, over a shared prefix).
+cudaError_t attend(const confkv_paged& kv, const AttendArgs& a, int batch, cudaStream_t s) {
+  const Pool& p = kv.pool;
+  // By the query rows of a sequence's KV head, on average (measured on GB300, us):
+  //  - up to 16 the streaming kernel (1 x 32768 tokens, 40/8 heads, d = 128: 10 rows 37
+  //    streamed, 42 with the padded tiles of 128; 20 rows 62 in two streamed tiles, 42)
+  //  - from 257 on units of two tiles, which share each K and V block, if they fill half
+  //    the GPU (8 x 8192 tokens: 385 rows 152, 194 in units of one tile; 1 x 32768 tokens,
+  //    whose 16 units do not: 260 rows 110, 87 in units of one)
+  //  - one kernel for the whole batch, so that chunks beside single tokens go with the
+  //    average: 128 rows over 2048 tokens and 64 x 1 row over 2048 (40/8 heads, d =
+  //    128) take 135 together, 32 and 88 in a call each; 512 rows over 2048 and 255 x 1
+  //    row 504, 62 and 310
+  //  - far fewer units of one tile than CTAs are cut into many pieces each, which a
+  //    kernel of its own joins on all SMs (1 x 32768 tokens, 65 rows: 58 joined by the
+  //    last CTA of each unit, 42)
+  const int64_t heads = static_cast<int64_t>(a.rows) * p.g, per = heads / batch;
+  if (per <= kFewRows) {
+    // at most (a row's heads fill one tile, or its sequence's last is part-filled)
+    const int64_t units = p.Hkv * std::min<int64_t>(static_cast<int64_t>(a.rows) * ((p.g + kFewRows - 1) / kFewRows),
+                                                    heads / kFewRows + batch);
+    const int cl = few_cluster(kv, batch, units, static_cast<int64_t>(a.bt.max_blocks) * p.ps);
+    const int ctas = cl > 1 ? cl * static_cast<int>(units) : kFewCtasPerSm * kv.limits.sms;
+    return launch_attend_few(p, a, kv.scratch, kv.maps, ctas, cl, s);
+  }
+  const int sms = kv.limits.sms;
+  const int64_t ones = p.Hkv * (heads / 128 + batch), twos = p.Hkv * (heads / kManyRows + batch);
+  const bool two = per > kManyRows && 2 * twos >= sms;
+  return launch_attend_many(p, a, kv.scratch, kv.maps, sms, two, !two && 4 * ones <= sms, s);
+}
+
+// [rows][heads][d] accumulators, [rows][heads] (maximum, sum)
+size_t partial_bytes(int rows, int heads, int d) { return static_cast<size_t>(rows) * heads * (d + 2) * sizeof(float); }
 
 }  // namespace
 
@@ -268,89 +369,182 @@ int confkv_paged_append(confkv_paged* kv, const confkv_paged_batch* batch, int l
                         void* q_out, int64_t q_out_stride, const int32_t* positions, const float* inv_freq,
                         int rotary_dim, int interleaved, void* stream) {
   if (!kv) return CONFKV_ERR_INVALID_ARG;
-  const Pool& p = kv->pool;
-  if (const char* m = check_batch(batch, false)) return fail(kv, CONFKV_ERR_INVALID_ARG, m);
-  if (layer < 0 || layer >= p.L) return fail(kv, CONFKV_ERR_INVALID_ARG, "no such layer");
-  if (rows < 0) return fail(kv, CONFKV_ERR_INVALID_ARG, "rows < 0");
+  AppendArgs a{};
+  const char* m = append_args(kv->pool, batch, layer, rows, k, k_stride, v, v_stride, q, q_stride, q_out, q_out_stride,
+                              positions, inv_freq, rotary_dim, interleaved, &a);
+  if (m) return fail(kv, CONFKV_ERR_INVALID_ARG, m);
   if (rows == 0) return CONFKV_OK;
-  if (!k || !v) return fail(kv, CONFKV_ERR_INVALID_ARG, "null k or v");
-  if ((q == nullptr) != (q_out == nullptr)) return fail(kv, CONFKV_ERR_INVALID_ARG, "q and q_out go together");
-  const int64_t wk = static_cast<int64_t>(p.Hkv) * p.d, wq = static_cast<int64_t>(p.Hq) * p.d;
-  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out))
-    return fail(kv, CONFKV_ERR_INVALID_ARG, "k, v, q and q_out must be 16-byte aligned");
-  if (!good_stride(k_stride, wk) || !good_stride(v_stride, wk) ||
-      (q && (!good_stride(q_stride, wq) || !good_stride(q_out_stride, wq))))
-    return fail(kv, CONFKV_ERR_INVALID_ARG, "a row stride is below the row's width or no multiple of 8");
-  if (!inv_freq) rotary_dim = 0;
-  else if (rotary_dim < 16 || rotary_dim % 16 || rotary_dim > p.d)
-    return fail(kv, CONFKV_ERR_INVALID_ARG, "rotary_dim must be a multiple of 16 up to head_dim");
-  if (interleaved < 0 || interleaved > 1) return fail(kv, CONFKV_ERR_INVALID_ARG, "interleaved must be 0 or 1");
-  if (!aligned4(positions) || !aligned4(inv_freq))
-    return fail(kv, CONFKV_ERR_INVALID_ARG, "positions and inv_freq must be 4-byte aligned");
-  if (q && !(q == q_out && q_stride == q_out_stride) &&
-      rows_overlap(q, q_stride, wq, q_out, q_out_stride, wq, rows))
-    return fail(kv, CONFKV_ERR_INVALID_ARG, "q_out overlaps q and is not q itself");
-  if (q && (rows_overlap(k, k_stride, wk, q_out, q_out_stride, wq, rows) ||
-            rows_overlap(v, v_stride, wk, q_out, q_out_stride, wq, rows)))
-    return fail(kv, CONFKV_ERR_INVALID_ARG, "q_out overlaps k or v");
   DeviceGuard guard(kv->device);
-  AppendArgs a{batch_of(batch), layer, rows, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
-               static_cast<const uint16_t*>(q), static_cast<uint16_t*>(q_out), k_stride, v_stride, q_stride,
-               q_out_stride, positions, inv_freq, rotary_dim, interleaved};
-  return launched(kv, launch_append(p, a, static_cast<cudaStream_t>(stream)));
+  return launched(kv, launch_append(kv->pool, a, static_cast<cudaStream_t>(stream)));
+}
+
+int confkv_paged_append_normed(confkv_paged* kv, const confkv_paged_batch* batch, int layer, int rows, const void* k,
+                               int64_t k_stride, const void* v, int64_t v_stride, const void* q, int64_t q_stride,
+                               void* q_out, int64_t q_out_stride, const int32_t* positions, const float* inv_freq,
+                               int rotary_dim, int interleaved, const confkv_paged_norm* norm, void* stream) {
+  if (!kv) return CONFKV_ERR_INVALID_ARG;
+  const Pool& p = kv->pool;
+  if (!norm) return fail(kv, CONFKV_ERR_INVALID_ARG, "null norm");
+  AppendArgs a{};
+  const char* m = append_args(p, batch, layer, rows, k, k_stride, v, v_stride, q, q_stride, q_out, q_out_stride,
+                              positions, inv_freq, rotary_dim, interleaved, &a);
+  if (m) return fail(kv, CONFKV_ERR_INVALID_ARG, m);
+  if (rows > 0 && norm->q_norm && !q) return fail(kv, CONFKV_ERR_INVALID_ARG, "q_norm without q");
+  if (norm->q_norm || norm->k_norm) {
+    if (norm->norm_dtype != CONFKV_FP32 && norm->norm_dtype != (p.bf16 ? CONFKV_BF16 : CONFKV_FP16))
+      return fail(kv, CONFKV_ERR_INVALID_ARG, "norm weights must be fp32 or of the cache's type");
+    if (!(norm->eps >= 1e-12f && std::isfinite(norm->eps)))
+      return fail(kv, CONFKV_ERR_INVALID_ARG, "eps must be finite and 1e-12 or more");
+  }
+  const bool wide = norm->norm_dtype == CONFKV_FP32;
+  const uintptr_t elem = wide ? 3 : 1;
+  if (((reinterpret_cast<uintptr_t>(norm->q_norm) | reinterpret_cast<uintptr_t>(norm->k_norm)) & elem) || !aligned4(norm->axis))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "q_norm and k_norm must be aligned to their type, axis 4-byte");
+  if (norm->axis && (norm->axes < 1 || norm->axes > 8 || !positions || !inv_freq))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "axis needs positions, inv_freq and 1 .. 8 axes");
+  if (q_out && rows > 0) {
+    const size_t n = (static_cast<size_t>(rows - 1) * q_out_stride + static_cast<size_t>(p.Hq) * p.d) * 2;
+    const size_t nw = static_cast<size_t>(p.d) * (elem + 1), nf = static_cast<size_t>(a.rot) * 2;
+    if ((norm->q_norm && overlap(q_out, n, norm->q_norm, nw)) || (norm->k_norm && overlap(q_out, n, norm->k_norm, nw)) ||
+        (positions && overlap(q_out, n, positions, static_cast<size_t>(rows) * (norm->axis ? norm->axes : 1) * 4)) ||
+        (inv_freq && overlap(q_out, n, inv_freq, nf)) || (norm->axis && overlap(q_out, n, norm->axis, nf)))
+      return fail(kv, CONFKV_ERR_INVALID_ARG, "q_out overlaps an input");
+  }
+  if (rows == 0) return CONFKV_OK;
+  a.q_norm = norm->q_norm;
+  a.k_norm = norm->k_norm;
+  a.norm_fp32 = wide;
+  a.eps = norm->eps;
+  a.axis = norm->axis;
+  a.axes = norm->axis ? norm->axes : 1;
+  DeviceGuard guard(kv->device);
+  return launched(kv, launch_append_normed(p, a, static_cast<cudaStream_t>(stream)));
 }
 
 int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int layer, int rows, const void* q,
                         int64_t q_stride, void* out, float* lse, float scale, void* stream) {
+  if (!kv) return CONFKV_ERR_INVALID_ARG;
+  AttendArgs a{};
+  if (const char* m = attend_args(kv->pool, batch, layer, rows, q, q_stride, out, lse, scale, &a))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, m);
+  if (rows == 0) return CONFKV_OK;
+  DeviceGuard guard(kv->device);
+  return launched(kv, attend(*kv, a, batch->batch, static_cast<cudaStream_t>(stream)));
+}
+
+size_t confkv_paged_partial(int rows, int heads, int head_dim) {
+  if (rows < 0 || heads < 1 || (head_dim != 64 && head_dim != 128) || static_cast<int64_t>(rows) * heads >= (1ll << 31)) return 0;
+  return partial_bytes(rows > 0 ? rows : 1, heads, head_dim);
+}
+
+int confkv_paged_attend_shared(confkv_paged* kv, const confkv_paged_batch* batch, const confkv_paged_prefix* prefix,
+                               int layer, int rows, const void* q, int64_t q_stride, void* out, float* lse, float scale,
+                               void* stream) {
+  if (!kv) return CONFKV_ERR_INVALID_ARG;
+  const Pool& p = kv->pool;
+  if (!prefix) return fail(kv, CONFKV_ERR_INVALID_ARG, "null prefix");
+  AttendArgs a{};
+  if (const char* m = attend_args(p, batch, layer, rows, q, q_stride, out, lse, scale, &a))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, m);
+  if (prefix->groups < 1 || prefix->groups > batch->batch)
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "groups must be in 1 .. batch");
+  if (!prefix->group_start || !prefix->prefix_len || !prefix->partial)
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "null group_start, prefix_len or partial");
+  if (!aligned4(prefix->group_start) || !aligned4(prefix->prefix_len) || !aligned16(prefix->partial))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "group_start and prefix_len must be 4-byte aligned, partial 16-byte");
+  if (rows == 0) return CONFKV_OK;
+  const size_t np = partial_bytes(rows, p.Hq, p.d), nr = static_cast<size_t>(rows), wq = static_cast<size_t>(p.Hq) * p.d;
+  if (prefix->partial_bytes < np) return fail(kv, CONFKV_ERR_CAPACITY, "partial is too small for the rows");
+  if (overlap(prefix->partial, np, q, ((nr - 1) * q_stride + wq) * 2) || overlap(prefix->partial, np, out, nr * wq * 2) ||
+      (lse && overlap(prefix->partial, np, lse, nr * p.Hq * 4)))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "partial overlaps q, out or lse");
+  DeviceGuard guard(kv->device);
+  a.part = static_cast<float*>(prefix->partial);
+  a.part_ml = a.part + nr * wq;
+  a.bt.groups = prefix->groups;
+  a.bt.group_start = prefix->group_start;
+  a.bt.prefix_len = prefix->prefix_len;
+  // the groups' rows over their prefixes, then each sequence's over the rest of its own
+  AttendArgs shared = a;
+  shared.bt.phase = 1;
+  shared.bt.B = prefix->groups;
+  shared.bt.mask = nullptr;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = attend(*kv, shared, prefix->groups, st);
+  a.bt.phase = 2;
+  if (e == cudaSuccess) e = attend(*kv, a, batch->batch, st);
+  return launched(kv, e);
+}
+
+int confkv_paged_weigh(confkv_paged* kv, const confkv_paged_batch* batch, int layer, int rows, const void* q, int64_t q_stride,
+                       const float* lse, const float* mass, float* mass_out, int32_t* pos, int cap, const int32_t* positions,
+                       float decay, float gain, float scale, void* stream) {
   if (!kv) return CONFKV_ERR_INVALID_ARG;
   const Pool& p = kv->pool;
   if (const char* m = check_batch(batch, true)) return fail(kv, CONFKV_ERR_INVALID_ARG, m);
   if (layer < 0 || layer >= p.L) return fail(kv, CONFKV_ERR_INVALID_ARG, "no such layer");
   if (rows < 0) return fail(kv, CONFKV_ERR_INVALID_ARG, "rows < 0");
   if (static_cast<int64_t>(rows) * p.Hq >= (1ll << 31)) return fail(kv, CONFKV_ERR_INVALID_ARG, "rows x heads must be below 2^31");
+  if (cap < 1) return fail(kv, CONFKV_ERR_INVALID_ARG, "cap must be positive");
   if (rows == 0) return CONFKV_OK;
-  if (!q || !out) return fail(kv, CONFKV_ERR_INVALID_ARG, "null q or out");
   const int64_t wq = static_cast<int64_t>(p.Hq) * p.d;
-  if (!aligned16(q) || !aligned16(out) || !aligned4(lse))
-    return fail(kv, CONFKV_ERR_INVALID_ARG, "q and out must be 16-byte aligned, lse 4-byte");
+  if (!q || !lse || !mass || !mass_out) return fail(kv, CONFKV_ERR_INVALID_ARG, "null q, lse, mass or mass_out");
+  if (!aligned16(q) || !aligned4(lse) || !aligned4(mass) || !aligned4(mass_out) || !aligned4(pos) || !aligned4(positions))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "q must be 16-byte aligned, lse, mass, mass_out, pos and positions 4-byte");
   if (!good_stride(q_stride, wq)) return fail(kv, CONFKV_ERR_INVALID_ARG, "q_stride is below the row's width or no multiple of 8");
   if (!(scale >= 0.0f && std::isfinite(scale))) return fail(kv, CONFKV_ERR_INVALID_ARG, "scale must be finite and not negative");
-  if (rows_overlap(q, q_stride, wq, out, wq, wq, rows))
-    return fail(kv, CONFKV_ERR_INVALID_ARG, "out overlaps q");
-  const size_t nr = static_cast<size_t>(rows);
-  if (lse && (overlap(lse, nr * p.Hq * 4, out, nr * wq * 2) ||
-              overlap(lse, nr * p.Hq * 4, q, ((nr - 1) * q_stride + wq) * 2)))
-    return fail(kv, CONFKV_ERR_INVALID_ARG, "lse overlaps q or out");
+  if (!std::isfinite(decay) || !std::isfinite(gain)) return fail(kv, CONFKV_ERR_INVALID_ARG, "decay and gain must be finite");
+  const size_t nm = static_cast<size_t>(batch->batch) * p.Hkv * cap * 4, nr = static_cast<size_t>(rows);
+  if (mass != mass_out && overlap(mass, nm, mass_out, nm))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "mass_out overlaps mass and is not mass itself");
+  for (const void* out : {static_cast<const void*>(mass_out), static_cast<const void*>(pos)})
+    if (out && (overlap(out, nm, q, ((nr - 1) * q_stride + wq) * 2) || overlap(out, nm, lse, nr * p.Hq * 4) ||
+                (positions && overlap(out, nm, positions, nr * 4))))
+      return fail(kv, CONFKV_ERR_INVALID_ARG, "mass_out or pos overlaps an input");
+  if (pos && (overlap(pos, nm, mass, nm) || overlap(pos, nm, mass_out, nm)))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "pos overlaps mass or mass_out");
   DeviceGuard guard(kv->device);
-  AttendArgs a{batch_of(batch), layer, rows, static_cast<const uint16_t*>(q), q_stride, static_cast<uint16_t*>(out),
-               lse, scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(p.d))};
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // By the query rows of a sequence's KV head, on average (measured on GB300, us):
-  //  - up to 16 the streaming kernel (1 x 32768 tokens, 40/8 heads, d = 128: 10 rows 37
-  //    streamed, 42 with the padded tiles of 128; 20 rows 62 in two streamed tiles, 42)
-  //  - from 257 on units of two tiles, which share each K and V block, if they fill half
-  //    the GPU (8 x 8192 tokens: 385 rows 152, 194 in units of one tile; 1 x 32768 tokens,
-  //    whose 16 units do not: 260 rows 110, 87 in units of one)
-  //  - one kernel for the whole batch, so that chunks beside single tokens go with the
-  //    average: 128 rows over 2048 tokens and 64 x 1 row over 2048 (40/8 heads, d =
-  //    128) take 135 together, 32 and 88 in a call each; 512 rows over 2048 and 255 x 1
-  //    row 504, 62 and 310
-  //  - far fewer units of one tile than CTAs are cut into many pieces each, which a
-  //    kernel of its own joins on all SMs (1 x 32768 tokens, 65 rows: 58 joined by the
-  //    last CTA of each unit, 42)
-  const int64_t heads = static_cast<int64_t>(rows) * p.g, per = heads / batch->batch;
-  if (per <= kFewRows) {
-    // at most (a row's heads fill one tile, or its sequence's last is part-filled)
-    const int64_t units = p.Hkv * std::min<int64_t>(static_cast<int64_t>(rows) * ((p.g + kFewRows - 1) / kFewRows),
-                                                    heads / kFewRows + batch->batch);
-    const int cl = few_cluster(*kv, batch->batch, units, static_cast<int64_t>(batch->max_blocks) * p.ps);
-    const int ctas = cl > 1 ? cl * static_cast<int>(units) : kFewCtasPerSm * kv->limits.sms;
-    return launched(kv, launch_attend_few(p, a, kv->scratch, kv->maps, ctas, cl, st));
-  }
-  const int sms = kv->limits.sms;
-  const int64_t ones = p.Hkv * (heads / 128 + batch->batch), twos = p.Hkv * (heads / kManyRows + batch->batch);
-  const bool two = per > kManyRows && 2 * twos >= sms;
-  return launched(kv, launch_attend_many(p, a, kv->scratch, kv->maps, sms, two, !two && 4 * ones <= sms, st));
+  const WeighArgs a{batch_of(batch), layer, rows, static_cast<const uint16_t*>(q), q_stride, lse, mass, mass_out, pos, cap,
+                    positions, decay, gain, scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(p.d))};
+  return launched(kv, launch_weigh(p, a, static_cast<cudaStream_t>(stream)));
+}
+
+int confkv_paged_evict(confkv_paged* kv, int batch, int max_blocks, const int32_t* page_table, const int32_t* length,
+                       int per_layer, const float* mass, const int32_t* pos, int cap, const int32_t* keep,
+                       const int32_t* first, int protect, float* mass_out, int32_t* pos_out, int32_t* new_len, void* stream) {
+  if (!kv) return CONFKV_ERR_INVALID_ARG;
+  const Pool& p = kv->pool;
+  if (batch < 0 || batch > 65536 || max_blocks < 1) return fail(kv, CONFKV_ERR_INVALID_ARG, "batch outside 0 .. 65536 or max_blocks < 1");
+  if (cap < 1 || cap > kMaxEvictTokens) return fail(kv, CONFKV_ERR_INVALID_ARG, "cap must be in 1 .. 524288");
+  if (protect < 0) return fail(kv, CONFKV_ERR_INVALID_ARG, "protect < 0");
+  if (per_layer < 0 || per_layer > 1) return fail(kv, CONFKV_ERR_INVALID_ARG, "per_layer must be 0 or 1");
+  if (static_cast<int64_t>(p.L) * batch * p.Hkv >= (1ll << 31)) return fail(kv, CONFKV_ERR_INVALID_ARG, "layers x batch x kv_heads must be below 2^31");
+  if (batch == 0) return CONFKV_OK;
+  if (!page_table || !length || !mass || !pos || !keep || !mass_out || !pos_out || !new_len)
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "null argument");
+  if (!aligned4(page_table) || !aligned4(length) || !aligned4(mass) || !aligned4(pos) || !aligned4(keep) || !aligned4(first) ||
+      !aligned4(mass_out) || !aligned4(pos_out) || !aligned4(new_len))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "arguments must be 4-byte aligned");
+  const size_t nb = static_cast<size_t>(batch) * 4, ns = per_layer ? nb * p.L : nb;
+  const size_t nm = static_cast<size_t>(p.L) * batch * p.Hkv * cap * 4;
+  if ((mass == mass_out) != (pos == pos_out)) return fail(kv, CONFKV_ERR_INVALID_ARG, "mass and pos are kept in place both or neither");
+  if (mass != mass_out && (overlap(mass, nm, mass_out, nm) || overlap(pos, nm, pos_out, nm)))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "an output overlaps its input and is not the input itself");
+  struct Range {
+    const void* at;
+    size_t n;
+  };
+  const Range in[] = {{page_table, nb * max_blocks}, {length, ns}, {keep, ns}, {first, first ? nb : 0}},
+              out[] = {{mass_out, nm}, {pos_out, nm}, {new_len, ns}};
+  for (const Range& o : out)
+    for (const Range& r : in)
+      if (r.n && overlap(o.at, o.n, r.at, r.n)) return fail(kv, CONFKV_ERR_INVALID_ARG, "an output overlaps an input");
+  if (overlap(mass_out, nm, pos_out, nm) || overlap(mass_out, nm, new_len, ns) || overlap(pos_out, nm, new_len, ns) ||
+      overlap(mass_out, nm, pos, nm) || overlap(pos_out, nm, mass, nm) || overlap(new_len, ns, mass, nm) || overlap(new_len, ns, pos, nm))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "outputs overlap one another or an input");
+  DeviceGuard guard(kv->device);
+  const EvictArgs a{batch, max_blocks, cap, protect, per_layer, page_table, length, keep, first, mass, pos, mass_out, pos_out, new_len};
+  return launched(kv, launch_evict(p, a, static_cast<cudaStream_t>(stream)));
 }
 
 int confkv_paged_commit(confkv_paged* kv, int batch, int max_blocks, const int32_t* page_table,

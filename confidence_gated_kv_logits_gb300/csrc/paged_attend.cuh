@@ -41,10 +41,44 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
   return ((x & E) == E ? 0xffffu : 0u) | (((x >> 16) & E) == E ? 0xffff0000u : 0u);
 }
 
-// N channels of an output row: acc / l (0 where nothing was seen), rounded once
-template <bool BF, int N>
-__device__ __forceinline__ void store_row(const AttendArgs& a, const Pool& p, int row, int hq, int ch, const float (&x)[N],
-                                          float m, float l) {
+// N channels of an output row: acc / l (0 where nothing was seen), rounded once.
+// SH: over a shared prefix, phase 1 leaves the row's partial result as it is, phase 2
+// joins it (`pre`: there is one) with its own, the prefix first.
+template <bool BF, bool SH, int N>
+__device__ __forceinline__ void store_row(const AttendArgs& a, const Pool& p, int row, int hq, int ch, float (&x)[N],
+                                          float m, float l, bool pre) {
+  if constexpr (SH) {
+    const size_t at = static_cast<size_t>(row) * p.Hq + hq;
+    float* acc = a.part + at * p.d + ch;
+    if (a.bt.phase == 1) {
+#pragma unroll
+      for (int e = 0; e < N; e += 4) *reinterpret_cast<float4*>(acc + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+      if (ch == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m, l);
+      return;
+    }
+    if (pre) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + 2 * at));
+      // a part in which the row saw nothing has the sum 0 and is left out; NaN scores leave
+      // the maximum at -inf, but the sum NaN, which has to reach the row
+      const float c = a.scale * 1.4426950408889634f, top = fmaxf(ml.x, m);
+      const bool none0 = ml.y == 0.0f, none1 = l == 0.0f;
+      const float f0 = ex2f((ml.x - top) * c), f1 = ex2f((m - top) * c);
+      auto join = [&](float prefix, float own) {
+        const float y = none1 ? 0.0f : f1 * own;
+        return none0 ? y : fmaf(f0, prefix, y);
+      };
+#pragma unroll
+      for (int e = 0; e < N; e += 4) {
+        const float4 z = __ldcg(reinterpret_cast<const float4*>(acc + e));
+        x[e] = join(z.x, x[e]);
+        x[e + 1] = join(z.y, x[e + 1]);
+        x[e + 2] = join(z.z, x[e + 2]);
+        x[e + 3] = join(z.w, x[e + 3]);
+      }
+      l = join(ml.y, l);
+      m = top;
+    }
+  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const size_t at = static_cast<size_t>(row) * p.Hq + hq;
   uint16_t* out = a.out + at * p.d + ch;

@@ -32,6 +32,11 @@ struct Batch {
   const int32_t* q_start;
   const uint32_t* mask;
   int mask_words;
+  // attention over a shared prefix: groups of neighbouring sequences (phase 1: B
+  // is the groups, seqs the sequences; phase 2: B is the sequences)
+  int phase, groups, seqs;
+  const int32_t* group_start;
+  const int32_t* prefix_len;
 };
 
 struct AppendArgs {
@@ -42,9 +47,16 @@ struct AppendArgs {
   const uint16_t* q;
   uint16_t* q_out;
   long long ks, vs, qs, qos;    // row strides in elements
-  const int32_t* pos;
+  const int32_t* pos;           // [rows], with axis [rows][axes]
   const float* inv_freq;
   int rot, interleaved;
+  // append_normed
+  const void* q_norm;
+  const void* k_norm;
+  int norm_fp32;                // weights are fp32, else of the cache's type
+  float eps;
+  const int32_t* axis;          // [rot / 2] or null
+  int axes;
 };
 
 struct AttendArgs {
@@ -55,6 +67,8 @@ struct AttendArgs {
   uint16_t* out;
   float* lse;
   float scale;
+  float* part;                  // shared prefix: [rows][heads][d] accumulators
+  float* part_ml;               // [rows][heads][2] (maximum, sum)
 };
 
 struct CommitArgs {
@@ -63,6 +77,33 @@ struct CommitArgs {
   const int32_t* ctx;
   const int32_t* path;
   const int32_t* path_len;
+  int32_t* new_len;
+};
+
+struct WeighArgs {
+  Batch bt;
+  int layer, rows;
+  const uint16_t* q;
+  long long qs;
+  const float* lse;
+  const float* mass;
+  float* mass_out;
+  int32_t* pos;
+  int cap;
+  const int32_t* positions;
+  float decay, gain, scale;
+};
+
+struct EvictArgs {
+  int B, max_blocks, cap, protect, per_layer;
+  const int32_t* table;
+  const int32_t* len;
+  const int32_t* keep;
+  const int32_t* first;
+  const float* mass;
+  const int32_t* pos;
+  float* mass_out;
+  int32_t* pos_out;
   int32_t* new_len;
 };
 
@@ -92,6 +133,11 @@ struct BeamArgs {
 };
 
 cudaError_t launch_append(const Pool& p, const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_append_normed(const Pool& p, const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_weigh(const Pool& p, const WeighArgs& a, cudaStream_t s);
+cudaError_t launch_evict(const Pool& p, const EvictArgs& a, cudaStream_t s);
+cudaError_t setup_evict();
+constexpr int kMaxEvictTokens = 1 << 19;            // cap limit of evict (confkv_paged.h)
 cudaError_t launch_commit(const Pool& p, const CommitArgs& a, cudaStream_t s);
 cudaError_t launch_fork(const Pool& p, const ForkArgs& a, cudaStream_t s);
 cudaError_t launch_beam(const BeamArgs& a, cudaStream_t s);

@@ -151,36 +151,131 @@ bool ready(const Object* ob) {
   return false;
 }
 
+// What both appends take of layer, k, v, q, q_out, .., inv_freq, interleaved, stream.
+struct Append {
+  int layer, rotary = 0, interleaved;
+  int64_t rows, ks, vs, qs = 0, os = 0;
+  void *k, *v, *q = nullptr, *out = nullptr, *pos = nullptr, *inv = nullptr, *s;
+};
+bool append_of(Object* ob, PyObject* const* a, PyObject* inv_freq, PyObject* interleaved, Append* x) {
+  if (!integer(a[0], &x->layer) || !rows_count(a[1], "k", &x->rows) ||
+      !rows_of(ob, a[1], "k", x->rows, ob->sizes[1], &x->k, &x->ks) || !rows_of(ob, a[2], "v", x->rows, ob->sizes[1], &x->v, &x->vs))
+    return false;
+  if (a[3] != Py_None || a[4] != Py_None) {
+    if (a[3] == Py_None || a[4] == Py_None) {
+      PyErr_SetString(PyExc_ValueError, "q and q_out go together");
+      return false;
+    }
+    if (!rows_of(ob, a[3], "q", x->rows, ob->sizes[0], &x->q, &x->qs) ||
+        !rows_of(ob, a[4], "q_out", x->rows, ob->sizes[0], &x->out, &x->os))
+      return false;
+  }
+  if (inv_freq != Py_None) {
+    int64_t half;
+    if (!rows_count(inv_freq, "inv_freq", &half) || !dense(ob, inv_freq, "inv_freq", at::kFloat, {half}, &x->inv)) return false;
+    x->rotary = half > 4096 ? 8192 : static_cast<int>(2 * half);
+  }
+  x->interleaved = PyObject_IsTrue(interleaved);
+  return x->interleaved >= 0;
+}
+
 // object, batch, layer, k, v, q, q_out, positions, inv_freq, interleaved, stream
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count(n, 11)) return nullptr;
   Object* ob = pointer<Object>(a[0]);
   const confkv_paged_batch* batch = pointer<confkv_paged_batch>(a[1]);
-  int layer;
-  int64_t rows, ks, vs, qs = 0, os = 0;
-  void *k, *v, *q = nullptr, *out = nullptr, *pos = nullptr, *inv = nullptr, *s;
-  int rotary = 0;
-  if (!ready(ob) || !integer(a[2], &layer) || !rows_count(a[3], "k", &rows) ||
-      !rows_of(ob, a[3], "k", rows, ob->sizes[1], &k, &ks) || !rows_of(ob, a[4], "v", rows, ob->sizes[1], &v, &vs))
+  Append x;
+  if (!ready(ob) || !append_of(ob, a + 2, a[8], a[9], &x) ||
+      (a[7] != Py_None && !dense(ob, a[7], "positions", at::kInt, {x.rows}, &x.pos)) || !stream_of(ob, a[10], &x.s))
     return nullptr;
-  if (a[5] != Py_None || a[6] != Py_None) {
-    if (a[5] == Py_None || a[6] == Py_None) {
-      PyErr_SetString(PyExc_ValueError, "q and q_out go together");
+  return PyLong_FromLong(confkv_paged_append(ob->kv, batch, x.layer, static_cast<int>(x.rows), x.k, x.ks, x.v, x.vs, x.q, x.qs,
+                                             x.out, x.os, static_cast<int32_t*>(x.pos), static_cast<float*>(x.inv), x.rotary,
+                                             x.interleaved, x.s));
+}
+
+// weights [head_dim], fp32 or of the cache's type, both alike
+bool weights(Object* ob, PyObject* o, const char* name, int* type, const void** out) {
+  if (o == Py_None) return true;
+  const at::Tensor* t = tensor(o, name);
+  if (!t) return false;
+  const int mine = t->scalar_type() == at::kFloat ? CONFKV_FP32 : ob->dtype;
+  void* at;
+  if (!dense(ob, o, name, type_of(mine), {ob->sizes[2]}, &at)) return false;
+  if (*type >= 0 && *type != mine) {
+    PyErr_SetString(PyExc_ValueError, "q_norm and k_norm differ in type");
+    return false;
+  }
+  *type = mine;
+  *out = at;
+  return true;
+}
+
+// object, batch, layer, k, v, q, q_out, positions, inv_freq, interleaved, q_norm, k_norm, eps, axis, stream
+PyObject* append_normed(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 15)) return nullptr;
+  Object* ob = pointer<Object>(a[0]);
+  const confkv_paged_batch* batch = pointer<confkv_paged_batch>(a[1]);
+  Append x;
+  confkv_paged_norm norm = {};
+  int type = -1;
+  if (!ready(ob)) return nullptr;
+  const double eps = PyFloat_AsDouble(a[12]);
+  if (eps == -1.0 && PyErr_Occurred()) return nullptr;
+  if (!append_of(ob, a + 2, a[8], a[9], &x) || !weights(ob, a[10], "q_norm", &type, &norm.q_norm) ||
+      !weights(ob, a[11], "k_norm", &type, &norm.k_norm))
+    return nullptr;
+  if (a[13] != Py_None) {
+    void* axis;
+    int64_t rows = x.rows, axes = 0;
+    if (!dense(ob, a[13], "axis", at::kInt, {x.rotary / 2}, &axis)) return nullptr;
+    if (a[7] == Py_None) {
+      PyErr_SetString(PyExc_ValueError, "axis needs positions [rows, axes]");
       return nullptr;
     }
-    if (!rows_of(ob, a[5], "q", rows, ob->sizes[0], &q, &qs) || !rows_of(ob, a[6], "q_out", rows, ob->sizes[0], &out, &os))
-      return nullptr;
+    if (!matrix(a[7], "positions", &rows, &axes) || !dense(ob, a[7], "positions", at::kInt, {x.rows, axes}, &x.pos)) return nullptr;
+    norm.axis = static_cast<int32_t*>(axis);
+    norm.axes = static_cast<int>(axes);
+  } else if (a[7] != Py_None && !dense(ob, a[7], "positions", at::kInt, {x.rows}, &x.pos)) {
+    return nullptr;
   }
-  if (a[7] != Py_None && !dense(ob, a[7], "positions", at::kInt, {rows}, &pos)) return nullptr;
-  if (a[8] != Py_None) {
-    int64_t half;
-    if (!rows_count(a[8], "inv_freq", &half) || !dense(ob, a[8], "inv_freq", at::kFloat, {half}, &inv)) return nullptr;
-    rotary = half > 4096 ? 8192 : static_cast<int>(2 * half);
+  if (!stream_of(ob, a[14], &x.s)) return nullptr;
+  norm.norm_dtype = type < 0 ? CONFKV_FP32 : type;
+  norm.eps = static_cast<float>(eps);
+  return PyLong_FromLong(confkv_paged_append_normed(ob->kv, batch, x.layer, static_cast<int>(x.rows), x.k, x.ks, x.v, x.vs, x.q,
+                                                    x.qs, x.out, x.os, static_cast<int32_t*>(x.pos), static_cast<float*>(x.inv),
+                                                    x.rotary, x.interleaved, &norm, x.s));
+}
+
+// The scale of an attention: 0 for the default.
+bool scale_of(PyObject* o, float* out) {
+  const double scale = PyFloat_AsDouble(o);
+  if (scale == -1.0 && PyErr_Occurred()) return false;
+  if (scale != 0.0 && static_cast<float>(scale) == 0.0f) {      // 0 would mean the default
+    PyErr_SetString(PyExc_ValueError, "scale is zero in 32 bits");
+    return false;
   }
-  const int inter = PyObject_IsTrue(a[9]);
-  if (inter < 0 || !stream_of(ob, a[10], &s)) return nullptr;
-  return PyLong_FromLong(confkv_paged_append(ob->kv, batch, layer, static_cast<int>(rows), k, ks, v, vs, q, qs, out, os,
-                                             static_cast<int32_t*>(pos), static_cast<float*>(inv), rotary, inter, s));
+  *out = static_cast<float>(scale);
+  return true;
+}
+bool mask_fits(int mask_rows, int64_t rows) {
+  if (mask_rows < 0 || mask_rows >= rows) return true;
+  PyErr_Format(PyExc_ValueError, "the batch's mask has %d rows, q has %lld", mask_rows, static_cast<long long>(rows));
+  return false;
+}
+
+// What both attends take of mask rows (-1: no mask), layer, q, out, lse, scale.
+struct Attend {
+  int mask_rows, layer;
+  int64_t rows, qs;
+  void *q, *out, *lse = nullptr, *s;
+  float scale;
+};
+bool attend_of(Object* ob, PyObject* const* a, Attend* x) {
+  return scale_of(a[5], &x->scale) && integer(a[0], &x->mask_rows) && integer(a[1], &x->layer) && rows_count(a[2], "q", &x->rows) &&
+         rows_of(ob, a[2], "q", x->rows, ob->sizes[0], &x->q, &x->qs) &&
+         dense(ob, a[3], "out", type_of(ob->dtype), {x->rows, ob->sizes[0], ob->sizes[2]}, &x->out) &&
+         mask_fits(x->mask_rows, x->rows) &&
+         (a[4] == Py_None || dense(ob, a[4], "lse", at::kFloat, {x->rows, ob->sizes[0]}, &x->lse));
 }
 
 // object, batch, mask rows (-1: no mask), layer, q, out, lse, scale, stream
@@ -188,28 +283,97 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count(n, 9)) return nullptr;
   Object* ob = pointer<Object>(a[0]);
   const confkv_paged_batch* batch = pointer<confkv_paged_batch>(a[1]);
-  int mask_rows, layer;
-  int64_t rows, qs;
-  void *q, *out, *lse = nullptr, *s;
+  Attend x;
+  if (!ready(ob) || !attend_of(ob, a + 2, &x) || !stream_of(ob, a[8], &x.s)) return nullptr;
+  return PyLong_FromLong(confkv_paged_attend(ob->kv, batch, x.layer, static_cast<int>(x.rows), x.q, x.qs, x.out,
+                                             static_cast<float*>(x.lse), x.scale, x.s));
+}
+
+// object, batch, prefix, mask rows (-1: no mask), layer, q, out, lse, scale, stream
+PyObject* attend_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 10)) return nullptr;
+  Object* ob = pointer<Object>(a[0]);
+  const confkv_paged_batch* batch = pointer<confkv_paged_batch>(a[1]);
+  const confkv_paged_prefix* prefix = pointer<confkv_paged_prefix>(a[2]);
+  Attend x;
+  if (!ready(ob) || !attend_of(ob, a + 3, &x) || !stream_of(ob, a[9], &x.s)) return nullptr;
+  return PyLong_FromLong(confkv_paged_attend_shared(ob->kv, batch, prefix, x.layer, static_cast<int>(x.rows), x.q, x.qs, x.out,
+                                                    static_cast<float*>(x.lse), x.scale, x.s));
+}
+
+// a contiguous tensor of the given type, [.., cap] behind `shape`
+bool table_of(Object* ob, PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape, int64_t* cap,
+              void** out) {
+  const at::Tensor* t = tensor(o, name);
+  if (!t) return false;
+  bool ok = t->scalar_type() == type && plain(ob, *t) && t->dim() == static_cast<int64_t>(shape.size()) + 1 && t->is_contiguous();
+  if (ok) {
+    int i = 0;
+    for (const int64_t n : shape) ok = ok && t->size(i++) == n;
+    ok = ok && t->size(i) <= INT32_MAX && (*cap < 0 || *cap == t->size(i));
+    if (ok) *cap = t->size(i);
+  }
+  if (!ok) return wrong(name, "a contiguous tensor of the documented type and shape on the object's device", o);
+  *out = t->data_ptr();
+  return true;
+}
+
+// object, batch, sequences, mask rows, layer, q, lse, mass, mass_out, pos, positions, decay, gain, scale, stream
+PyObject* weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 15)) return nullptr;
+  Object* ob = pointer<Object>(a[0]);
+  const confkv_paged_batch* batch = pointer<confkv_paged_batch>(a[1]);
+  int B, mask_rows, layer;
+  int64_t rows, qs, cap = -1;
+  void *q, *lse, *mass, *out, *pos = nullptr, *positions = nullptr, *s;
+  float scale;
   if (!ready(ob)) return nullptr;
-  const double scale = PyFloat_AsDouble(a[7]);
-  if (scale == -1.0 && PyErr_Occurred()) return nullptr;
-  if (scale != 0.0 && static_cast<float>(scale) == 0.0f) {      // 0 would mean the default
-    PyErr_SetString(PyExc_ValueError, "scale is zero in 32 bits");
+  const double decay = PyFloat_AsDouble(a[11]);
+  if (decay == -1.0 && PyErr_Occurred()) return nullptr;
+  const double gain = PyFloat_AsDouble(a[12]);
+  if (gain == -1.0 && PyErr_Occurred()) return nullptr;
+  const int64_t H = ob->sizes[1];
+  if (!scale_of(a[13], &scale) || !integer(a[2], &B) || !integer(a[3], &mask_rows) || !integer(a[4], &layer) ||
+      !rows_count(a[5], "q", &rows) || !rows_of(ob, a[5], "q", rows, ob->sizes[0], &q, &qs) || !mask_fits(mask_rows, rows) ||
+      !dense(ob, a[6], "lse", at::kFloat, {rows, ob->sizes[0]}, &lse) ||
+      !table_of(ob, a[7], "mass", at::kFloat, {B, H}, &cap, &mass) || !table_of(ob, a[8], "mass_out", at::kFloat, {B, H}, &cap, &out) ||
+      (a[9] != Py_None && !table_of(ob, a[9], "pos", at::kInt, {B, H}, &cap, &pos)) ||
+      (a[10] != Py_None && !dense(ob, a[10], "positions", at::kInt, {rows}, &positions)) || !stream_of(ob, a[14], &s))
     return nullptr;
-  }
-  if (!integer(a[2], &mask_rows) || !integer(a[3], &layer) || !rows_count(a[4], "q", &rows) ||
-      !rows_of(ob, a[4], "q", rows, ob->sizes[0], &q, &qs) ||
-      !dense(ob, a[5], "out", type_of(ob->dtype), {rows, ob->sizes[0], ob->sizes[2]}, &out))
+  return PyLong_FromLong(confkv_paged_weigh(ob->kv, batch, layer, static_cast<int>(rows), q, qs, static_cast<float*>(lse),
+                                            static_cast<float*>(mass), static_cast<float*>(out), static_cast<int32_t*>(pos),
+                                            static_cast<int>(cap), static_cast<int32_t*>(positions), static_cast<float>(decay),
+                                            static_cast<float>(gain), scale, s));
+}
+
+// object, layers, page_table, length, mass, pos, keep, mass_out, pos_out, new_len, protect, first, stream
+PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 13)) return nullptr;
+  Object* ob = pointer<Object>(a[0]);
+  int layers, protect;
+  int64_t B, blocks, cap = -1;
+  void *table, *len, *mass, *pos, *keep, *mo, *po, *out, *first = nullptr, *s;
+  if (!ready(ob) || !integer(a[1], &layers) || !matrix(a[2], "page_table", &B, &blocks) ||
+      !dense(ob, a[2], "page_table", at::kInt, {B, blocks}, &table))
     return nullptr;
-  if (mask_rows >= 0 && mask_rows < rows) {
-    PyErr_Format(PyExc_ValueError, "the batch's mask has %d rows, q has %lld", mask_rows, static_cast<long long>(rows));
+  const at::Tensor* t = tensor(a[3], "length");
+  if (!t) return nullptr;
+  const int per_layer = t->dim() == 2;
+  auto lengths = [&](PyObject* o, const char* name, void** p) {
+    return per_layer ? dense(ob, o, name, at::kInt, {layers, B}, p) : dense(ob, o, name, at::kInt, {B}, p);
+  };
+  const int64_t H = ob->sizes[1];
+  if (!lengths(a[3], "length", &len) || !table_of(ob, a[4], "mass", at::kFloat, {layers, B, H}, &cap, &mass) ||
+      !table_of(ob, a[5], "pos", at::kInt, {layers, B, H}, &cap, &pos) || !lengths(a[6], "keep", &keep) ||
+      !table_of(ob, a[7], "mass_out", at::kFloat, {layers, B, H}, &cap, &mo) ||
+      !table_of(ob, a[8], "pos_out", at::kInt, {layers, B, H}, &cap, &po) || !lengths(a[9], "new_len", &out) ||
+      !integer(a[10], &protect) || (a[11] != Py_None && !dense(ob, a[11], "first", at::kInt, {B}, &first)) || !stream_of(ob, a[12], &s))
     return nullptr;
-  }
-  if (a[6] != Py_None && !dense(ob, a[6], "lse", at::kFloat, {rows, ob->sizes[0]}, &lse)) return nullptr;
-  if (!stream_of(ob, a[8], &s)) return nullptr;
-  return PyLong_FromLong(confkv_paged_attend(ob->kv, batch, layer, static_cast<int>(rows), q, qs, out,
-                                             static_cast<float*>(lse), static_cast<float>(scale), s));
+  return PyLong_FromLong(confkv_paged_evict(ob->kv, static_cast<int>(B), static_cast<int>(blocks), static_cast<int32_t*>(table),
+                                            static_cast<int32_t*>(len), per_layer, static_cast<float*>(mass),
+                                            static_cast<int32_t*>(pos), static_cast<int>(cap), static_cast<int32_t*>(keep),
+                                            static_cast<int32_t*>(first), protect, static_cast<float*>(mo),
+                                            static_cast<int32_t*>(po), static_cast<int32_t*>(out), s));
 }
 
 // object, page_table, ctx_len, path, path_len, new_len, stream
@@ -335,7 +499,11 @@ PyObject* safe(PyObject* self, PyObject* const* a, Py_ssize_t n) noexcept {
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(safe<f>))
 PyMethodDef kMethods[] = {{"append", FAST(append), METH_FASTCALL, nullptr},
+                          {"append_normed", FAST(append_normed), METH_FASTCALL, nullptr},
                           {"attend", FAST(attend), METH_FASTCALL, nullptr},
+                          {"attend_shared", FAST(attend_shared), METH_FASTCALL, nullptr},
+                          {"weigh", FAST(weigh), METH_FASTCALL, nullptr},
+                          {"evict", FAST(evict), METH_FASTCALL, nullptr},
                           {"commit", FAST(commit), METH_FASTCALL, nullptr},
                           {"fork", FAST(fork), METH_FASTCALL, nullptr},
                           {"select", FAST(select), METH_FASTCALL, nullptr},

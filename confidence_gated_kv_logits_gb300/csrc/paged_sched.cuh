@@ -21,6 +21,7 @@ struct Sched {          // of one CTA: sched_warp, or for more than 32 sequences
   long long seq0, head;  // head: work of one of its heads
   int b, T, ctx, len, row0;
   int whole;             // units are not cut: each counts as 1, whatever its length
+  int tb, pre;           // SH: as in WalkState
 };
 
 // 64-bit quotients of numbers that mostly fit 32 bits (a 64-bit division costs
@@ -48,10 +49,25 @@ struct WalkState {
   int unit_done;                // the walk is behind the unit's last piece
   int more;                     // there is a piece
   int whole;                    // of Sched
+  // SH: the page table's row, and the tokens of the prefix that phase 1 has done
+  // (phase 2; lo and hi count the blocks from the sequence's first on, n those behind)
+  int tb, pre;
 };
 
-template <int TM, int KB, int kOverhead>
+// Tokens of the shared prefix that are taken once for a group: whole blocks of
+// either kernel, so that neither phase needs a mask at the border (each sequence
+// takes the rest, fewer than 128 tokens, from its own pages), and fewer than the page
+// table names, so that phase 2 has a token for every row.
+constexpr int kPrefixStep = 128;
+__device__ __forceinline__ int shared_tokens(int prefix, long long cap) {
+  const long long n = prefix < cap ? prefix : cap - 1;
+  return n > 0 ? static_cast<int>(n) & ~(kPrefixStep - 1) : 0;
+}
+
+// SH: one phase of the attention over a shared prefix (Batch::phase)
+template <int TM, int KB, int kOverhead, bool SH = false>
 struct Walk : WalkState {
+  static constexpr bool kShared = SH;
   const Pool& p;
   const Batch& bt;
   int rows;
@@ -61,6 +77,9 @@ struct Walk : WalkState {
   // what of sequence b's lengths is usable; `flag` collects what is not
   __device__ __forceinline__ void sequence(int b_, int& flag) {
     b = b_;
+    if constexpr (SH) {
+      if (bt.phase == 1) return group(flag);
+    }
     int s0 = bt.q_start[b], s1 = bt.q_start[b + 1];
     ctx = bt.ctx[b];
     if (ctx < 0) {
@@ -72,6 +91,14 @@ struct Walk : WalkState {
     row0 = s0;
     T = s1 - s0;
     const long long cap = static_cast<long long>(bt.max_blocks) << p.ps_shift;
+    if constexpr (SH) {
+      tb = b;
+      pre = prefix_of(cap);
+      if (ctx < pre) {            // shorter than its group's prefix: no rows
+        if (T) flag |= CONFKV_FLAG_BAD_INDEX;
+        T = 0;
+      }
+    }
     long long l = static_cast<long long>(ctx) + T;
     if (l > cap) {
       if (T) flag |= CONFKV_FLAG_CAPACITY;
@@ -82,6 +109,35 @@ struct Walk : WalkState {
     if (ctx > len) ctx = len;
     m = static_cast<int>((static_cast<long long>(T) * p.g + TM - 1) / TM);
   }
+  // phase 1: group b's rows over its shared prefix, which all of them see
+  __device__ __forceinline__ void group(int& flag) {
+    int g0 = bt.group_start[b], g1 = bt.group_start[b + 1];
+    const int n = bt.prefix_len[b];
+    if (g0 < 0 || g1 < g0 || g1 > bt.seqs || n < 0) flag |= CONFKV_FLAG_BAD_INDEX;
+    g0 = g0 < 0 ? 0 : g0 > bt.seqs ? bt.seqs : g0;
+    g1 = g1 < g0 ? g0 : g1 > bt.seqs ? bt.seqs : g1;
+    tb = g0;
+    pre = 0;
+    ctx = len = shared_tokens(n, static_cast<long long>(bt.max_blocks) << p.ps_shift);
+    int s0 = bt.q_start[g0], s1 = bt.q_start[g1];
+    s0 = s0 < 0 ? 0 : s0 > rows ? rows : s0;
+    s1 = s1 < s0 ? s0 : s1 > rows ? rows : s1;
+    row0 = s0;
+    T = ctx > 0 && g1 > g0 ? s1 - s0 : 0;
+    m = static_cast<int>((static_cast<long long>(T) * p.g + TM - 1) / TM);
+  }
+  // phase 2: tokens of the prefix of sequence b's group
+  __device__ __forceinline__ int prefix_of(long long cap) const {
+    int lo = 0, hi = bt.groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (bt.group_start[mid] <= b) lo = mid;
+      else hi = mid;
+    }
+    const int n = bt.prefix_len[lo];
+    return bt.group_start[lo] <= b && b < bt.group_start[lo + 1] ? shared_tokens(n, cap) : 0;
+  }
+  __device__ __forceinline__ int skip() const { return SH ? pre / KB : 0; }      // blocks that phase 1 has done
   // tokens that some row of tile t may see
   __device__ __forceinline__ int tile_len(int t) const {
     if (bt.mask) return len;
@@ -90,7 +146,7 @@ struct Walk : WalkState {
     last = last > static_cast<uint32_t>(T) ? T : last;
     return last < static_cast<uint32_t>(len - ctx) ? ctx + static_cast<int>(last) : len;
   }
-  __device__ __forceinline__ int blocks(int t) const { return (tile_len(t) + KB - 1) / KB; }
+  __device__ __forceinline__ int blocks(int t) const { return (tile_len(t) + KB - 1) / KB - skip(); }
   // work of one head of the sequence
   __device__ __forceinline__ long long head_work() const {
     if (bt.mask || m <= 1) return static_cast<long long>(m) * (blocks(0 < m ? m - 1 : 0) + kOverhead);
@@ -112,6 +168,10 @@ struct Walk : WalkState {
     ctx = s.ctx;
     len = s.len;
     row0 = s.row0;
+    if constexpr (SH) {
+      tb = s.tb;
+      pre = s.pre;
+    }
     m = static_cast<int>((static_cast<long long>(T) * p.g + TM - 1) / TM);
     h = static_cast<int>(quotient(cur - s.seq0, s.head));
     ustart = s.seq0 + h * s.head;
@@ -151,8 +211,8 @@ struct Walk : WalkState {
       }
       n = blocks(mt);
       if (whole) {
-        lo = 0;
-        hi = n;
+        lo = skip();
+        hi = lo + n;
         first_cta = blockIdx.x;
         pieces = 1;
         ++cur;
@@ -170,6 +230,10 @@ struct Walk : WalkState {
       cur = x1;
       unit_done = x1 == uend;
       if (hi > lo) {
+        if constexpr (SH) {
+          lo += skip();
+          hi += skip();
+        }
         more = 1;
         return true;
       }
@@ -238,6 +302,10 @@ __device__ __forceinline__ Sched sched_warp(W& w, long long min_share, int uncut
   s.ctx = __shfl_sync(0xffffffffu, w.ctx, b);
   s.len = __shfl_sync(0xffffffffu, w.len, b);
   s.row0 = __shfl_sync(0xffffffffu, w.row0, b);
+  if constexpr (W::kShared) {
+    s.tb = __shfl_sync(0xffffffffu, w.tb, b);
+    s.pre = __shfl_sync(0xffffffffu, w.pre, b);
+  }
   return s;
 }
 
@@ -294,6 +362,10 @@ __device__ __forceinline__ void sched_init(W& w, Sched* s, long long* s_scan, lo
     s->ctx = w.ctx;
     s->len = w.len;
     s->row0 = w.row0;
+    if constexpr (W::kShared) {
+      s->tb = w.tb;
+      s->pre = w.pre;
+    }
     s->seq0 = at;
     s->head = quotient(x, w.p.Hkv);
     s->whole = 0;

@@ -43,6 +43,16 @@ class BatchStruct(ctypes.Structure):
                 ("mask_words", ctypes.c_int32)]
 
 
+class PrefixStruct(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("group_start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p),
+                ("partial", ctypes.c_void_p), ("partial_bytes", ctypes.c_size_t)]
+
+
+class NormStruct(ctypes.Structure):
+    _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("norm_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("axis", ctypes.c_void_p), ("axes", ctypes.c_int32)]
+
+
 def declare(L):
     """Argument types of the functions in include/confkv_paged.h."""
     vp, ci, cl, cf, sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
@@ -62,6 +72,16 @@ def declare(L):
                                       ci, vp]
     L.confkv_paged_attend.restype = ci
     L.confkv_paged_attend.argtypes = [vp, vp, ci, ci, vp, cl, vp, vp, cf, vp]
+    L.confkv_paged_append_normed.restype = ci
+    L.confkv_paged_append_normed.argtypes = [vp, vp, ci, ci, vp, cl, vp, cl, vp, cl, vp, cl, vp, vp, ci, ci, vp, vp]
+    L.confkv_paged_partial.restype = sz
+    L.confkv_paged_partial.argtypes = [ci, ci, ci]
+    L.confkv_paged_attend_shared.restype = ci
+    L.confkv_paged_attend_shared.argtypes = [vp, vp, vp, ci, ci, vp, cl, vp, vp, cf, vp]
+    L.confkv_paged_weigh.restype = ci
+    L.confkv_paged_weigh.argtypes = [vp, vp, ci, ci, vp, cl, vp, vp, vp, vp, ci, vp, cf, cf, cf, vp]
+    L.confkv_paged_evict.restype = ci
+    L.confkv_paged_evict.argtypes = [vp, ci, ci, vp, vp, ci, vp, vp, ci, vp, vp, ci, vp, vp, vp, vp]
     L.confkv_paged_commit.restype = ci
     L.confkv_paged_commit.argtypes = [vp, ci, ci, vp, vp, vp, ci, vp, vp, vp]
     L.confkv_paged_fork.restype = ci
@@ -124,6 +144,18 @@ class PagedBatch:
         self._tensors = tensors
         self.size = batch
         self.mask_rows = mask_rows
+
+
+class SharedPrefix:
+    """Prefixes that groups of neighbouring sequences share (``PagedKV.prefix``),
+    and the attention's scratch for them: calls with one object must be ordered."""
+
+    def __init__(self, struct, tensors, rows, index):
+        self._struct = struct
+        self._index = index
+        self._ref = ctypes.addressof(struct)
+        self._tensors = tensors
+        self.rows = rows
 
 
 class PagedKV(_Device):
@@ -206,25 +238,82 @@ class PagedKV(_Device):
             s.mask_words = mask.shape[1]
         return PagedBatch(s, (page_table, ctx_len, q_start, mask), B, rows, self._index)
 
+    def prefix(self, group_start, prefix_len, rows):
+        """Shared prefixes: sequences group_start[g] .. group_start[g + 1] - 1 (int32
+        [groups + 1]) have their first prefix_len[g] (int32 [groups]) cached tokens in
+        common, for ``attend`` of up to `rows` rows.  Their contents are read by each call."""
+        from . import ConfKVError, ERR_INVALID_ARG
+        if prefix_len.dim() != 1 or prefix_len.shape[0] < 1:
+            raise ValueError("prefix_len: want [groups], one at least")
+        groups = prefix_len.shape[0]
+        n = self._L.confkv_paged_partial(rows, self.heads, self.head_dim)
+        if not n:
+            raise ConfKVError(ERR_INVALID_ARG, f"{rows} rows are not supported")
+        scratch = torch.empty(n, dtype=torch.uint8, device=self.device)
+        s = PrefixStruct(groups, self._dense(group_start, (groups + 1,), "group_start"),
+                         self._dense(prefix_len, (groups,), "prefix_len"), scratch.data_ptr(), n)
+        return SharedPrefix(s, (group_start, prefix_len, scratch), rows, self._index)
+
     def append(self, layer, batch, k, v, *, q=None, q_out=None, positions=None, inv_freq=None,
-               interleaved=False, stream=None):
+               interleaved=False, q_norm=None, k_norm=None, eps=1e-6, axis=None, stream=None):
         """Stores k, v [rows, kv_heads, head_dim] of the batch's new tokens in
         layer `layer`, k rotated by `positions` (int32 [rows]; None: places in
         the sequence) x `inv_freq` (fp32 [rotary / 2]; None: not rotated), and
-        rotates q [rows, heads, head_dim] into q_out (q itself allowed)."""
+        rotates q [rows, heads, head_dim] into q_out (q itself allowed).  q_norm, k_norm
+        [head_dim] (fp32 or the cache's type): each head of q, of k is divided by its
+        root mean square (eps beside the mean) and multiplied by them before.  axis int32
+        [rotary / 2]: positions are [rows, axes], pair i turns by the axis[i]-th."""
         if batch._index != self._index:
             raise ValueError("the batch's tensors are on another device")
+        if q_norm is not None or k_norm is not None or axis is not None:
+            rc = _ops.append_normed(self._ob, batch._ref, layer, k, v, q, q_out, positions, inv_freq, interleaved,
+                                    q_norm, k_norm, eps, axis, stream)
+            if rc:
+                self._check(rc)
+            return
         rc = _ops.append(self._ob, batch._ref, layer, k, v, q, q_out, positions, inv_freq, interleaved, stream)
         if rc:
             self._check(rc)
 
-    def attend(self, layer, batch, q, out, *, lse=None, scale=0.0, stream=None):
+    def attend(self, layer, batch, q, out, *, lse=None, scale=0.0, prefix=None, stream=None):
         """Attention of q [rows, heads, head_dim] over layer `layer` into out
         (contiguous, same shape and type); lse fp32 [rows, heads] or None;
-        scale 0: 1 / sqrt(head_dim)."""
+        scale 0: 1 / sqrt(head_dim).  prefix (``prefix``): what groups of the batch's
+        sequences share is read once for the group."""
         if batch._index != self._index:
             raise ValueError("the batch's tensors are on another device")
+        if prefix is not None:
+            if prefix._index != self._index:
+                raise ValueError("the prefix's tensors are on another device")
+            rc = _ops.attend_shared(self._ob, batch._ref, prefix._ref, batch.mask_rows, layer, q, out, lse, scale, stream)
+            if rc:
+                self._check(rc)
+            return
         rc = _ops.attend(self._ob, batch._ref, batch.mask_rows, layer, q, out, lse, scale, stream)
+        if rc:
+            self._check(rc)
+
+    def weigh(self, layer, batch, q, lse, mass, mass_out, pos=None, *, positions=None, decay=1.0, gain=1.0, scale=0.0,
+              stream=None):
+        """Adds the attention weights of q's rows (lse as ``attend`` gave it) to each
+        token's accumulated weight: mass_out = decay mass + gain sum, fp32 [batch,
+        kv_heads, cap] (mass_out may be mass).  New tokens start from 0; pos int32
+        likewise receives their positions (int32 [rows]; None: their places)."""
+        if batch._index != self._index:
+            raise ValueError("the batch's tensors are on another device")
+        rc = _ops.weigh(self._ob, batch._ref, batch.size, batch.mask_rows, layer, q, lse, mass, mass_out, pos, positions,
+                        decay, gain, scale, stream)
+        if rc:
+            self._check(rc)
+
+    def evict(self, page_table, length, mass, pos, keep, mass_out, pos_out, new_len, *, protect=0, first=None, stream=None):
+        """Keeps the keep[b] tokens of the largest mass of every layer and KV head (before
+        them places below first[b] and the `protect` newest positions) and moves those behind
+        into evicted ones' places; mass, pos [layers, batch, kv_heads, cap] and their
+        outputs (both may be the inputs); length, keep, new_len int32 [batch] or
+        [layers, batch]."""
+        rc = _ops.evict(self._ob, self.layers, page_table, length, mass, pos, keep, mass_out, pos_out, new_len, protect,
+                        first, stream)
         if rc:
             self._check(rc)
 

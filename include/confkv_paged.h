@@ -7,8 +7,10 @@
  * steps of a decode loop around them: prompt chunks, single tokens and trees
  * of drafted tokens are appended (rotated by their positions on the way) and
  * attended in the same way, an accepted path is taken over with
- * confkv_paged_commit, and beams are selected from the logits with
- * confkv_beam_select and reordered with confkv_paged_fork.
+ * confkv_paged_commit, tokens are weighed by the attention that they get and
+ * evicted by it with confkv_paged_weigh and confkv_paged_evict, and beams are
+ * selected from the logits with confkv_beam_select and reordered with
+ * confkv_paged_fork.
  *
  * Conventions (those of confkv.h hold here too):
  *   - Tensor arguments are DEVICE pointers on the cache's GPU, owned by the
@@ -147,6 +149,30 @@ int confkv_paged_append(confkv_paged* kv, const confkv_paged_batch* batch, int l
                         int interleaved, void* stream);
 
 /*
+ * confkv_paged_append_normed -- the same with each head of q and k normed before
+ * it is rotated, y_c = x_c w_c / sqrt(sum_c x_c^2 / head_dim + eps), and with
+ * several positions per row (an image's patch has a time, a height and a width).
+ * Norm, rotation and what lies between are fp32; q_out and K are rounded once.
+ */
+typedef struct confkv_paged_norm {
+  const void* q_norm;          /* [head_dim] weights of q's heads, or NULL: not normed */
+  const void* k_norm;          /* [head_dim] weights of k's heads, or NULL */
+  int32_t norm_dtype;          /* of both: CONFKV_FP32 or the cache's type */
+  float eps;                   /* 1e-12 or more */
+  const int32_t* axis;         /* [rotary_dim / 2] or NULL.  With it positions is
+                                  [rows][axes], and channel pair i turns by
+                                  positions[row][axis[i]] * inv_freq[i]; a pair
+                                  whose axis is none is not turned
+                                  (CONFKV_FLAG_BAD_INDEX). */
+  int32_t axes;                /* 1 .. 8 */
+} confkv_paged_norm;
+int confkv_paged_append_normed(confkv_paged* kv, const confkv_paged_batch* batch, int layer, int rows,
+                               const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                               const int32_t* positions, const float* inv_freq, int rotary_dim,
+                               int interleaved, const confkv_paged_norm* norm, void* stream);
+
+/*
  * confkv_paged_attend -- attention of the new rows over their sequences'
  * cached tokens and the new tokens that the batch's mask lets them see (whose
  * K and V append has stored): out = softmax(scale q k) v.
@@ -172,6 +198,84 @@ int confkv_paged_append(confkv_paged* kv, const confkv_paged_batch* batch, int l
 int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int layer, int rows,
                         const void* q, int64_t q_stride, void* out, float* lse, float scale,
                         void* stream);
+
+/*
+ * confkv_paged_attend_shared -- the same where groups of neighbouring sequences
+ * share a prefix (the beams of a prompt, requests behind one instruction), which is
+ * read once for a group.  Sequences group_start[g] .. group_start[g + 1] - 1 are
+ * group g; their first prefix_len[g] cached tokens are the same in each and are
+ * taken from the pages of the first one (whose table the others' need not
+ * repeat; the prefix's last, less than 128 tokens each sequence reads from its own
+ * pages, so those must be there).  Sequences in no group are taken as attend takes
+ * them.  Any page_size and prefix length (0 too).
+ * A sequence with fewer cached tokens than its group's prefix is left out: its rows
+ * stay as they were (CONFKV_FLAG_BAD_INDEX); that flag too for starts that
+ * fall or leave 0 .. batch and for negative lengths.
+ * Every row's result is joined from two parts, in fp32, the prefix's first: within
+ * attend's precision, but not the same bits.
+ */
+typedef struct confkv_paged_prefix {
+  int32_t groups;              /* 1 .. batch */
+  const int32_t* group_start;  /* [groups + 1] sequences, not decreasing */
+  const int32_t* prefix_len;   /* [groups] */
+  void* partial;               /* scratch, 16-byte aligned, written and read by
+                                  each call: calls that share it must be ordered */
+  size_t partial_bytes;        /* confkv_paged_partial of the rows or more */
+} confkv_paged_prefix;
+size_t confkv_paged_partial(int rows, int heads, int head_dim);    /* 0 for sizes that are refused */
+int confkv_paged_attend_shared(confkv_paged* kv, const confkv_paged_batch* batch,
+                               const confkv_paged_prefix* prefix, int layer, int rows, const void* q,
+                               int64_t q_stride, void* out, float* lse, float scale, void* stream);
+
+/*
+ * confkv_paged_weigh -- adds the new rows' attention weights to the accumulated
+ * weight of each token that they see: for KV head h of sequence b
+ *   mass_out[b][h][t] = decay mass[b][h][t] + gain sum exp(scale q k_t - lse)
+ * over b's new rows and h's query heads, for every cached token t; new tokens
+ * (places ctx_len[b] on) start from 0.  Rows see what they see in attend (causal,
+ * or by the batch's mask); k is read from layer `layer`'s pages.
+ *   q, lse: what attend was given and gave (a row with lse -inf adds nothing)
+ *   mass, mass_out: fp32 [batch][kv_heads][cap] (mass_out may be mass itself)
+ *   pos: int32 [batch][kv_heads][cap] or NULL: receives the new tokens' positions
+ *        (`positions` [rows], or NULL: their places)
+ *   scale: 0 means 1 / sqrt(head_dim)
+ * gain 1, decay 1 add the weights up; gain (1 - decay) / (heads / kv_heads) makes
+ * the running mean over the group's heads that confkv_step ranks by.  Sums are
+ * fp32, in one order.  Sequences without new rows stay as they are, as do
+ * places from ctx_len + new tokens on.  Places from cap on are dropped
+ * (CONFKV_FLAG_CAPACITY).  A NaN in a row that sees a token or in the token's k makes its
+ * mass NaN.
+ */
+int confkv_paged_weigh(confkv_paged* kv, const confkv_paged_batch* batch, int layer, int rows, const void* q,
+                       int64_t q_stride, const float* lse, const float* mass, float* mass_out, int32_t* pos,
+                       int cap, const int32_t* positions, float decay, float gain, float scale, void* stream);
+
+/*
+ * confkv_paged_evict -- every KV head of every sequence and layer keeps N =
+ * min(length[b], keep[b]) of its cached tokens: its places below first[b] (a
+ * prefix that others share, the first tokens of a text) before the tokens of the
+ * `protect` newest positions (above the head's largest position - protect) before
+ * those of the larger mass; equal ones by the lower place, NaN last.  The kept tokens
+ * from place N on take the places of evicted ones below N, the r-th of them the
+ * r-th such place, with K, V, mass and position; the other kept ones stay.
+ *   length, keep, new_len: int32 [batch], or with per_layer 1 [layers][batch];
+ *         new_len = N, not length itself.  keep can be confkv_confidence_noalloc's
+ *         budget.
+ *   mass, mass_out: fp32 [layers][batch][kv_heads][cap], pos, pos_out: int32
+ *         likewise; the outputs are both the inputs themselves, or neither, and then
+ *         places from N on are not written.  cap <= 524288.
+ *   first: int32 [batch] or NULL (0)
+ * Heads and layers keep different tokens: a place means another token in each.
+ * The pages of places that change (those of places first[b] .. N - 1) belong to one
+ * sequence each.  A sequence with a negative length, budget or first, or longer than
+ * its table or cap, stays as it is, with its length (a flag); a token whose
+ * page or whose new place's page is outside the pool is not moved
+ * (CONFKV_FLAG_BAD_PAGE).
+ */
+int confkv_paged_evict(confkv_paged* kv, int batch, int max_blocks, const int32_t* page_table,
+                       const int32_t* length, int per_layer, const float* mass, const int32_t* pos, int cap,
+                       const int32_t* keep, const int32_t* first, int protect, float* mass_out,
+                       int32_t* pos_out, int32_t* new_len, void* stream);
 
 /*
  * confkv_paged_commit -- keeps an accepted path of drafted tokens: in every
