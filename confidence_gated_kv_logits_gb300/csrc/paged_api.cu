@@ -2,6 +2,7 @@
 // handle lifetime, argument checks and launches.  No call but create, free
 // and status synchronises or allocates.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <mutex>
@@ -10,6 +11,36 @@
 #include "paged_attend.cuh"
 
 using namespace confkv::paged;
+
+namespace confkv {
+namespace paged {
+
+cudaError_t encode_map(CUtensorMap* map, bool bf16, int rank, void* at, const cuuint64_t* dims, const cuuint64_t* strides,
+                       const cuuint32_t* box, bool nan_outside) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<Encode> known{nullptr};
+  Encode enc = known.load();
+  if (!enc) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    enc = reinterpret_cast<Encode>(fn);
+    known.store(enc);
+  }
+  const cuuint32_t steps[3] = {1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, at, dims, strides, box, steps,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             nan_outside ? CU_TENSOR_MAP_FLOAT_OOB_FILL_NAN_REQUEST_ZERO_FMA : CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+}  // namespace paged
+}  // namespace confkv
 
 namespace {
 
@@ -88,35 +119,20 @@ const char* check_batch(const confkv_paged_batch* b, bool masked) {
 // channels (128 bytes, swizzled) x as many rows as a page and the kernel's tile share.
 // Rows outside the pool (kNoRows) read as NaN from K's maps and as zero from V's.
 cudaError_t encode_maps(const Pool& p, AttendMaps* m) {
-  void* fn = nullptr;
-  cudaDriverEntryPointQueryResult q;
-  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
-  if (e != cudaSuccess) return e;
-  if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  const Encode enc = reinterpret_cast<Encode>(fn);
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.d),
                               static_cast<cuuint64_t>(p.L) * p.NP * p.Hkv * p.ps};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.d) * 2};
-  const cuuint32_t steps[2] = {1, 1};
   const int few = std::min(p.ps, kFewChunk / p.d), many = std::min(p.ps, kManyBlock);
   struct {
     CUtensorMap* map;
     uint16_t* pool;
     int rows;
-    CUtensorMapFloatOOBfill outside;
-  } const all[] = {{&m->k_few, p.k, few, CU_TENSOR_MAP_FLOAT_OOB_FILL_NAN_REQUEST_ZERO_FMA},
-                   {&m->v_few, p.v, few, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE},
-                   {&m->k_many, p.k, many, CU_TENSOR_MAP_FLOAT_OOB_FILL_NAN_REQUEST_ZERO_FMA},
-                   {&m->v_many, p.v, many, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE}};
+    bool nan_outside;
+  } const all[] = {{&m->k_few, p.k, few, true}, {&m->v_few, p.v, few, false}, {&m->k_many, p.k, many, true}, {&m->v_many, p.v, many, false}};
   for (const auto& x : all) {
     const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(x.rows)};
-    if (enc(x.map, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x.pool, dims,
-            strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, x.outside) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
+    const cudaError_t e = encode_map(x.map, p.bf16, 2, x.pool, dims, strides, box, x.nan_outside);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
@@ -135,6 +151,7 @@ cudaError_t device_ready(int dev, Limits* limits) {
     if (e == cudaSuccess) e = setup_attend_few();
     if (e == cudaSuccess) e = setup_attend_many();
     if (e == cudaSuccess) e = setup_evict();
+    if (e == cudaSuccess) e = setup_weigh();
     if (e == cudaSuccess) e = few_clusters(2, &n.clusters2);
     if (e == cudaSuccess) e = few_clusters(4, &n.clusters4);
     if (e == cudaSuccess) e = few_clusters(8, &n.clusters8);
@@ -506,7 +523,7 @@ int confkv_paged_weigh(confkv_paged* kv, const confkv_paged_batch* batch, int la
   DeviceGuard guard(kv->device);
   const WeighArgs a{batch_of(batch), layer, rows, static_cast<const uint16_t*>(q), q_stride, lse, mass, mass_out, pos, cap,
                     positions, decay, gain, scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(p.d))};
-  return launched(kv, launch_weigh(p, a, static_cast<cudaStream_t>(stream)));
+  return launched(kv, launch_weigh(p, a, kv->maps, kv->limits.sms, static_cast<cudaStream_t>(stream)));
 }
 
 int confkv_paged_evict(confkv_paged* kv, int batch, int max_blocks, const int32_t* page_table, const int32_t* length,

@@ -33,6 +33,13 @@ cudaError_t launch_attend_many(const Pool& p, const AttendArgs& a, const Scratch
 cudaError_t setup_attend_few();
 cudaError_t few_clusters(int size, int* fit);       // clusters of `size` CTAs that run at once
 cudaError_t setup_attend_many();
+cudaError_t launch_weigh(const Pool& p, const WeighArgs& a, const AttendMaps& m, int ctas, cudaStream_t s);
+cudaError_t setup_weigh();
+
+// A tensor map of 16-bit elements whose boxes are 64 channels (128 bytes, swizzled)
+// wide; what lies outside reads as NaN or as zero (paged_api.cu).
+cudaError_t encode_map(CUtensorMap* map, bool bf16, int rank, void* at, const cuuint64_t* dims, const cuuint64_t* strides,
+                       const cuuint32_t* box, bool nan_outside);
 
 // 0xffff in each half of a word whose element is NaN or infinite
 template <bool BF>
