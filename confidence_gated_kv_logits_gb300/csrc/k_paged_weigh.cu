@@ -164,9 +164,11 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
   tc_fence_after();
   const uint32_t tmem = s.tmem;
   unsigned plan = 0;
-  auto next_item = [&] {
-    return bar_wait_warp(b_plan + 8 * (plan % kPlan), (plan / kPlan) & 1, &s.abort) && s.plan[plan % kPlan].more;
+  auto wait_item = [&](unsigned ahead) {  // the planned item that many further is there (behind the last one there is none)
+    return bar_wait_warp(b_plan + 8 * ((plan + ahead) % kPlan), ((plan + ahead) / kPlan) & 1, &s.abort);
   };
+  auto item = [&](unsigned ahead) -> const Item& { return s.plan[(plan + ahead) % kPlan]; };
+  auto next_item = [&] { return wait_item(0) && item(0).more; };
   auto item_done = [&] {
     __syncwarp();
     if (lane == 0) bar_arrive(b_read + 8 * (plan % kPlan));
@@ -222,28 +224,38 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
     unsigned slot = 0;
     int flag = 0;
     bool ok = true;
-    while (ok && next_item()) {
-      const Item& w = s.plan[plan % kPlan];
-      const int32_t* table = a.bt.table + static_cast<size_t>(w.b) * a.bt.max_blocks;
-      for (int j0 = w.j0; ok && j0 < w.len && j0 < w.j0 + BT * gb; j0 += BT, ++slot) {
+    // lane i asks for box i of the item: both token tiles' boxes, their channel halves side by side
+    constexpr int HV = D / 64;
+    const int x = lane / (16 / 2 * HV), i = lane % (16 / 2 * HV) / HV, half = lane % HV;
+    auto page_of = [&](const Item& w) {   // the lane's page
+      const int j = w.j0 + x * BT + i * rows_per;
+      return w.more && x < gb && i < boxes && j < w.len ? a.bt.table[static_cast<size_t>(w.b) * a.bt.max_blocks + (j >> p.ps_shift)] : 0;
+    };
+    ok = wait_item(0);
+    int page = ok ? page_of(item(0)) : 0;
+    while (ok && item(0).more) {
+      const Item& w = item(0);
+      ok = wait_item(1);                  // the next item's pages are asked for before this one's boxes
+      if (!ok) break;
+      const int page1 = page_of(item(1));
+      const bool none = static_cast<unsigned>(page) >= static_cast<unsigned>(p.NP);
+      for (int y = 0; y < gb && w.j0 + y * BT < w.len; ++y, ++slot) {
         const unsigned st = slot % SK;
-        const int live = (w.len - j0 + rows_per - 1) / rows_per, n = live < boxes ? live : boxes;
-        const int i = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
-        const int j = j0 + i * rows_per;
-        const int page = lane < n * (D / 64) ? table[j >> p.ps_shift] : 0;
         if (slot >= SK && !bar_wait_warp(b_ke + 8 * st, (slot / SK - 1) & 1, &s.abort)) {
           ok = false;
           break;
         }
+        const int j0 = w.j0 + y * BT, live = (w.len - j0 + rows_per - 1) / rows_per, n = live < boxes ? live : boxes;
         if (lane == 0) bar_expect(b_kf + 8 * st, static_cast<unsigned>(n * rows_per * D * 2));
         __syncwarp();
-        if (lane < n * (D / 64)) {
-          const bool none = static_cast<unsigned>(page) >= static_cast<unsigned>(p.NP);
+        if (x == y && i < n) {
           if (none) flag = CONFKV_FLAG_BAD_PAGE;
-          const int y = none ? kNoRows : (((a.layer * p.NP + page) * p.Hkv + w.h) << p.ps_shift) + (j & (p.ps - 1));
-          tma_box(k_ring + st * W::TILE + half * W::HALF + i * rows_per * 128, &mk, 64 * half, y, b_kf + 8 * st, pol);
+          const int j = j0 + i * rows_per;
+          const int row = none ? kNoRows : (((a.layer * p.NP + page) * p.Hkv + w.h) << p.ps_shift) + (j & (p.ps - 1));
+          tma_box(k_ring + st * W::TILE + half * W::HALF + i * rows_per * 128, &mk, 64 * half, row, b_kf + 8 * st, pol);
         }
       }
+      page = page1;
       item_done();
     }
     if (flag) atomicOr(p.err, flag);
@@ -254,7 +266,7 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
     unsigned slot = 0;
     bool ok = true;
     while (ok && next_item()) {
-      const Item& w = s.plan[plan % kPlan];
+      const Item& w = item(0);
       for (int t = w.tile0; ok && t < w.tiles; ++t, ++slot) {
         const unsigned st = slot % SQ;
         if (slot >= SQ && !bar_wait_warp(b_qe + 8 * st, (slot / SQ - 1) & 1, &s.abort)) {
@@ -281,7 +293,7 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
     unsigned used[2][2] = {};             // products into an accumulator so far
     bool ok = true;
     while (ok && next_item()) {
-      const Item& w = s.plan[plan % kPlan];
+      const Item& w = item(0);
       const int blocks = min(gb, (w.len - w.j0 + BT - 1) / BT);
       for (int x = 0; ok && x < blocks; ++x) ok = bar_wait_warp(b_kf + 8 * ((ks + x) % SK), ((ks + x) / SK) & 1, &s.abort);
       for (int t = w.tile0; ok && t < w.tiles; ++t, ++qs, ++ns) {
@@ -327,27 +339,34 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
     const float c = a.scale * kL2E;
     const int rt = r / p.g, rh = r - rt * p.g;
     unsigned ns = 0, used0 = 0, used1 = 0;                // tiles of rows so far; those of its two accumulators
-    while (!group_any(x, !next_item())) {
-      const Item& w = s.plan[plan % kPlan];
+    // an item's mass, and the lse of a column of its tile t
+    auto mass_of = [&](const Item& w) {
+      const int j = w.j0 + x * BT + r;
+      return w.more && x < gb && j < w.len && j < w.ctx ? a.mass[(static_cast<size_t>(w.b) * p.Hkv + w.h) * a.cap + j] : 0.0f;
+    };
+    auto lse_of = [&](const Item& w, int t) {
+      const int tok = t * tb + rt;
+      return w.more && t < w.tiles && rt < tb && tok < w.T ? a.lse[static_cast<size_t>(w.row0 + tok) * p.Hq + w.h * p.g + rh] : -INFINITY;
+    };
+    bool ok = wait_item(0);
+    float before = ok ? mass_of(item(0)) : 0.0f, next = ok ? lse_of(item(0), item(0).tile0) : 0.0f;
+    while (!group_any(x, !(ok && item(0).more))) {
+      const Item& w = item(0);
       const int j = w.j0 + x * BT + r;
       const bool here = w.j0 + x * BT < w.len && x < gb;  // the item has this token tile
       const bool live = here && j < w.len;
       const size_t at = (static_cast<size_t>(w.b) * p.Hkv + w.h) * a.cap + j;
-      const float before = live && j < w.ctx ? a.mass[at] : 0.0f;
-      auto lse_of = [&](int t) {
-        const int tok = t * tb + rt;
-        float v = -INFINITY;
-        if (here && t < w.tiles && rt < tb && tok < w.T) v = a.lse[static_cast<size_t>(w.row0 + tok) * p.Hq + w.h * p.g + rh];
-        return v;
-      };
-      float next = lse_of(w.tile0), sum0 = 0.0f, sum1 = 0.0f;
+      // the next item's mass and lse come while this one's products are waited for
+      ok = wait_item(1);
+      const float before1 = ok ? mass_of(item(1)) : 0.0f, first1 = ok ? lse_of(item(1), item(1).tile0) : 0.0f;
+      float sum0 = 0.0f, sum1 = 0.0f;
       bool dead = false;
       for (int t = w.tile0; t < w.tiles; ++t, ++ns) {
         if (!here) continue;                              // (it counts the tile all the same)
         const unsigned par = ns & 1, acc = 2 * x + par;
         float* lse = s.lse[x][par];
         lse[r] = next == -INFINITY ? INFINITY : next * kL2E;
-        next = lse_of(t + 1);
+        if (t + 1 < w.tiles) next = lse_of(w, t + 1);
         const bool got = bar_wait_warp(b_s + 8 * acc, (par ? used1 : used0) & 1, &s.abort);
         if (par) ++used1;
         else ++used0;
@@ -362,13 +381,13 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
         const bool masked = a.bt.mask && w.j0 + x * BT + BT > w.ctx;
         const int from = a.bt.mask || past <= 0 ? 0 : past * p.g;
         const uint32_t ts = tmem + lanes + acc * BR;
-        for (int q = 0; q < n; q += 32) {
-          uint32_t sv[32];
-          __syncwarp();
-          tmem_ld32(sv, ts + q);
-          tmem_wait_ld(sv);
-          const float4* lq = reinterpret_cast<const float4*>(lse + q);
-          if (!masked && q + 32 <= n && !__any_sync(0xffffffffu, from > q)) {
+        int q = 0;
+        if (!masked && !__any_sync(0xffffffffu, from > 0)) {
+          for (; q + 32 <= n; q += 32) {
+            uint32_t sv[32];
+            tmem_ld32(sv, ts + q);
+            tmem_wait_ld(sv);
+            const float4* lq = reinterpret_cast<const float4*>(lse + q);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float4 l = lq[e];
@@ -377,18 +396,23 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
               sum0 += ex2f(fmaf(__uint_as_float(sv[4 * e + 2]), c, -l.z));
               sum1 += ex2f(fmaf(__uint_as_float(sv[4 * e + 3]), c, -l.w));
             }
-          } else {
+          }
+        }
+        for (; q < n; q += 8) {
+          uint32_t sv[8];
+          __syncwarp();
+          tmem_ld8(sv, ts + q);
+          tmem_wait_ld(sv);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int col = q + e;
-              bool seen = col >= from && col < n;
-              if (masked && seen) {
-                const int tok = t * tb + col / p.g;
-                seen = seen_bits(a.bt, static_cast<size_t>(w.row0 + tok), tok, w.ctx, w.len, j) & 1u;
-              }
-              const float y = ex2f(fmaf(__uint_as_float(sv[e]), c, -lse[seen ? col : 0]));
-              (e & 1 ? sum1 : sum0) += seen ? y : 0.0f;
+          for (int e = 0; e < 8; ++e) {
+            const int col = q + e;
+            bool seen = col >= from && col < n;
+            if (masked && seen) {
+              const int tok = t * tb + col / p.g;
+              seen = seen_bits(a.bt, static_cast<size_t>(w.row0 + tok), tok, w.ctx, w.len, j) & 1u;
             }
+            const float y = ex2f(fmaf(__uint_as_float(sv[e]), c, -lse[col]));
+            (e & 1 ? sum1 : sum0) += seen ? y : 0.0f;
           }
         }
         tc_fence_before();
@@ -399,6 +423,8 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
         a.mass_out[at] = a.decay * before + a.gain * (sum0 + sum1);
         if (j >= w.ctx && a.pos) a.pos[at] = a.positions ? a.positions[w.row0 + j - w.ctx] : j;
       }
+      before = before1;
+      next = first1;
       item_done();
     }
   }
