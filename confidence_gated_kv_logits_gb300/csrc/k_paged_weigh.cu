@@ -348,19 +348,46 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
       const int tok = t * tb + rt;
       return w.more && t < w.tiles && rt < tb && tok < w.T ? a.lse[static_cast<size_t>(w.row0 + tok) * p.Hq + w.h * p.g + rh] : -INFINITY;
     };
-    bool ok = wait_item(0);
-    float before = ok ? mass_of(item(0)) : 0.0f, next = ok ? lse_of(item(0), item(0).tile0) : 0.0f;
-    while (!group_any(x, !(ok && item(0).more))) {
+    // N columns' weights into four sums, in the columns' order; the steps of neighbouring groups of eight are
+    // interleaved (written in order: the schedule is otherwise one chain after another)
+    uint64_t sum[4];
+    auto weights = [&](auto const& sv, const float* lse, auto keep) {
+      constexpr int N = sizeof(sv) / 4;
+      const float4* lq = reinterpret_cast<const float4*>(lse);
+      float z[2][8];
+      uint64_t e[2][4];
+      auto args = [&](int g) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float4 l = lq[2 * g + y];
+          z[g & 1][4 * y] = fma_o(__uint_as_float(sv[8 * g + 4 * y]), c, -l.x);
+          z[g & 1][4 * y + 1] = fma_o(__uint_as_float(sv[8 * g + 4 * y + 1]), c, -l.y);
+          z[g & 1][4 * y + 2] = fma_o(__uint_as_float(sv[8 * g + 4 * y + 2]), c, -l.z);
+          z[g & 1][4 * y + 3] = fma_o(__uint_as_float(sv[8 * g + 4 * y + 3]), c, -l.w);
+        }
+      };
+      args(0);
+#pragma unroll
+      for (int g = 0; g <= N / 8; ++g) {
+        if (g + 1 < N / 8) args(g + 1);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          if (g < N / 8) {
+            const float e0 = ex2_o(z[g & 1][2 * y]), e1 = ex2_o(z[g & 1][2 * y + 1]);
+            e[g & 1][y] = pair(keep(8 * g + 2 * y, e0), keep(8 * g + 2 * y + 1, e1));
+          }
+          if (g > 0) sum[y] = add2_o(sum[y], e[(g - 1) & 1][y]);
+        }
+      }
+    };
+    // One item, whose mass and first lse were asked for two items ago; false: there is none, or a wait gave up.
+    bool ok = true;
+    auto step = [&](float& before, float& next) {
+      if (group_any(x, !(ok && item(0).more))) return false;
       const Item& w = item(0);
       const int j = w.j0 + x * BT + r;
       const bool here = w.j0 + x * BT < w.len && x < gb;  // the item has this token tile
-      const bool live = here && j < w.len;
-      const size_t at = (static_cast<size_t>(w.b) * p.Hkv + w.h) * a.cap + j;
-      // the next item's mass and lse come while this one's products are waited for
-      ok = wait_item(1);
-      const float before1 = ok ? mass_of(item(1)) : 0.0f, first1 = ok ? lse_of(item(1), item(1).tile0) : 0.0f;
-      float sum0 = 0.0f, sum1 = 0.0f;
-      bool dead = false;
+      sum[0] = sum[1] = sum[2] = sum[3] = 0ull;
       for (int t = w.tile0; t < w.tiles; ++t, ++ns) {
         if (!here) continue;                              // (it counts the tile all the same)
         const unsigned par = ns & 1, acc = 2 * x + par;
@@ -370,10 +397,7 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
         const bool got = bar_wait_warp(b_s + 8 * acc, (par ? used1 : used0) & 1, &s.abort);
         if (par) ++used1;
         else ++used0;
-        if (group_any(x, !got)) {
-          dead = true;
-          break;
-        }
+        if (group_any(x, !got)) return false;
         tc_fence_after();
         const int n = rows_of(w, t);
         // columns that see this token: causal ones from its own row on
@@ -381,51 +405,78 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
         const bool masked = a.bt.mask && w.j0 + x * BT + BT > w.ctx;
         const int from = a.bt.mask || past <= 0 ? 0 : past * p.g;
         const uint32_t ts = tmem + lanes + acc * BR;
-        int q = 0;
-        if (!masked && !__any_sync(0xffffffffu, from > 0)) {
-          for (; q + 32 <= n; q += 32) {
-            uint32_t sv[32];
-            tmem_ld32(sv, ts + q);
+        if (masked) {
+          // by the batch's mask, column by column
+          int tok = t * tb, left = p.g;                   // the column's new token, its columns that are left
+#pragma unroll 1
+          for (int q = 0; q < n; q += 8) {
+            uint32_t sv[8];
+            __syncwarp();
+            tmem_ld8(sv, ts + q);
             tmem_wait_ld(sv);
-            const float4* lq = reinterpret_cast<const float4*>(lse + q);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float4 l = lq[e];
-              sum0 += ex2f(fmaf(__uint_as_float(sv[4 * e]), c, -l.x));
-              sum1 += ex2f(fmaf(__uint_as_float(sv[4 * e + 1]), c, -l.y));
-              sum0 += ex2f(fmaf(__uint_as_float(sv[4 * e + 2]), c, -l.z));
-              sum1 += ex2f(fmaf(__uint_as_float(sv[4 * e + 3]), c, -l.w));
+              const bool seen = q + e < n && (seen_bits(a.bt, static_cast<size_t>(w.row0 + tok), tok, w.ctx, w.len, j) & 1u);
+              const float y = seen ? ex2f(fmaf(__uint_as_float(sv[e]), c, -lse[q + e])) : 0.0f;
+              sum[e >> 1] = add2(sum[e >> 1], e & 1 ? pair(0.0f, y) : pair(y, 0.0f));
+              if (--left == 0) {
+                left = p.g;
+                if (tok + 1 < w.T) ++tok;
+              }
             }
           }
-        }
-        for (; q < n; q += 8) {
-          uint32_t sv[8];
-          __syncwarp();
-          tmem_ld8(sv, ts + q);
-          tmem_wait_ld(sv);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int col = q + e;
-            bool seen = col >= from && col < n;
-            if (masked && seen) {
-              const int tok = t * tb + col / p.g;
-              seen = seen_bits(a.bt, static_cast<size_t>(w.row0 + tok), tok, w.ctx, w.len, j) & 1u;
+        } else {
+          int q = 0;
+          if (!__any_sync(0xffffffffu, from > 0)) {
+#pragma unroll 1
+            for (; q + 32 <= n; q += 32) {
+              uint32_t sv[32];
+              tmem_ld32(sv, ts + q);
+              tmem_wait_ld(sv);
+              weights(sv, lse + q, [](int, float y) { return y; });
             }
-            const float y = ex2f(fmaf(__uint_as_float(sv[e]), c, -lse[col]));
-            (e & 1 ? sum1 : sum0) += seen ? y : 0.0f;
+          }
+#pragma unroll 1
+          for (; q < n; q += 8) {
+            uint32_t sv[8];
+            tmem_ld8(sv, ts + q);
+            tmem_wait_ld(sv);
+            weights(sv, lse + q, [&](int col, float y) { return q + col >= from && q + col < n ? y : 0.0f; });
           }
         }
         tc_fence_before();
         bar_arrive(b_free + 8 * acc);
       }
-      if (dead) break;
-      if (live) {
-        a.mass_out[at] = a.decay * before + a.gain * (sum0 + sum1);
+      if (here && j < w.len) {
+        const size_t at = (static_cast<size_t>(w.b) * p.Hkv + w.h) * a.cap + j;
+        const float2 y = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+        a.mass_out[at] = a.decay * before + a.gain * (y.x + y.y);
         if (j >= w.ctx && a.pos) a.pos[at] = a.positions ? a.positions[w.row0 + j - w.ctx] : j;
       }
-      before = before1;
-      next = first1;
+      // the one after the next (the next is there, it may be the end)
+      ok = wait_item(1);
+      if (ok && item(1).more) {
+        ok = wait_item(2);
+        if (ok) {
+          before = mass_of(item(2));
+          next = lse_of(item(2), item(2).tile0);
+        }
+      }
       item_done();
+      return true;
+    };
+    float before0 = 0.0f, before1 = 0.0f, next0 = 0.0f, next1 = 0.0f;
+    ok = wait_item(0);
+    if (ok && item(0).more) {
+      before0 = mass_of(item(0));
+      next0 = lse_of(item(0), item(0).tile0);
+      ok = wait_item(1);
+      if (ok) {
+        before1 = mass_of(item(1));
+        next1 = lse_of(item(1), item(1).tile0);
+      }
+    }
+    while (step(before0, next0) && step(before1, next1)) {
     }
   }
   __syncthreads();
