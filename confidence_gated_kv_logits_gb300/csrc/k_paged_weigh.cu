@@ -9,15 +9,16 @@
 // Tokens are the products' M (tiles of 128, full whatever the rows are) and query
 // rows their N (16 to 128), S = K Q^T in tensor memory: a thread owns a token, so
 // the sum over rows needs no other thread, a single token's few rows cost a
-// product of N = 16, and there is nothing to join.  An item is up to 256 tokens
-// (two tiles) of one KV head of one sequence; its K stays in shared memory while the
-// rows' tiles of up to 128 (whole new tokens, as the heads of a group lie side by
-// side) go by.  Items are laid end to end by their cost and cut into equal shares.
+// product of N = 16, and there is nothing to join.  An item is some token tiles of
+// one KV head of one sequence: two where the rows need several tiles of up to 128
+// (whole new tokens, as the heads of a group lie side by side), which go by while K
+// stays in shared memory, up to eight where one tile holds all rows.  Items are laid
+// end to end by their cost and cut into equal shares.
 //
-// Roles of a CTA's twelve warps: two warpgroups take the exponentials of one of the
-// item's token tiles each, warp 8 issues the products, warp 9 moves K, warp 10 the
-// query rows (both by TMA), warp 11 plans.  Two accumulators per token tile let the
-// products of one tile of rows run beside the exponentials of another.
+// Roles of a CTA's twelve warps: two warpgroups take the exponentials of every second
+// token tile each, warp 8 issues the products, warp 9 moves K, warp 10 the
+// query rows (both by TMA), warp 11 plans.  Each warpgroup has two accumulators, so
+// that products run beside exponentials.
 #include <algorithm>
 #include <cstddef>
 
@@ -48,14 +49,14 @@ struct Weigh {
 struct Item {
   int more;                               // 0: the CTA's share ends here
   int b, h, T, ctx, len, row0;
-  int j0;                                 // first token
+  int j0, nb;                             // first token, token tiles
   int tile0, tiles;                       // tiles of rows that see it
 };
 
 struct __align__(16) Shared {             // behind the stages
   unsigned long long bars[2 * 6 + 2 * 5 + 4 + 4 + 2 * kPlan + 1];
   Item plan[kPlan];
-  __align__(16) float lse[2][2][BR];      // [token tile][tile parity]: lse log2 e, +inf for rows that add nothing
+  __align__(16) float lse[2][2][BR];      // [warpgroup][parity]: lse log2 e, +inf for rows that add nothing
   Sched sched;
   long long scan[kThreads / 32];
   uint32_t tmem;
@@ -65,13 +66,16 @@ static_assert(offsetof(Shared, lse) % 16 == 0, "lse is read in 16-byte words");
 
 // The items of a sequence's heads.
 struct Items : Walk<BR, BT, 0> {
-  const int cap, tb, gb;                  // places of the mass; new tokens of a tile of rows; token tiles of an item
-  int tiles, items;                       // of the sequence
-  __device__ __forceinline__ Items(const Pool& p_, const WeighArgs& a, int tb_, int gb_)
-      : Walk(p_, a.bt, a.rows), cap(a.cap), tb(tb_), gb(gb_) {}
+  const int cap, tb, gb1, gb2;            // places of the mass; new tokens of a tile of rows; token tiles of an item
+                                          // whose rows are one tile, several
+  int tiles, gb, items, all;              // of the sequence: tiles of rows, token tiles of an item, items, token tiles
+  __device__ __forceinline__ Items(const Pool& p_, const WeighArgs& a, int tb_, int gb1_)
+      : Walk(p_, a.bt, a.rows), cap(a.cap), tb(tb_), gb1(gb1_), gb2(gb1_ < 2 ? 1 : 2) {}
   __device__ __forceinline__ void shape() {
     tiles = (T + tb - 1) / tb;
-    items = (len + BT * gb - 1) / (BT * gb);
+    gb = tiles > 1 ? gb2 : gb1;
+    all = (len + BT - 1) / BT;
+    items = (all + gb - 1) / gb;
   }
   __device__ __forceinline__ void sequence(int b_, int& flag) {
     Walk::sequence(b_, flag);
@@ -86,17 +90,26 @@ struct Items : Walk<BR, BT, 0> {
     const int x = i * BT * gb - ctx;
     return bt.mask || x <= 0 ? 0 : x / tb;
   }
-  __device__ __forceinline__ int full_items() const {       // those that every row sees
-    return bt.mask || items <= ctx / (BT * gb) + 1 ? items : ctx / (BT * gb) + 1;
+  __device__ __forceinline__ int count(int i) const { return all - i * gb < gb ? all - i * gb : gb; }      // its token tiles
+  __device__ __forceinline__ int full_items() const {       // those of gb tiles that every row sees
+    const int whole = all / gb, seen = ctx / (BT * gb) + 1;
+    return bt.mask || whole < seen ? whole : seen;
   }
-  __device__ __forceinline__ int cost(int i) const { return kFixed + tiles - first_tile(i); }
+  __device__ __forceinline__ int cost(int i) const { return count(i) * (kFixed + tiles - first_tile(i)); }
   __device__ __forceinline__ long long head_work() const {
     const int n = full_items();
-    long long w = static_cast<long long>(n) * (kFixed + tiles);
+    long long w = static_cast<long long>(n) * (gb * (kFixed + tiles));
+#pragma unroll 1
     for (int i = n; i < items; ++i) w += cost(i);
     return w;
   }
 };
+
+// bar_wait_warp with its polling out of line: the roles' loops have to stay in the instruction cache
+__device__ __noinline__ bool wait_on(uint32_t bar, unsigned parity, volatile int* abort) { return bar_wait_warp(bar, parity, abort); }
+__device__ __forceinline__ bool wait_bar(uint32_t bar, unsigned parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, bar_try(bar, parity)) || wait_on(bar, parity, abort);
+}
 
 // warps of one warpgroup decide together whether they go on (and see what all wrote)
 __device__ __forceinline__ bool group_any(int group, bool mine) {
@@ -122,7 +135,7 @@ struct QueryMaps {                        // q as [rows][heads][d], boxes of 64 
 
 template <bool BF, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ CUtensorMap mk, const __grid_constant__ QueryMaps mq) {
+k_weigh(const Pool p, const WeighArgs a, const int gb1, const __grid_constant__ CUtensorMap mk, const __grid_constant__ QueryMaps mq) {
   using W = Weigh<D>;
   constexpr int SK = W::SK, SQ = W::SQ;
   extern __shared__ __align__(1024) unsigned char s_raw[];
@@ -156,7 +169,7 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
   tc_fence_before();
   const int tb = mq.n_all;
   if (a.bt.B > 32) {
-    Items w(p, a, tb, gb);
+    Items w(p, a, tb, gb1);
     sched_init<kThreads>(w, &s.sched, s.scan, 1);
   } else {
     __syncthreads();
@@ -165,7 +178,7 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
   const uint32_t tmem = s.tmem;
   unsigned plan = 0;
   auto wait_item = [&](unsigned ahead) {  // the planned item that many further is there (behind the last one there is none)
-    return bar_wait_warp(b_plan + 8 * ((plan + ahead) % kPlan), ((plan + ahead) / kPlan) & 1, &s.abort);
+    return wait_bar(b_plan + 8 * ((plan + ahead) % kPlan), ((plan + ahead) / kPlan) & 1, &s.abort);
   };
   auto item = [&](unsigned ahead) -> const Item& { return s.plan[(plan + ahead) % kPlan]; };
   auto next_item = [&] { return wait_item(0) && item(0).more; };
@@ -179,7 +192,7 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
 
   if (warp == 11) {
     // ---- the plan ----
-    Items w(p, a, tb, gb);
+    Items w(p, a, tb, gb1);
     Sched sh;
     if (a.bt.B <= 32) sh = sched_warp(w, 1, 0, blockIdx.x, gridDim.x);
     else sh = s.sched;
@@ -195,7 +208,7 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
       // the share's first item: the first that starts in it
       w.h = static_cast<int>(quotient(cur - sh.seq0, sh.head));
       at = sh.seq0 + w.h * sh.head;
-      const int full = kFixed + w.tiles, n = w.full_items();
+      const int full = w.gb * (kFixed + w.tiles), n = w.full_items();
       const long long j = quotient(cur - at + full - 1, full);
       i = j < n ? static_cast<int>(j) : n;
       at += static_cast<long long>(i) * full;
@@ -210,9 +223,9 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
         }
       }
       more = cur < sh.end && at < sh.end;
-      if (plan >= kPlan && !bar_wait_warp(b_read + 8 * (plan % kPlan), (plan / kPlan - 1) & 1, &s.abort)) break;
+      if (plan >= kPlan && !wait_bar(b_read + 8 * (plan % kPlan), (plan / kPlan - 1) & 1, &s.abort)) break;
       if (lane == 0) {
-        s.plan[plan % kPlan] = more ? Item{1, w.b, w.h, w.T, w.ctx, w.len, w.row0, i * BT * gb, w.first_tile(i), w.tiles} : Item{};
+        s.plan[plan % kPlan] = more ? Item{1, w.b, w.h, w.T, w.ctx, w.len, w.row0, i * BT * w.gb, w.count(i), w.first_tile(i), w.tiles} : Item{};
         bar_arrive(b_plan + 8 * (plan % kPlan));
       }
       if (more) at += w.cost(i++);
@@ -224,38 +237,45 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
     unsigned slot = 0;
     int flag = 0;
     bool ok = true;
-    // lane i asks for box i of the item: both token tiles' boxes, their channel halves side by side
+    // two token tiles at a time: a lane has one box, both tiles' boxes and their channel halves side by side
     constexpr int HV = D / 64;
-    const int x = lane / (16 / 2 * HV), i = lane % (16 / 2 * HV) / HV, half = lane % HV;
-    auto page_of = [&](const Item& w) {   // the lane's page
-      const int j = w.j0 + x * BT + i * rows_per;
-      return w.more && x < gb && i < boxes && j < w.len ? a.bt.table[static_cast<size_t>(w.b) * a.bt.max_blocks + (j >> p.ps_shift)] : 0;
+    const int x = lane / (8 * HV), i = lane % (8 * HV) / HV, half = lane % HV;
+    auto page_of = [&](const Item& w, int y0) {
+      const int j = w.j0 + (y0 + x) * BT + i * rows_per;
+      return w.more && x < 2 && y0 + x < w.nb && i < boxes && j < w.len
+                 ? a.bt.table[static_cast<size_t>(w.b) * a.bt.max_blocks + (j >> p.ps_shift)] : 0;
     };
     ok = wait_item(0);
-    int page = ok ? page_of(item(0)) : 0;
+    int page = ok ? page_of(item(0), 0) : 0;
     while (ok && item(0).more) {
       const Item& w = item(0);
-      ok = wait_item(1);                  // the next item's pages are asked for before this one's boxes
-      if (!ok) break;
-      const int page1 = page_of(item(1));
-      const bool none = static_cast<unsigned>(page) >= static_cast<unsigned>(p.NP);
-      for (int y = 0; y < gb && w.j0 + y * BT < w.len; ++y, ++slot) {
-        const unsigned st = slot % SK;
-        if (slot >= SK && !bar_wait_warp(b_ke + 8 * st, (slot / SK - 1) & 1, &s.abort)) {
+      for (int y0 = 0; ok && y0 < w.nb; y0 += 2) {
+        // the next boxes' pages are asked for before these boxes
+        const bool ends = y0 + 2 >= w.nb;
+        if (ends && !wait_item(1)) {
           ok = false;
           break;
         }
-        const int j0 = w.j0 + y * BT, live = (w.len - j0 + rows_per - 1) / rows_per, n = live < boxes ? live : boxes;
-        if (lane == 0) bar_expect(b_kf + 8 * st, static_cast<unsigned>(n * rows_per * D * 2));
-        __syncwarp();
-        if (x == y && i < n) {
-          if (none) flag = CONFKV_FLAG_BAD_PAGE;
-          const int j = j0 + i * rows_per;
-          const int row = none ? kNoRows : (((a.layer * p.NP + page) * p.Hkv + w.h) << p.ps_shift) + (j & (p.ps - 1));
-          tma_box(k_ring + st * W::TILE + half * W::HALF + i * rows_per * 128, &mk, 64 * half, row, b_kf + 8 * st, pol);
+        const int page1 = ends ? page_of(item(1), 0) : page_of(w, y0 + 2);
+        const bool none = static_cast<unsigned>(page) >= static_cast<unsigned>(p.NP);
+        for (int y = y0; y < y0 + 2 && y < w.nb; ++y, ++slot) {
+          const unsigned st = slot % SK;
+          if (slot >= SK && !wait_bar(b_ke + 8 * st, (slot / SK - 1) & 1, &s.abort)) {
+            ok = false;
+            break;
+          }
+          const int j0 = w.j0 + y * BT, live = (w.len - j0 + rows_per - 1) >> (p.ps < BT ? p.ps_shift : 7), n = live < boxes ? live : boxes;
+          if (lane == 0) bar_expect(b_kf + 8 * st, static_cast<unsigned>(n * rows_per * D * 2));
+          __syncwarp();
+          if (x == y - y0 && i < n) {
+            if (none) flag = CONFKV_FLAG_BAD_PAGE;
+            const int j = j0 + i * rows_per;
+            const int row = none ? kNoRows : (((a.layer * p.NP + page) * p.Hkv + w.h) << p.ps_shift) + (j & (p.ps - 1));
+            tma_box(k_ring + st * W::TILE + half * W::HALF + i * rows_per * 128, &mk, 64 * half, row, b_kf + 8 * st, pol);
+          }
         }
+        page = page1;
       }
-      page = page1;
       item_done();
     }
     if (flag) atomicOr(p.err, flag);
@@ -269,7 +289,7 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
       const Item& w = item(0);
       for (int t = w.tile0; ok && t < w.tiles; ++t, ++slot) {
         const unsigned st = slot % SQ;
-        if (slot >= SQ && !bar_wait_warp(b_qe + 8 * st, (slot / SQ - 1) & 1, &s.abort)) {
+        if (slot >= SQ && !wait_bar(b_qe + 8 * st, (slot / SQ - 1) & 1, &s.abort)) {
           ok = false;
           break;
         }
@@ -289,41 +309,35 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
     // ---- products: S[token tile x][parity] = K Q^T (the warp stays together; one elected thread issues) ----
     constexpr uint32_t hi = umma_hi(1024);
     const uint32_t k_lo = uniform(umma_lo(k_ring, 16)), q_lo = uniform(umma_lo(q_ring, 16));
-    unsigned ks = 0, qs = 0, ns = 0;      // stages taken; tiles of rows so far
-    unsigned used[2][2] = {};             // products into an accumulator so far
+    unsigned ks = 0, qs = 0, used[2] = {0, 0};            // stages taken; products for each warpgroup
     bool ok = true;
     while (ok && next_item()) {
       const Item& w = item(0);
-      const int blocks = min(gb, (w.len - w.j0 + BT - 1) / BT);
-      for (int x = 0; ok && x < blocks; ++x) ok = bar_wait_warp(b_kf + 8 * ((ks + x) % SK), ((ks + x) / SK) & 1, &s.abort);
-      for (int t = w.tile0; ok && t < w.tiles; ++t, ++qs, ++ns) {
+      const int nb = w.nb;
+      for (int t = w.tile0; ok && t < w.tiles; ++t, ++qs) {
         const unsigned st = qs % SQ;
-        ok = bar_wait_warp(b_qf + 8 * st, (qs / SQ) & 1, &s.abort);
-        const uint32_t idesc = umma_idesc(BF, 128, (rows_of(w, t) + 15) & ~15, false);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok || x >= blocks) break;
-          const uint32_t acc = 2 * x + (ns & 1);
-          const unsigned before = ns & 1 ? used[x][1] : used[x][0];
-          if (before) ok = bar_wait_warp(b_free + 8 * acc, (before - 1) & 1, &s.abort);
+        ok = wait_bar(b_qf + 8 * st, (qs / SQ) & 1, &s.abort);
+        const uint32_t idesc = umma_idesc(BF, 128, (rows_of(w, t) + 15) & ~15, false), qt = uniform(q_lo + st * (W::TILE / 16));
+        for (int x = 0; ok && x < nb; ++x) {
+          const unsigned k = ks + x, n = x & 1 ? used[1]++ : used[0]++;
+          const uint32_t acc = 2 * (x & 1) + (n & 1);
+          if (t == w.tile0) ok = wait_bar(b_kf + 8 * (k % SK), (k / SK) & 1, &s.abort);
+          if (ok && n >= 2) ok = wait_bar(b_free + 8 * acc, (n / 2 - 1) & 1, &s.abort);
           if (!ok) break;
-          if (ns & 1) ++used[x][1];
-          else ++used[x][0];
           tc_fence_after();
-          const uint32_t kt = uniform(k_lo + ((ks + x) % SK) * (W::TILE / 16)), qt = uniform(q_lo + st * (W::TILE / 16));
-          const uint32_t d = uniform(tmem + acc * BR);
+          const uint32_t kt = uniform(k_lo + (k % SK) * (W::TILE / 16)), d = uniform(tmem + acc * BR);
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             const uint32_t o = ((c >> 2) * W::HALF + (c & 3) * 32) / 16;
             umma_ss(d, kt + o, hi, qt + o, hi, idesc, c > 0);
           }
           umma_commit(b_s + 8 * acc);
+          if (t + 1 == w.tiles) umma_commit(b_ke + 8 * (k % SK));
         }
         if (ok) umma_commit(b_qe + 8 * st);
       }
       if (!ok) break;
-      for (int x = 0; x < blocks; ++x) umma_commit(b_ke + 8 * ((ks + x) % SK));
-      ks += blocks;
+      ks += nb;
       item_done();
     }
     // products in flight end before the CTA does
@@ -334,15 +348,14 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
     __syncwarp();
   } else {
     // ---- weights ----
-    const int x = warp >> 2, r = tid & 127;               // token tile of the item; token of the tile, and column whose lse it brings
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int g = warp >> 2, r = tid & 127;               // warpgroup; token of a tile, and column whose lse it brings
+    const uint32_t ts0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 2 * g * BR;
     const float c = a.scale * kL2E;
     const int rt = r / p.g, rh = r - rt * p.g;
-    unsigned ns = 0, used0 = 0, used1 = 0;                // tiles of rows so far; those of its two accumulators
-    // an item's mass, and the lse of a column of its tile t
-    auto mass_of = [&](const Item& w) {
+    // the mass of tile x's token, and the lse of a column of rows' tile t
+    auto mass_of = [&](const Item& w, int x) {
       const int j = w.j0 + x * BT + r;
-      return w.more && x < gb && j < w.len && j < w.ctx ? a.mass[(static_cast<size_t>(w.b) * p.Hkv + w.h) * a.cap + j] : 0.0f;
+      return w.more && x < w.nb && j < w.len && j < w.ctx ? a.mass[(static_cast<size_t>(w.b) * p.Hkv + w.h) * a.cap + j] : 0.0f;
     };
     auto lse_of = [&](const Item& w, int t) {
       const int tok = t * tb + rt;
@@ -356,127 +369,123 @@ k_weigh(const Pool p, const WeighArgs a, const int gb, const __grid_constant__ C
       const float4* lq = reinterpret_cast<const float4*>(lse);
       float z[2][8];
       uint64_t e[2][4];
-      auto args = [&](int g) {
+      auto args = [&](int k) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const float4 l = lq[2 * g + y];
-          z[g & 1][4 * y] = fma_o(__uint_as_float(sv[8 * g + 4 * y]), c, -l.x);
-          z[g & 1][4 * y + 1] = fma_o(__uint_as_float(sv[8 * g + 4 * y + 1]), c, -l.y);
-          z[g & 1][4 * y + 2] = fma_o(__uint_as_float(sv[8 * g + 4 * y + 2]), c, -l.z);
-          z[g & 1][4 * y + 3] = fma_o(__uint_as_float(sv[8 * g + 4 * y + 3]), c, -l.w);
+          const float4 l = lq[2 * k + y];
+          z[k & 1][4 * y] = fma_o(__uint_as_float(sv[8 * k + 4 * y]), c, -l.x);
+          z[k & 1][4 * y + 1] = fma_o(__uint_as_float(sv[8 * k + 4 * y + 1]), c, -l.y);
+          z[k & 1][4 * y + 2] = fma_o(__uint_as_float(sv[8 * k + 4 * y + 2]), c, -l.z);
+          z[k & 1][4 * y + 3] = fma_o(__uint_as_float(sv[8 * k + 4 * y + 3]), c, -l.w);
         }
       };
       args(0);
 #pragma unroll
-      for (int g = 0; g <= N / 8; ++g) {
-        if (g + 1 < N / 8) args(g + 1);
+      for (int k = 0; k <= N / 8; ++k) {
+        if (k + 1 < N / 8) args(k + 1);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          if (g < N / 8) {
-            const float e0 = ex2_o(z[g & 1][2 * y]), e1 = ex2_o(z[g & 1][2 * y + 1]);
-            e[g & 1][y] = pair(keep(8 * g + 2 * y, e0), keep(8 * g + 2 * y + 1, e1));
+          if (k < N / 8) {
+            const float e0 = ex2_o(z[k & 1][2 * y]), e1 = ex2_o(z[k & 1][2 * y + 1]);
+            e[k & 1][y] = pair(keep(8 * k + 2 * y, e0), keep(8 * k + 2 * y + 1, e1));
           }
-          if (g > 0) sum[y] = add2_o(sum[y], e[(g - 1) & 1][y]);
+          if (k > 0) sum[y] = add2_o(sum[y], e[(k - 1) & 1][y]);
         }
       }
     };
-    // One item, whose mass and first lse were asked for two items ago; false: there is none, or a wait gave up.
-    bool ok = true;
-    auto step = [&](float& before, float& next) {
-      if (group_any(x, !(ok && item(0).more))) return false;
+    unsigned used = 0, steps = 0;                         // products; tiles of rows
+    bool ok = wait_item(0);
+    float before = ok ? mass_of(item(0), g) : 0.0f, next = ok ? lse_of(item(0), item(0).tile0) : 0.0f;
+    while (!group_any(g, !(ok && item(0).more))) {
       const Item& w = item(0);
-      const int j = w.j0 + x * BT + r;
-      const bool here = w.j0 + x * BT < w.len && x < gb;  // the item has this token tile
+      const int nb = w.nb;
       sum[0] = sum[1] = sum[2] = sum[3] = 0ull;
-      for (int t = w.tile0; t < w.tiles; ++t, ++ns) {
-        if (!here) continue;                              // (it counts the tile all the same)
-        const unsigned par = ns & 1, acc = 2 * x + par;
-        float* lse = s.lse[x][par];
+      ok = wait_item(1);
+      bool dead = !ok;
+      for (int t = w.tile0; t < w.tiles; ++t, ++steps) {
+        float* lse = s.lse[g][steps & 1];
         lse[r] = next == -INFINITY ? INFINITY : next * kL2E;
+        // the next tile's lse, the next item's behind the last
         if (t + 1 < w.tiles) next = lse_of(w, t + 1);
-        const bool got = bar_wait_warp(b_s + 8 * acc, (par ? used1 : used0) & 1, &s.abort);
-        if (par) ++used1;
-        else ++used0;
-        if (group_any(x, !got)) return false;
-        tc_fence_after();
+        else if (ok) next = lse_of(item(1), item(1).tile0);
+        if (group_any(g, dead)) {
+          dead = true;
+          break;
+        }
         const int n = rows_of(w, t);
-        // columns that see this token: causal ones from its own row on
-        const int past = j - w.ctx - t * tb;              // new tokens of the tile that come before it
-        const bool masked = a.bt.mask && w.j0 + x * BT + BT > w.ctx;
-        const int from = a.bt.mask || past <= 0 ? 0 : past * p.g;
-        const uint32_t ts = tmem + lanes + acc * BR;
-        if (masked) {
-          // by the batch's mask, column by column
-          int tok = t * tb, left = p.g;                   // the column's new token, its columns that are left
 #pragma unroll 1
-          for (int q = 0; q < n; q += 8) {
-            uint32_t sv[8];
-            __syncwarp();
-            tmem_ld8(sv, ts + q);
-            tmem_wait_ld(sv);
+        for (int x = g; x < nb; x += 2, ++used) {
+          const int j = w.j0 + x * BT + r;
+          const uint32_t acc = used & 1, ts = ts0 + acc * BR;
+          const bool last = t + 1 == w.tiles;
+          float after = before;
+          if (last) after = x + 2 < nb ? mass_of(w, x + 2) : ok ? mass_of(item(1), g) : 0.0f;
+          if (!wait_bar(b_s + 8 * (2 * g + acc), (used >> 1) & 1, &s.abort)) {
+            dead = true;                  // the others learn of it at the next decision, to which all four warps come
+            break;
+          }
+          tc_fence_after();
+          // columns that see this token: causal ones from its own row on
+          const int past = j - w.ctx - t * tb;            // new tokens of the tile that come before it
+          const bool masked = a.bt.mask && w.j0 + x * BT + BT > w.ctx;
+          const int from = a.bt.mask || past <= 0 ? 0 : past * p.g;
+          if (masked) {
+            // by the batch's mask, column by column
+            int tok = t * tb, left = p.g;                 // the column's new token, its columns that are left
+#pragma unroll 1
+            for (int q = 0; q < n; q += 8) {
+              uint32_t sv[8];
+              __syncwarp();
+              tmem_ld8(sv, ts + q);
+              tmem_wait_ld(sv);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const bool seen = q + e < n && (seen_bits(a.bt, static_cast<size_t>(w.row0 + tok), tok, w.ctx, w.len, j) & 1u);
-              const float y = seen ? ex2f(fmaf(__uint_as_float(sv[e]), c, -lse[q + e])) : 0.0f;
-              sum[e >> 1] = add2(sum[e >> 1], e & 1 ? pair(0.0f, y) : pair(y, 0.0f));
-              if (--left == 0) {
-                left = p.g;
-                if (tok + 1 < w.T) ++tok;
+              for (int e = 0; e < 8; ++e) {
+                const bool seen = q + e < n && (seen_bits(a.bt, static_cast<size_t>(w.row0 + tok), tok, w.ctx, w.len, j) & 1u);
+                const float y = seen ? ex2f(fmaf(__uint_as_float(sv[e]), c, -lse[q + e])) : 0.0f;
+                sum[e >> 1] = add2(sum[e >> 1], e & 1 ? pair(0.0f, y) : pair(y, 0.0f));
+                if (--left == 0) {
+                  left = p.g;
+                  if (tok + 1 < w.T) ++tok;
+                }
               }
             }
-          }
-        } else {
-          int q = 0;
-          if (!__any_sync(0xffffffffu, from > 0)) {
+          } else {
+            int q = 0;
+            if (!__any_sync(0xffffffffu, from > 0)) {
 #pragma unroll 1
-            for (; q + 32 <= n; q += 32) {
-              uint32_t sv[32];
-              tmem_ld32(sv, ts + q);
+              for (; q + 32 <= n; q += 32) {
+                uint32_t sv[32];
+                tmem_ld32(sv, ts + q);
+                tmem_wait_ld(sv);
+                weights(sv, lse + q, [](int, float y) { return y; });
+              }
+            }
+#pragma unroll 1
+            for (; q < n; q += 8) {
+              uint32_t sv[8];
+              tmem_ld8(sv, ts + q);
               tmem_wait_ld(sv);
-              weights(sv, lse + q, [](int, float y) { return y; });
+              weights(sv, lse + q, [&](int col, float y) { return q + col >= from && q + col < n ? y : 0.0f; });
             }
           }
-#pragma unroll 1
-          for (; q < n; q += 8) {
-            uint32_t sv[8];
-            tmem_ld8(sv, ts + q);
-            tmem_wait_ld(sv);
-            weights(sv, lse + q, [&](int col, float y) { return q + col >= from && q + col < n ? y : 0.0f; });
+          tc_fence_before();
+          bar_arrive(b_free + 8 * (2 * g + acc));
+          if (last) {
+            if (j < w.len) {
+              const size_t at = (static_cast<size_t>(w.b) * p.Hkv + w.h) * a.cap + j;
+              const float2 y = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+              a.mass_out[at] = a.decay * before + a.gain * (y.x + y.y);
+              if (j >= w.ctx && a.pos) a.pos[at] = a.positions ? a.positions[w.row0 + j - w.ctx] : j;
+            }
+            sum[0] = sum[1] = sum[2] = sum[3] = 0ull;
           }
-        }
-        tc_fence_before();
-        bar_arrive(b_free + 8 * acc);
-      }
-      if (here && j < w.len) {
-        const size_t at = (static_cast<size_t>(w.b) * p.Hkv + w.h) * a.cap + j;
-        const float2 y = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
-        a.mass_out[at] = a.decay * before + a.gain * (y.x + y.y);
-        if (j >= w.ctx && a.pos) a.pos[at] = a.positions ? a.positions[w.row0 + j - w.ctx] : j;
-      }
-      // the one after the next (the next is there, it may be the end)
-      ok = wait_item(1);
-      if (ok && item(1).more) {
-        ok = wait_item(2);
-        if (ok) {
-          before = mass_of(item(2));
-          next = lse_of(item(2), item(2).tile0);
+          before = after;
         }
       }
+      // (a warpgroup without a tile in this item has not read the next one's mass)
+      if (nb <= g && ok) before = mass_of(item(1), g);
+      ok = ok && !dead;
       item_done();
-      return true;
-    };
-    float before0 = 0.0f, before1 = 0.0f, next0 = 0.0f, next1 = 0.0f;
-    ok = wait_item(0);
-    if (ok && item(0).more) {
-      before0 = mass_of(item(0));
-      next0 = lse_of(item(0), item(0).tile0);
-      ok = wait_item(1);
-      if (ok) {
-        before1 = mass_of(item(1));
-        next1 = lse_of(item(1), item(1).tile0);
-      }
-    }
-    while (step(before0, next0) && step(before1, next1)) {
     }
   }
   __syncthreads();
@@ -519,9 +528,10 @@ cudaError_t launch_weigh(const Pool& p, const WeighArgs& a, const AttendMaps& m,
     const cudaError_t e = encode_map(x.map, p.bf16, 3, const_cast<uint16_t*>(a.q), dims, strides, box, false);
     if (e != cudaSuccess) return e;
   }
-  // Two token tiles to an item where there are more tiles than CTAs (the tables' width is what the host knows).
-  const long long tiles = (static_cast<long long>(a.bt.max_blocks) * p.ps + BT - 1) / BT;
-  const int gb = static_cast<long long>(a.bt.B) * p.Hkv * tiles <= ctas ? 1 : 2;
+  // Token tiles of an item: one where each finds a CTA of its own, two where there are not many to a CTA, then more, so
+  // that an item's cost is spread (the tables' width is what the host knows of the lengths).
+  const long long tiles = static_cast<long long>(a.bt.B) * p.Hkv * ((static_cast<long long>(a.bt.max_blocks) * p.ps + BT - 1) / BT);
+  const int gb = tiles <= ctas ? 1 : tiles < 64ll * ctas ? 2 : tiles < 128ll * ctas ? 4 : 8;
   const cudaError_t e = each_weigh([&](auto kernel, bool bf, int d, int smem) {
     if (bf != (p.bf16 != 0) || d != p.d) return cudaSuccess;
     return launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem + sizeof(Shared), s, p, a, gb, m.k_many, mq);
