@@ -15,10 +15,11 @@
 // stays in shared memory, up to eight where one tile holds all rows.  Items are laid
 // end to end by their cost and cut into equal shares.
 //
-// Roles of a CTA's twelve warps: two warpgroups take the exponentials of every second
-// token tile each, warp 8 issues the products, warp 9 moves K, warp 10 the
-// query rows (both by TMA), warp 11 plans.  Each warpgroup has two accumulators, so
-// that products run beside exponentials.
+// Roles of a CTA's thirteen warps: two warpgroups take the exponentials of every
+// second token tile each, warps 8 and 12 issue their products (one warp alone takes
+// as long to issue both's as the exponentials do), warp 9 moves K, warp 10 the query
+// rows (both by TMA), warp 11 plans.  Each warpgroup has two accumulators, so that
+// products run beside exponentials.
 #include <algorithm>
 #include <cstddef>
 
@@ -28,13 +29,13 @@ namespace confkv {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 416;
 constexpr int BT = 128;                   // tokens of a tile (kManyBlock: the boxes are attend's)
 constexpr int BR = 128;                   // most query rows of a tile
 constexpr float kL2E = 1.4426950408889634f;
 constexpr int kFixed = 2;                 // an item's fixed cost in tiles of rows: its K from memory
 constexpr int kPlan = 8;                  // items in the planned ring
-constexpr int kReaders = 11;              // warps that read it
+constexpr int kReaders = 12;              // warps that read it
 
 static_assert(BT == kManyBlock, "boxes of the pools");
 
@@ -54,7 +55,7 @@ struct Item {
 };
 
 struct __align__(16) Shared {             // behind the stages
-  unsigned long long bars[2 * 6 + 2 * 5 + 4 + 4 + 2 * kPlan + 1];
+  unsigned long long bars[2 * 6 + 2 * 5 + 4 + 4 + 2 * kPlan + 2];
   Item plan[kPlan];
   __align__(16) float lse[2][2][BR];      // [warpgroup][parity]: lse log2 e, +inf for rows that add nothing
   Sched sched;
@@ -145,7 +146,16 @@ k_weigh(const Pool p, const WeighArgs a, const int gb1, const __grid_constant__ 
   const uint32_t b_kf = bars, b_ke = b_kf + 8 * SK, b_qf = b_ke + 8 * SK, b_qe = b_qf + 8 * SQ, b_s = b_qe + 8 * SQ,
                  b_free = b_s + 32, b_plan = b_free + 32, b_read = b_plan + 8 * kPlan, b_end = b_read + 8 * kPlan;
   if (tid == 0) {
-    for (int i = 0; i < 2 * (SK + SQ); ++i) bar_init(b_kf + 8 * i, 1);
+    // both issuing warps wait for every stage in turn, their own or not, and both give every stage back (were
+    // the other's stages passed over, a stage that changes hands could answer a wait by an earlier phase)
+    for (int i = 0; i < SK; ++i) {
+      bar_init(b_kf + 8 * i, 1);
+      bar_init(b_ke + 8 * i, 2);
+    }
+    for (int i = 0; i < SQ; ++i) {
+      bar_init(b_qf + 8 * i, 1);
+      bar_init(b_qe + 8 * i, 2);
+    }
     for (int i = 0; i < 4; ++i) {
       bar_init(b_s + 8 * i, 1);
       bar_init(b_free + 8 * i, 128);
@@ -155,6 +165,7 @@ k_weigh(const Pool p, const WeighArgs a, const int gb1, const __grid_constant__ 
       bar_init(b_read + 8 * i, kReaders);
     }
     bar_init(b_end, 1);
+    bar_init(b_end + 8, 1);
     s.abort = 0;
     fence_bar_init();
     fence_async();
@@ -305,11 +316,12 @@ k_weigh(const Pool p, const WeighArgs a, const int gb1, const __grid_constant__ 
     }
     if (!ok)
       for (unsigned k = slot > SQ ? slot - SQ : 0; k < slot; ++k) bar_drain(b_qf + 8 * (k % SQ), (k / SQ) & 1);
-  } else if (warp == 8) {
-    // ---- products: S[token tile x][parity] = K Q^T (the warp stays together; one elected thread issues) ----
+  } else if (warp == 8 || warp == 12) {
+    // ---- a warpgroup's products, S = K Q^T (the warp stays together; one elected thread issues) ----
+    const int g = warp == 12;
     constexpr uint32_t hi = umma_hi(1024);
     const uint32_t k_lo = uniform(umma_lo(k_ring, 16)), q_lo = uniform(umma_lo(q_ring, 16));
-    unsigned ks = 0, qs = 0, used[2] = {0, 0};            // stages taken; products for each warpgroup
+    unsigned ks = 0, qs = 0, used = 0;                    // stages passed; products so far
     bool ok = true;
     while (ok && next_item()) {
       const Item& w = item(0);
@@ -319,9 +331,14 @@ k_weigh(const Pool p, const WeighArgs a, const int gb1, const __grid_constant__ 
         ok = wait_bar(b_qf + 8 * st, (qs / SQ) & 1, &s.abort);
         const uint32_t idesc = umma_idesc(BF, 128, (rows_of(w, t) + 15) & ~15, false), qt = uniform(q_lo + st * (W::TILE / 16));
         for (int x = 0; ok && x < nb; ++x) {
-          const unsigned k = ks + x, n = x & 1 ? used[1]++ : used[0]++;
-          const uint32_t acc = 2 * (x & 1) + (n & 1);
+          const unsigned k = ks + x;
           if (t == w.tile0) ok = wait_bar(b_kf + 8 * (k % SK), (k / SK) & 1, &s.abort);
+          if ((x & 1) != g) {
+            if (ok && t == w.tile0) bar_arrive_warp(b_ke + 8 * (k % SK));
+            continue;
+          }
+          const unsigned n = used++;
+          const uint32_t acc = 2 * g + (n & 1);
           if (ok && n >= 2) ok = wait_bar(b_free + 8 * acc, (n / 2 - 1) & 1, &s.abort);
           if (!ok) break;
           tc_fence_after();
@@ -342,8 +359,8 @@ k_weigh(const Pool p, const WeighArgs a, const int gb1, const __grid_constant__ 
     }
     // products in flight end before the CTA does
     if (!ok) {
-      umma_commit(b_end);
-      bar_drain(b_end, 0);
+      umma_commit(b_end + 8 * g);
+      bar_drain(b_end + 8 * g, 0);
     }
     __syncwarp();
   } else {

@@ -464,6 +464,24 @@ def test_weigh_gives_the_same_bits(pkg):
         assert torch.equal(out, first)
 
 
+@pytest.mark.parametrize("heads,kv_heads,d,n,most,t", [(64, 8, 64, 32, 6000, 1), (40, 8, 128, 20, 4000, 1), (40, 8, 128, 9, 3000, 40), (16, 16, 64, 40, 700, 9)])
+def test_weigh_many_items_launch_after_launch(pkg, heads, kv_heads, d, n, most, t):
+    """Many items to a CTA, with even and odd numbers of token tiles: right, and the same bits on every run."""
+    r = np.random.default_rng(n)
+    c = Case(torch.bfloat16, heads, kv_heads, d, 64, [int(x) for x in r.integers(0, most, n)], [int(x) for x in r.integers(0, 2 * t, n)], seed=n)
+    _, kv = run_weigh(pkg, c)
+    batch, lse = c.batch(kv), torch.randn(c.rows, heads, device=DEV) + 9
+    mass = torch.rand(n, kv_heads, most + 2 * t, generator=c.g, device=DEV)
+    outs = [torch.zeros_like(mass) for _ in range(4)]
+    kv.weigh(1, batch, c.q, lse, mass, outs[0])
+    first = outs[0].clone()
+    for _ in range(50):
+        for o in outs:
+            kv.weigh(1, batch, c.q, lse, mass, o)
+    assert all(torch.equal(o, first) for o in outs)
+    assert kv.status() == 0
+
+
 def test_weigh_masks_that_leave_nothing_and_masked_nans(pkg):
     c = Case(torch.float16, 10, 2, 64, 16, [0, 20], [5, 40], seed=5)
     bits = tree_bits(c.new)
