@@ -18,7 +18,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kU = 8;                   // loads of a thread in flight
 constexpr uint32_t kFirst = 0xffffffffu, kNewest = 0xfffffffeu;
-constexpr int kKeysShared = 40960;      // keys up to here stay in shared memory
+constexpr int kKeysShared = 24576;      // keys and positions up to here stay in shared memory
+constexpr int kList = 8192;             // moves at a time beyond
+constexpr int kFew = kWarps;            // evicted places that are found one by one
 
 // A mass as an unsigned number in the same order; NaN below everything, -0 as 0.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -49,32 +51,18 @@ __device__ __forceinline__ int scan(int x, int* s_warp, int& all) {
   return before + incl - x;
 }
 
-// The place of the r-th one among words [lo, hi) with `before` ones before each.
-template <typename Word>
-__device__ __forceinline__ int place_of(const int* before, int lo, int hi, int r, Word&& word) {
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (before[mid] <= r) lo = mid;
-    else hi = mid;
-  }
-  return 32 * lo + static_cast<int>(__fns(word(lo), 0, r - before[lo] + 1));
-}
-
-// One CTA: a KV head of a sequence in a layer.  KEYS: its keys lie in shared memory
-// (else they are made again from mass and position wherever they are needed).
+// One CTA: a KV head of a sequence in a layer.  KEYS: its keys and positions lie in shared memory
+// (else they are read again wherever they are needed).
 template <bool KEYS, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 k_evict(const Pool p, const EvictArgs a) {
   extern __shared__ uint32_t s_dyn[];
   __shared__ unsigned s_count[256];
   __shared__ int s_warp[kWarps];
   __shared__ int s_top;
   __shared__ unsigned s_key, s_want;
-  const int words_cap = (a.cap + 31) >> 5;
-  uint32_t* s_kept = s_dyn;                                   // [words]
-  // [words + 1]: holes in the words before; from the word of place N on, one place further, movers
-  int* s_before = reinterpret_cast<int*>(s_dyn + words_cap);
-  uint32_t* s_keys = s_dyn + 2 * words_cap + 1;
+  __shared__ unsigned long long s_min[2][kWarps];
+  __shared__ int s_gone[kFew];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -85,7 +73,7 @@ k_evict(const Pool p, const EvictArgs a) {
   int flag = 0;
   if (n < 0 || budget < 0 || first < 0) flag = CONFKV_FLAG_BAD_INDEX;
   if (n > a.cap || n > static_cast<long long>(a.max_blocks) << p.ps_shift) flag |= CONFKV_FLAG_CAPACITY;
-  const int N = flag ? n : budget < n ? budget : n;
+  const int N = flag ? n : budget < n ? budget : n, gone = n - N;
   if (tid == 0) {
     if (flag) atomicOr(p.err, flag);
     if (h == 0 && (a.per_layer || l == 0)) a.new_len[seq] = N;
@@ -97,6 +85,29 @@ k_evict(const Pool p, const EvictArgs a) {
   float* mass_out = a.mass_out + unit * a.cap;
   int32_t* pos_out = a.pos_out + unit * a.cap;
   const bool copy = mass_out != mass;
+  const int32_t* table = a.table + static_cast<size_t>(b) * a.max_blocks;
+  const int layer = l * p.NP;           // (rows of a pool stay below 2^31)
+  constexpr int LR = D / 8;             // lanes of a row, K's and then V's
+  const int half = lane % (2 * LR) < LR ? 0 : 1, ch = lane % LR * 8;
+  uint16_t* pool = half ? p.v : p.k;
+  auto row_of = [&](int page, int j) { return (((layer + page) * p.Hkv + h) << p.ps_shift) + (j & (p.ps - 1)); };
+  uint32_t* s_keys = s_dyn;
+  int* s_pos = reinterpret_cast<int*>(s_dyn + a.cap);
+
+  // Few evicted places: a warp takes each place from N on, whose rows may have to move, and fetches them while
+  // the keys come.
+  const bool few = gone <= kFew;
+  uint4 row = {};
+  float row_mass = 0.0f;
+  int row_pos = 0, row_page = 0;
+  if (few && warp < gone && N > 0) {
+    const int j = N + warp;
+    row_page = table[j >> p.ps_shift];
+    row_mass = mass[j];
+    row_pos = pos[j];
+    if (row_page >= 0 && row_page < p.NP && lane < 2 * LR)
+      row = *reinterpret_cast<const uint4*>(pool + static_cast<size_t>(row_of(row_page, j)) * D + ch);
+  }
   // masses and positions once: the kept part's copy, the newest position, keys without classes
   int top = INT32_MIN;
   for (int j0 = tid; j0 < n; j0 += kU * kThreads) {
@@ -115,7 +126,10 @@ k_evict(const Pool p, const EvictArgs a) {
       const int j = j0 + u * kThreads;
       if (j < n) {
         top = max(top, y[u]);
-        if (KEYS) s_keys[j] = order_of(x[u]);
+        if (KEYS) {
+          s_keys[j] = order_of(x[u]);
+          s_pos[j] = y[u];
+        }
         if (copy && j < N) {
           mass_out[j] = x[u];
           pos_out[j] = y[u];
@@ -123,15 +137,64 @@ k_evict(const Pool p, const EvictArgs a) {
       }
     }
   }
-  if (N == n || N == 0) return;
+  if (gone == 0 || N == 0) return;
   top = __reduce_max_sync(0xffffffffu, top);
   __syncthreads();
   if (lane == 0) atomicMax(&s_top, top);
   __syncthreads();
   const long long edge = static_cast<long long>(s_top) - a.protect;     // positions above it are the newest
   auto fresh_key = [&](int j) {
-    return j < first ? kFirst : pos[j] > edge ? kNewest : KEYS ? s_keys[j] : order_of(mass[j]);
+    return j < first ? kFirst : (KEYS ? s_pos[j] : pos[j]) > edge ? kNewest : KEYS ? s_keys[j] : order_of(mass[j]);
   };
+  if (few) {
+    // rounds of a minimum over (key, last place first), each thread's own beforehand
+    auto least = [&](int skip) {        // of the thread's places but those that have gone in rounds before `skip`
+      unsigned long long m = ~0ull;
+      for (int j = tid; j < n; j += kThreads) {
+        bool out = false;
+        for (int i = 0; i < skip; ++i) out |= s_gone[i] == j;
+        const unsigned long long x = static_cast<unsigned long long>(fresh_key(j)) << 32 | static_cast<unsigned>(INT32_MAX - j);
+        if (!out && x < m) m = x;
+      }
+      return m;
+    };
+    unsigned long long mine = least(0);
+    for (int i = 0; i < gone; ++i) {
+      const unsigned hi = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(mine >> 32));
+      const unsigned lo = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(mine >> 32) == hi ? static_cast<unsigned>(mine) : ~0u);
+      if (lane == 0) s_min[i & 1][warp] = static_cast<unsigned long long>(hi) << 32 | lo;
+      __syncthreads();
+      unsigned long long m = s_min[i & 1][0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) m = min(m, s_min[i & 1][w]);
+      if (m == mine) {                  // (one thread: places differ)
+        s_gone[i] = INT32_MAX - static_cast<int>(static_cast<unsigned>(m));
+        mine = i + 1 < gone ? least(i + 1) : ~0ull;
+      }
+    }
+    __syncthreads();
+    if (warp >= gone) return;
+    // this warp's place from N on: kept, and the how manieth of those; the hole of that rank
+    const int j = N + warp, g = lane < gone ? s_gone[lane] : INT32_MAX;
+    if (__any_sync(0xffffffffu, g == j)) return;
+    const int rank = warp - __popc(__ballot_sync(0xffffffffu, g >= N && g < j));
+    int below = 0;
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) below += __shfl_sync(0xffffffffu, g, i) < g;
+    const unsigned at = __ballot_sync(0xffffffffu, g < N && below == rank);
+    const int to = __shfl_sync(0xffffffffu, g, __ffs(at) - 1), page = table[to >> p.ps_shift];
+    if (page < 0 || page >= p.NP || row_page < 0 || row_page >= p.NP) {
+      if (lane == 0) atomicOr(p.err, CONFKV_FLAG_BAD_PAGE);
+      return;
+    }
+    if (lane < 2 * LR)
+      *reinterpret_cast<uint4*>(pool + static_cast<size_t>(row_of(page, to)) * D + ch) = row;
+    if (lane == 0) {
+      mass_out[to] = row_mass;
+      pos_out[to] = row_pos;
+    }
+    return;
+  }
   if (KEYS) {
     for (int j = tid; j < n; j += kThreads) s_keys[j] = fresh_key(j);
     __syncthreads();
@@ -161,6 +224,8 @@ k_evict(const Pool p, const EvictArgs a) {
   }
   // what stays, a bit for each place; of the keys equal to the N-th the first `want`
   const int words = (n + 31) >> 5;
+  uint32_t* s_kept = s_dyn + (KEYS ? 2 * a.cap : 2 * kList);                // [words]
+  int* s_before = reinterpret_cast<int*>(s_kept + ((a.cap + 31) >> 5));     // [words + 1]: as below
   for (int w0 = 0; w0 < words; w0 += kWarps) {
     const int j = 32 * (w0 + warp) + lane;
     const unsigned k = j < n ? key(j) : 0u;
@@ -196,60 +261,72 @@ k_evict(const Pool p, const EvictArgs a) {
   holes = scan(holes, s_warp, all);
   movers = scan(movers, s_warp, moves);
   __syncthreads();                      // s_before's bits have been read
+  // holes in the words before a word up to N's; from N's on, one place further, movers in those before
   for (int w = w_lo; w < w_hi; ++w) {
     if (w <= wn) s_before[w] = holes;
     holes += __popc(hole_word(w));
     if (w >= wn) s_before[w + 1] = movers;
     movers += __popc(mover_word(w));
   }
-  __syncthreads();
-  // the moves: a lane finds one, the warp copies its rows
-  const int32_t* table = a.table + static_cast<size_t>(b) * a.max_blocks;
-  const size_t layer = static_cast<size_t>(l) * p.NP;
-  constexpr int LR = D / 8;             // lanes of a row
+  // The moves' places, as many as the lists hold at a time (all, where the keys were in shared memory: they make
+  // room, and there are no more moves than half the places), then the moves: a lane works one out, the warp copies its rows.
+  int* s_to = reinterpret_cast<int*>(s_dyn);
+  const int room = KEYS ? a.cap : kList;
+  int* s_from = s_to + room;
   constexpr int PER = 32 / (2 * LR);    // moves of a warp at once, K and V
   constexpr int kM = 8;                 // and so many in flight
-  flag = 0;
-  for (int r0 = 32 * warp; r0 < moves; r0 += kThreads) {
-    long long from = -1, to = -1;       // rows in head h's pool
-    if (r0 + lane < moves) {
-      const int jt = place_of(s_before, 0, wn + 1, r0 + lane, hole_word);
-      const int jf = place_of(s_before + 1, wn, words, r0 + lane, mover_word);
-      const int pt = table[jt >> p.ps_shift], pf = table[jf >> p.ps_shift];
-      if (pt < 0 || pt >= p.NP || pf < 0 || pf >= p.NP) {
-        flag = CONFKV_FLAG_BAD_PAGE;
-      } else {
-        to = ((layer + pt) * p.Hkv + h) * p.ps + (jt & (p.ps - 1));
-        from = ((layer + pf) * p.Hkv + h) * p.ps + (jf & (p.ps - 1));
-        mass_out[jt] = mass[jf];
-        pos_out[jt] = pos[jf];
+  for (int c0 = 0; c0 < moves; c0 += room) {
+    __syncthreads();
+    for (int w = warp; w < words; w += kWarps) {
+      const uint32_t hole = hole_word(w), mover = mover_word(w), lower = (1u << lane) - 1u;
+      if (hole >> lane & 1u) {
+        const int r = s_before[w] + __popc(hole & lower) - c0;
+        if (r >= 0 && r < room) s_to[r] = 32 * w + lane;
+      }
+      if (mover >> lane & 1u) {
+        const int r = s_before[w + 1] + __popc(mover & lower) - c0;
+        if (r >= 0 && r < room) s_from[r] = 32 * w + lane;
       }
     }
-    const int live = min(32, moves - r0);
-    const int slot = lane / (2 * LR), x = lane % (2 * LR);
-    uint16_t* pool = x < LR ? p.k : p.v;
-    const int ch = (x % LR) * 8;
-    for (int i0 = 0; i0 < live; i0 += PER * kM) {
-      uint4 v[kM];
-      long long t[kM];
-#pragma unroll
-      for (int u = 0; u < kM; ++u) {
-        const int i = i0 + u * PER + slot;
-        const long long f = __shfl_sync(0xffffffffu, from, i & 31);
-        t[u] = __shfl_sync(0xffffffffu, to, i & 31);
-        if (i >= live || f < 0) t[u] = -1;
-        else v[u] = *reinterpret_cast<const uint4*>(pool + f * D + ch);
+    __syncthreads();
+    const int here = min(room, moves - c0);
+    for (int r0 = 32 * warp; r0 < here; r0 += kThreads) {
+      int from = -1, to = -1;           // rows of the pool
+      if (r0 + lane < here) {
+        const int jt = s_to[r0 + lane], jf = s_from[r0 + lane];
+        const int pt = table[jt >> p.ps_shift], pf = table[jf >> p.ps_shift];
+        if (pt < 0 || pt >= p.NP || pf < 0 || pf >= p.NP) {
+          flag = CONFKV_FLAG_BAD_PAGE;
+        } else {
+          to = row_of(pt, jt);
+          from = row_of(pf, jf);
+          mass_out[jt] = mass[jf];
+          pos_out[jt] = pos[jf];
+        }
       }
+      const int live = min(32, here - r0), slot = lane / (2 * LR);
+      for (int i0 = 0; i0 < live; i0 += PER * kM) {
+        uint4 v[kM];
+        int t[kM];
 #pragma unroll
-      for (int u = 0; u < kM; ++u)
-        if (t[u] >= 0) *reinterpret_cast<uint4*>(pool + t[u] * D + ch) = v[u];
+        for (int u = 0; u < kM; ++u) {
+          const int i = i0 + u * PER + slot;
+          const int f = __shfl_sync(0xffffffffu, from, i & 31);
+          t[u] = __shfl_sync(0xffffffffu, to, i & 31);
+          if (i >= live || f < 0) t[u] = -1;
+          else v[u] = *reinterpret_cast<const uint4*>(pool + static_cast<size_t>(f) * D + ch);
+        }
+#pragma unroll
+        for (int u = 0; u < kM; ++u)
+          if (t[u] >= 0) *reinterpret_cast<uint4*>(pool + static_cast<size_t>(t[u]) * D + ch) = v[u];
+      }
     }
   }
   if (flag) atomicOr(p.err, flag);
 }
 
 size_t shared_bytes(int cap, bool keys) {
-  return (2 * static_cast<size_t>((cap + 31) >> 5) + 1 + (keys ? cap : 0)) * 4;
+  return (2 * static_cast<size_t>((cap + 31) >> 5) + 1 + 2 * (keys ? cap : kList)) * 4;
 }
 template <typename F>
 cudaError_t each_evict(F&& f) {
