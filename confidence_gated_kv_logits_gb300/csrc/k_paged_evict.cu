@@ -18,7 +18,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kU = 8;                   // loads of a thread in flight
 constexpr uint32_t kFirst = 0xffffffffu, kNewest = 0xfffffffeu;
-constexpr int kKeysShared = 24576;      // keys and positions up to here stay in shared memory
+constexpr int kKeysShared = 40960;      // keys up to here stay in shared memory
+constexpr int kPosShared = 4096;        // positions too up to here
 constexpr int kList = 8192;             // moves at a time beyond
 constexpr int kFew = kWarps;            // evicted places that are found one by one
 
@@ -51,8 +52,8 @@ __device__ __forceinline__ int scan(int x, int* s_warp, int& all) {
   return before + incl - x;
 }
 
-// One CTA: a KV head of a sequence in a layer.  KEYS: its keys and positions lie in shared memory
-// (else they are read again wherever they are needed).
+// One CTA: a KV head of a sequence in a layer.  KEYS: its keys lie in shared memory, and its positions too
+// where that leaves room for as many CTAs (else they are read again wherever they are needed).
 template <bool KEYS, int D>
 __global__ void __launch_bounds__(kThreads, 4)
 k_evict(const Pool p, const EvictArgs a) {
@@ -92,6 +93,7 @@ k_evict(const Pool p, const EvictArgs a) {
   uint16_t* pool = half ? p.v : p.k;
   auto row_of = [&](int page, int j) { return (((layer + page) * p.Hkv + h) << p.ps_shift) + (j & (p.ps - 1)); };
   uint32_t* s_keys = s_dyn;
+  const bool with_pos = KEYS && a.cap <= kPosShared;
   int* s_pos = reinterpret_cast<int*>(s_dyn + a.cap);
 
   // Few evicted places: a warp takes each place from N on, whose rows may have to move, and fetches them while
@@ -128,7 +130,7 @@ k_evict(const Pool p, const EvictArgs a) {
         top = max(top, y[u]);
         if (KEYS) {
           s_keys[j] = order_of(x[u]);
-          s_pos[j] = y[u];
+          if (with_pos) s_pos[j] = y[u];
         }
         if (copy && j < N) {
           mass_out[j] = x[u];
@@ -144,7 +146,7 @@ k_evict(const Pool p, const EvictArgs a) {
   __syncthreads();
   const long long edge = static_cast<long long>(s_top) - a.protect;     // positions above it are the newest
   auto fresh_key = [&](int j) {
-    return j < first ? kFirst : (KEYS ? s_pos[j] : pos[j]) > edge ? kNewest : KEYS ? s_keys[j] : order_of(mass[j]);
+    return j < first ? kFirst : (with_pos ? s_pos[j] : pos[j]) > edge ? kNewest : KEYS ? s_keys[j] : order_of(mass[j]);
   };
   if (few) {
     // rounds of a minimum over (key, last place first), each thread's own beforehand
@@ -224,7 +226,7 @@ k_evict(const Pool p, const EvictArgs a) {
   }
   // what stays, a bit for each place; of the keys equal to the N-th the first `want`
   const int words = (n + 31) >> 5;
-  uint32_t* s_kept = s_dyn + (KEYS ? 2 * a.cap : 2 * kList);                // [words]
+  uint32_t* s_kept = s_dyn + (KEYS ? (with_pos ? 2 : 1) * a.cap : 2 * kList);   // [words]
   int* s_before = reinterpret_cast<int*>(s_kept + ((a.cap + 31) >> 5));     // [words + 1]: as below
   for (int w0 = 0; w0 < words; w0 += kWarps) {
     const int j = 32 * (w0 + warp) + lane;
@@ -271,7 +273,7 @@ k_evict(const Pool p, const EvictArgs a) {
   // The moves' places, as many as the lists hold at a time (all, where the keys were in shared memory: they make
   // room, and there are no more moves than half the places), then the moves: a lane works one out, the warp copies its rows.
   int* s_to = reinterpret_cast<int*>(s_dyn);
-  const int room = KEYS ? a.cap : kList;
+  const int room = KEYS ? a.cap >> 1 : kList;
   int* s_from = s_to + room;
   constexpr int PER = 32 / (2 * LR);    // moves of a warp at once, K and V
   constexpr int kM = 8;                 // and so many in flight
@@ -326,7 +328,7 @@ k_evict(const Pool p, const EvictArgs a) {
 }
 
 size_t shared_bytes(int cap, bool keys) {
-  return (2 * static_cast<size_t>((cap + 31) >> 5) + 1 + 2 * (keys ? cap : kList)) * 4;
+  return (2 * static_cast<size_t>((cap + 31) >> 5) + 1 + (!keys ? 2 * kList : cap <= kPosShared ? 2 * cap : cap)) * 4;
 }
 template <typename F>
 cudaError_t each_evict(F&& f) {
