@@ -198,7 +198,11 @@ k_evict(const Pool p, const EvictArgs a) {
     return;
   }
   if (KEYS) {
-    for (int j = tid; j < n; j += kThreads) s_keys[j] = fresh_key(j);
+#pragma unroll 8
+    for (int j = tid; j < n; j += kThreads) {
+      const bool newest = (with_pos ? s_pos[j] : pos[j]) > edge;
+      if (j < first || newest) s_keys[j] = j < first ? kFirst : kNewest;
+    }
     __syncthreads();
   }
   auto key = [&](int j) { return KEYS ? s_keys[j] : fresh_key(j); };
