@@ -277,17 +277,15 @@ k_append_normed(const Pool p, const AppendArgs a) {
     }
 #pragma unroll
     for (int o = 1; o < LP; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    float scale = 1.0f, inv = rsqrtf(ss * (1.0f / D) + a.eps);
+    float inv = rsqrtf(ss * (1.0f / D) + a.eps);
     if (__any_sync(0xffffffffu, !(ss < INFINITY))) {
       float big = 0.0f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) big = fmaf(x[i] * kTiny, x[i] * kTiny, big);
 #pragma unroll
       for (int o = 1; o < LP; o <<= 1) big += __shfl_xor_sync(0xffffffffu, big, o);
-      if (!(ss < INFINITY)) {
-        scale = kTiny;
-        inv = rsqrtf(big * (1.0f / D));
-      }
+      // (from 2^126 on a subnormal number, good to 2^-21 of itself at least)
+      if (!(ss < INFINITY)) inv = kTiny * rsqrtf(big * (1.0f / D));
     }
     if (kind != 2) {
       if (kind == 0 ? a.q_norm != nullptr : a.k_norm != nullptr) {
@@ -295,10 +293,10 @@ k_append_normed(const Pool p, const AppendArgs a) {
         const float4 w4[4] = {w[lo >> 2], w[(lo >> 2) + 1], w[hi >> 2], w[(hi >> 2) + 1]};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[4 * i] = x[4 * i] * scale * inv * w4[i].x;
-          x[4 * i + 1] = x[4 * i + 1] * scale * inv * w4[i].y;
-          x[4 * i + 2] = x[4 * i + 2] * scale * inv * w4[i].z;
-          x[4 * i + 3] = x[4 * i + 3] * scale * inv * w4[i].w;
+          x[4 * i] *= inv * w4[i].x;
+          x[4 * i + 1] *= inv * w4[i].y;
+          x[4 * i + 2] *= inv * w4[i].z;
+          x[4 * i + 3] *= inv * w4[i].w;
         }
       }
       if (turned) {
