@@ -89,8 +89,14 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
   if (tid == 0) s_abort = 0;
   fence_bar_init();
   fence_async();
-  pdl_wait();
-  pdl_trigger();
+  // Phase 2 of a shared prefix needs phase 1 only where it joins the two (and where it uses the scratch): its own
+  // tiles, which the kernels before phase 1 stored, come meanwhile (phase 1 lets its dependents start
+  // only behind its own wait for those).  Its dependents in turn start behind phase 1.
+  bool waited = !SH || a.bt.phase != 2;
+  if (waited) {
+    pdl_wait();
+    pdl_trigger();
+  }
   fence_async_global();
 
   // the walk stays in shared memory: its registers are the accumulators' between pieces
@@ -356,6 +362,11 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
     __syncthreads();
     // set before the barrier or not at all; a cluster's CTAs leave together, below
     if (CL == 1 && s_abort) break;
+    if (SH && !waited) {
+      waited = true;
+      pdl_wait();
+      pdl_trigger();
+    }
     constexpr int PER = kRows * D / kThreads;        // 16 or 8 channels of one row
     const int row = tid / (D / PER), ch0 = (tid % (D / PER)) * PER;
     const bool whole = w.pieces == 1;
@@ -513,6 +524,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
     }
     __syncthreads();
   }
+  if (SH && !waited) pdl_wait();       // (no launch may end before phase 1 has)
   if (s_abort && tid == 0) atomicOr(p.err, CONFKV_FLAG_TIMEOUT);
 }
 

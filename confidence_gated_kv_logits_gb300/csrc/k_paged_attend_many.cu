@@ -154,8 +154,12 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_addr(&s_tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
-  pdl_wait();
-  pdl_trigger();
+  // (phase 2 of a shared prefix waits for phase 1 where it joins the two: k_paged_attend.cu)
+  const bool joins = SH && a.bt.phase == 2;
+  if (!joins) {
+    pdl_wait();
+    pdl_trigger();
+  }
   fence_async_global();
   tc_fence_before();
   if (a.bt.B > 32) {
@@ -355,6 +359,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
     const float c = a.scale * kL2E;
     unsigned ns = 0, no = 0, slot0 = 0;
     int4 cut = make_int4(0, 0, 0, 0);                     // the unit whose first piece this CTA ends with
+    bool waited = !joins;
     while (!soft_any(!next_piece())) {
       const Piece& w = s_plan[plan % kPlan];
       const int nb = w.hi - w.lo;
@@ -516,6 +521,11 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
         bar_arrive(b_p + 16 * s + 8 * (i & 1));
       }
       const bool whole = w.pieces == 1;
+      if (SH && !waited) {
+        waited = true;
+        pdl_wait();
+        pdl_trigger();
+      }
       if (tid == 0 && !whole) {
         // all other pieces done: this one is joined as it is, without a way through memory
         s_last = !defer && *const_cast<volatile unsigned int*>(sc.ticket + w.first_cta) == static_cast<unsigned>(w.pieces - 1);
@@ -633,6 +643,7 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
       if (defer && tid == 0 && !whole && own == 0) cut = make_int4(w.pieces, w.b, w.h, w.mt);
       piece_done();
     }
+    if (SH && !waited) pdl_wait();
     if (defer && tid == 0) sc.cut[blockIdx.x] = cut;
     tc_fence_before();
   }
