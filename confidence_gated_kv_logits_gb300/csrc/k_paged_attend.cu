@@ -40,18 +40,17 @@ namespace paged {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
 constexpr int kRows = kFewRows;
 // Chunks of a unit that one CTA takes whole, while every unit finds a CTA of its
 // own and no cluster shares it. Cut against whole, one row: 1 x 128 tokens of
 // 40/8 x 128 heads 11.1 against 8.4 us, 8 x 700 tokens of 12/12 x 64 13.9 against
 // 9.0; at 16 chunks a warp (1 x 1024 tokens, d 128) 12.1 against 15.2.
-constexpr int kUncut = 8 * kWarps;
+constexpr int kUncut = 8 * kWarps;       // (of a CTA of kWarps warps)
 constexpr int kChunkBytes = 4 * kFewChunk;
 constexpr float kL2E = 1.4426950408889634f;
 
-template <int D>
+template <int D, int W>
 struct Few {
   static constexpr int CH = kFewChunk / D;             // tokens of a chunk
   static constexpr int NT = CH / 8;                // score column tiles
@@ -59,28 +58,31 @@ struct Few {
   static constexpr int OT = D / 8;                 // output column tiles
   static constexpr int KV = CH * D * 2;            // bytes of K (of V) in a chunk
   static constexpr int HALF = CH * 128;            // bytes of one 64-channel half
-  static constexpr int OVER = 2 * kWarps;          // a unit's fixed cost in chunks
+  static constexpr int OVER = 2 * W;               // a unit's fixed cost in chunks
+  static constexpr int SMEM = W * kStages * kChunkBytes + 1024;
 };
 
 // CL > 1: the CTAs of a cluster share each of their units, which are not cut
 // otherwise, and join them through distributed shared memory.
-template <bool BF, int D, int CL, bool SH>
-__global__ void __launch_bounds__(kThreads, 1)
+// W: warps of a CTA, 8, or 4 with two CTAs per SM.
+template <bool BF, int D, int CL, bool SH, int W>
+__global__ void __launch_bounds__(32 * W, 8 / W)
 k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_constant__ CUtensorMap mk,
              const __grid_constant__ CUtensorMap mv) {
-  using F = Few<D>;
+  using F = Few<D, W>;
+  constexpr int kThreads = 32 * W;
   extern __shared__ unsigned char s_raw[];
-  __shared__ __align__(8) unsigned long long s_bar[kWarps * kStages];
-  __shared__ float s_ml[kWarps][kRows][2];
+  __shared__ __align__(8) unsigned long long s_bar[W * kStages];
+  __shared__ float s_ml[W][kRows][2];
   __shared__ Sched s_sched;
   __shared__ WalkState s_walk;
-  __shared__ long long s_scan[kWarps];
+  __shared__ long long s_scan[W];
   __shared__ float s_all[kRows][2];                 // CL > 1: the CTA's (maximum, sum) of each row
   __shared__ int s_abort, s_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int STEP = kWarps * CL;                 // a warp's next chunk
-  const int rank = CL > 1 ? blockIdx.x % CL : 0, wid = rank * kWarps + warp;
+  constexpr int STEP = W * CL;                 // a warp's next chunk
+  const int rank = CL > 1 ? blockIdx.x % CL : 0, wid = rank * W + warp;
   const uint32_t ring0 = (smem_addr(s_raw) + 1023u) & ~1023u;
   const uint32_t ring = ring0 + warp * (kStages * kChunkBytes);
   const uint32_t bar = smem_addr(&s_bar[warp * kStages]);
@@ -103,14 +105,14 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
   using WalkF = Walk<kRows, F::CH, F::OVER, SH>;
   if (a.bt.B > 32) {
     WalkF w(p, a.bt, a.rows);
-    sched_init<kThreads>(w, &s_sched, s_scan, 2 * kWarps);
+    sched_init<kThreads>(w, &s_sched, s_scan, 2 * W);
   }
   if (warp == 0) {
     WalkF w(p, a.bt, a.rows);
     if (a.bt.B > 32) {
       w.start(s_sched);
     } else {
-      const Sched sh = sched_warp(w, 2 * kWarps, CL > 1 ? -1 : kUncut, blockIdx.x / CL, gridDim.x / CL);
+      const Sched sh = sched_warp(w, 2 * W, CL > 1 ? -1 : kUncut * W / 8, blockIdx.x / CL, gridDim.x / CL);
       w.start(sh);
     }
     w.next();
@@ -372,11 +374,11 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
     const bool whole = w.pieces == 1;
     float m = -INFINITY, l = 0.0f, x[PER];
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) m = fmaxf(m, s_ml[i][row][0]);
+    for (int i = 0; i < W; ++i) m = fmaxf(m, s_ml[i][row][0]);
 #pragma unroll
     for (int e = 0; e < PER; ++e) x[e] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < W; ++i) {
       const float li = s_ml[i][row][1];
       if (li == 0.0f) continue;                       // nothing seen (scores that are all NaN leave m at -inf, l NaN)
       const float f = ex2f((s_ml[i][row][0] - m) * c);
@@ -462,7 +464,7 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
         // through L2 one piece after another took 3 to 6 us for 9 pieces).
         const int live = R - base < kRows ? R - base : kRows;
         const int per_piece = live * (D / 4) + live / 2 + 1;            // 16-byte words, (maximum, sum) pairs behind
-        const int batch = kWarps * kStages * kChunkBytes / (16 * per_piece);
+        const int batch = W * kStages * kChunkBytes / (16 * per_piece);
         m = -INFINITY;
         l = 0.0f;
 #pragma unroll
@@ -533,14 +535,16 @@ template <typename F>
 cudaError_t each_few(F&& f) {
   cudaError_t e = cudaSuccess;
   auto of = [&](auto bf, auto d) {
-    auto one = [&](auto cl, auto sh) {
+    auto one = [&](auto cl, auto sh, auto w) {
+      constexpr int D = decltype(d)::value, W = decltype(w)::value;
       if (e == cudaSuccess)
-        e = f(bf, d, cl, sh, k_attend_few<decltype(bf)::value, decltype(d)::value, decltype(cl)::value, decltype(sh)::value>);
+        e = f(bf, d, cl, sh, w, k_attend_few<decltype(bf)::value, D, decltype(cl)::value, decltype(sh)::value, W>, Few<D, W>::SMEM);
     };
     auto both = [&](auto cl) {
-      one(cl, std::false_type{});
-      one(cl, std::true_type{});
+      one(cl, std::false_type{}, std::integral_constant<int, 8>{});
+      one(cl, std::true_type{}, std::integral_constant<int, 8>{});
     };
+    one(std::integral_constant<int, 1>{}, std::true_type{}, std::integral_constant<int, 4>{});
     both(std::integral_constant<int, 1>{});
     both(std::integral_constant<int, 2>{});
     both(std::integral_constant<int, 4>{});
@@ -556,13 +560,12 @@ cudaError_t each_few(F&& f) {
 }  // namespace
 
 cudaError_t launch_attend_few(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
-                              int ctas, int cluster, cudaStream_t s) {
-  const size_t smem = kWarps * kStages * kChunkBytes + 1024;
-  return each_few([&](auto bf, auto d, auto cl, auto sh, auto kernel) {
-    if (bf != p.bf16 || d != p.d || cl != cluster || sh != (a.bt.phase != 0)) return cudaSuccess;
+                              int ctas, int cluster, int warps, cudaStream_t s) {
+  return each_few([&](auto bf, auto d, auto cl, auto sh, auto w, auto kernel, int smem) {
+    if (bf != p.bf16 || d != p.d || cl != cluster || sh != (a.bt.phase != 0) || w != warps) return cudaSuccess;
     cudaError_t e;
-    if (cl > 1) e = launch_pdl_cluster(kernel, dim3(ctas), dim3(kThreads), cl, smem, s, p, a, sc, m.k_few, m.v_few);
-    else e = launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem, s, p, a, sc, m.k_few, m.v_few);
+    if (cl > 1) e = launch_pdl_cluster(kernel, dim3(ctas), dim3(32 * w), cl, smem, s, p, a, sc, m.k_few, m.v_few);
+    else e = launch_pdl(kernel, dim3(ctas), dim3(32 * w), smem, s, p, a, sc, m.k_few, m.v_few);
     return e != cudaSuccess ? e : cudaGetLastError();
   });
 }
@@ -570,7 +573,7 @@ cudaError_t launch_attend_few(const Pool& p, const AttendArgs& a, const Scratch&
 cudaError_t few_clusters(int size, int* fit) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(size);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.dynamicSmemBytes = kWarps * kStages * kChunkBytes + 1024;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
@@ -580,18 +583,17 @@ cudaError_t few_clusters(int size, int* fit) {
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   *fit = INT_MAX;
-  return each_few([&](auto, auto, auto cl, auto, auto kernel) {
+  return each_few([&](auto, auto, auto cl, auto, auto w, auto kernel, int) {
     int n = INT_MAX;
-    const cudaError_t e = cl == size ? cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) : cudaSuccess;
+    const cudaError_t e = cl == size && w == kWarps ? cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) : cudaSuccess;
     *fit = n < *fit ? n : *fit;
     return e;
   });
 }
 
 cudaError_t setup_attend_few() {
-  return each_few([](auto, auto, auto, auto, auto kernel) {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kWarps * kStages * kChunkBytes + 1024);
+  return each_few([](auto, auto, auto, auto, auto, auto kernel, int smem) {
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
 }
 

@@ -284,8 +284,9 @@ cudaError_t attend(const confkv_paged& kv, const AttendArgs& a, int batch, cudaS
     const int64_t units = p.Hkv * std::min<int64_t>(static_cast<int64_t>(a.rows) * ((p.g + kFewRows - 1) / kFewRows),
                                                     heads / kFewRows + batch);
     const int cl = few_cluster(kv, batch, units, static_cast<int64_t>(a.bt.max_blocks) * p.ps);
+    if (a.bt.phase == 2 && cl == 1) return launch_attend_few(p, a, kv.scratch, kv.maps, 2 * kv.limits.sms, 1, 4, s);
     const int ctas = cl > 1 ? cl * static_cast<int>(units) : kFewCtasPerSm * kv.limits.sms;
-    return launch_attend_few(p, a, kv.scratch, kv.maps, ctas, cl, s);
+    return launch_attend_few(p, a, kv.scratch, kv.maps, ctas, cl, 8, s);
   }
   const int sms = kv.limits.sms;
   const int64_t ones = p.Hkv * (heads / 128 + batch), twos = p.Hkv * (heads / kManyRows + batch);

@@ -27,7 +27,7 @@ constexpr int kNoRows = -kManyBlock;
 constexpr int kFewCtasPerSm = 1;
 
 cudaError_t launch_attend_few(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
-                              int ctas, int cluster, cudaStream_t s);
+                              int ctas, int cluster, int warps, cudaStream_t s);
 cudaError_t launch_attend_many(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
                                int ctas, bool two_tiles, bool defer, cudaStream_t s);
 cudaError_t setup_attend_few();
