@@ -284,7 +284,11 @@ cudaError_t attend(const confkv_paged& kv, const AttendArgs& a, int batch, cudaS
     const int64_t units = p.Hkv * std::min<int64_t>(static_cast<int64_t>(a.rows) * ((p.g + kFewRows - 1) / kFewRows),
                                                     heads / kFewRows + batch);
     const int cl = few_cluster(kv, batch, units, static_cast<int64_t>(a.bt.max_blocks) * p.ps);
-    if (a.bt.phase == 2 && cl == 1) return launch_attend_few(p, a, kv.scratch, kv.maps, 2 * kv.limits.sms, 1, 4, s);
+    // Behind a shared prefix many sequences have few tokens of their own: from 32 on CTAs of four warps, two per SM, so
+    // that one's joins run beside another's tiles (40/8 heads of 128, one row each, us, of eight warps and of four: 32
+    // sequences of 200 own tokens 45.0, 35.3; 64 of 700 76.3, 68.8; 128 of 2000 151, 142; 32 of 8000 134.6, 134.8; 16 of
+    // 300 33.2, 36.1)
+    if (a.bt.phase == 2 && cl == 1 && batch >= 32) return launch_attend_few(p, a, kv.scratch, kv.maps, 2 * kv.limits.sms, 1, 4, s);
     const int ctas = cl > 1 ? cl * static_cast<int>(units) : kFewCtasPerSm * kv.limits.sms;
     return launch_attend_few(p, a, kv.scratch, kv.maps, ctas, cl, 8, s);
   }
