@@ -265,7 +265,7 @@ const char* attend_args(const Pool& p, const confkv_paged_batch* batch, int laye
 // Launches the attention of `batch` sequences (groups, over a shared prefix).
 cudaError_t attend(const confkv_paged& kv, const AttendArgs& a, int batch, cudaStream_t s) {
   const Pool& p = kv.pool;
-  // By the query rows of a sequence's KV head, on average (measured on GB300, us):
+  // By the query rows of a sequence's (a group's) KV head, on average (measured on GB300, us):
   //  - up to 16 the streaming kernel (1 x 32768 tokens, 40/8 heads, d = 128: 10 rows 37
   //    streamed, 42 with the padded tiles of 128; 20 rows 62 in two streamed tiles, 42)
   //  - from 257 on units of two tiles, which share each K and V block, if they fill half
@@ -279,7 +279,10 @@ cudaError_t attend(const confkv_paged& kv, const AttendArgs& a, int batch, cudaS
   //    kernel of its own joins on all SMs (1 x 32768 tokens, 65 rows: 58 joined by the
   //    last CTA of each unit, 42)
   const int64_t heads = static_cast<int64_t>(a.rows) * p.g, per = heads / batch;
-  if (per <= kFewRows) {
+  //  - behind a shared prefix, where sequences have few tokens of their own, the streaming kernel up to 40 rows in its tiles
+  //    of 16 (two groups of 8 sequences of 300 own tokens behind 6000, 64/8 heads, d = 64: 18 rows 30 streamed, 43; 36 rows
+  //    40, 46; 72 rows 52, 48; of 2000 own tokens 36 rows 49, 47)
+  if (per <= (a.bt.phase == 2 ? 40 : kFewRows)) {
     // at most (a row's heads fill one tile, or its sequence's last is part-filled)
     const int64_t units = p.Hkv * std::min<int64_t>(static_cast<int64_t>(a.rows) * ((p.g + kFewRows - 1) / kFewRows),
                                                     heads / kFewRows + batch);
