@@ -279,6 +279,40 @@ def test_attend_shared_sizes(pkg, heads, kv_heads, d, groups, tail, new):
     assert first[2].status() == 0
 
 
+def test_attend_shared_more_groups_than_lanes(pkg):
+    r = np.random.default_rng(4)
+    groups = [(int(n), int(p)) for n, p in zip(r.integers(1, 4, 70), r.integers(0, 700, 70))]
+    c = Grouped(torch.float16, 8, 2, 64, 16, groups, [0, 5, 33, 140], [1, 0, 2], seed=16)
+    got = run_shared(pkg, c)
+    check_shared(c, got, reference(c))
+    assert got[2].status() == 0
+
+
+def test_attend_shared_calls_one_after_another(pkg):
+    """Calls of several shapes with one handle, each right behind the other: the second phase of one starts early."""
+    cases = [Grouped(torch.bfloat16, 40, 8, 128, 64, g, [7, 300], n, seed=i)
+             for i, (g, n) in enumerate([([(4, 1000)], [1]), ([(40, 512)], [1]), ([(3, 2000), (2, 640)], [30]), ([(2, 300)], [150])])]
+    pools = [(c.k, c.v) for c in cases]
+    kvs = [pkg.PagedKV(k, v, 40) for k, v in pools]
+    outs = []
+    for _ in range(3):
+        outs.append([])
+        for c, kv in zip(cases, kvs):
+            prefix = kv.prefix(c.starts_of_groups(), ints(c.prefixes), c.rows)
+            batch = c.batch(kv)
+            for _ in range(2):
+                out, lse = torch.full_like(c.q, 7), torch.full((c.rows, 40), 7.0, device=DEV)
+                kv.attend(1, batch, c.q, out, lse=lse, prefix=prefix)
+                kv.attend(1, batch, out, torch.empty_like(out))          # reads what the call before it wrote
+                outs[-1].append((out, lse, prefix, batch))
+    torch.cuda.synchronize()
+    for i, c in enumerate(cases):
+        want = reference(c)
+        for o in outs:
+            for x in o[2 * i:2 * i + 2]:
+                check_shared(c, x, want)
+
+
 def test_attend_shared_large_scores(pkg):
     c = Grouped(torch.bfloat16, 8, 2, 128, 64, [(3, 500)], [7, 200], [1, 40], seed=9)
     c.q *= 12
@@ -480,6 +514,40 @@ def test_weigh_many_items_launch_after_launch(pkg, heads, kv_heads, d, n, most, 
             kv.weigh(1, batch, c.q, lse, mass, o)
     assert all(torch.equal(o, first) for o in outs)
     assert kv.status() == 0
+
+
+def test_weigh_in_a_graph_and_on_two_streams(pkg):
+    c = Case(torch.bfloat16, 40, 8, 128, 64, [3000, 128, 700], [1, 2, 60], seed=11)
+    kv, other = pkg.PagedKV(c.k, c.v, 40), pkg.PagedKV(c.k, c.v, 40)
+    batch, batch2 = c.batch(kv), c.batch(other)
+    lse = torch.randn(c.rows, 40, device=DEV) + 9
+    mass = torch.rand(3, 8, 3100, generator=c.g, device=DEV)
+    outs = [torch.zeros_like(mass) for _ in range(4)]
+    kv.weigh(1, batch, c.q, lse, mass, outs[0])
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        kv.weigh(1, batch, c.q, lse, mass, outs[1])
+    for _ in range(5):
+        outs[1].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], outs[1])
+    for _ in range(20):                                    # one handle on two streams too: nothing is shared
+        kv.weigh(1, batch, c.q, lse, mass, outs[2])
+        kv.weigh(1, batch, c.q, lse, mass, outs[3], stream=side)
+        other.weigh(1, batch2, c.q, lse, mass, outs[1], stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+    assert kv.status() == 0 and other.status() == 0
+
+
+def test_weigh_strided_queries(pkg):
+    c = Case(torch.float16, 10, 2, 64, 16, [300, 20], [3, 40], seed=12)
+    wide = torch.full((c.rows, 17, 64), math.nan, dtype=c.dt, device=DEV)
+    wide[:, 2:12] = c.q
+    c.q = wide[:, 2:12]
+    run_weigh(pkg, c, in_place=True)
 
 
 def test_weigh_masks_that_leave_nothing_and_masked_nans(pkg):
