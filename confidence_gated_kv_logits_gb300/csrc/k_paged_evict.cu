@@ -8,20 +8,24 @@
 // stay.  Evicted places below N (holes) and kept places from N on (movers) are
 // equally many; the r-th hole takes the r-th mover's rows, which no other move
 // reads or writes, so all moves are independent.
+#include <type_traits>
+
 #include "paged_internal.cuh"
 
 namespace confkv {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kU = 8;                   // loads of a thread in flight
 constexpr uint32_t kFirst = 0xffffffffu, kNewest = 0xfffffffeu;
 constexpr int kKeysShared = 40960;      // keys up to here stay in shared memory
 constexpr int kPosShared = 4096;        // positions too up to here
 constexpr int kList = 8192;             // moves at a time beyond
-constexpr int kFew = kWarps;            // evicted places that are found one by one
+constexpr int kFew = 8;                 // evicted places that are found one by one, a warp each
+// Places (of the mass's rows) from which on units that leave SMs idle are worth 1024 threads instead of 256.  us, 256 and
+// 1024: 8 units of 1500 places, 1000 kept, 14.9, 16.6; of 4000, 1000 kept, 24.8, 22.7; of 16000, 2000 kept, 66.6, 44.0; 64
+// of 4000 42.3, 27.5; 152 of 10000, 5000 kept, 137.5, 89.8; 64 of 2049, one evicted, 4.2, 5.3.
+constexpr int kWide = 2500;
 
 // A mass as an unsigned number in the same order; NaN below everything, -0 as 0.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -31,6 +35,7 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 
 // What the threads before give, and the CTA's sum.
+template <int kWarps>
 __device__ __forceinline__ int scan(int x, int* s_warp, int& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = x;
@@ -54,9 +59,11 @@ __device__ __forceinline__ int scan(int x, int* s_warp, int& all) {
 
 // One CTA: a KV head of a sequence in a layer.  KEYS: its keys lie in shared memory, and its positions too
 // where that leaves room for as many CTAs (else they are read again wherever they are needed).
-template <bool KEYS, int D>
-__global__ void __launch_bounds__(kThreads, 4)
+// T: threads, 256 or, where there are fewer units than SMs, 1024.
+template <bool KEYS, int D, int T>
+__global__ void __launch_bounds__(T, 1024 / T)
 k_evict(const Pool p, const EvictArgs a) {
+  constexpr int kThreads = T, kWarps = T / 32;
   extern __shared__ uint32_t s_dyn[];
   __shared__ unsigned s_count[256];
   __shared__ int s_warp[kWarps];
@@ -206,10 +213,17 @@ k_evict(const Pool p, const EvictArgs a) {
     __syncthreads();
   }
   auto key = [&](int j) { return KEYS ? s_keys[j] : fresh_key(j); };
-  // the N-th largest key, byte by byte
+  // what stays, a bit for each place, by the N-th largest key, found byte by byte: of the keys equal to it the first
+  // `want` stay
+  const int words = (n + 31) >> 5;
+  uint32_t* s_kept = s_dyn + (KEYS ? (with_pos ? 2 : 1) * a.cap : 2 * kList);   // [words]
+  int* s_before = reinterpret_cast<int*>(s_kept + ((a.cap + 31) >> 5));         // [words + 1]: as below
+  // (each thread takes a run of words, so that its sums go on from word to word)
+  const int per = (words + kThreads - 1) / kThreads, w_lo = min(words, tid * per), w_hi = min(words, w_lo + per);
+  int all;
   unsigned prefix = 0, want = N;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    s_count[tid] = 0;
+    if (tid < 256) s_count[tid] = 0;
     __syncthreads();
     for (int j = tid; j < n; j += kThreads) {
       const unsigned k = key(j);
@@ -218,9 +232,9 @@ k_evict(const Pool p, const EvictArgs a) {
     __syncthreads();
     // thread t: byte 255 - t, the keys above it
     int all;
-    const unsigned mine = s_count[255 - tid];
-    const unsigned above = scan(static_cast<int>(mine), s_warp, all);
-    if (above < want && want <= above + mine) {
+    const unsigned mine = tid < 256 ? s_count[255 - tid] : 0u;
+    const unsigned above = scan<kWarps>(static_cast<int>(mine), s_warp, all);
+    if (tid < 256 && above < want && want <= above + mine) {
       s_key = prefix | static_cast<unsigned>(255 - tid) << shift;
       s_want = want - above;
     }
@@ -228,10 +242,6 @@ k_evict(const Pool p, const EvictArgs a) {
     prefix = s_key;
     want = s_want;
   }
-  // what stays, a bit for each place; of the keys equal to the N-th the first `want`
-  const int words = (n + 31) >> 5;
-  uint32_t* s_kept = s_dyn + (KEYS ? (with_pos ? 2 : 1) * a.cap : 2 * kList);   // [words]
-  int* s_before = reinterpret_cast<int*>(s_kept + ((a.cap + 31) >> 5));     // [words + 1]: as below
   for (int w0 = 0; w0 < words; w0 += kWarps) {
     const int j = 32 * (w0 + warp) + lane;
     const unsigned k = j < n ? key(j) : 0u;
@@ -242,11 +252,9 @@ k_evict(const Pool p, const EvictArgs a) {
     }
   }
   __syncthreads();
-  // (each thread takes a run of words, so that its sums go on from word to word)
-  const int per = (words + kThreads - 1) / kThreads, w_lo = min(words, tid * per), w_hi = min(words, w_lo + per);
-  int all, equal = 0;
+  int equal = 0;
   for (int w = w_lo; w < w_hi; ++w) equal += __popc(s_before[w]);
-  int eq = scan(equal, s_warp, all);
+  int eq = scan<kWarps>(equal, s_warp, all);
   for (int w = w_lo; w < w_hi; ++w) {
     unsigned same = s_before[w];
     const int left = static_cast<int>(want) - eq, here = __popc(same);
@@ -264,8 +272,8 @@ k_evict(const Pool p, const EvictArgs a) {
     movers += __popc(mover_word(w));
   }
   int moves;
-  holes = scan(holes, s_warp, all);
-  movers = scan(movers, s_warp, moves);
+  holes = scan<kWarps>(holes, s_warp, all);
+  movers = scan<kWarps>(movers, s_warp, moves);
   __syncthreads();                      // s_before's bits have been read
   // holes in the words before a word up to N's; from N's on, one place further, movers in those before
   for (int w = w_lo; w < w_hi; ++w) {
@@ -336,26 +344,36 @@ size_t shared_bytes(int cap, bool keys) {
 }
 template <typename F>
 cudaError_t each_evict(F&& f) {
-  cudaError_t e = f(k_evict<true, 64>, true, 64);
-  if (e == cudaSuccess) e = f(k_evict<true, 128>, true, 128);
-  if (e == cudaSuccess) e = f(k_evict<false, 64>, false, 64);
-  return e == cudaSuccess ? f(k_evict<false, 128>, false, 128) : e;
+  cudaError_t e = cudaSuccess;
+  auto of = [&](auto d, auto t) {
+    constexpr int D = decltype(d)::value, T = decltype(t)::value;
+    if (e == cudaSuccess) e = f(k_evict<true, D, T>, true, D, T);
+    if (e == cudaSuccess) e = f(k_evict<false, D, T>, false, D, T);
+  };
+  using std::integral_constant;
+  of(integral_constant<int, 64>{}, integral_constant<int, 256>{});
+  of(integral_constant<int, 128>{}, integral_constant<int, 256>{});
+  of(integral_constant<int, 64>{}, integral_constant<int, 1024>{});
+  of(integral_constant<int, 128>{}, integral_constant<int, 1024>{});
+  return e;
 }
 
 }  // namespace
 
 cudaError_t setup_evict() {
-  return each_evict([](auto kernel, bool keys, int) {
+  return each_evict([](auto kernel, bool keys, int, int) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(shared_bytes(keys ? kKeysShared : kMaxEvictTokens, keys)));
   });
 }
 
-cudaError_t launch_evict(const Pool& p, const EvictArgs& a, cudaStream_t s) {
+cudaError_t launch_evict(const Pool& p, const EvictArgs& a, int sms, cudaStream_t s) {
   const bool in_shared = a.cap <= kKeysShared;
-  const cudaError_t e = each_evict([&](auto kernel, bool keys, int d) {
-    if (keys != in_shared || d != p.d) return cudaSuccess;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(p.L) * a.B * p.Hkv), dim3(kThreads), shared_bytes(a.cap, keys), s, p, a);
+  const unsigned units = static_cast<unsigned>(p.L) * a.B * p.Hkv;
+  const int threads = units <= static_cast<unsigned>(sms) && a.cap > kWide ? 1024 : 256;
+  const cudaError_t e = each_evict([&](auto kernel, bool keys, int d, int t) {
+    if (keys != in_shared || d != p.d || t != threads) return cudaSuccess;
+    return launch_pdl(kernel, dim3(units), dim3(t), shared_bytes(a.cap, keys), s, p, a);
   });
   return e != cudaSuccess ? e : cudaGetLastError();
 }

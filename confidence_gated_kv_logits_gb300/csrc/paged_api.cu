@@ -569,7 +569,7 @@ int confkv_paged_evict(confkv_paged* kv, int batch, int max_blocks, const int32_
     return fail(kv, CONFKV_ERR_INVALID_ARG, "outputs overlap one another or an input");
   DeviceGuard guard(kv->device);
   const EvictArgs a{batch, max_blocks, cap, protect, per_layer, page_table, length, keep, first, mass, pos, mass_out, pos_out, new_len};
-  return launched(kv, launch_evict(p, a, static_cast<cudaStream_t>(stream)));
+  return launched(kv, launch_evict(p, a, kv->limits.sms, static_cast<cudaStream_t>(stream)));
 }
 
 int confkv_paged_commit(confkv_paged* kv, int batch, int max_blocks, const int32_t* page_table,

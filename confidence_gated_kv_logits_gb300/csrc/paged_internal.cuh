@@ -134,7 +134,7 @@ struct BeamArgs {
 
 cudaError_t launch_append(const Pool& p, const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_append_normed(const Pool& p, const AppendArgs& a, cudaStream_t s);
-cudaError_t launch_evict(const Pool& p, const EvictArgs& a, cudaStream_t s);
+cudaError_t launch_evict(const Pool& p, const EvictArgs& a, int sms, cudaStream_t s);
 cudaError_t setup_evict();
 constexpr int kMaxEvictTokens = 1 << 19;            // cap limit of evict (confkv_paged.h)
 cudaError_t launch_commit(const Pool& p, const CommitArgs& a, cudaStream_t s);
