@@ -7,7 +7,16 @@
 // rounds of counting one byte each, and of the keys equal to it the lowest places
 // stay.  Evicted places below N (holes) and kept places from N on (movers) are
 // equally many; the r-th hole takes the r-th mover's rows, which no other move
-// reads or writes, so all moves are independent.
+// reads or writes, so all moves are independent.  Up to eight evicted places are
+// found one by one instead, as minima, while the rows behind the budget, which
+// may have to move, are on their way.
+//
+// The work is bytes: masses and positions once, moved rows twice.  64 layers x 8 x 8 heads
+// of 2049 tokens that lose one, out of place (137 MB): 33 us, 61% of the copy rate,
+// bound by each CTA's chain (length -> masses -> newest position -> minimum -> page) at
+// four CTAs per SM; 97.6 by counting bytes.  16 layers x 4 x 8 heads of 8192 that come down to 1024
+// or 2048 (665 MB): 148 us, 66%, rows of 256 bytes scattered over the pools; 203 with
+// the r-th set bit searched for by each lane, 207 with positions in shared memory (three CTAs per SM instead of four).
 #include <type_traits>
 
 #include "paged_internal.cuh"

@@ -49,7 +49,8 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
 }
 
 // N channels of an output row: acc / l (0 where nothing was seen), rounded once.
-// SH: over a shared prefix, phase 1 leaves the row's partial result as it is, phase 2
+// SH: over a shared prefix, which is read once for a group of sequences (phase 1: all the
+// group's rows over it), phase 1 leaves the row's partial result as it is, phase 2
 // joins it (`pre`: there is one) with its own, the prefix first.
 template <bool BF, bool SH, int N>
 __device__ __forceinline__ void store_row(const AttendArgs& a, const Pool& p, int row, int hq, int ch, float (&x)[N],
