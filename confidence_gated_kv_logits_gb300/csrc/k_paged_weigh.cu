@@ -52,7 +52,7 @@ template <int D>
 struct Weigh {
   static constexpr int KH = BT * 128, QH = BR * 128;        // bytes of 64 channels of a K or Q tile
   static constexpr int KT = KH * D / 64, QT = QH * D / 64;
-  static constexpr int SK = D == 128 ? 4 : 6, SQ = D == 128 ? 3 : 5;      // stages
+  static constexpr int SK = D == 128 ? 4 : 6, SQ = D == 128 ? 3 : 5;      // stages (10 of K at d = 64 change nothing)
   static constexpr int SMEM = SK * KT + SQ * QT;
 };
 
@@ -227,8 +227,23 @@ k_weigh(const Pool p, const WeighArgs a, const int sh1, const __grid_constant__ 
     // ---- the plan ----
     Items w(p, a, tb, sh1);
     Sched sh;
-    if (a.bt.B <= 32) sh = sched_warp(w, 1, 0, blockIdx.x, gridDim.x);
-    else sh = s.sched;
+    if (a.bt.B == 1) {                    // without the scans over sequences (one token over 2048: 7.1 us with them, 6.8)
+      int bad = 0;
+      w.sequence(0, bad);
+      if (bad && blockIdx.x == 0 && lane == 0) atomicOr(p.err, bad);
+      sh.b = 0;
+      sh.T = w.T;
+      sh.ctx = w.ctx;
+      sh.len = w.len;
+      sh.row0 = w.row0;
+      sh.seq0 = 0;
+      sh.head = w.T > 0 ? w.head_work() : 0;
+      sched_share<Items>(&sh, sh.head * p.Hkv, blockIdx.x, gridDim.x, 1);
+    } else if (a.bt.B <= 32) {
+      sh = sched_warp(w, 1, 0, blockIdx.x, gridDim.x);
+    } else {
+      sh = s.sched;
+    }
     long long at = 0;                     // the cost at which the next item starts
     int i = 0, flag = 0;
     const bool any = sh.cur < sh.end;
@@ -600,7 +615,7 @@ cudaError_t each_weigh(F&& f) {
   if (e == cudaSuccess) e = f(k_weigh<false, 64>, false, 64, Weigh<64>::SMEM);
   return e == cudaSuccess ? f(k_weigh<false, 128>, false, 128, Weigh<128>::SMEM) : e;
 }
-static_assert(Weigh<128>::SMEM + sizeof(Shared) <= 232448, "a CTA's shared memory");
+static_assert(Weigh<128>::SMEM + sizeof(Shared) <= 232448 && Weigh<64>::SMEM + sizeof(Shared) <= 232448, "a CTA's shared memory");
 
 }  // namespace
 
