@@ -23,11 +23,11 @@
 // one token tile's, the pair's two sums are joined at the item's end.
 //
 // 32 sequences x 1 token over up to 16384, 64/8 heads of 64, bf16 (389 MB): 74 us, 5.3 TB/s,
-// 78% of the copy rate; 64 rows of 4 sequences over 12000, 40/8 heads of 128 (31.5 GFLOP):
+// 78% of the copy rate, 850 cycles of fixed steps per token tile in the moving and issuing warps; 64 rows of 4 sequences over 12000, 40/8 heads of 128 (31.5 GFLOP):
 // 46 us, 690 TFLOP/s, bound by the exponentials' instructions (a column's share of a
 // warp's issue slots) and the steps between products; one token over 2048, 12/12 heads
-// of 64: 7 us, of which planning takes 2 and the chain page -> K -> product 2.  Two warpgroups instead of
-// four: 71, 56 and 6.6 us; one issuing warp 73 (32 sequences); items of one token tile, and columns in unrolled code that did
+// of 64: 6.8 us, of which the chain page -> K -> product takes 2 and planning the same (7.1 with the scans that
+// several sequences need).  Two warpgroups instead of four: 71, 56 and 6.6 us; one issuing warp 73 (32 sequences); items of one token tile, and columns in unrolled code that did
 // not fit the instruction cache, 147 to 176.
 #include <algorithm>
 #include <cstddef>

@@ -185,11 +185,11 @@ int few_cluster(const confkv_paged& kv, int batch, int64_t units, int64_t tokens
 // places per CTA, as a CTA's share cuts at most the unit it starts in and the
 // one it ends in
 constexpr size_t kTicketsAt = 256;
-size_t scratch_rows(int sms) { return 2 * static_cast<size_t>(sms) * std::max(kFewCtasPerSm * kFewRows, kManyRows); }
+size_t scratch_rows(int sms) { return 2 * static_cast<size_t>(sms) * std::max(kFewCtasMost * kFewRows, kManyRows); }
 size_t scratch_bytes_of(int sms, int d) { return CONFKV_PAGED_ZEROED + scratch_rows(sms) * (2 + d) * sizeof(float); }
 constexpr size_t kCutAt = 8192;
 bool tickets_fit(int sms) {
-  return kTicketsAt + sizeof(unsigned int) * kFewCtasPerSm * sms <= kCutAt && kCutAt + sizeof(int4) * sms <= CONFKV_PAGED_ZEROED;
+  return kTicketsAt + sizeof(unsigned int) * kFewCtasMost * sms <= kCutAt && kCutAt + sizeof(int4) * sms <= CONFKV_PAGED_ZEROED;
 }
 
 Batch batch_of(const confkv_paged_batch* b) {
@@ -291,7 +291,7 @@ cudaError_t attend(const confkv_paged& kv, const AttendArgs& a, int batch, cudaS
     // that one's joins run beside another's tiles (40/8 heads of 128, one row each, us, of eight warps and of four: 32
     // sequences of 200 own tokens 45.0, 35.3; 64 of 700 76.3, 68.8; 128 of 2000 151, 142; 32 of 8000 134.6, 134.8; 16 of
     // 300 33.2, 36.1)
-    if (a.bt.phase == 2 && cl == 1 && batch >= 32) return launch_attend_few(p, a, kv.scratch, kv.maps, 2 * kv.limits.sms, 1, 4, s);
+    if (a.bt.phase == 2 && cl == 1 && batch >= 32) return launch_attend_few(p, a, kv.scratch, kv.maps, kFewCtasMost * kv.limits.sms, 1, 4, s);
     const int ctas = cl > 1 ? cl * static_cast<int>(units) : kFewCtasPerSm * kv.limits.sms;
     return launch_attend_few(p, a, kv.scratch, kv.maps, ctas, cl, 8, s);
   }

@@ -23,8 +23,8 @@ constexpr int kManyBlock = 128;        // tokens of a block
 // page's tokens, and with them the rows that see one, are NaN.
 constexpr int kNoRows = -kManyBlock;
 
-// CTAs of a launch: one per SM
-constexpr int kFewCtasPerSm = 1;
+// CTAs of a launch: one per SM, of four warps two
+constexpr int kFewCtasPerSm = 1, kFewCtasMost = 2;
 
 cudaError_t launch_attend_few(const Pool& p, const AttendArgs& a, const Scratch& sc, const AttendMaps& m,
                               int ctas, int cluster, int warps, cudaStream_t s);

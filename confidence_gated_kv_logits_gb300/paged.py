@@ -148,7 +148,8 @@ class PagedBatch:
 
 class SharedPrefix:
     """Prefixes that groups of neighbouring sequences share (``PagedKV.prefix``),
-    and the attention's scratch for them: calls with one object must be ordered."""
+    and the attention's scratch for them: calls with one object must be ordered, and
+    it is kept until their work is done."""
 
     def __init__(self, struct, tensors, rows, index):
         self._struct = struct

@@ -208,9 +208,9 @@ int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int l
  * repeat; the prefix's last, less than 128 tokens each sequence reads from its own
  * pages, so those must be there).  Sequences in no group are taken as attend takes
  * them.  Any page_size and prefix length (0 too).
- * A sequence with fewer cached tokens than its group's prefix is left out: its rows
- * stay as they were (CONFKV_FLAG_BAD_INDEX); that flag too for starts that
- * fall or leave 0 .. batch and for negative lengths.
+ * A sequence with fewer cached tokens than the whole steps of 128 of its group's
+ * prefix is left out: its rows stay as they were (CONFKV_FLAG_BAD_INDEX); that flag
+ * too for starts that fall or leave 0 .. batch and for negative lengths.
  * Every row's result is joined from two parts, in fp32, the prefix's first: within
  * attend's precision, but not the same bits.
  */

@@ -344,6 +344,36 @@ def test_attend_shared_reads_the_first_sequences_pages(pkg):
     assert got[2].status() == 0
 
 
+def test_attend_shared_sequences_that_hold_the_whole_steps_alone(pkg):
+    """A prefix of 200 tokens is shared in steps of 128: sequences of 128 to 199 cached tokens have what they need."""
+    c = Grouped(torch.float16, 8, 2, 64, 32, [(3, 128)], [20, 0, 72], [2, 3], seed=15)
+    kv = pkg.PagedKV(c.k, c.v, 8)
+    check_shared(c, run_shared(pkg, c, kv=kv, prefix=kv.prefix(ints([0, 3]), ints([200]), c.rows)), reference(c))
+    assert kv.status() == 0
+    c = Grouped(torch.float16, 8, 2, 64, 32, [(3, 127)], [20, 0, 72], [2, 3], seed=15)
+    out = run_shared(pkg, c, kv=(kv := pkg.PagedKV(c.k, c.v, 8)), prefix=kv.prefix(ints([0, 3]), ints([200]), c.rows))[0]
+    at = slice(c.starts[1], c.starts[2])                # 127 cached tokens: left out
+    assert kv.status(check=False) == 16 and (out[at] == 7).all() and not (out[:c.starts[1]] == 7).any()
+
+
+@pytest.mark.parametrize("tail,new", [([9, 200], [2]), ([300], [60])])
+def test_attend_shared_nans_reach_what_they_touch(pkg, tail, new):
+    c = Grouped(torch.bfloat16, 8, 2, 128, 32, [(3, 300)], tail, new, seed=16)
+    o, l, tol, tol_l = reference(c)
+    c.k[1, int(c.table[0, 0]), 0, 5] = math.nan         # a shared token of one KV head
+    c.k[1, int(c.table[1, 9]), 1, 15] = math.nan        # place 303, of the second sequence alone, of the other
+    out, lse, kv = run_shared(pkg, c)
+    bad = torch.zeros_like(lse, dtype=torch.bool)
+    bad[:c.starts[3], :4] = True
+    bad[c.starts[1]:c.starts[2], 4:] = True
+    assert torch.equal(lse.isnan(), bad) and torch.equal(out.isnan(), bad[..., None].expand_as(out))
+    n = c.starts[3]
+    good = ~bad[:n]
+    vmax = float(torch.nan_to_num(c.v.double(), 0, 0, 0).abs().max())
+    assert ((out[:n].double() - o).abs()[good] <= tol[good] + 2.0 ** -20 * vmax).all()
+    assert ((lse[:n].double() - l).abs()[good] <= tol_l[good] + 2.0 ** -20).all()
+
+
 def test_attend_shared_bad_pages_and_lengths(pkg):
     c = Grouped(torch.float16, 8, 2, 64, 32, [(2, 400), (2, 300)], [9], [2], seed=13)
     kv = pkg.PagedKV(c.k, c.v, 8)
@@ -589,6 +619,20 @@ def test_weigh_beyond_cap_and_bad_pages(pkg):
     assert out[1, :, 16:32].isnan().all() and torch.isfinite(out[0]).all() and torch.isfinite(out[1, :, :16]).all()
 
 
+def test_weigh_a_single_sequence_without_rows_and_of_bad_lengths(pkg):
+    c = Case(torch.bfloat16, 8, 2, 64, 16, [300], [0], seed=13)
+    assert run_weigh(pkg, c)[1].status() == 0
+    c = Case(torch.bfloat16, 8, 2, 64, 16, [100], [4], seed=14)
+    kv, lse = pkg.PagedKV(c.k, c.v, 8), torch.zeros(c.rows, 8, device=DEV) + 30
+    mass = torch.full((1, 2, 200), 3.0, device=DEV)
+    for ctx, starts, flag in ((-5, [0, 4], 16), (100000, [0, 4], 2), (100, [-3, 1], 0), (100, [4, 0], 0)):
+        out = mass.clone()
+        kv.weigh(1, kv.batch(c.table, ints([ctx]), ints(starts)), c.q, lse, mass, out)
+        assert kv.status(check=False) & flag == flag
+        assert (out[:, :, 128:] == 3).all()             # (the table has 8 pages)
+    assert torch.equal(out, mass)                       # starts that fall: no rows
+
+
 def test_weigh_scale_and_long_lse(pkg):
     c = Case(torch.bfloat16, 8, 2, 128, 64, [500, 90], [1, 40], seed=8)
     c.q *= 4
@@ -713,7 +757,7 @@ def test_evict_a_budget_for_each_layer(pkg):
     run_evict(pkg, L=3, length=[[50, 40], [30, 40], [50, 1]], keep=[[20, 40], [30, 39], [1, 1]], per_layer=True, in_place=True)
 
 
-@pytest.mark.parametrize("length,keep,cap", [(9000, 1000, 9001), (5000, 4990, 60001), (45000, 44000, 45001)])
+@pytest.mark.parametrize("length,keep,cap", [(9000, 1000, 9001), (5000, 4990, 60001), (4000, 3995, 4001), (45000, 44000, 45001)])
 def test_evict_long(pkg, length, keep, cap):
     run_evict(pkg, L=1, B=1, H=1, heads=1, page=256, length=(length,), keep=(keep,), cap=cap, protect=50, first=(5,))
 
