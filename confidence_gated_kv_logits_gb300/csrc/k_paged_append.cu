@@ -290,7 +290,7 @@ k_append_normed(const Pool p, const AppendArgs a) {
       for (int i = 0; i < 16; ++i) big = fmaf(x[i] * kTiny, x[i] * kTiny, big);
 #pragma unroll
       for (int o = 1; o < LP; o <<= 1) big += __shfl_xor_sync(0xffffffffu, big, o);
-      // (from 2^126 on a subnormal number, good to 2^-21 of itself at least)
+      // (from 2^126 on a subnormal number, good to 2^-21 of itself at least, and x inv with it)
       if (!(ss < INFINITY)) inv = kTiny * rsqrtf(big * (1.0f / D));
     }
     if (kind != 2) {
@@ -298,11 +298,11 @@ k_append_normed(const Pool p, const AppendArgs a) {
         const float4* w = reinterpret_cast<const float4*>(s_w[kind]);
         const float4 w4[4] = {w[lo >> 2], w[(lo >> 2) + 1], w[hi >> 2], w[(hi >> 2) + 1]};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[4 * i] *= inv * w4[i].x;
-          x[4 * i + 1] *= inv * w4[i].y;
-          x[4 * i + 2] *= inv * w4[i].z;
-          x[4 * i + 3] *= inv * w4[i].w;
+        for (int i = 0; i < 4; ++i) {      // (inv * w first could leave fp32's range where the row's values do not)
+          x[4 * i] = x[4 * i] * inv * w4[i].x;
+          x[4 * i + 1] = x[4 * i + 1] * inv * w4[i].y;
+          x[4 * i + 2] = x[4 * i + 2] * inv * w4[i].z;
+          x[4 * i + 3] = x[4 * i + 3] * inv * w4[i].w;
         }
       }
       if (turned) {
