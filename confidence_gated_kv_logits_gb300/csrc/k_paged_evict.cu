@@ -96,12 +96,18 @@ k_evict(const Pool p, const EvictArgs a) {
     if (h == 0 && (a.per_layer || l == 0)) a.new_len[seq] = N;
     s_top = INT32_MIN;
   }
-  if (flag) return;                     // such a sequence stays as it is
   const float* mass = a.mass + unit * a.cap;
   const int32_t* pos = a.pos + unit * a.cap;
   float* mass_out = a.mass_out + unit * a.cap;
   int32_t* pos_out = a.pos_out + unit * a.cap;
   const bool copy = mass_out != mass;
+  if (flag) {                           // such a sequence stays as it is, its masses in the outputs too
+    for (int j = tid; copy && j < min(n, a.cap); j += kThreads) {
+      mass_out[j] = mass[j];
+      pos_out[j] = pos[j];
+    }
+    return;
+  }
   const int32_t* table = a.table + static_cast<size_t>(b) * a.max_blocks;
   const int layer = l * p.NP;           // (rows of a pool stay below 2^31)
   constexpr int LR = D / 8;             // lanes of a row, K's and then V's

@@ -268,9 +268,9 @@ int confkv_paged_weigh(confkv_paged* kv, const confkv_paged_batch* batch, int la
  * Heads and layers keep different tokens: a place means another token in each.
  * The pages of places that change (those of places first[b] .. N - 1) belong to one
  * sequence each.  A sequence with a negative length, budget or first, or longer than
- * its table or cap, stays as it is, with its length (a flag); a token whose
- * page or whose new place's page is outside the pool is not moved
- * (CONFKV_FLAG_BAD_PAGE).
+ * its table or cap, stays as it is, with its length (a flag; outputs of their own
+ * receive its places, up to cap); a token whose page or whose new place's page is
+ * outside the pool is not moved (CONFKV_FLAG_BAD_PAGE).
  */
 int confkv_paged_evict(confkv_paged* kv, int batch, int max_blocks, const int32_t* page_table,
                        const int32_t* length, int per_layer, const float* mass, const int32_t* pos, int cap,

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests.test_paged_budget_gpu import check_append
-from tests.test_paged_gpu import DT, Case
+from tests.test_paged_gpu import Case, ints
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -45,3 +45,32 @@ def test_append_normed_tiny_rows_under_huge_weights(pkg, wide):
     x = (c.randn(6, 4, 64).float() * 10.0 ** -torch.arange(20, 26, device=DEV).float()[:, None, None]).to(torch.bfloat16)
     w = [(1e33 * (1 + torch.rand(64, generator=c.g, device=DEV))).to(torch.float32 if wide else torch.bfloat16) for _ in range(2)]
     check_append(pkg, c, 64, True, 0, w[0], w[1], eps=1e-12, q=x, k=x.flip(0).contiguous())
+
+
+# ---------------------------------------------------------------------------
+# eviction
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("cap", [64, 5000, 41000])
+@pytest.mark.parametrize("length,keep,first,flag", [
+    ([-1, 40], [5, 30], None, 16), ([60, 40], [-2, 30], None, 16), ([60, 40], [10, 30], [-1, 0], 16), ([65, 40], [10, 30], None, 2),
+    ([1 << 30, 40], [10, 30], None, 2)])
+def test_evict_out_of_place_what_it_refuses_stays(pkg, length, keep, first, flag, cap):
+    """A refused sequence's masses and positions are in the outputs, as its length is; behind them nothing is written."""
+    g = torch.Generator(device=DEV).manual_seed(cap)
+    k = torch.randn(2, 9, 2, 16, 64, generator=g, device=DEV).half()
+    v, k0 = k.clone(), k.clone()
+    table = torch.arange(8, device=DEV).view(2, 4).int()
+    mass = torch.rand(2, 2, 2, cap, generator=g, device=DEV)
+    pos = torch.arange(cap, device=DEV).int().expand(2, 2, 2, cap).contiguous()
+    mo, po, new = torch.full_like(mass, -5), torch.full_like(pos, -5), ints([-7, -7])
+    kv = pkg.PagedKV(k, v, 4)
+    kv.evict(table, ints(length), mass, pos, ints(keep), mo, po, new, first=ints(first) if first else None)
+    assert kv.status(check=False) == flag
+    n = min(max(length[0], 0), cap)
+    assert new.tolist() == [length[0], 30]
+    assert torch.equal(mo[:, 0, :, :n], mass[:, 0, :, :n]) and torch.equal(po[:, 0, :, :n], pos[:, 0, :, :n])
+    assert (mo[:, 0, :, n:] == -5).all() and (po[:, 0, :, n:] == -5).all()
+    pages = table[0].long()
+    assert torch.equal(k[:, pages], k0[:, pages]) and torch.equal(v[:, pages], k0[:, pages])
+    # the other sequence is evicted: the 30 largest of its masses (positions rise, none is protected)
+    assert torch.equal(mo[:, 1, :, :30].sort(2).values, mass[:, 1, :, :40].sort(2).values[..., 10:])
