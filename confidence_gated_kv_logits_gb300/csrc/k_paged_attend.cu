@@ -93,11 +93,14 @@ k_attend_few(const Pool p, const AttendArgs a, const Scratch sc, const __grid_co
   fence_async();
   // Phase 2 of a shared prefix needs phase 1 only where it joins the two (and where it uses the scratch): its own
   // tiles, which the kernels before phase 1 stored, come meanwhile (phase 1 lets its dependents start
-  // only behind its own wait for those).  Its dependents in turn start behind phase 1.
+  // only behind its own wait for those, when their stores have reached L2; the fence here, that no line which L1
+  // still holds from before answers for them: 0.3 us).  Its dependents in turn start behind phase 1.
   bool waited = !SH || a.bt.phase != 2;
   if (waited) {
     pdl_wait();
     pdl_trigger();
+  } else {
+    __threadfence();
   }
   fence_async_global();
 

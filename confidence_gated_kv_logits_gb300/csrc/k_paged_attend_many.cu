@@ -159,6 +159,8 @@ k_attend_many(const Pool p, const AttendArgs a, const Scratch sc, const int defe
   if (!joins) {
     pdl_wait();
     pdl_trigger();
+  } else {
+    __threadfence();
   }
   fence_async_global();
   tc_fence_before();

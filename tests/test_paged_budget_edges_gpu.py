@@ -1,13 +1,11 @@
 """Normed appends, attention over shared prefixes, accumulated weights and eviction where calls meet the ends
 of their ranges and one another.  Tolerances: those of test_paged_budget_gpu.py."""
-import math
-
 import numpy as np
 import pytest
 import torch
 
 from tests.test_paged_budget_gpu import check_append
-from tests.test_paged_gpu import Case, ints
+from tests.test_paged_gpu import DT, Case, ints
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -45,6 +43,82 @@ def test_append_normed_tiny_rows_under_huge_weights(pkg, wide):
     x = (c.randn(6, 4, 64).float() * 10.0 ** -torch.arange(20, 26, device=DEV).float()[:, None, None]).to(torch.bfloat16)
     w = [(1e33 * (1 + torch.rand(64, generator=c.g, device=DEV))).to(torch.float32 if wide else torch.bfloat16) for _ in range(2)]
     check_append(pkg, c, 64, True, 0, w[0], w[1], eps=1e-12, q=x, k=x.flip(0).contiguous())
+
+
+# ---------------------------------------------------------------------------
+# attention over shared prefixes
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("heads,H,d,B,T,tail", [
+    (40, 8, 128, 4, 1, 60),            # phase 2 by clusters or whole units of eight warps
+    (12, 12, 64, 40, 1, 200),          # by CTAs of four warps
+    (64, 8, 64, 8, 5, 300),            # 40 rows of a KV head, streamed
+    (40, 8, 128, 3, 60, 500)])         # by the prompt kernel
+def test_attend_shared_right_behind_what_wrote_its_inputs(pkg, dt, heads, H, d, B, T, tail):
+    """Lengths, tables, masks, queries and rows change in place right before the call, eagerly and in a replayed graph: phase 2,
+    which starts before phase 1 has ended, sees what the calls before wrote.  The same calls with waits between them say
+    what it has to be, bit for bit."""
+    P, page, V = 640, 32, 6
+    g = torch.Generator(device=DEV).manual_seed(B + T)
+    full, own, n = P // page, -(-(tail + T) // page), B * T
+    pages = full + V * B * own                       # each variant has tails of its own
+    k_pool, v_pool = (torch.randn(2, pages, H, page, d, generator=g, device=DEV).to(DT[dt]) for _ in range(2))
+    order = torch.randperm(pages, generator=g, device=DEV).int()
+    kv = pkg.PagedKV(k_pool, v_pool, heads)
+    inv = (10000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)).float().cuda()
+    words = -(-T // 32)
+
+    def variant(i):
+        tails = order[full + i * B * own:full + (i + 1) * B * own].view(B, own)
+        return [torch.cat([order[:full].expand(B, full), tails], 1).contiguous(),
+                (P + torch.randint(0, tail + 1, (B,), generator=g, device=DEV)).int(),
+                torch.randint(-(1 << 31), 1 << 31, (n, words), generator=g, device=DEV).int()] + [
+                    torch.randn(n, x, d, generator=g, device=DEV).to(DT[dt]) for x in (heads, H, H)]
+
+    variants = [variant(i) for i in range(V)]
+    staged, live = [x.clone() for x in variants[0]], [x.clone() for x in variants[0]]
+    table, ctx, mask, q, k, v = live
+    batch = kv.batch(table, ctx, ints([T * b for b in range(B + 1)]), mask)
+    prefix = kv.prefix(ints([0, B]), ints([P]), n)
+    q_rot, out, out2, lse = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q), torch.empty(n, heads, device=DEV)
+    none = lambda: None  # noqa: E731
+
+    def step(between=none):
+        for x, y in zip(live, staged):
+            x.copy_(y)
+        between()
+        kv.append(1, batch, k, v, q=q, q_out=q_rot, inv_freq=inv)
+        between()
+        kv.attend(1, batch, q_rot, out, lse=lse, prefix=prefix)
+        between()
+        kv.attend(1, batch, out, out2, prefix=prefix)          # reads what the call before it wrote
+        between()
+
+    def stage(i):
+        for x, y in zip(staged, variants[i]):
+            x.copy_(y)
+
+    want = []
+    for i in range(V):
+        stage(i)
+        step(torch.cuda.synchronize)
+        want.append([x.clone() for x in (q_rot, out, lse, out2)])
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    got, picks = [], np.random.default_rng(T).integers(0, V, 80).tolist()
+    for j, i in enumerate(picks):
+        stage(i)
+        graph.replay() if j % 2 else step()
+        got.append([x.clone() for x in (q_rot, out, lse, out2)])
+    torch.cuda.synchronize()
+    for i, have in zip(picks, got):
+        for x, y in zip(have, want[i]):
+            assert torch.equal(x, y)
+    assert kv.status() == 0
+    assert all(torch.isfinite(x).all() for w in want for x in (w[0], w[1]))
 
 
 # ---------------------------------------------------------------------------
