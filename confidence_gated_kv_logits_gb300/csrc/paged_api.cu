@@ -115,6 +115,15 @@ const char* check_batch(const confkv_paged_batch* b, bool masked) {
   return nullptr;
 }
 
+// An output shares a byte with the batch's own tensors.  (CTAs plan for themselves from what these hold: were they
+// to change while a kernel runs, one could look for sequences behind the last.)
+bool in_batch(const confkv_paged_batch* b, int rows, const void* out, size_t n) {
+  const size_t seqs = static_cast<size_t>(b->batch);
+  return overlap(out, n, b->page_table, seqs * b->max_blocks * 4) || overlap(out, n, b->ctx_len, seqs * 4) ||
+         overlap(out, n, b->q_start, (seqs + 1) * 4) ||
+         (b->mask && b->mask_words > 0 && overlap(out, n, b->mask, static_cast<size_t>(rows) * b->mask_words * 4));
+}
+
 // Tensor maps of both pools for both kernels: rows of d elements in boxes of 64
 // channels (128 bytes, swizzled) x as many rows as a page and the kernel's tile share.
 // Rows outside the pool (kNoRows) read as NaN from K's maps and as zero from V's.
@@ -221,6 +230,8 @@ const char* append_args(const Pool& p, const confkv_paged_batch* batch, int laye
   if (q && (rows_overlap(k, k_stride, wk, q_out, q_out_stride, wq, rows) ||
             rows_overlap(v, v_stride, wk, q_out, q_out_stride, wq, rows)))
     return "q_out overlaps k or v";
+  if (q && in_batch(batch, rows, q_out, (static_cast<size_t>(rows - 1) * q_out_stride + wq) * 2))
+    return "q_out overlaps the batch's tensors";
   *a = AppendArgs{};
   a->bt = batch_of(batch);
   a->layer = layer;
@@ -257,6 +268,8 @@ const char* attend_args(const Pool& p, const confkv_paged_batch* batch, int laye
   const size_t nr = static_cast<size_t>(rows);
   if (lse && (overlap(lse, nr * p.Hq * 4, out, nr * wq * 2) || overlap(lse, nr * p.Hq * 4, q, ((nr - 1) * q_stride + wq) * 2)))
     return "lse overlaps q or out";
+  if (in_batch(batch, rows, out, nr * wq * 2) || (lse && in_batch(batch, rows, lse, nr * p.Hq * 4)))
+    return "out or lse overlaps the batch's tensors";
   *a = AttendArgs{batch_of(batch), layer, rows, static_cast<const uint16_t*>(q), q_stride, static_cast<uint16_t*>(out), lse,
                   scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(p.d)), nullptr, nullptr};
   return nullptr;
@@ -483,6 +496,13 @@ int confkv_paged_attend_shared(confkv_paged* kv, const confkv_paged_batch* batch
   if (overlap(prefix->partial, np, q, ((nr - 1) * q_stride + wq) * 2) || overlap(prefix->partial, np, out, nr * wq * 2) ||
       (lse && overlap(prefix->partial, np, lse, nr * p.Hq * 4)))
     return fail(kv, CONFKV_ERR_INVALID_ARG, "partial overlaps q, out or lse");
+  const size_t groups = static_cast<size_t>(prefix->groups);
+  auto in_prefix = [&](const void* at, size_t n) {
+    return overlap(at, n, prefix->group_start, (groups + 1) * 4) || overlap(at, n, prefix->prefix_len, groups * 4);
+  };
+  if (in_batch(batch, rows, prefix->partial, np) || in_prefix(prefix->partial, np) || in_prefix(out, nr * wq * 2) ||
+      (lse && in_prefix(lse, nr * p.Hq * 4)))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "out, lse or partial overlaps the batch's or the prefix's tensors");
   DeviceGuard guard(kv->device);
   a.part = static_cast<float*>(prefix->partial);
   a.part_ml = a.part + nr * wq;
@@ -526,6 +546,8 @@ int confkv_paged_weigh(confkv_paged* kv, const confkv_paged_batch* batch, int la
     if (out && (overlap(out, nm, q, ((nr - 1) * q_stride + wq) * 2) || overlap(out, nm, lse, nr * p.Hq * 4) ||
                 (positions && overlap(out, nm, positions, nr * 4))))
       return fail(kv, CONFKV_ERR_INVALID_ARG, "mass_out or pos overlaps an input");
+  if (in_batch(batch, rows, mass_out, nm) || (pos && in_batch(batch, rows, pos, nm)))
+    return fail(kv, CONFKV_ERR_INVALID_ARG, "mass_out or pos overlaps the batch's tensors");
   if (pos && (overlap(pos, nm, mass, nm) || overlap(pos, nm, mass_out, nm)))
     return fail(kv, CONFKV_ERR_INVALID_ARG, "pos overlaps mass or mass_out");
   DeviceGuard guard(kv->device);

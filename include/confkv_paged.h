@@ -15,7 +15,8 @@
  * Conventions (those of confkv.h hold here too):
  *   - Tensor arguments are DEVICE pointers on the cache's GPU, owned by the
  *     caller, row-major in the stated layout, and only touched by work
- *     enqueued on `stream` during the call.  Element types are fp16 or bf16
+ *     enqueued on `stream` during the call.  No output lies in an input or in
+ *     the batch's tensors unless a function allows it.  Element types are fp16 or bf16
  *     bit patterns (CONFKV_FP16 / CONFKV_BF16) unless stated otherwise.
  *   - Calls return CONFKV_OK or a negative CONFKV_ERR_* code; argument errors
  *     are found on the host before any work is enqueued.  What only the GPU

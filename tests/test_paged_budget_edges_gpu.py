@@ -148,3 +148,69 @@ def test_evict_out_of_place_what_it_refuses_stays(pkg, length, keep, first, flag
     assert torch.equal(k[:, pages], k0[:, pages]) and torch.equal(v[:, pages], k0[:, pages])
     # the other sequence is evicted: the 30 largest of its masses (positions rise, none is protected)
     assert torch.equal(mo[:, 1, :, :30].sort(2).values, mass[:, 1, :, :40].sort(2).values[..., 10:])
+
+
+# ---------------------------------------------------------------------------
+# refusals
+# ---------------------------------------------------------------------------
+def test_outputs_in_the_batchs_own_tensors_are_refused(pkg):
+    """One buffer holds the table, lengths, starts, mask and groups, and outputs that begin or end in one of them."""
+    B, H, heads, d, n = 3, 2, 4, 64, 3
+    k, v = (torch.zeros(1, 9, H, 16, d, device=DEV, dtype=torch.float16) for _ in range(2))
+    kv = pkg.PagedKV(k, v, heads)
+    q, lse = torch.zeros(n, heads, d, device=DEV, dtype=torch.float16), torch.zeros(n, heads, device=DEV)
+    room = n * heads * d // 2                                  # words of an out or q_out
+    apart = 2 * room + 64                                      # an output meets one tensor at a time
+    buf = torch.zeros(8 * apart, device=DEV, dtype=torch.int32)
+
+    def cut(at, *shape):
+        size = int(np.prod(shape))
+        return buf[at:at + size].view(*shape)
+
+    places = [(B, 2), (B,), (B + 1,), (n, 1), (2,), (1,)]      # table, ctx, q_start, mask, group_start, prefix_len
+    starts = [room + apart * i for i in range(len(places))]
+    table, ctx, start, mask, group, length = (cut(at, *s) for at, s in zip(starts, places))
+    start.copy_(torch.arange(B + 1))
+    batch = kv.batch(table, ctx, start, mask)
+    prefix = kv.prefix(group, length, n)
+    far = torch.zeros_like(q)
+    mass, cap = torch.zeros(B, H, 30, device=DEV), 30
+    calls = 0
+    for at, shape in zip(starts, places):
+        own, last = at < starts[4], at + int(np.prod(shape)) - 1
+        for words, where in ((room, last // 4 * 4), (room, (at + 4 - room) // 4 * 4)):          # the tensor's last word is the
+            out = cut(where, words).view(torch.float16).view(n, heads, d)                       # output's first, its first the last
+            assert where <= last and where + words > at
+            bad = [lambda: kv.attend(0, batch, q, out, prefix=prefix)]
+            if own:
+                bad += [lambda: kv.attend(0, batch, q, out)]
+            if own and at != starts[3]:
+                bad += [lambda: kv.append(0, batch, far[:, :H], far[:, H:], q=q, q_out=out),
+                        lambda: kv.append(0, batch, far[:, :H], far[:, H:], q=q, q_out=out, q_norm=torch.ones(d, device=DEV))]
+            for call in bad:
+                with pytest.raises(pkg.ConfKVError, match="overlaps"):
+                    call()
+                calls += 1
+        for words in (B * H * cap, n * heads):
+            x = cut(last, words)
+            if words == n * heads:
+                l = x.view(torch.float32).view(n, heads)
+                bad = [lambda: kv.attend(0, batch, q, far, lse=l, prefix=prefix)] + ([lambda: kv.attend(0, batch, q, far, lse=l)] if own else [])
+            elif own:
+                m, p = x.view(torch.float32).view(B, H, cap), x.view(B, H, cap)
+                bad = [lambda: kv.weigh(0, batch, q, lse, mass, m), lambda: kv.weigh(0, batch, q, lse, m, m),
+                       lambda: kv.weigh(0, batch, q, lse, mass, mass, p)]
+            else:
+                bad = []
+            for call in bad:
+                with pytest.raises(pkg.ConfKVError, match="overlaps"):
+                    call()
+                calls += 1
+        # the scratch
+        from confidence_gated_kv_logits_gb300.paged import PrefixStruct, SharedPrefix
+        need = pkg.load_library().confkv_paged_partial(n, heads, d)
+        scratch = PrefixStruct(1, group.data_ptr(), length.data_ptr(), buf.data_ptr() + last // 4 * 16, need)
+        with pytest.raises(pkg.ConfKVError, match="overlaps"):
+            kv.attend(0, batch, q, far, prefix=SharedPrefix(scratch, (), n, kv._index))
+    assert calls == 3 * 8 + 4 + 2 * 2 + 4 * 5 + 2
+    assert kv.status() == 0
