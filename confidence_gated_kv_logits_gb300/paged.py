@@ -312,7 +312,8 @@ class PagedKV(_Device):
         them places below first[b] and the `protect` newest positions) and moves those behind
         into evicted ones' places; mass, pos [layers, batch, kv_heads, cap] and their
         outputs (both may be the inputs); length, keep, new_len int32 [batch] or
-        [layers, batch]."""
+        [layers, batch].  Places from first[b] on lie in pages that no other sequence
+        names: what several share is below it, and never changes."""
         rc = _ops.evict(self._ob, self.layers, page_table, length, mass, pos, keep, mass_out, pos_out, new_len, protect,
                         first, stream)
         if rc:

@@ -268,7 +268,8 @@ int confkv_paged_weigh(confkv_paged* kv, const confkv_paged_batch* batch, int la
  *   first: int32 [batch] or NULL (0)
  * Heads and layers keep different tokens: a place means another token in each.
  * The pages of places that change (those of places first[b] .. N - 1) belong to one
- * sequence each.  A sequence with a negative length, budget or first, or longer than
+ * sequence each: where sequences share a prefix's pages, first[b] is the tokens in
+ * them or more (which pages are shared is not looked at).  A sequence with a negative length, budget or first, or longer than
  * its table or cap, stays as it is, with its length (a flag; outputs of their own
  * receive its places, up to cap); a token whose page or whose new place's page is
  * outside the pool is not moved (CONFKV_FLAG_BAD_PAGE).

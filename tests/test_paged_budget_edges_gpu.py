@@ -150,6 +150,38 @@ def test_evict_out_of_place_what_it_refuses_stays(pkg, length, keep, first, flag
     assert torch.equal(mo[:, 1, :, :30].sort(2).values, mass[:, 1, :, :40].sort(2).values[..., 10:])
 
 
+@pytest.mark.parametrize("keep", [[150, 200, 130], [297, 295, 150]])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_behind_a_shared_prefix(pkg, keep, in_place):
+    """Three sequences name the same pages for 128 tokens, which weigh least: with `first` they stay, and each sequence's own
+    tokens are evicted as they are without the others."""
+    P, page, L, H, d, B, n = 128, 32, 2, 2, 64, 3, 300
+    g = torch.Generator(device=DEV).manual_seed(keep[0])
+    own = -(-(n - P) // page)
+    k, v = (torch.randn(L, P // page + B * own, H, page, d, generator=g, device=DEV).half() for _ in range(2))
+    order = torch.randperm(k.shape[1], generator=g, device=DEV).int()
+    table = torch.stack([torch.cat([order[:P // page], order[P // page + b * own:P // page + (b + 1) * own]]) for b in range(B)])
+    mass = torch.rand(L, B, H, n, generator=g, device=DEV) + 1
+    mass[..., :P] *= 1e-3
+    pos = torch.rand(L, B, H, n, generator=g, device=DEV).argsort(3).int()
+    alone = []
+    for b in range(B):                                     # each with pools of its own
+        k1, v1, m1, p1 = k.clone(), v.clone(), mass[:, b:b + 1].clone(), pos[:, b:b + 1].clone()
+        pkg.PagedKV(k1, v1, 4).evict(table[b:b + 1].contiguous(), ints([n]), m1, p1, ints(keep[b:b + 1]), m1, p1, ints([0]), protect=9, first=ints([P]))
+        alone.append((k1, v1, m1, p1))
+    shared, k0, v0 = order[:P // page].long(), k.clone(), v.clone()
+    kv = pkg.PagedKV(k, v, 4)
+    mo, po, new = (mass, pos, ints([0] * B)) if in_place else (torch.zeros_like(mass), torch.zeros_like(pos), ints([0] * B))
+    kv.evict(table, ints([n] * B), mass, pos, ints(keep), mo, po, new, protect=9, first=ints([P] * B))
+    torch.cuda.synchronize()
+    assert new.tolist() == keep and kv.status() == 0
+    assert torch.equal(k[:, shared], k0[:, shared]) and torch.equal(v[:, shared], v0[:, shared])
+    for b, (k1, v1, m1, p1) in enumerate(alone):
+        mine = table[b, P // page:].long()
+        assert torch.equal(k[:, mine], k1[:, mine]) and torch.equal(v[:, mine], v1[:, mine])
+        assert torch.equal(mo[:, b, :, :keep[b]], m1[:, 0, :, :keep[b]]) and torch.equal(po[:, b, :, :keep[b]], p1[:, 0, :, :keep[b]])
+
+
 # ---------------------------------------------------------------------------
 # refusals
 # ---------------------------------------------------------------------------
