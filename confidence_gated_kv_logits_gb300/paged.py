@@ -299,7 +299,8 @@ class PagedKV(_Device):
         """Adds the attention weights of q's rows (lse as ``attend`` gave it) to each
         token's accumulated weight: mass_out = decay mass + gain sum, fp32 [batch,
         kv_heads, cap] (mass_out may be mass).  New tokens start from 0; pos int32
-        likewise receives their positions (int32 [rows]; None: their places)."""
+        likewise receives their positions (int32 [rows]; None: their places).  A drafted
+        tree is weighed behind ``commit``, by its accepted rows alone."""
         if batch._index != self._index:
             raise ValueError("the batch's tensors are on another device")
         rc = _ops.weigh(self._ob, batch._ref, batch.size, batch.mask_rows, layer, q, lse, mass, mass_out, pos, positions,
@@ -321,7 +322,8 @@ class PagedKV(_Device):
 
     def commit(self, page_table, ctx_len, path, path_len, new_len, stream=None):
         """Moves the accepted drafted tokens path [B, cap] (path_len [B] of them)
-        behind the cached ones in every layer; new_len [B] receives ctx_len + path_len."""
+        behind the cached ones in every layer; new_len [B] receives ctx_len + path_len.
+        Masses do not move (``weigh``)."""
         rc = _ops.commit(self._ob, page_table, ctx_len, path, path_len, new_len, stream)
         if rc:
             self._check(rc)
@@ -329,7 +331,7 @@ class PagedKV(_Device):
     def fork(self, parent, beams, table_in, len_in, tail_pages, table_out, len_out, stream=None):
         """Reorders beams: row r of [batch x beams] takes over its parent's pages,
         the part-filled last one as a copy in tail_pages[r].  parent: int32
-        [rows] or [batch, beams]."""
+        [rows] or [batch, beams].  Masses and positions are gathered by the caller."""
         rc = _ops.fork(self._ob, parent, beams, table_in, len_in, tail_pages, table_out, len_out, stream)
         if rc:
             self._check(rc)

@@ -244,7 +244,14 @@ int confkv_paged_attend_shared(confkv_paged* kv, const confkv_paged_batch* batch
  * the running mean over the group's heads that confkv_step ranks by.  Sums are
  * fp32, in one order.  Sequences without new rows stay as they are, as do
  * places from ctx_len + new tokens on.  Places from cap on are dropped
- * (CONFKV_FLAG_CAPACITY).  A NaN in a row that sees a token or in the token's k makes its
+ * (CONFKV_FLAG_CAPACITY).  Every sequence's k is read through its own table from its
+ * first token on, behind a shared prefix too: a page outside the pool, which
+ * attend_shared would not look at, makes its tokens' masses NaN (CONFKV_FLAG_BAD_PAGE).
+ * commit and fork move no masses.  A drafted tree is weighed behind commit, by the
+ * accepted path's rows of q and lse alone (its rows see one another in order, so
+ * without the mask; ctx_len as it was before): weighed before, its drafts' masses would
+ * stay at the drafts' places and rejected ones' weight on the cached tokens.  Behind fork
+ * the caller gathers mass and pos by parent as it does its own states.  A NaN in a row that sees a token or in the token's k makes its
  * mass NaN.
  */
 int confkv_paged_weigh(confkv_paged* kv, const confkv_paged_batch* batch, int layer, int rows, const void* q,
@@ -287,7 +294,8 @@ int confkv_paged_evict(confkv_paged* kv, int batch, int max_blocks, const int32_
  *   path: [B][path_cap], rising (path[b][0] < path[b][1] < ...), path_cap
  *   <= 1024; path_len: [B]; new_len: [B], not ctx_len itself.
  * A sequence whose path is no such path stays as it is, with new_len = ctx_len
- * and a flag.  The pages of the drafted tokens belong to one sequence each.
+ * and a flag.  The pages of the drafted tokens belong to one sequence each.  Masses and
+ * positions of confkv_paged_weigh do not move: weigh the accepted rows afterwards.
  */
 int confkv_paged_commit(confkv_paged* kv, int batch, int max_blocks, const int32_t* page_table,
                         const int32_t* ctx_len, const int32_t* path, int path_cap,
@@ -305,6 +313,7 @@ int confkv_paged_commit(confkv_paged* kv, int batch, int max_blocks, const int32
  * tail_pages are pages that no row of this call reads (free, or of an earlier
  * step), all different, except that tail_pages[r] may be p's own last page if
  * no other row takes it.  table_out and len_out are not table_in and len_in.
+ * Masses and positions of confkv_paged_weigh are gathered by the caller.
  */
 int confkv_paged_fork(confkv_paged* kv, int rows, int beams, int max_blocks, const int32_t* parent,
                       const int32_t* table_in, const int32_t* len_in, const int32_t* tail_pages,

@@ -4,8 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_paged_budget_gpu import check_append
-from tests.test_paged_gpu import DT, Case, ints
+from tests.test_paged_budget_gpu import Grouped, check_append, run_shared, run_weigh, weigh_reference
+from tests.test_paged_gpu import DT, Case, ints, mask_words, reference, tree_bits
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -119,6 +119,57 @@ def test_attend_shared_right_behind_what_wrote_its_inputs(pkg, dt, heads, H, d, 
             assert torch.equal(x, y)
     assert kv.status() == 0
     assert all(torch.isfinite(x).all() for w in want for x in (w[0], w[1]))
+
+
+# ---------------------------------------------------------------------------
+# accumulated weights
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("heads,H,d,page,T", [(40, 8, 128, 32, 12), (12, 12, 64, 16, 40)])
+def test_weigh_the_accepted_rows_behind_commit(pkg, dt, heads, H, d, page, T):
+    """Trees of drafts are attended by their mask, a path of each is kept, and its rows, gathered, are weighed without the
+    mask: the places that they came to hold hold their masses and positions."""
+    c = Case(DT[dt], heads, H, d, page, [200, 0, 33, 129], [T, T, 0, T - 3], seed=T)
+    bits = tree_bits(c.new, 3)
+    mask = mask_words(bits + [0] * (c.rows - len(bits)), -(-T // 32))
+    kv = pkg.PagedKV(c.k, c.v, heads)
+    out, lse = torch.empty_like(c.q), torch.empty(c.rows, heads, device=DEV)
+    kv.attend(1, c.batch(kv, mask), c.q, out, lse=lse)
+    paths = [[j for j in range(T) if t and bits[c.starts[b] + t - 1] >> j & 1] for b, t in enumerate(c.new)]     # to the last draft
+    assert any(1 < len(p) < t for p, t in zip(paths, c.new))
+    new_len = ints([0] * 4)
+    kv.commit(c.table, ints(c.ctx), ints([p + [0] * (T - len(p)) for p in paths]), ints([len(p) for p in paths]), new_len)
+    rows = torch.tensor([c.starts[b] + j for b, p in enumerate(paths) for j in p], device=DEV)
+    c.new = [len(p) for p in paths]
+    c.starts = [sum(c.new[:b]) for b in range(5)]
+    c.rows, c.q = c.starts[-1], c.q[rows]
+    _, kv = run_weigh(pkg, c, lse=lse[rows], kv=kv)
+    assert new_len.tolist() == [a + t for a, t in zip(c.ctx, c.new)] and kv.status() == 0
+    # and it is what attention of the committed rows gives
+    again, lse2 = torch.empty_like(c.q), torch.empty(c.rows, heads, device=DEV)
+    kv.attend(1, c.batch(kv), c.q, again, lse=lse2)
+    _, l, _, tol = reference(c)
+    for x in (lse2, lse[rows]):
+        assert ((x.double() - l).abs() <= tol).all()
+
+
+def test_weigh_reads_every_sequences_own_pages(pkg):
+    """Behind a prefix whose pages the others' tables do not name, attend has what it needs and weigh does not: flagged, NaN."""
+    c = Grouped(torch.bfloat16, 8, 2, 128, 32, [(3, 300)], [9], [2], seed=12)
+    o, l, tol, _ = reference(c)
+    kept = c.table.clone()
+    c.table[1:, :8] = -5                               # 256 of the prefix's 300 tokens
+    out, lse, kv = run_shared(pkg, c)
+    assert kv.status() == 0
+    mass = torch.rand(3, 2, 330, generator=c.g, device=DEV)
+    before = mass.clone()
+    kv.weigh(1, c.batch(kv), c.q, lse, mass, mass, decay=0.75, gain=0.5)
+    assert kv.status(check=False) == 8
+    assert mass[1:, :, :256].isnan().all()
+    c.table = kept
+    want, tol = weigh_reference(c, lse[:c.starts[-1]], before, 0.75, 0.5)
+    assert ((mass.double() - want).abs()[:1] <= tol[:1]).all()
+    assert ((mass.double() - want).abs()[1:, :, 256:] <= tol[1:, :, 256:]).all()
 
 
 # ---------------------------------------------------------------------------
