@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_paged_budget_gpu import Grouped, check_append, run_shared, run_weigh, weigh_reference
+from tests.test_paged_budget_gpu import Grouped, check_append, check_shared, run_shared, run_weigh, weigh_reference
 from tests.test_paged_gpu import DT, Case, ints, mask_words, reference, tree_bits
 
 pytestmark = pytest.mark.gpu
@@ -121,6 +121,47 @@ def test_attend_shared_right_behind_what_wrote_its_inputs(pkg, dt, heads, H, d, 
     assert all(torch.isfinite(x).all() for w in want for x in (w[0], w[1]))
 
 
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("heads,H,d,page,groups,tail,new", [
+    # by the rows of a KV head, on average (152 SMs): from 257 on tiles of 256 rows, if there are 76 or more
+    (64, 8, 64, 64, [(8, 700), (9, 520), (7, 260)], [0, 33, 300], [12]),                # phase 1; phase 2 in tiles of 128
+    (40, 8, 128, 32, [(5, 400), (7, 130), (6, 900), (5, 128), (8, 0), (3, 640)], [5, 140], [12, 11, 13]),
+    (40, 8, 128, 64, [(4, 300), (4, 500)], [10, 200], [60, 61, 55]),                    # both phases
+    (16, 16, 64, 16, [(3, 256), (2, 390)], [7], [300, 120, 200]),
+    # from 32 sequences on phase 2 by CTAs of four warps
+    (12, 12, 64, 16, [(40, 300)], [0, 5, 200], [1]),
+    (40, 8, 128, 64, [(30, 512), (3, 200), (20, 128)], [1, 90, 400], [1, 2, 0, 8]),
+    (16, 1, 128, 256, [(33, 1000)], [3, 600], [1, 2])])
+def test_attend_shared_every_form(pkg, dt, heads, H, d, page, groups, tail, new):
+    c = Grouped(DT[dt], heads, H, d, page, groups, tail, new, seed=heads + len(groups))
+    first = run_shared(pkg, c)
+    check_shared(c, first, reference(c))
+    bits = tree_bits(c.new, 2)
+    check_shared(c, run_shared(pkg, c, bits, kv=first[2]), reference(c, bits=bits))
+    assert first[2].status() == 0
+
+
+def test_attend_shared_repeats_itself_between_other_calls(pkg):
+    """The same bits on every run, whatever ran before on the same handle and scratch."""
+    cases = [Grouped(DT[dt], 40, 8, 128, 64, g, [7, 300], n, seed=i)
+             for i, (dt, g, n) in enumerate([("bf16", [(4, 1000)], [1]), ("fp16", [(64, 2000)], [1]), ("bf16", [(8, 2000), (3, 640)], [12]),
+                                             ("bf16", [(3, 1200), (2, 200)], [90])])]
+    calls = []
+    for c in cases:
+        kv = pkg.PagedKV(c.k, c.v, 40)
+        prefix, batch = kv.prefix(c.starts_of_groups(), ints(c.prefixes), c.rows), c.batch(kv)
+        calls.append(lambda out, lse, c=c, kv=kv, prefix=prefix, batch=batch: kv.attend(1, batch, c.q, out, lse=lse, prefix=prefix))
+    want = []
+    for c, call in zip(cases, calls):
+        want.append((torch.zeros_like(c.q), torch.zeros(c.rows, 40, device=DEV)))
+        call(*want[-1])
+        torch.cuda.synchronize()
+    for i in np.random.default_rng(0).integers(0, len(cases), 300).tolist():
+        out, lse = torch.zeros_like(cases[i].q), torch.zeros(cases[i].rows, 40, device=DEV)
+        calls[i](out, lse)
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
 # ---------------------------------------------------------------------------
 # accumulated weights
 # ---------------------------------------------------------------------------
@@ -231,6 +272,79 @@ def test_evict_behind_a_shared_prefix(pkg, keep, in_place):
         mine = table[b, P // page:].long()
         assert torch.equal(k[:, mine], k1[:, mine]) and torch.equal(v[:, mine], v1[:, mine])
         assert torch.equal(mo[:, b, :, :keep[b]], m1[:, 0, :, :keep[b]]) and torch.equal(po[:, b, :, :keep[b]], p1[:, 0, :, :keep[b]])
+
+
+def evict_want(k, v, table, length, mass, pos, keep, protect, first, page):
+    """Head by head on the GPU: a stable sort by class and mass."""
+    k, v, mo, po = k.clone(), v.clone(), {}, {}
+    L, B, H, cap = mass.shape
+    for l in range(L):
+        for b in range(B):
+            n, N = length[b], min(length[b], keep[b])
+            t, j = table[b].long(), torch.arange(n, device=DEV)
+            for h in range(H):
+                m, p = mass[l, b, h, :n], pos[l, b, h, :n]
+                rank = torch.where(p > (p.max() if n else 0) - protect, 1e200, m.double())
+                rank = torch.where(j < (first[b] if first else 0), 1e300, rank)
+                kept = torch.zeros(n, dtype=torch.bool, device=DEV)
+                kept[rank.sort(descending=True, stable=True).indices[:N]] = True
+                to, fr = (~kept & (j < N)).nonzero()[:, 0], (kept & (j >= N)).nonzero()[:, 0]
+                source = j[:N].clone()
+                source[to] = fr
+                mo[l, b, h], po[l, b, h] = m[source], p[source]
+                for pool in (k, v):
+                    pool[l, t[to // page], h, to % page] = pool[l, t[fr // page], h, fr % page]
+    return k, v, mo, po
+
+
+# Units x places decide the kernel's form (152 SMs): 1024 threads up to a unit an SM above 2500 places, else 256; positions in
+# shared memory up to 4096, masses up to 40960, moves listed in one go up to 8192 beyond.
+LONG, MIXED = [45000], [4100, 0, 9, 300, 4099, 2500, 4097, 1, 33, 3000]
+EVICTS = [
+    # d, page, L, B, H, lengths, budgets, cap, first
+    (64, 32, 2, 10, 8, MIXED, [1000, 5, 4, 299, 4090, 2499, 2048, 1, 1, 2999], 4100, None),           # 160 units of 256 threads
+    (128, 64, 2, 10, 8, MIXED, [4000, 5, 4, 100, 4098, 1, 17, 1, 32, 1500], 4100, [40] * 10),
+    (64, 256, 1, 40, 4, [41000] + [200, 77, 1500] * 13, [20000] + [100, 70, 1499] * 13, 41001, None),    # and masses read again
+    (128, 256, 1, 40, 4, [20500] + [200, 77, 1500] * 13, [20495] + [100, 76, 3] * 13, 41001, [3] * 40),
+    (128, 128, 1, 3, 2, [4000, 2700, 3999], [1000, 2695, 3998], 4000, [128, 0, 5]),                      # 1024 threads
+    (128, 128, 1, 2, 1, [9000, 5000], [4000, 4995], 9001, None),
+    (128, 256, 1, 1, 1, LONG, [22000], 45001, [7]),                                                      # more moves than a list holds
+    (64, 256, 1, 1, 2, LONG, [30000], 45001, None)]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("alike", [False, True])
+@pytest.mark.parametrize("case", range(len(EVICTS)))
+def test_evict_every_form(pkg, case, alike, in_place):
+    d, page, L, B, H, length, keep, cap, first = EVICTS[case]
+    g = torch.Generator(device=DEV).manual_seed(case)
+    blocks = [-(-n // page) for n in length]
+    pages = sum(blocks) + 1
+    k, v = (torch.randn(L, pages, H, page, d, generator=g, device=DEV).to(torch.bfloat16 if case % 2 else torch.float16) for _ in range(2))
+    order = torch.randperm(pages, generator=g, device=DEV).tolist()
+    table = ints([[order.pop() for _ in range(n)] + [-1] * (max(blocks) - n) for n in blocks])
+    mass = torch.rand(L, B, H, cap, generator=g, device=DEV)
+    if alike:                                          # a few different masses: ties by the lower place
+        mass = (mass * 3).floor() * 0.5
+    pos = torch.rand(L, B, H, cap, generator=g, device=DEV).argsort(3).int()
+    want = evict_want(k, v, table, length, mass, pos, keep, 20, first, page)
+    kv = pkg.PagedKV(k, v, H)
+    mass0, pos0 = mass.clone(), pos.clone()
+    mo, po = (mass, pos) if in_place else (torch.full_like(mass, -5), torch.full_like(pos, -5))
+    new = ints([-7] * B)
+    kv.evict(table, ints(length), mass, pos, ints(keep), mo, po, new, protect=20, first=ints(first) if first else None)
+    torch.cuda.synchronize()
+    assert new.tolist() == [min(n, x) for n, x in zip(length, keep)] and kv.status() == 0
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+    for (l, b, h), m in want[2].items():
+        n = len(m)
+        assert torch.equal(mo[l, b, h, :n], m) and torch.equal(po[l, b, h, :n], want[3][l, b, h])
+        if in_place:
+            assert torch.equal(mo[l, b, h, n:], mass0[l, b, h, n:]) and torch.equal(po[l, b, h, n:], pos0[l, b, h, n:])
+        else:
+            assert (mo[l, b, h, n:] == -5).all() and (po[l, b, h, n:] == -5).all()
+    if not in_place:
+        assert torch.equal(mass, mass0) and torch.equal(pos, pos0)
 
 
 # ---------------------------------------------------------------------------
