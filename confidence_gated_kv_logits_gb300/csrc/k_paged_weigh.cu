@@ -42,7 +42,7 @@ constexpr int kThreads = 4 * 128 + 4 * 32;      // (a 21st warp would leave each
 constexpr int BT = 128;                   // tokens of a tile (kManyBlock: the boxes are attend's)
 constexpr int BR = 112;                   // most query rows of a tile (three tiles of 128 beside four of K leave no room)
 constexpr float kL2E = 1.4426950408889634f;
-constexpr int kFixed = 2;                 // an item's fixed cost in tiles of rows: its K from memory
+constexpr int kFixed = 2;                 // an item's fixed cost in tiles of rows: its K from memory (1 and 4: the same times within 1%)
 constexpr int kPlan = 8;                  // items in the planned ring
 constexpr int kReaders = 19;              // warps that read it
 
@@ -640,10 +640,14 @@ cudaError_t launch_weigh(const Pool& p, const WeighArgs& a, const AttendMaps& m,
     const cudaError_t e = encode_map(x.map, p.bf16, 3, const_cast<uint16_t*>(a.q), dims, strides, box, false);
     if (e != cudaSuccess) return e;
   }
-  // Token tiles of an item: one where each finds a CTA of its own, two where there are not many to a CTA, then more, so
-  // that an item's cost is spread (the tables' width is what the host knows of the lengths).
+  // Token tiles of an item: one where each finds a CTA of its own, then as many as leave a CTA several items, so that an
+  // item's fixed cost is spread (the tables' width is what the host knows of the lengths).  us with one, two, four and
+  // eight tiles an item, by the tiles to a CTA: 1.3 (1 x 2048 tokens, 12/12 heads of 64) 6.6, 6.5, 6.8, 8.1; 3.4 (16 x 500,
+  // 40/8 of 128) 10.1, 8.0, 7.3, 7.3; 6.7 (4 x 4000) 14.6, 11.4, 10.3, 10.2; 13 (8 x 4000, 64/8 of 64) 23.4, 15.0, 13.3,
+  // 12.1; 27 (32 x 2000) 41.4, 24.8, 19.1, 18.8; 210 (32 x up to 16384) 154, 85, 65, 57; with 80 rows, 20 (4 x 12000,
+  // 40/8 of 128) 37.7, 25.3, 22.0, 22.5.
   const long long tiles = static_cast<long long>(a.bt.B) * p.Hkv * ((static_cast<long long>(a.bt.max_blocks) * p.ps + BT - 1) / BT);
-  const int sh1 = tiles <= ctas ? 0 : tiles < 16ll * ctas ? 1 : tiles < 64ll * ctas ? 2 : 3;
+  const int sh1 = tiles <= ctas ? 0 : tiles < 2ll * ctas ? 1 : tiles < 6ll * ctas ? 2 : 3;
   const cudaError_t e = each_weigh([&](auto kernel, bool bf, int d, int smem) {
     if (bf != (p.bf16 != 0) || d != p.d) return cudaSuccess;
     return launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem + sizeof(Shared), s, p, a, sh1, m.k_many, mq);
