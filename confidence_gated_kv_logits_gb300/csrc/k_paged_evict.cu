@@ -66,6 +66,14 @@ __device__ __forceinline__ int scan(int x, int* s_warp, int& all) {
   return before + incl - x;
 }
 
+// n places as they are (out of line: the kernel's registers are the other paths')
+__device__ __noinline__ void pass_on(const float* mass, const int32_t* pos, float* mass_out, int32_t* pos_out, int n) {
+  for (int j = threadIdx.x; j < n; j += blockDim.x) {
+    mass_out[j] = mass[j];
+    pos_out[j] = pos[j];
+  }
+}
+
 // One CTA: a KV head of a sequence in a layer.  KEYS: its keys lie in shared memory, and its positions too
 // where that leaves room for as many CTAs (else they are read again wherever they are needed).
 // T: threads, 256 or, where there are fewer units than SMs, 1024.
@@ -96,18 +104,15 @@ k_evict(const Pool p, const EvictArgs a) {
     if (h == 0 && (a.per_layer || l == 0)) a.new_len[seq] = N;
     s_top = INT32_MIN;
   }
+  if (flag) {                           // such a sequence stays as it is, its masses in the outputs too
+    if (a.mass_out != a.mass) pass_on(a.mass + unit * a.cap, a.pos + unit * a.cap, a.mass_out + unit * a.cap, a.pos_out + unit * a.cap, min(n, a.cap));
+    return;
+  }
   const float* mass = a.mass + unit * a.cap;
   const int32_t* pos = a.pos + unit * a.cap;
   float* mass_out = a.mass_out + unit * a.cap;
   int32_t* pos_out = a.pos_out + unit * a.cap;
   const bool copy = mass_out != mass;
-  if (flag) {                           // such a sequence stays as it is, its masses in the outputs too
-    for (int j = tid; copy && j < min(n, a.cap); j += kThreads) {
-      mass_out[j] = mass[j];
-      pos_out[j] = pos[j];
-    }
-    return;
-  }
   const int32_t* table = a.table + static_cast<size_t>(b) * a.max_blocks;
   const int layer = l * p.NP;           // (rows of a pool stay below 2^31)
   constexpr int LR = D / 8;             // lanes of a row, K's and then V's
