@@ -33,7 +33,11 @@ constexpr int kList = 8192;             // moves at a time beyond
 constexpr int kFew = 8;                 // evicted places that are found one by one, a warp each
 // Places (of the mass's rows) from which on units that leave SMs idle are worth 1024 threads instead of 256.  us, 256 and
 // 1024: 8 units of 1500 places, 1000 kept, 14.9, 16.6; of 4000, 1000 kept, 24.8, 22.7; of 16000, 2000 kept, 66.6, 44.0; 64
-// of 4000 42.3, 27.5; 152 of 10000, 5000 kept, 137.5, 89.8; 64 of 2049, one evicted, 4.2, 5.3.
+// of 4000 42.3, 27.5; 152 of 10000, 5000 kept, 137.5, 89.8; 64 of 2049, one evicted, 4.2, 5.3.  With more units than SMs
+// four CTAs of 256 do more than one of 1024 while shared memory holds them: 160 of 4000, 1000 kept, 51.4, 65.4; of 10000,
+// 5000 kept, 143, 156; 304 of 16000, 2000 kept, 182, 150.  From some 20000 places on it holds two at most, and 256 are the
+// slower ones (160 of 30000, half kept, 674, 398; 608 of 45000, 4000 kept, 1833, 689) but for rows that are far longer
+// than their sequences (160 of 1000 in 30000 20, 27; 304 in 100000 17, 29), which the host cannot tell: left as it is.
 constexpr int kWide = 2500;
 
 // A mass as an unsigned number in the same order; NaN below everything, -0 as 0.

@@ -176,6 +176,9 @@ cudaError_t device_ready(int dev, Limits* limits) {
 // the scratch take 3 to 4, but holds 96 of 152 SMs at worst, so it is for units
 // that all run at once and sequences that cannot be long (a table's width is
 // what the host knows): from 9 chunks (below, one CTA does) to 16 a warp.
+// Behind a shared prefix the width holds the prefix too, which says little of the tokens that phase 2 has left; us, cut
+// against clusters: 12/12 heads of 64, 4 x 300 own tokens behind 1000 10.6, 15.6; 3000 own 24.6, 21.7; 40/8 heads of 128,
+// 2 x 300 behind 300 12.0, 12.8; 1500 own 22.3, 13.3; 1 x 300 behind 4000 14.7, 19.5; 3000 own 25.9, 21.6.
 // One row, us, cut against clusters: 12/12 heads of 64, 1 x 512 tokens 8.5, 7.6;
 // 1 x 2048 10.6, 8.5; 1 x 16384 18.5, 16.7; 2 x 4000 13.6, 11.1; 40/8 heads of 128,
 // 1 x 1024 12.1, 9.1; 1 x 8192 19.0, 17.0; 1 x 16384 24.9, 24.9; 4 x 2000 18.3,
@@ -293,8 +296,12 @@ cudaError_t attend(const confkv_paged& kv, const AttendArgs& a, int batch, cudaS
   //    last CTA of each unit, 42)
   const int64_t heads = static_cast<int64_t>(a.rows) * p.g, per = heads / batch;
   //  - behind a shared prefix, where sequences have few tokens of their own, the streaming kernel up to 40 rows in its tiles
-  //    of 16 (two groups of 8 sequences of 300 own tokens behind 6000, 64/8 heads, d = 64: 18 rows 30 streamed, 43; 36 rows
-  //    40, 46; 72 rows 52, 48; of 2000 own tokens 36 rows 49, 47)
+  //    of 16.  Neither is the faster one throughout: few or ragged units leave the prompt kernel's SMs idle, many or long
+  //    ones are faster there from 20 to 30 rows on.  Streamed and in padded tiles: 32/4 heads of 64, 11 ragged sequences of
+  //    up to 400 own tokens, 32 rows 28.1, 40.1; 40/8 of 128, 5 ragged of up to 1000, 25 rows 43.5, 53.1; 3, 23 rows 27.9,
+  //    45.9; 64/8 of 64, two groups of 4 of 300 own behind 6000, 18 rows 27.7, 32.2, 40 rows 43.0, 40.4; two of 8, 18 rows
+  //    43.2, 39.1, 32 rows 51.5, 38.8; two of 32, 18 rows 70.4, 83.4, 40 rows 116, 114; two of 8 of 2000 own, 32 rows 66.4,
+  //    57.1; 72 rows 52, 48
   if (per <= (a.bt.phase == 2 ? 40 : kFewRows)) {
     // at most (a row's heads fill one tile, or its sequence's last is part-filled)
     const int64_t units = p.Hkv * std::min<int64_t>(static_cast<int64_t>(a.rows) * ((p.g + kFewRows - 1) / kFewRows),

@@ -306,6 +306,8 @@ EVICTS = [
     (128, 64, 2, 10, 8, MIXED, [4000, 5, 4, 100, 4098, 1, 17, 1, 32, 1500], 4100, [40] * 10),
     (64, 256, 1, 40, 4, [41000] + [200, 77, 1500] * 13, [20000] + [100, 70, 1499] * 13, 41001, None),    # and masses read again
     (128, 256, 1, 40, 4, [20500] + [200, 77, 1500] * 13, [20495] + [100, 76, 3] * 13, 41001, [3] * 40),
+    (64, 256, 1, 40, 4, [20000] + [9999, 77, 1500] * 13, [9000] + [5000, 70, 1499] * 13, 20000, None),   # and masses in shared memory
+    (128, 256, 1, 40, 4, [20001] + [9999, 77, 1500] * 13, [9000] + [5000, 70, 1499] * 13, 20001, [3] * 40),
     (128, 128, 1, 3, 2, [4000, 2700, 3999], [1000, 2695, 3998], 4000, [128, 0, 5]),                      # 1024 threads
     (128, 128, 1, 2, 1, [9000, 5000], [4000, 4995], 9001, None),
     (128, 256, 1, 1, 1, LONG, [22000], 45001, [7]),                                                      # more moves than a list holds
