@@ -1,5 +1,7 @@
 """Normed appends, attention over shared prefixes, accumulated weights and eviction where calls meet the ends
 of their ranges and one another.  Tolerances: those of test_paged_budget_gpu.py."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -347,6 +349,196 @@ def test_evict_every_form(pkg, case, alike, in_place):
             assert (mo[l, b, h, n:] == -5).all() and (po[l, b, h, n:] == -5).all()
     if not in_place:
         assert torch.equal(mass, mass0) and torch.equal(pos, pos0)
+
+
+# ---------------------------------------------------------------------------
+# the oddest batches, all four
+# ---------------------------------------------------------------------------
+def lost_rows(c, sequences):
+    lost = torch.zeros(c.starts[-1], dtype=torch.bool, device=DEV)
+    for b in sequences:
+        lost[c.starts[b]:c.starts[b + 1]] = True
+    return lost
+
+
+def check_but(c, got, want, lost):
+    """Lost rows are NaN, the others within the tolerance."""
+    n = c.starts[-1]
+    assert got[0][:n][lost].isnan().all() and got[1][:n][lost].isnan().all()
+    out, lse = got[0].clone(), got[1].clone()
+    out[:n][lost], lse[:n][lost] = want[0][lost].to(c.dt), want[1][lost].float()
+    check_shared(c, (out, lse), want)
+
+
+FORMS = {    # heads, kv heads, d, page, groups, tails, new rows
+    "clusters": (12, 12, 64, 16, [(2, 300), (2, 130)], [20, 40], [1]),
+    "four warps": (40, 8, 128, 32, [(20, 256), (14, 400)], [5, 60], [1]),
+    "cut": (16, 2, 64, 16, [(2, 6000), (1, 700)], [17, 900], [1]),
+    "tiles": (40, 8, 128, 64, [(3, 900), (2, 300)], [30, 200], [25, 31]),
+    "two tiles": (64, 8, 64, 64, [(8, 700), (9, 520), (7, 260)], [0, 33], [12])}
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("form", list(FORMS))
+def test_attend_shared_over_bad_pages(pkg, form, dt):
+    """A page of a group's prefix that is none voids the group, one of a sequence's own tokens that sequence."""
+    heads, H, d, page, groups, tail, new = FORMS[form]
+    c = Grouped(DT[dt], heads, H, d, page, groups, tail, new, seed=3)
+    want, first = reference(c), groups[0][0]
+    kept = c.table.clone()
+    c.table[first, 1] = 1 << 30                        # the second group's prefix, by the table of its first sequence
+    c.table[1, (c.ctx[1] + c.new[1] - 1) // page] = -1     # the last page of sequence 1
+    got = run_shared(pkg, c)
+    assert got[2].status(check=False) == pkg.FLAG_BAD_PAGE
+    check_but(c, got, want, lost_rows(c, [1] + list(range(first, first + groups[1][0]))))
+    c.table = kept
+    check_shared(c, run_shared(pkg, c, kv=got[2]), want)   # nothing stays behind
+    assert got[2].status() == 0
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("form", list(FORMS))
+def test_attend_shared_infinite_values(pkg, form, dt):
+    """Infinities in V of the prefix, of own tokens and of drafts that some rows do not see reach the rows that see them alone."""
+    heads, H, d, page, groups, tail, new = FORMS[form]
+    c = Grouped(DT[dt], heads, H, d, page, groups, tail, new, seed=4)
+    for b, j, ch in ((0, 7, 3), (groups[0][0], groups[1][1] // 128 * 128 - 1, 5), (1, c.ctx[1], 9), (1, c.ctx[1] - 1, 11)):
+        c.v[:, int(c.table[b, j // page]), H - 1, j % page, ch] = math.inf if ch != 5 else -math.inf
+    check_shared(c, run_shared(pkg, c), reference(c))
+    bits = tree_bits(c.new, 6)
+    check_shared(c, run_shared(pkg, c, bits), reference(c, bits=bits))
+
+
+@pytest.mark.parametrize("where", ["prefix", "own"])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_attend_shared_huge_scores_leave_the_largest(pkg, form, where):
+    """Scores of 1e10, the next lower one a hundredth of it away or further: one token, of the prefix or of the sequence's own
+    cached ones, has all the weight."""
+    heads, H, d, page, groups, tail, new = FORMS[form]
+    most = 6e4
+    c = Grouped(torch.bfloat16, heads, H, d, page, groups, [x + 3 for x in tail], new, seed=5)
+    P = [p for n, p in groups for _ in range(n)]
+    best = []
+    for b, (a, t) in enumerate(zip(c.ctx, c.new)):
+        size = -most * torch.arange(1, a + t + 1, dtype=torch.float64) / (a + t) * 0.5
+        best.append(P[b] // 2 if where == "prefix" else P[b] + 1)
+        size[best[-1]] = most
+        if where == "own":
+            size[P[b] // 2] = most / 2
+        at = torch.arange(a + t, device=DEV)
+        c.k[:, c.table[b].long()[at // page], :, at % page] = size.to(c.dt).to(DEV)[None, :, None, None].expand(2, -1, H, d).transpose(0, 1)
+    # (the groups' prefixes are written by each of their sequences: alike but for the rest of negative sizes)
+    c.q[:] = most
+    out, lse, kv = run_shared(pkg, c)
+    for b, (a, t) in enumerate(zip(c.ctx, c.new)):
+        v = c.get(c.v, 1, b, a + t)[best[b]].repeat_interleave(heads // H, 0)
+        assert torch.equal(out[c.starts[b]:c.starts[b + 1]], v[None].expand(t, -1, -1))
+        z = float(torch.tensor(most, dtype=c.dt)) ** 2 * d ** 0.5
+        assert torch.allclose(lse[c.starts[b]:c.starts[b + 1]].double(), torch.full((t, heads), z, dtype=torch.float64, device=DEV), rtol=(d + 4) * 2.0 ** -23, atol=0)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("heads,H,d,ctx,new,blocks,prefix", [
+    (12, 12, 64, 300, 1, 17, 256), (12, 12, 64, 300, 1, 16, 256), (40, 8, 128, 250, 40, 16, 250), (16, 1, 64, 600, 3, 8, 500), (40, 8, 128, 128, 300, 9, 128)])
+def test_attend_shared_and_weigh_past_the_page_table(pkg, dt, heads, H, d, ctx, new, blocks, prefix):
+    """Sequences longer than their table end where it does, whatever of that is the prefix."""
+    c = Grouped(DT[dt], heads, H, d, 16, [(2, prefix)], [ctx - prefix], [new], seed=blocks)
+    cap = 16 * blocks
+    kv = pkg.PagedKV(c.k, c.v, heads)
+    batch = kv.batch(c.table[:, :blocks].contiguous(), ints(c.ctx), ints(c.starts))
+    out, lse = (torch.full((c.rows, heads, *x), 7.0, dtype=y, device=DEV) for x, y in (((d,), c.dt), ((), torch.float32)))
+    kv.attend(1, batch, c.q, out, lse=lse, prefix=kv.prefix(ints([0, 2]), ints([prefix]), c.rows))
+    assert kv.status(check=False) == pkg.FLAG_CAPACITY
+    # the same rows over the tokens that there are: drafts behind the table's end are seen by none
+    seen = max(0, cap - c.ctx[0])
+    if c.ctx[0] >= cap:                                # cached tokens alone, all rows alike
+        c.ctx = [cap] * 2
+        want = reference(c, bits=[0] * c.starts[-1])
+    else:
+        want = reference(c, bits=[(1 << min(i + 1, seen)) - 1 for t in c.new for i in range(t)])
+    check_shared(c, (out, lse), want)
+    mass = torch.full((2, H, ctx + new), 3.0, device=DEV)
+    kv.weigh(1, batch, c.q, lse, mass, mass, decay=0.0, gain=1.0)
+    assert kv.status(check=False) == pkg.FLAG_CAPACITY
+    assert (mass[:, :, cap:] == 3).all()
+    # each row's weights sum to 1, within twice 2 ds, of the weights and of lse: scale sum |q k| is 12 at most for these rows
+    # (its mean is 7.2 at d = 128, 5.1 at 64, six deviations 4.6), 4 (d + 4) 2^-23 12 < 2^-10, the sums' roundings far below
+    total = mass[:, :, :cap].double().sum(2)
+    assert ((total - new * (heads // H)).abs() <= 2.0 ** -9 * new * (heads // H)).all()
+
+
+@pytest.mark.parametrize("new", [[1, 0, 2], [40, 70, 0]])
+def test_rows_before_the_first_sequence_are_left_as_they_were(pkg, new):
+    c = Grouped(torch.bfloat16, 8, 2, 64, 16, [(2, 256), (1, 130)], [9, 30], new, seed=5)
+    n, lead = c.starts[-1], 5
+    q = torch.cat([c.randn(lead, 8, 64), c.q])
+    want = reference(c)
+    kv = pkg.PagedKV(c.k, c.v, 8)
+    batch = kv.batch(c.table, ints(c.ctx), ints([lead + x for x in c.starts]))
+    out, lse = torch.full_like(q, 7), torch.full(q.shape[:2], 7.0, device=DEV)
+    kv.attend(1, batch, q, out, lse=lse, prefix=kv.prefix(c.starts_of_groups(), ints(c.prefixes), len(q)))
+    assert (out[:lead] == 7).all() and (lse[:lead] == 7).all()
+    check_shared(c, (out[lead:], lse[lead:]), want)
+    mass = torch.rand(3, 2, 400, generator=c.g, device=DEV)
+    before, where = mass.clone(), torch.full((3, 2, 400), -9, dtype=torch.int32, device=DEV)
+    given = torch.randint(0, 1000, (len(q),), device=DEV, dtype=torch.int32)
+    kv.weigh(1, batch, q, lse, mass, mass, where, positions=given, decay=0.75, gain=0.5)
+    w, tol = weigh_reference(c, lse[lead:lead + n], before, 0.75, 0.5)
+    assert ((mass.double() - w).abs() <= tol).all()
+    for b, (a, t) in enumerate(zip(c.ctx, new)):
+        assert (where[b, :, a:a + t] == given[lead + c.starts[b]:lead + c.starts[b + 1]]).all()
+        assert (where[b, :, :a] == -9).all() and (where[b, :, a + t:] == -9).all()
+    k, v, q_out, w = c.randn(len(q), 2, 64), c.randn(len(q), 2, 64), torch.full_like(q, 7), torch.ones(64, device=DEV)
+    k0 = c.k.clone()
+    kv.append(0, batch, k, v, q=q, q_out=q_out, q_norm=w, k_norm=w)
+    assert (q_out[:lead] == 7).all() and (q_out[lead + n:] == 7).all() and not (q_out[lead:lead + n] == 7).all(2).any()
+    for b, (a, t) in enumerate(zip(c.ctx, new)):
+        at = torch.arange(a, a + t, device=DEV)
+        assert torch.equal(c.get(c.v, 0, b, a + t)[a:], v[lead + c.starts[b]:lead + c.starts[b + 1]])
+        k0[0, c.table[b].long()[at // 16], :, at % 16] = c.k[0, c.table[b].long()[at // 16], :, at % 16]
+    assert torch.equal(c.k.view(torch.int16), k0.view(torch.int16)) and kv.status() == 0
+
+
+@pytest.mark.parametrize("t", [40, 70])
+def test_drafts_past_the_masks_words_are_seen_by_no_row(pkg, t):
+    c = Grouped(torch.float16, 6, 2, 64, 16, [(3, 200)], [10], [t], seed=t)
+    bits = [(1 << 32) - 1] * (3 * t)
+    kv = pkg.PagedKV(c.k, c.v, 6)
+    batch = kv.batch(c.table, ints(c.ctx), ints(c.starts), mask_words(bits + [0] * 3, 1))
+    out, lse = torch.full_like(c.q, 7), torch.full((c.rows, 6), 7.0, device=DEV)
+    kv.attend(1, batch, c.q, out, lse=lse, prefix=kv.prefix(c.starts_of_groups(), ints(c.prefixes), c.rows))
+    check_shared(c, (out, lse), reference(c, bits=bits))
+    mass = torch.rand(3, 2, 210 + t, generator=c.g, device=DEV)
+    before = mass.clone()
+    kv.weigh(1, batch, c.q, lse, mass, mass, decay=0.5, gain=1.0)
+    w, tol = weigh_reference(c, lse[:3 * t], before, 0.5, 1.0, bits)
+    assert ((mass.double() - w).abs() <= tol).all()
+    assert (mass[:, :, 210 + 32:] == 0).all() and kv.status() == 0
+
+
+def test_append_normed_bad_pages_and_lengths(pkg):
+    """Rows whose place is none are not stored, their queries are; flags as of append."""
+    c = Case(torch.float16, 8, 2, 128, 16, [20, 14, 40, 100], [3, 4, 1, 2], seed=9, extra_rows=1)
+    kv = pkg.PagedKV(c.k, c.v, 8)
+    wq, wk = (1 + 0.1 * torch.randn(128, generator=c.g, device=DEV) for _ in range(2))
+    q, k, v = c.randn(c.rows, 8, 128), c.randn(c.rows, 2, 128), c.randn(c.rows, 2, 128)
+    inv = torch.rand(32, generator=c.g, device=DEV)
+    pos, axis = torch.randint(0, 999, (c.rows, 2), generator=c.g, device=DEV, dtype=torch.int32), (torch.arange(32, device=DEV) % 2).int()
+    want = torch.zeros_like(q)
+    kv.append(0, c.batch(kv), k, v, q=q, q_out=want, positions=pos, inv_freq=inv, q_norm=wq, k_norm=wk, axis=axis)
+    assert kv.status() == 0
+    c.table[1, 1] = c.k.shape[1]                       # sequence 1: places 14, 15 and 16, 17
+    k0, v0 = c.k.clone(), c.v.clone()
+    out = torch.zeros_like(q)
+    kv.append(1, kv.batch(c.table[:, :4].contiguous(), ints([20, 14, -1, 100]), ints(c.starts)), k, v, q=q, q_out=out, positions=pos, inv_freq=inv,
+              q_norm=wq, k_norm=wk, axis=axis)
+    assert kv.status(check=False) == pkg.FLAG_BAD_PAGE | 16 | pkg.FLAG_CAPACITY
+    assert torch.equal(out, want)
+    for b, i, at in ((0, 0, 20), (0, 1, 21), (0, 2, 22), (1, 0, 14), (1, 1, 15)):
+        pg = int(c.table[b, at // 16])
+        assert torch.equal(c.v[1, pg, :, at % 16], v[c.starts[b] + i]) and torch.equal(c.k[1, pg, :, at % 16], c.k[0, pg, :, at % 16])
+        k0[1, pg, :, at % 16], v0[1, pg, :, at % 16] = c.k[1, pg, :, at % 16], c.v[1, pg, :, at % 16]
+    assert torch.equal(c.k.view(torch.int16), k0.view(torch.int16)) and torch.equal(c.v.view(torch.int16), v0.view(torch.int16))
 
 
 # ---------------------------------------------------------------------------
