@@ -541,6 +541,110 @@ def test_append_normed_bad_pages_and_lengths(pkg):
     assert torch.equal(c.k.view(torch.int16), k0.view(torch.int16)) and torch.equal(c.v.view(torch.int16), v0.view(torch.int16))
 
 
+def test_pages_behind_two_to_the_31_elements(pkg):
+    """Offsets that do not fit 32 bits: three layers of 2^30 elements each, the work in the last one; eviction in all."""
+    c = Grouped(torch.float16, 4, 2, 64, 256, [(2, 600), (1, 300)], [40, 500], [1, 30], layers=3, spare=2 ** 15 - 20, seed=31)
+    assert c.k.numel() > 2 ** 31 and c.k[:2].numel() * 2 > 2 ** 31
+    kv = pkg.PagedKV(c.k, c.v, 4)
+    n = c.starts[-1]
+    q, k, v, w = c.q.clone(), c.randn(c.rows, 2, 64), c.randn(c.rows, 2, 64), torch.ones(64, device=DEV)
+    kv.append(2, c.batch(kv), k, v, q=q, q_out=c.q, q_norm=w, k_norm=w, eps=1e-6)
+    torch.cuda.synchronize()
+    for x, y in ((torch.cat([c.get(c.k, 2, b, a + t)[a:] for b, (a, t) in enumerate(zip(c.ctx, c.new))]), k[:n]), (c.q[:n], q[:n])):
+        y = y.double() / torch.sqrt((y.double() ** 2).mean(2, keepdim=True) + 1e-6)
+        assert ((x.double() - y).abs() <= (2.0 ** -11 + 2.0 ** -19) * y.abs() + 2.0 ** -25).all()
+    out, lse, _ = run_shared(pkg, c, kv=kv, layer=2)
+    check_shared(c, (out, lse), reference(c, layer=2))
+    mass = torch.rand(3, 3, 2, 1200, generator=c.g, device=DEV)
+    before = mass[2].clone()
+    kv.weigh(2, c.batch(kv), c.q, lse, mass[2], mass[2], decay=0.75, gain=0.5)
+    want, tol = weigh_reference(c, lse, before, 0.75, 0.5, layer=2)
+    assert ((mass[2].double() - want).abs() <= tol).all()
+    pos = torch.rand(3, 3, 2, 1200, generator=c.g, device=DEV).argsort(3).int()
+    length, keep = [a + t for a, t in zip(c.ctx, c.new)], [620, 600, 341 - 4]
+    first = [512, 512, 0]                              # the pages that the group shares
+    want = evict_want(c.k, c.v, c.table, length, mass, pos, keep, 9, first, 256)
+    new = ints([0, 0, 0])
+    kv.evict(c.table, ints(length), mass, pos, ints(keep), mass, pos, new, protect=9, first=ints(first))
+    assert kv.status() == 0 and new.tolist() == keep
+    assert torch.equal(c.k.view(torch.int16), want[0].view(torch.int16)) and torch.equal(c.v.view(torch.int16), want[1].view(torch.int16))
+    for (l, b, h), m in want[2].items():
+        assert torch.equal(mass[l, b, h, :len(m)], m) and torch.equal(pos[l, b, h, :len(m)], want[3][l, b, h])
+
+
+def test_the_most_sequences(pkg):
+    """65536 sequences in groups of four behind 128 tokens, up to 40 of their own: append, attend, weigh, evict."""
+    B, H, heads, d, page, n = 65536, 1, 2, 64, 16, 176
+    g = torch.Generator(device=DEV).manual_seed(2)
+    G = B // 4
+    own = torch.randint(0, 40, (B,), generator=g, device=DEV, dtype=torch.int32)
+    ctx = own + 128
+    pages = G * 8 + B * 3
+    order = torch.randperm(pages, generator=g, device=DEV).int()
+    table = torch.cat([order[:G * 8].view(G, 1, 8).expand(G, 4, 8).reshape(B, 8), order[G * 8:].view(B, 3)], 1).contiguous()
+    k, v = (torch.randn(1, pages, H, page, d, generator=g, device=DEV).half() for _ in range(2))
+    kv = pkg.PagedKV(k, v, heads)
+    qkv = torch.randn(B, heads + 2 * H, d, generator=g, device=DEV).half()
+    q, w = torch.empty(B, heads, d, dtype=torch.float16, device=DEV), torch.ones(d, device=DEV)
+    batch = kv.batch(table, ctx, torch.arange(B + 1, dtype=torch.int32, device=DEV))
+    prefix = kv.prefix(torch.arange(0, B + 1, 4, dtype=torch.int32, device=DEV), torch.full((G,), 128, dtype=torch.int32, device=DEV), B)
+    kv.append(0, batch, qkv[:, heads:heads + H], qkv[:, heads + H:], q=qkv[:, :heads], q_out=q, q_norm=w)
+    out, lse = torch.empty_like(q), torch.empty(B, heads, device=DEV)
+    kv.attend(0, batch, q, out, lse=lse, prefix=prefix)
+    mass = torch.rand(B, H, n, generator=g, device=DEV)
+    mass0, pos = mass.clone(), torch.arange(n, dtype=torch.int32, device=DEV).expand(B, H, n).contiguous()
+    kv.weigh(0, batch, q, lse, mass, mass, pos, decay=0.5, gain=0.25)
+    assert kv.status() == 0
+    row, at = torch.arange(B, device=DEV), torch.arange(n, device=DEV)
+    y = qkv[:, :heads].double()
+    y = y / torch.sqrt((y * y).mean(2, keepdim=True) + 1e-6)
+    assert ((q.double() - y).abs() <= (2.0 ** -11 + 2.0 ** -19) * y.abs() + 2.0 ** -25).all()
+    u, scale = 2.0 ** -11, d ** -0.5
+    for lo in range(0, B, 8192):
+        s = slice(lo, lo + 8192)
+        K, V = (x[0][table[s].long()].transpose(1, 2).reshape(8192, n, d).double() for x in (k, v))
+        assert torch.equal(K[torch.arange(8192, device=DEV), ctx[s].long()], qkv[s, heads].double())
+        z = torch.einsum("bhd,bnd->bhn", q[s].double(), K) * scale
+        z = torch.where(at <= ctx[s, None, None], z, -math.inf)
+        p = torch.softmax(z, 2)
+        o, A = torch.einsum("bhn,bnd->bhd", p, V), torch.einsum("bhn,bnd->bhd", p, V.abs())
+        # scale sum |q k| <= scale |q| |k|, |q| = sqrt(d) of a normed row
+        ds = (d + 4) * 2.0 ** -23 * float(K.norm(dim=2).amax()) * 1.001
+        assert ((out[s].double() - o).abs() <= u * o.abs() + (u + 2 * ds + n * 2.0 ** -23) * A + n * 2.0 ** -25 * float(V.abs().amax()) + 2.0 ** -20 * float(V.abs().amax())).all()
+        total = torch.logsumexp(z, 2)
+        assert ((lse[s].double() - total).abs() <= ds + n * 2.0 ** -23 + 2.0 ** -22 * (1 + total.abs()) + 2.0 ** -20).all()
+        wt = torch.where(at <= ctx[s, None, None], (z - lse[s].double()[..., None]).exp(), 0.0)
+        err = (wt * (2 * ds + 2.0 ** -21 * (1 + torch.where(z == -math.inf, 0.0, z).abs() + total.abs()[..., None]) + heads * 2.0 ** -24) + 2.0 ** -126).sum(1)
+        old = torch.where(at < ctx[s, None], 0.5 * mass0[s, 0].double(), 0.0)
+        want = torch.where(at <= ctx[s, None], old + 0.25 * wt.sum(1), mass0[s, 0].double())
+        tol = torch.where(at <= ctx[s, None], 0.25 * err + 2.0 ** -22 * want.abs(), 0.0)
+        assert ((mass[s, 0].double() - want).abs() <= tol).all()
+    assert (pos == at.int()).all()
+    # each keeps its prefix, its newest two and the largest of the rest, up to 140
+    keep, new = torch.full((B,), 140, dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    length = ctx + 1
+    k0, m0 = k.clone(), mass.clone()
+    mo, po = torch.zeros_like(mass), torch.full_like(pos, -1)
+    kv.evict(table, length, mass[None], pos[None], keep, mo[None], po[None], new, protect=2, first=torch.full((B,), 128, dtype=torch.int32, device=DEV))
+    assert kv.status() == 0 and torch.equal(new, torch.minimum(length, keep)) and torch.equal(mass, m0)
+    rank = torch.where(at[None] > ctx[:, None] - 2, 1e200, mass[:, 0].double())
+    rank = torch.where(at < 128, 1e300, rank)
+    rank = torch.where(at[None] < length[:, None], rank, -math.inf)
+    by = rank.sort(dim=1, descending=True, stable=True).indices
+    stays = torch.zeros(B, n, dtype=torch.bool, device=DEV).scatter_(1, by, at[None] < new[:, None])
+    assert torch.equal(po[:, 0].clamp(min=0).long().sum(1), (stays * at).sum(1))           # (positions are the places here)
+    live = at[None] < new[:, None]
+    assert (po[:, 0][~live] == -1).all()
+    assert torch.equal(mo[:, 0][live], mass[:, 0].gather(1, po[:, 0].clamp(min=0).long())[live])
+    still = live & stays
+    assert torch.equal(po[:, 0][still], at.int().expand(B, n)[still])
+    moved = (live & ~stays).nonzero()
+    fr = po[moved[:, 0], 0, moved[:, 1]].long()
+    assert torch.equal(k[0, table[moved[:, 0], moved[:, 1] // page].long(), 0, moved[:, 1] % page], k0[0, table[moved[:, 0], fr // page].long(), 0, fr % page])
+    shared = order[:G * 8].long()
+    assert torch.equal(k[:, shared], k0[:, shared])
+
+
 # ---------------------------------------------------------------------------
 # refusals
 # ---------------------------------------------------------------------------
