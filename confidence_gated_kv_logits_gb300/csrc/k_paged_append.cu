@@ -223,7 +223,7 @@ k_append(const Pool p, const AppendArgs a) {
 //
 // 4 prompts' chunks, 40 + 2 x 8 heads of 128 channels, three axes, bf16, 116 MB: 28.5 us,
 // 60% of the copy rate (append without norms 22.0).  Bound by issue slots (63% of active
-// cycles used) and the row's chain before its barrier.  Slower: paired arithmetic (31.3),
+// cycles used) and the row's chain before its barrier; without axis 30.6 (64 registers, 48 with it).  Slower: paired arithmetic (31.3),
 // 40 registers for six CTAs per SM (29.4), CTAs that take row after row with the next
 // one's place and sines found by two warps of their own (33.0).
 constexpr float kTiny = 7.888609052210118e-31f;      // 2^-100

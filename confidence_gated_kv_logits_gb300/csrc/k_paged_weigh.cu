@@ -4,11 +4,12 @@
 //
 // over the rows r (new tokens x the group's query heads) that see token t, with
 // the rows' lse as attend gave it: the weights are final at once, nothing is
-// rescaled, and each token's sum is one thread's, in one order.
+// rescaled.  Each token's sum is one thread's where one tile holds all rows; of several tiles
+// two threads take every second one each and join once: in one order either way.
 //
 // Tokens are the products' M (tiles of 128, full whatever the rows are) and query
 // rows their N (16 to 112), S = K Q^T in tensor memory: a thread owns a token, so
-// the sum over rows needs no other thread, a single token's few rows cost a
+// a tile's sum over rows needs no other thread, a single token's few rows cost a
 // product of N = 16, and there is little to join.  An item is some token tiles of
 // one KV head of one sequence: two where the rows need several tiles of up to 112
 // (whole new tokens, as the heads of a group lie side by side), which go by while K

@@ -213,7 +213,9 @@ int confkv_paged_attend(confkv_paged* kv, const confkv_paged_batch* batch, int l
  * prefix is left out: its rows stay as they were (CONFKV_FLAG_BAD_INDEX); that flag
  * too for starts that fall or leave 0 .. batch and for negative lengths.
  * Every row's result is joined from two parts, in fp32, the prefix's first: within
- * attend's precision, but not the same bits.
+ * attend's precision, but not the same bits.  Two launches in a row: faster than attend on
+ * the same tables where the prefixes' K and V, counted for every sequence, are more than
+ * L2 holds (some 130 MB) and rows are few; slower below that.
  */
 typedef struct confkv_paged_prefix {
   int32_t groups;              /* 1 .. batch */
@@ -241,8 +243,8 @@ int confkv_paged_attend_shared(confkv_paged* kv, const confkv_paged_batch* batch
  *        (`positions` [rows], or NULL: their places)
  *   scale: 0 means 1 / sqrt(head_dim)
  * gain 1, decay 1 add the weights up; gain (1 - decay) / (heads / kv_heads) makes
- * the running mean over the group's heads that confkv_step ranks by.  Sums are
- * fp32, in one order.  Sequences without new rows stay as they are, as do
+ * the running mean over the group's heads (confkv_step's is over all heads, and it ranks
+ * by more than that).  Sums are fp32, in one order.  Sequences without new rows stay as they are, as do
  * places from ctx_len + new tokens on.  Places from cap on are dropped
  * (CONFKV_FLAG_CAPACITY).  Every sequence's k is read through its own table from its
  * first token on, behind a shared prefix too: a page outside the pool, which
