@@ -300,7 +300,8 @@ class PagedKV(_Device):
         """Adds the attention weights of q's rows (lse as ``attend`` gave it) to each
         token's accumulated weight: mass_out = decay mass + gain sum, fp32 [batch,
         kv_heads, cap] (mass_out may be mass).  New tokens start from 0; pos int32
-        likewise receives their positions (int32 [rows]; None: their places).  A drafted
+        likewise receives their positions (int32 [rows]; None: their places).  Sequences
+        without new rows are not written, in a mass_out of its own either.  A drafted
         tree is weighed behind ``commit``, by its accepted rows alone."""
         if batch._index != self._index:
             raise ValueError("the batch's tensors are on another device")

@@ -244,9 +244,10 @@ int confkv_paged_attend_shared(confkv_paged* kv, const confkv_paged_batch* batch
  *   scale: 0 means 1 / sqrt(head_dim)
  * gain 1, decay 1 add the weights up; gain (1 - decay) / (heads / kv_heads) makes
  * the running mean over the group's heads (confkv_step's is over all heads, and it ranks
- * by more than that).  Sums are fp32, in one order.  Sequences without new rows stay as they are, as do
- * places from ctx_len + new tokens on.  Places from cap on are dropped
- * (CONFKV_FLAG_CAPACITY).  Every sequence's k is read through its own table from its
+ * by more than that).  Sums are fp32, in one order.  Nothing is written for sequences without new rows and
+ * for places from ctx_len + new tokens on: a mass_out of its own holds what it held there
+ * (a cache that goes on from step to step is weighed in place).  Places from cap on are
+ * dropped (CONFKV_FLAG_CAPACITY).  Every sequence's k is read through its own table from its
  * first token on, behind a shared prefix too: a page outside the pool, which
  * attend_shared would not look at, makes its tokens' masses NaN (CONFKV_FLAG_BAD_PAGE).
  * commit and fork move no masses.  A drafted tree is weighed behind commit, by the

@@ -215,6 +215,34 @@ def test_weigh_reads_every_sequences_own_pages(pkg):
     assert ((mass.double() - want).abs()[1:, :, 256:] <= tol[1:, :, 256:]).all()
 
 
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("heads,H,d,n,most,t", [
+    (40, 8, 128, 20, 4000, 22), (64, 8, 64, 24, 3000, 14), (16, 2, 128, 40, 3500, 14), (32, 32, 64, 12, 2500, 112), (5, 1, 128, 60, 9000, 3)])
+def test_weigh_many_tiles_an_item_by_trees(pkg, dt, heads, H, d, n, most, t):
+    """Items of eight token tiles (six tiles a CTA or more) and all rows in one tile of rows, causal and by the batch's mask."""
+    r = np.random.default_rng(n)
+    c = Case(DT[dt], heads, H, d, 64, [int(x) for x in r.integers(0, most, n)], [int(x) for x in r.integers(0, t + 1, n)], seed=n)
+    assert n * H * c.table.shape[1] * 64 >= 6 * 152 * 128
+    assert run_weigh(pkg, c, in_place=True)[1].status() == 0
+    assert run_weigh(pkg, c, tree_bits(c.new, 4))[1].status() == 0
+
+
+def test_weigh_writes_nothing_else(pkg):
+    """A mass_out of its own keeps what it held for sequences without rows and behind the new tokens."""
+    c = Case(torch.bfloat16, 10, 2, 64, 16, [300, 40, 0, 7], [2, 0, 5, 0], seed=2)
+    kv = pkg.PagedKV(c.k, c.v, 10)
+    lse = torch.randn(c.rows, 10, device=DEV) + 8
+    mass = torch.rand(4, 2, 320, generator=c.g, device=DEV)
+    out, pos = torch.full_like(mass, -5), torch.full((4, 2, 320), -9, dtype=torch.int32, device=DEV)
+    kv.weigh(1, c.batch(kv), c.q, lse, mass, out, pos)
+    assert kv.status() == 0
+    for b, (a, t) in enumerate(zip(c.ctx, c.new)):
+        n = a + t if t else 0
+        assert (out[b, :, :n] >= 0).all() and (out[b, :, n:] == -5).all()
+        assert (pos[b, :, :a] == -9).all() and (pos[b, :, a + t:] == -9).all()
+        assert torch.equal(pos[b, :, a:a + t], torch.arange(a, a + t, device=DEV).int().expand(2, t))
+
+
 # ---------------------------------------------------------------------------
 # eviction
 # ---------------------------------------------------------------------------
